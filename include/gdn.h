@@ -400,6 +400,227 @@ int gdn_backward(const gdn_desc *d,
                  float *ddt_bias, float *dnorm_w, float *dinitial_state,
                  void *workspace, size_t workspace_bytes, gdn_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Operators of the layers that stand beside the gated delta rule: a gated
+ * linear recurrence with one state value per channel, rotary positions, and
+ * group norm with an activation. They follow the conventions at the top of this
+ * file (device pointers, no allocation, no synchronisation, metadata checks
+ * only, a status word in the workspace where the device checks something). The
+ * pages describe none of them; their definitions stand here in full.
+ *
+ * Alignment: every tensor needs the alignment of its own element type; rows that
+ * are 16-byte aligned (base pointer, strides and row length) take the vector
+ * kernels, others element-wise ones with the same results.
+ */
+
+/*
+ * Gated linear recurrence. Per sequence and channel c, with the decay written as
+ * the gated delta rule's:
+ *     g_t     = -exp(A_log[c]) * softplus(a_t + dt_bias[c])      (<= 0)
+ *     alpha_t = exp(g_t)
+ *     u_t     = sqrt(1 - alpha_t^2) * sigmoid(b_t) * x_t
+ *     h_t     = alpha_t * h_{t-1} + u_t,        out_t = h_t
+ * h before a sequence's first token is its initial state (zeros without one).
+ * Gates, state and every sum are fp32; out is h rounded once. Results are
+ * run-to-run identical.
+ */
+#define GDN_RECURRENCE_CHUNK 64 /* tokens between two rows of chunk_states */
+
+typedef struct {
+    int32_t B, T;        /* batch rows, tokens per row; with cu_seqlens: B = 1 and
+                            T = total packed tokens */
+    int32_t N;           /* sequences: B without cu_seqlens, else cu_seqlens has N+1 entries */
+    int32_t D;           /* channels */
+    int32_t dtype;       /* gdn_dtype of x, a, b, out and their gradients */
+    int32_t reserved0;
+    /* (batch, token) element strides; channel stride is 1 */
+    int64_t x_stride_b, x_stride_t;
+    int64_t a_stride_b, a_stride_t;
+    int64_t b_stride_b, b_stride_t;
+} gdn_recurrence_desc;
+
+/* Fill *d for contiguous x, a, b [B,T,D]. packed as in gdn_desc_init. Returns the
+ * validation status of the filled descriptor. */
+int gdn_recurrence_desc_init(gdn_recurrence_desc *d, int B, int T, int packed, int D, int dtype);
+
+/* Bytes of workspace of the forward (a status word) and of the backward (the
+ * status word, partial sums of the parameter gradients, chunk states). */
+int gdn_recurrence_workspace_bytes(const gdn_recurrence_desc *d, size_t *bytes);
+int gdn_recurrence_backward_workspace_bytes(const gdn_recurrence_desc *d, size_t *bytes);
+
+/*
+ * Forward over B rows or packed sequences.
+ *   x, a, b        [B,T,D] at their strides
+ *   A_log, dt_bias fp32 [D]
+ *   cu_seqlens     NULL, or int32 [N+1] (then B == 1); sequences may be empty
+ *   initial_state  NULL (zeros) or fp32 [N][D]
+ *   out            [B,T,D] contiguous
+ *   final_state    NULL or fp32 [N][D]: h after each sequence's last token, its
+ *                  initial state (zeros without one) where it is empty
+ *   chunk_states   NULL or fp32 [B][ceil(T/64)][D]: the state carried into tokens
+ *                  0, 64, 128, ... of each row, for gdn_recurrence_backward
+ *   workspace      >= gdn_recurrence_workspace_bytes(), 256-byte aligned;
+ *                  gdn_device_status reads its status word
+ * x, a, b and out may be NULL when B*T == 0. initial_state and final_state may
+ * alias; other outputs must not overlap the inputs. A malformed cu_seqlens sets
+ * GDN_ERR_DEVICE_SEQLENS and nothing else is written.
+ */
+int gdn_recurrence_forward(const gdn_recurrence_desc *d, const void *x, const void *a, const void *b,
+                           const float *A_log, const float *dt_bias, const int32_t *cu_seqlens,
+                           const float *initial_state, void *out, float *final_state,
+                           float *chunk_states, void *workspace, size_t workspace_bytes,
+                           gdn_stream_t stream);
+
+/*
+ * Gradients of sum(grad_out * out) + sum(grad_final * final_state).
+ *   chunk_states   as written by the forward of the same inputs, or NULL: the call
+ *                  then recomputes them in its workspace (one more pass over x, a, b)
+ *   grad_out       [B,T,D] contiguous; grad_final NULL (zeros) or fp32 [N][D]
+ *   dx, da, db     [B,T,D] contiguous, act dtype
+ *   dA_log, ddt_bias  fp32 [D], sums over all tokens in a fixed order
+ *   dinitial_state NULL or fp32 [N][D]; grad_final's row where a sequence is empty
+ *   workspace      >= gdn_recurrence_backward_workspace_bytes(), 256-byte aligned
+ * Outputs are written in full. Where g_t = 0 in fp32 (no decay, so no write), the
+ * derivative of sqrt(1 - alpha^2) is taken as its limit in a, 0.
+ */
+int gdn_recurrence_backward(const gdn_recurrence_desc *d, const void *x, const void *a, const void *b,
+                            const float *A_log, const float *dt_bias, const int32_t *cu_seqlens,
+                            const float *initial_state, const float *chunk_states,
+                            const void *grad_out, const float *grad_final, void *dx, void *da,
+                            void *db, float *dA_log, float *ddt_bias, float *dinitial_state,
+                            void *workspace, size_t workspace_bytes, gdn_stream_t stream);
+
+/*
+ * One more token of each of B sequences (d->T == 1, N == B): the state, fp32
+ * [B][D], is read and overwritten with h; out [B,1,D] contiguous. No workspace.
+ */
+int gdn_recurrence_step(const gdn_recurrence_desc *d, const void *x, const void *a, const void *b,
+                        const float *A_log, const float *dt_bias, float *state, void *out,
+                        gdn_stream_t stream);
+
+/*
+ * Rotary positions. The first `rot` channels of every head are rotated in pairs
+ * (x1, x2) by the angle of the token's position p and the pair's index i:
+ *     y1 = scale * (x1 cos - x2 sin),  y2 = scale * (x2 cos + x1 sin),
+ * with sin negated for inverse != 0 (the gradient of the rotation, and its undoing
+ * when scale is 1). The other channels are copied. The angle is 2 pi times the
+ * fraction of p * turns[i] / 2^64: the product wraps in 64 bits, so far positions
+ * lose nothing.
+ */
+typedef enum {
+    GDN_ROTARY_HALF = 0,        /* pairs (i, i + rot/2) */
+    GDN_ROTARY_INTERLEAVED = 1  /* pairs (2i, 2i + 1) */
+} gdn_rotary_layout;
+typedef enum {
+    GDN_ROTARY_PLAIN = 0,    /* f_i = theta^(-2i/rot) radians per position */
+    GDN_ROTARY_LINEAR = 1,   /* f_i / factor */
+    GDN_ROTARY_BY_PARTS = 2  /* keep_i f_i + (1 - keep_i) f_i / factor, where keep_i =
+                                clamp((r_i - low) / (high - low), 0, 1) and r_i =
+                                original * f_i / (2 pi), the pair's turns over the
+                                original context */
+} gdn_rotary_scaling;
+
+typedef struct {
+    int32_t B, T, N;     /* as in gdn_recurrence_desc */
+    int32_t Hq, Hk;      /* heads of q and of k; Hk = 0: no k */
+    int32_t d;           /* channels per head */
+    int32_t rot;         /* rotated channels per head: even, 2..d */
+    int32_t layout;      /* gdn_rotary_layout */
+    int32_t inverse;     /* 0 or 1 */
+    int32_t dtype;       /* gdn_dtype of q, k and their outputs */
+    float scale;         /* 1, or the attention factor of a scaled table */
+    int32_t reserved0;
+    /* (batch, token) element strides; a token's heads and channels are contiguous */
+    int64_t q_stride_b, q_stride_t, k_stride_b, k_stride_t;
+    int64_t q_out_stride_b, q_out_stride_t, k_out_stride_b, k_out_stride_t;
+} gdn_rotary_desc;
+
+/* Fill *d for contiguous q [B,T,Hq*d], k [B,T,Hk*d] and outputs, rot = d (d - 1
+ * where d is odd), half layout, inverse 0, scale 1. Returns the validation status. */
+int gdn_rotary_desc_init(gdn_rotary_desc *d, int B, int T, int packed, int Hq, int Hk, int head_dim,
+                         int dtype);
+
+/* Host function: the rot/2 table entries f_i / (2 pi) turns per position in units
+ * of 2^-64 turns, from fp64 arithmetic, into the HOST array `turns`. factor, low,
+ * high and original are read by the scalings that use them. Returns
+ * GDN_ERR_INVALID_ARG for an odd or non-positive rot, theta <= 0, factor <= 0,
+ * high <= low or original <= 0. */
+int gdn_rotary_table(int rot, double theta, int scaling, double factor, double low, double high,
+                     double original, uint64_t *turns);
+
+int gdn_rotary_workspace_bytes(const gdn_rotary_desc *d, size_t *bytes);
+
+/*
+ *   q, k           [B,T,H*d] at their strides (k and k_out NULL when Hk == 0)
+ *   turns          device uint64 [rot/2] (gdn_rotary_table)
+ *   positions      NULL, or int32 [B][T] contiguous: the tokens' positions (any sign)
+ *   cu_seqlens     NULL, or int32 [N+1] (then B == 1): without `positions`, a token's
+ *                  position counts from its sequence's first token
+ *   offsets        NULL, or int32 [N]: added to the positions of sequence n's tokens
+ *                  (the length of its cache, for instance); not together with `positions`
+ *   q_out, k_out   may be q and k themselves (same strides), else must not overlap them
+ *   workspace      >= gdn_rotary_workspace_bytes(), 256-byte aligned (status word). A
+ *                  malformed cu_seqlens sets GDN_ERR_DEVICE_SEQLENS and q_out, k_out
+ *                  are not written.
+ */
+int gdn_rotary(const gdn_rotary_desc *d, const void *q, const void *k, const uint64_t *turns,
+               const int32_t *positions, const int32_t *cu_seqlens, const int32_t *offsets,
+               void *q_out, void *k_out, void *workspace, size_t workspace_bytes,
+               gdn_stream_t stream);
+
+/*
+ * Group norm with an activation, channels last. For every instance n and group of
+ * C/G adjacent channels, mean and (biased) variance over the instance's L positions
+ * and the group's channels; then
+ *     xh = (x - mean) * rsqrt(var + eps),  z = weight[c] * xh + bias[c],
+ *     out = z (GDN_ACT_NONE) or z * sigmoid(z) (GDN_ACT_SILU).
+ * L = 1 is the per-token norm of a layer's heads. All arithmetic is fp32; out is
+ * rounded once. Results are run-to-run identical.
+ */
+typedef enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 } gdn_activation;
+
+typedef struct {
+    int32_t N, L;          /* instances, positions per instance (either may be 0) */
+    int32_t C, G;          /* channels, groups (C % G == 0) */
+    int32_t dtype;         /* gdn_dtype of x, out, grad_out, dx */
+    int32_t weight_dtype;  /* of weight and bias: dtype, or GDN_F32 */
+    int32_t act;           /* gdn_activation */
+    float eps;             /* 1e-5 */
+    int64_t x_stride_n, x_stride_l; /* element strides of x; channel stride is 1 */
+} gdn_group_norm_desc;
+
+/* Fill *d for contiguous x [N,L,C], weight in the act dtype, SiLU, eps 1e-5.
+ * Returns the validation status. */
+int gdn_group_norm_desc_init(gdn_group_norm_desc *d, int N, int L, int C, int G, int dtype);
+int gdn_group_norm_workspace_bytes(const gdn_group_norm_desc *d, size_t *bytes);
+int gdn_group_norm_backward_workspace_bytes(const gdn_group_norm_desc *d, size_t *bytes);
+
+/*
+ *   x            [N,L,C] at its strides
+ *   weight, bias [C] or NULL (ones, zeros)
+ *   out          [N,L,C] contiguous
+ *   mean, rstd   NULL, or fp32 [N][G]: the statistics, for the backward
+ *   workspace    >= gdn_group_norm_workspace_bytes(), 256-byte aligned
+ * out must not overlap x. Nothing is written when N*L == 0.
+ */
+int gdn_group_norm_forward(const gdn_group_norm_desc *d, const void *x, const void *weight,
+                           const void *bias, void *out, float *mean, float *rstd, void *workspace,
+                           size_t workspace_bytes, gdn_stream_t stream);
+
+/*
+ * Gradients of sum(grad_out * out), with mean and rstd from the forward of the same x.
+ *   grad_out       [N,L,C] contiguous
+ *   dx             [N,L,C] contiguous
+ *   dweight, dbias NULL, or fp32 [C] (written also when weight or bias is NULL; zeros
+ *                  when N*L == 0)
+ *   workspace      >= gdn_group_norm_backward_workspace_bytes(), 256-byte aligned
+ */
+int gdn_group_norm_backward(const gdn_group_norm_desc *d, const void *x, const void *weight,
+                            const void *bias, const float *mean, const float *rstd,
+                            const void *grad_out, void *dx, float *dweight, float *dbias,
+                            void *workspace, size_t workspace_bytes, gdn_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

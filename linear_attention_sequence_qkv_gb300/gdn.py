@@ -37,7 +37,19 @@ EXPORTS = ("gdn_desc_init", "gdn_workspace_bytes", "gdn_workspace_offsets", "gdn
            "gdn_status_string", "gdn_chunk_kernel_kind", "gdn_forward_static_ws",
            "gdn_static_ws_device_status", "gdn_set_wait_test_mode",
            "gdn_decode_workspace_bytes", "gdn_decode_step", "gdn_backward_workspace_bytes",
-           "gdn_backward", "gdn_forward_with_prefix", "gdn_span_scan")
+           "gdn_backward", "gdn_forward_with_prefix", "gdn_span_scan",
+           "gdn_recurrence_desc_init", "gdn_recurrence_workspace_bytes",
+           "gdn_recurrence_backward_workspace_bytes", "gdn_recurrence_forward",
+           "gdn_recurrence_backward", "gdn_recurrence_step", "gdn_rotary_desc_init",
+           "gdn_rotary_table", "gdn_rotary_workspace_bytes", "gdn_rotary",
+           "gdn_group_norm_desc_init", "gdn_group_norm_workspace_bytes",
+           "gdn_group_norm_backward_workspace_bytes", "gdn_group_norm_forward",
+           "gdn_group_norm_backward")
+
+GDN_RECURRENCE_CHUNK = 64
+ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
+ROTARY_SCALINGS = {"plain": 0, "linear": 1, "by_parts": 2}
+ACTIVATIONS = {"none": 0, "silu": 1}
 
 # bytes of the library's fixed device scratch used by gdn_forward_static_ws
 GDN_STATIC_WORKSPACE_BYTES = 16 * 1024 * 1024
@@ -70,6 +82,24 @@ class gdn_desc(ctypes.Structure):
 class gdn_workspace_layout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in
                 ("status", "chunk_off", "q", "k", "v", "beta", "gamma", "o", "tpt", "total")]
+
+
+class gdn_recurrence_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "N", "D", "dtype", "reserved0")] + [
+        (n, ctypes.c_int64) for n in ("x_stride_b", "x_stride_t", "a_stride_b", "a_stride_t", "b_stride_b",
+                                      "b_stride_t")]
+
+
+class gdn_rotary_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "N", "Hq", "Hk", "d", "rot", "layout", "inverse", "dtype")] + [
+        ("scale", ctypes.c_float), ("reserved0", ctypes.c_int32)] + [
+        (n, ctypes.c_int64) for n in ("q_stride_b", "q_stride_t", "k_stride_b", "k_stride_t", "q_out_stride_b",
+                                      "q_out_stride_t", "k_out_stride_b", "k_out_stride_t")]
+
+
+class gdn_group_norm_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("N", "L", "C", "G", "dtype", "weight_dtype", "act")] + [
+        ("eps", ctypes.c_float), ("x_stride_n", ctypes.c_int64), ("x_stride_l", ctypes.c_int64)]
 
 
 _lib = None
@@ -105,6 +135,23 @@ def load(path: str = LIB_PATH):
     L.gdn_span_scan.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp]
     L.gdn_backward_workspace_bytes.argtypes = [dp, ctypes.POINTER(sz)]
     L.gdn_backward.argtypes = [dp] + [vp] * 25 + [vp, sz, vp]
+    rp, tp, np_ = (ctypes.POINTER(c) for c in (gdn_recurrence_desc, gdn_rotary_desc, gdn_group_norm_desc))
+    f64, szp = ctypes.c_double, ctypes.POINTER(sz)
+    L.gdn_recurrence_desc_init.argtypes = [rp] + [i32] * 5
+    L.gdn_recurrence_workspace_bytes.argtypes = [rp, szp]
+    L.gdn_recurrence_backward_workspace_bytes.argtypes = [rp, szp]
+    L.gdn_recurrence_forward.argtypes = [rp] + [vp] * 10 + [vp, sz, vp]
+    L.gdn_recurrence_backward.argtypes = [rp] + [vp] * 16 + [vp, sz, vp]
+    L.gdn_recurrence_step.argtypes = [rp] + [vp] * 7 + [vp]
+    L.gdn_rotary_desc_init.argtypes = [tp] + [i32] * 7
+    L.gdn_rotary_table.argtypes = [i32, f64, i32, f64, f64, f64, f64, vp]
+    L.gdn_rotary_workspace_bytes.argtypes = [tp, szp]
+    L.gdn_rotary.argtypes = [tp] + [vp] * 8 + [vp, sz, vp]
+    L.gdn_group_norm_desc_init.argtypes = [np_] + [i32] * 5
+    L.gdn_group_norm_workspace_bytes.argtypes = [np_, szp]
+    L.gdn_group_norm_backward_workspace_bytes.argtypes = [np_, szp]
+    L.gdn_group_norm_forward.argtypes = [np_] + [vp] * 6 + [vp, sz, vp]
+    L.gdn_group_norm_backward.argtypes = [np_] + [vp] * 9 + [vp, sz, vp]
     for name in EXPORTS:
         if name != "gdn_status_string":
             getattr(L, name).restype = i32
@@ -300,6 +347,117 @@ def gdn_backward(d, q_raw, k_raw, v_raw, a, b, gate, conv_w, A_log, dt_bias, nor
     return rc
 
 
+def _query(name, d) -> int:
+    n = ctypes.c_size_t(0)
+    _check(getattr(load(), name)(ctypes.byref(d), ctypes.byref(n)), name)
+    return n.value
+
+
+def gdn_recurrence_desc_init(B, T, packed, D, dtype) -> gdn_recurrence_desc:
+    d = gdn_recurrence_desc()
+    _check(load().gdn_recurrence_desc_init(ctypes.byref(d), B, T, packed, D, dtype), "gdn_recurrence_desc_init")
+    return d
+
+
+def gdn_recurrence_workspace_bytes(d) -> int:
+    return _query("gdn_recurrence_workspace_bytes", d)
+
+
+def gdn_recurrence_backward_workspace_bytes(d) -> int:
+    return _query("gdn_recurrence_backward_workspace_bytes", d)
+
+
+def gdn_recurrence_forward(d, x, a, b, A_log, dt_bias, cu_seqlens, initial_state, out, final_state, chunk_states,
+                           workspace, workspace_bytes, stream=None, check=True) -> int:
+    rc = load().gdn_recurrence_forward(ctypes.byref(d), _ptr(x), _ptr(a), _ptr(b), _ptr(A_log), _ptr(dt_bias),
+                                       _ptr(cu_seqlens), _ptr(initial_state), _ptr(out), _ptr(final_state),
+                                       _ptr(chunk_states), _ptr(workspace), int(workspace_bytes), _stream(stream))
+    if check:
+        _check(rc, "gdn_recurrence_forward")
+    return rc
+
+
+def gdn_recurrence_backward(d, x, a, b, A_log, dt_bias, cu_seqlens, initial_state, chunk_states, grad_out, grad_final,
+                            dx, da, db, dA_log, ddt_bias, dinitial_state, workspace, workspace_bytes, stream=None,
+                            check=True) -> int:
+    rc = load().gdn_recurrence_backward(ctypes.byref(d), _ptr(x), _ptr(a), _ptr(b), _ptr(A_log), _ptr(dt_bias),
+                                        _ptr(cu_seqlens), _ptr(initial_state), _ptr(chunk_states), _ptr(grad_out),
+                                        _ptr(grad_final), _ptr(dx), _ptr(da), _ptr(db), _ptr(dA_log), _ptr(ddt_bias),
+                                        _ptr(dinitial_state), _ptr(workspace), int(workspace_bytes), _stream(stream))
+    if check:
+        _check(rc, "gdn_recurrence_backward")
+    return rc
+
+
+def gdn_recurrence_step(d, x, a, b, A_log, dt_bias, state, out, stream=None, check=True) -> int:
+    rc = load().gdn_recurrence_step(ctypes.byref(d), _ptr(x), _ptr(a), _ptr(b), _ptr(A_log), _ptr(dt_bias),
+                                    _ptr(state), _ptr(out), _stream(stream))
+    if check:
+        _check(rc, "gdn_recurrence_step")
+    return rc
+
+
+def gdn_rotary_desc_init(B, T, packed, Hq, Hk, d, dtype) -> gdn_rotary_desc:
+    r = gdn_rotary_desc()
+    _check(load().gdn_rotary_desc_init(ctypes.byref(r), B, T, packed, Hq, Hk, d, dtype), "gdn_rotary_desc_init")
+    return r
+
+
+def gdn_rotary_table(rot, theta, scaling, factor, low, high, original, turns) -> None:
+    """Fill ``turns``, a HOST int64 tensor of rot/2 entries (the bits of the uint64 table)."""
+    if turns.device.type != "cpu" or turns.dtype != torch.int64 or not turns.is_contiguous() or turns.numel() < rot // 2:
+        raise ValueError("turns: a contiguous host int64 tensor of rot/2 entries")
+    _check(load().gdn_rotary_table(int(rot), float(theta), int(scaling), float(factor), float(low), float(high),
+                                   float(original), _ptr(turns)), "gdn_rotary_table")
+
+
+def gdn_rotary_workspace_bytes(d) -> int:
+    return _query("gdn_rotary_workspace_bytes", d)
+
+
+def gdn_rotary(d, q, k, turns, positions, cu_seqlens, offsets, q_out, k_out, workspace, workspace_bytes, stream=None,
+               check=True) -> int:
+    rc = load().gdn_rotary(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(turns), _ptr(positions), _ptr(cu_seqlens),
+                           _ptr(offsets), _ptr(q_out), _ptr(k_out), _ptr(workspace), int(workspace_bytes),
+                           _stream(stream))
+    if check:
+        _check(rc, "gdn_rotary")
+    return rc
+
+
+def gdn_group_norm_desc_init(N, L, C, G, dtype) -> gdn_group_norm_desc:
+    d = gdn_group_norm_desc()
+    _check(load().gdn_group_norm_desc_init(ctypes.byref(d), N, L, C, G, dtype), "gdn_group_norm_desc_init")
+    return d
+
+
+def gdn_group_norm_workspace_bytes(d) -> int:
+    return _query("gdn_group_norm_workspace_bytes", d)
+
+
+def gdn_group_norm_backward_workspace_bytes(d) -> int:
+    return _query("gdn_group_norm_backward_workspace_bytes", d)
+
+
+def gdn_group_norm_forward(d, x, weight, bias, out, mean, rstd, workspace, workspace_bytes, stream=None,
+                           check=True) -> int:
+    rc = load().gdn_group_norm_forward(ctypes.byref(d), _ptr(x), _ptr(weight), _ptr(bias), _ptr(out), _ptr(mean),
+                                       _ptr(rstd), _ptr(workspace), int(workspace_bytes), _stream(stream))
+    if check:
+        _check(rc, "gdn_group_norm_forward")
+    return rc
+
+
+def gdn_group_norm_backward(d, x, weight, bias, mean, rstd, grad_out, dx, dweight, dbias, workspace, workspace_bytes,
+                            stream=None, check=True) -> int:
+    rc = load().gdn_group_norm_backward(ctypes.byref(d), _ptr(x), _ptr(weight), _ptr(bias), _ptr(mean), _ptr(rstd),
+                                        _ptr(grad_out), _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(workspace),
+                                        int(workspace_bytes), _stream(stream))
+    if check:
+        _check(rc, "gdn_group_norm_backward")
+    return rc
+
+
 # --------------------------------------------------- tensors -> descriptor
 def desc_for(q_raw, k_raw, v_raw, a, b, gate, norm_w, *, Hk, Hv, dk, dv,
              cu_seqlens=None, l2_eps=1e-6, norm_eps=1e-5, scale=1.0) -> gdn_desc:
@@ -426,4 +584,316 @@ def backward(inp, grad_out, grad_final=None, grads: Optional[Grads] = None, stre
                  grads.dq_raw, grads.dk_raw, grads.dv_raw, grads.da, grads.db, grads.dgate, grads.dconv_w,
                  grads.dA_log, grads.ddt_bias, grads.dnorm_w, grads.dinitial_state, grads.workspace,
                  grads.workspace.numel(), stream)
+    return grads
+
+
+# ------------------------- operators beside the gated delta rule, on tensors
+def _expect(t, name, shape, dtype, device, contiguous=True):
+    """One tensor argument of the functions below: what a kernel would take on trust is checked here."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+
+
+def _strides(t, name):
+    """(batch, token) element strides of a [B, T, C] view. A dimension of one element has no
+    stride of its own, whatever torch reports for it."""
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name}: a [B, T, C] view with contiguous channels")
+    st = t.stride(1) if t.shape[1] > 1 else t.shape[2]
+    return t.stride(0) if t.shape[0] > 1 else st * t.shape[1], st
+
+
+def _on_current(t):
+    """The library launches on the current device: a tensor elsewhere is refused."""
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def recurrence_desc_for(x, a, b, cu_seqlens=None) -> gdn_recurrence_desc:
+    """Descriptor of the gated linear recurrence over [B, T, D] views x, a, b."""
+    B, T, D = x.shape
+    for t, name in ((a, "a"), (b, "b")):
+        _expect(t, name, x.shape, x.dtype, x.device, contiguous=False)
+    d = gdn_recurrence_desc_init(B, T, 0 if cu_seqlens is None else cu_seqlens.numel() - 1, D, DTYPE_CODES[x.dtype])
+    for name, t in (("x", x), ("a", a), ("b", b)):
+        sb, st = _strides(t, name)
+        setattr(d, f"{name}_stride_b", sb)
+        setattr(d, f"{name}_stride_t", st)
+    return d
+
+
+@dataclass
+class RecurrenceBuffers:
+    desc: gdn_recurrence_desc
+    out: torch.Tensor
+    final_state: Optional[torch.Tensor]
+    chunk_states: Optional[torch.Tensor]
+    workspace: torch.Tensor
+
+    @property
+    def ws_bytes(self) -> int:
+        return self.workspace.numel()
+
+
+def alloc_recurrence(desc, device, want_final_state=True, want_chunk_states=False) -> RecurrenceBuffers:
+    """Output buffers of gdn_recurrence_forward; chunk_states are what its backward reads."""
+    f32 = dict(dtype=torch.float32, device=device)
+    chunks = -(-desc.T // GDN_RECURRENCE_CHUNK)
+    return RecurrenceBuffers(
+        desc, torch.empty((desc.B, desc.T, desc.D), dtype=ACT_TORCH[desc.dtype], device=device),
+        torch.empty((desc.N, desc.D), **f32) if want_final_state else None,
+        torch.empty((desc.B, chunks, desc.D), **f32) if want_chunk_states else None,
+        torch.empty(gdn_recurrence_workspace_bytes(desc), dtype=torch.uint8, device=device))
+
+
+@dataclass
+class RecurrenceGrads:
+    dx: torch.Tensor
+    da: torch.Tensor
+    db: torch.Tensor
+    dA_log: torch.Tensor
+    ddt_bias: torch.Tensor
+    dinitial_state: Optional[torch.Tensor]
+    workspace: torch.Tensor
+
+    @property
+    def ws_bytes(self) -> int:
+        return self.workspace.numel()
+
+
+def alloc_recurrence_grads(desc, device, want_dinitial=True) -> RecurrenceGrads:
+    """Gradient buffers and workspace of gdn_recurrence_backward."""
+    f32 = dict(dtype=torch.float32, device=device)
+    tok = lambda: torch.empty((desc.B, desc.T, desc.D), dtype=ACT_TORCH[desc.dtype], device=device)  # noqa: E731
+    return RecurrenceGrads(tok(), tok(), tok(), torch.empty(desc.D, **f32), torch.empty(desc.D, **f32),
+                           torch.empty((desc.N, desc.D), **f32) if want_dinitial else None,
+                           torch.empty(gdn_recurrence_backward_workspace_bytes(desc), dtype=torch.uint8, device=device))
+
+
+def _check_recurrence(d, x, A_log, dt_bias, cu_seqlens, initial_state):
+    _on_current(x)
+    for t, name in ((A_log, "A_log"), (dt_bias, "dt_bias")):
+        _expect(t, name, (d.D,), torch.float32, x.device)
+    _expect(cu_seqlens, "cu_seqlens", (d.N + 1,), torch.int32, x.device)
+    _expect(initial_state, "initial_state", (d.N, d.D), torch.float32, x.device)
+
+
+def recurrence_forward(x, a, b, A_log, dt_bias, cu_seqlens=None, initial_state=None, want_final_state=True,
+                       want_chunk_states=False, bufs: Optional[RecurrenceBuffers] = None,
+                       stream=None) -> RecurrenceBuffers:
+    """Gated linear recurrence (see gdn_recurrence_forward in include/gdn.h) of [B, T, D] views on the
+    GPU; packed sequences with cu_seqlens (int32 [N+1], B = 1). want_chunk_states keeps what
+    ``recurrence_backward`` can use."""
+    d = recurrence_desc_for(x, a, b, cu_seqlens)
+    _check_recurrence(d, x, A_log, dt_bias, cu_seqlens, initial_state)
+    if bufs is None:
+        bufs = alloc_recurrence(d, x.device, want_final_state, want_chunk_states)
+    else:
+        _expect(bufs.out, "bufs.out", (d.B, d.T, d.D), x.dtype, x.device)
+        _expect(bufs.final_state, "bufs.final_state", (d.N, d.D), torch.float32, x.device)
+        _expect(bufs.chunk_states, "bufs.chunk_states", (d.B, -(-d.T // GDN_RECURRENCE_CHUNK), d.D), torch.float32,
+                x.device)
+        bufs.desc = d
+    gdn_recurrence_forward(d, x, a, b, A_log, dt_bias, cu_seqlens, initial_state, bufs.out, bufs.final_state,
+                           bufs.chunk_states, bufs.workspace, bufs.ws_bytes, stream)
+    return bufs
+
+
+def recurrence_backward(x, a, b, A_log, dt_bias, grad_out, grad_final=None, chunk_states=None, cu_seqlens=None,
+                        initial_state=None, grads: Optional[RecurrenceGrads] = None, stream=None) -> RecurrenceGrads:
+    """Gradients of sum(grad_out * out) + sum(grad_final * final_state). chunk_states: the forward's of
+    the same inputs, or None (recomputed)."""
+    d = recurrence_desc_for(x, a, b, cu_seqlens)
+    _check_recurrence(d, x, A_log, dt_bias, cu_seqlens, initial_state)
+    _expect(grad_out, "grad_out", (d.B, d.T, d.D), x.dtype, x.device)
+    _expect(grad_final, "grad_final", (d.N, d.D), torch.float32, x.device)
+    _expect(chunk_states, "chunk_states", (d.B, -(-d.T // GDN_RECURRENCE_CHUNK), d.D), torch.float32, x.device)
+    if grads is None:
+        grads = alloc_recurrence_grads(d, x.device)
+    else:
+        for name in ("dx", "da", "db"):
+            _expect(getattr(grads, name), f"grads.{name}", (d.B, d.T, d.D), x.dtype, x.device)
+        for name in ("dA_log", "ddt_bias"):
+            _expect(getattr(grads, name), f"grads.{name}", (d.D,), torch.float32, x.device)
+        _expect(grads.dinitial_state, "grads.dinitial_state", (d.N, d.D), torch.float32, x.device)
+    gdn_recurrence_backward(d, x, a, b, A_log, dt_bias, cu_seqlens, initial_state, chunk_states, grad_out, grad_final,
+                            grads.dx, grads.da, grads.db, grads.dA_log, grads.ddt_bias, grads.dinitial_state,
+                            grads.workspace, grads.ws_bytes, stream)
+    return grads
+
+
+def recurrence_step(x, a, b, A_log, dt_bias, state, out=None, stream=None) -> torch.Tensor:
+    """One more token of each sequence: x, a, b [B, 1, D] views, state fp32 [B, D] updated in place."""
+    d = recurrence_desc_for(x, a, b)
+    _check_recurrence(d, x, A_log, dt_bias, None, None)
+    _expect(state, "state", (d.B, d.D), torch.float32, x.device)
+    if out is None:
+        out = torch.empty((d.B, d.T, d.D), dtype=x.dtype, device=x.device)
+    _expect(out, "out", (d.B, 1, d.D), x.dtype, x.device)
+    gdn_recurrence_step(d, x, a, b, A_log, dt_bias, state, out, stream)
+    return out
+
+
+def rotary_table(rot, theta=10000.0, scaling="plain", factor=1.0, low=1.0, high=4.0, original=8192, device="cuda"):
+    """The table of turns for ``rotary`` on ``device``: int64 [rot/2] holding the bits of the uint64
+    entries (see gdn_rotary_table and gdn_rotary_scaling in include/gdn.h)."""
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"scaling: one of {sorted(ROTARY_SCALINGS)}, not {scaling!r}")
+    turns = torch.empty(max(int(rot) // 2, 0), dtype=torch.int64)
+    gdn_rotary_table(rot, theta, ROTARY_SCALINGS[scaling], factor, low, high, original, turns)
+    return turns.to(device)
+
+
+def rotary_desc_for(q, k, q_out, k_out, *, d, rot=None, layout="half", inverse=False, scale=1.0,
+                    cu_seqlens=None) -> gdn_rotary_desc:
+    """Descriptor of ``rotary`` for [B, T, H*d] views (k and k_out None: no k)."""
+    if layout not in ROTARY_LAYOUTS:
+        raise ValueError(f"layout: one of {sorted(ROTARY_LAYOUTS)}, not {layout!r}")
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out: both or neither")
+    B, T = q.shape[:2]
+    for name, t, like in (("q_out", q_out, q), ("k_out", k_out, k)):
+        if like is not None:
+            _expect(t, name, like.shape, q.dtype, q.device, contiguous=False)
+    if k is not None:
+        _expect(k, "k", (B, T, k.shape[-1]), q.dtype, q.device, contiguous=False)
+    heads = []
+    for name, t in (("q", q), ("k", k)):
+        if t is not None and t.shape[-1] % d:
+            raise ValueError(f"{name}: {t.shape[-1]} channels, not a multiple of the head's {d}")
+        heads.append(0 if t is None else t.shape[-1] // d)
+    r = gdn_rotary_desc_init(B, T, 0 if cu_seqlens is None else cu_seqlens.numel() - 1, heads[0], heads[1], d,
+                             DTYPE_CODES[q.dtype])
+    for name, t in (("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out)):
+        if t is not None:
+            sb, st = _strides(t, name)
+            setattr(r, f"{name}_stride_b", sb)
+            setattr(r, f"{name}_stride_t", st)
+    r.rot = d if rot is None else rot
+    r.layout, r.inverse, r.scale = ROTARY_LAYOUTS[layout], int(bool(inverse)), scale
+    return r
+
+
+def rotary(q, k, table, *, d, rot=None, layout="half", inverse=False, scale=1.0, positions=None, cu_seqlens=None,
+           offsets=None, q_out=None, k_out=None, workspace=None, stream=None):
+    """Rotary positions of q and k (k may be None): (q_out, k_out), new tensors unless given; pass q and
+    k themselves to rotate in place. inverse=True is the gradient. positions int32 [B, T], or offsets
+    int32 [N] added to the positions counted from each sequence's start."""
+    _on_current(q)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    r = rotary_desc_for(q, k, q_out, k_out, d=d, rot=rot, layout=layout, inverse=inverse, scale=scale,
+                        cu_seqlens=cu_seqlens)
+    _expect(table, "table", (r.rot // 2,), torch.int64, q.device)
+    _expect(positions, "positions", (r.B, r.T), torch.int32, q.device)
+    _expect(cu_seqlens, "cu_seqlens", (r.N + 1,), torch.int32, q.device)
+    _expect(offsets, "offsets", (r.N,), torch.int32, q.device)
+    if workspace is None:
+        workspace = torch.empty(gdn_rotary_workspace_bytes(r), dtype=torch.uint8, device=q.device)
+    gdn_rotary(r, q, k, table, positions, cu_seqlens, offsets, q_out, k_out, workspace, workspace.numel(), stream)
+    return q_out, k_out
+
+
+def group_norm_desc_for(x, weight=None, *, groups, act="silu", eps=1e-5) -> gdn_group_norm_desc:
+    """Descriptor of the group norm of a [N, L, C] view."""
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act: one of {sorted(ACTIVATIONS)}, not {act!r}")
+    N, L, C = x.shape
+    d = gdn_group_norm_desc_init(N, L, C, groups, DTYPE_CODES[x.dtype])
+    d.x_stride_n, d.x_stride_l = _strides(x, "x")
+    if weight is not None:
+        d.weight_dtype = DTYPE_CODES[weight.dtype]
+    d.act, d.eps = ACTIVATIONS[act], eps
+    return d
+
+
+@dataclass
+class GroupNormBuffers:
+    desc: gdn_group_norm_desc
+    out: torch.Tensor
+    mean: Optional[torch.Tensor]
+    rstd: Optional[torch.Tensor]
+    workspace: torch.Tensor
+
+    @property
+    def ws_bytes(self) -> int:
+        return self.workspace.numel()
+
+
+def alloc_group_norm(desc, device) -> GroupNormBuffers:
+    f32 = dict(dtype=torch.float32, device=device)
+    return GroupNormBuffers(
+        desc, torch.empty((desc.N, desc.L, desc.C), dtype=ACT_TORCH[desc.dtype], device=device),
+        torch.empty((desc.N, desc.G), **f32), torch.empty((desc.N, desc.G), **f32),
+        torch.empty(gdn_group_norm_workspace_bytes(desc), dtype=torch.uint8, device=device))
+
+
+@dataclass
+class GroupNormGrads:
+    dx: torch.Tensor
+    dweight: Optional[torch.Tensor]
+    dbias: Optional[torch.Tensor]
+    workspace: torch.Tensor
+
+    @property
+    def ws_bytes(self) -> int:
+        return self.workspace.numel()
+
+
+def alloc_group_norm_grads(desc, device) -> GroupNormGrads:
+    f32 = dict(dtype=torch.float32, device=device)
+    return GroupNormGrads(torch.empty((desc.N, desc.L, desc.C), dtype=ACT_TORCH[desc.dtype], device=device),
+                          torch.empty(desc.C, **f32), torch.empty(desc.C, **f32),
+                          torch.empty(gdn_group_norm_backward_workspace_bytes(desc), dtype=torch.uint8, device=device))
+
+
+def _check_group_norm(d, x, weight, bias):
+    _on_current(x)
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        _expect(t, name, (d.C,), ACT_TORCH[d.weight_dtype], x.device)
+
+
+def group_norm_forward(x, weight=None, bias=None, *, groups, act="silu", eps=1e-5,
+                       bufs: Optional[GroupNormBuffers] = None, stream=None) -> GroupNormBuffers:
+    """Group norm with an activation of a [N, L, C] view (see gdn_group_norm_forward in include/gdn.h);
+    mean and rstd are kept for ``group_norm_backward``."""
+    d = group_norm_desc_for(x, weight if weight is not None else bias, groups=groups, act=act, eps=eps)
+    _check_group_norm(d, x, weight, bias)
+    if bufs is None:
+        bufs = alloc_group_norm(d, x.device)
+    else:
+        _expect(bufs.out, "bufs.out", x.shape, x.dtype, x.device)
+        for name in ("mean", "rstd"):
+            _expect(getattr(bufs, name), f"bufs.{name}", (d.N, d.G), torch.float32, x.device)
+        bufs.desc = d
+    gdn_group_norm_forward(d, x, weight, bias, bufs.out, bufs.mean, bufs.rstd, bufs.workspace, bufs.ws_bytes, stream)
+    return bufs
+
+
+def group_norm_backward(x, weight, bias, mean, rstd, grad_out, *, groups, act="silu", eps=1e-5,
+                        grads: Optional[GroupNormGrads] = None, stream=None) -> GroupNormGrads:
+    """Gradients of sum(grad_out * out) with the forward's mean and rstd."""
+    d = group_norm_desc_for(x, weight if weight is not None else bias, groups=groups, act=act, eps=eps)
+    _check_group_norm(d, x, weight, bias)
+    _expect(grad_out, "grad_out", x.shape, x.dtype, x.device)
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        _expect(t, name, (d.N, d.G), torch.float32, x.device)
+    if grads is None:
+        grads = alloc_group_norm_grads(d, x.device)
+    else:
+        _expect(grads.dx, "grads.dx", x.shape, x.dtype, x.device)
+        for name in ("dweight", "dbias"):
+            _expect(getattr(grads, name), f"grads.{name}", (d.C,), torch.float32, x.device)
+    gdn_group_norm_backward(d, x, weight, bias, mean, rstd, grad_out, grads.dx, grads.dweight, grads.dbias,
+                            grads.workspace, grads.ws_bytes, stream)
     return grads
