@@ -425,7 +425,7 @@ int gdn_backward(const gdn_desc *d,
  * Gates, state and every sum are fp32; out is h rounded once. Results are
  * run-to-run identical.
  */
-#define GDN_RECURRENCE_CHUNK 64 /* tokens between two rows of chunk_states */
+#define GDN_RECURRENCE_CHUNK 8 /* tokens between two rows of chunk_states */
 
 typedef struct {
     int32_t B, T;        /* batch rows, tokens per row; with cu_seqlens: B = 1 and
@@ -458,13 +458,14 @@ int gdn_recurrence_backward_workspace_bytes(const gdn_recurrence_desc *d, size_t
  *   out            [B,T,D] contiguous
  *   final_state    NULL or fp32 [N][D]: h after each sequence's last token, its
  *                  initial state (zeros without one) where it is empty
- *   chunk_states   NULL or fp32 [B][ceil(T/64)][D]: the state carried into tokens
- *                  0, 64, 128, ... of each row, for gdn_recurrence_backward
+ *   chunk_states   NULL or fp32 [B][ceil(T/8)][D]: the state carried into tokens
+ *                  0, 8, 16, ... of each row, for gdn_recurrence_backward
  *   workspace      >= gdn_recurrence_workspace_bytes(), 256-byte aligned;
  *                  gdn_device_status reads its status word
  * x, a, b and out may be NULL when B*T == 0. initial_state and final_state may
  * alias; other outputs must not overlap the inputs. A malformed cu_seqlens sets
- * GDN_ERR_DEVICE_SEQLENS and nothing else is written.
+ * GDN_ERR_DEVICE_SEQLENS and nothing else is written. Copies into shared memory are
+ * waited for about a second at most (GDN_ERR_DEVICE_TIMEOUT, results invalid).
  */
 int gdn_recurrence_forward(const gdn_recurrence_desc *d, const void *x, const void *a, const void *b,
                            const float *A_log, const float *dt_bias, const int32_t *cu_seqlens,

@@ -263,6 +263,7 @@ int forward_impl(const gdn_desc *d, const void *q_raw, const void *k_raw, const 
 }  // namespace
 
 namespace gdn {
+int wait_test_mode() { return g_wait_test_mode.load(); }
 int forward_single_stream(const gdn_desc *d, const void *q_raw, const void *k_raw, const void *v_raw,
                           const void *a, const void *b, const void *gate, const void *conv_w,
                           const float *A_log, const float *dt_bias, const void *norm_w,

@@ -986,6 +986,22 @@ bool encode_tile_map_pitch(CUtensorMap *m, const void *base, uint64_t rows, uint
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_token_map(CUtensorMap *m, int dtype, const void *base, uint64_t batch, uint64_t tokens, uint64_t channels,
+                      uint64_t pitch_b, uint64_t pitch_t, uint32_t box_t, uint32_t box_c) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {channels, tokens, batch};
+    const cuuint64_t strides[2] = {pitch_t, pitch_b};
+    const cuuint32_t box[3] = {box_c, box_t, 1};
+    const cuuint32_t es[3] = {1, 1, 1};
+    const CUtensorMapDataType type = dtype == GDN_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : dtype == GDN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return fn(m, type, 3, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool chunk_tc_supports(const gdn_desc &d) {
     return (d.dtype == GDN_BF16 || d.dtype == GDN_F16) && (d.dk == 64 || d.dk == 128 || d.dk == 256) &&
            d.dv >= 64 && d.dv % 64 == 0;

@@ -17,6 +17,9 @@ inline int check_workspace(const void *ws, size_t have, size_t need) {
     return ws && ptr_aligned(ws, 256) && have >= need ? GDN_OK : GDN_ERR_WORKSPACE;
 }
 
+// gdn_set_wait_test_mode's state (gdn_api.cu)
+int wait_test_mode();
+
 // Whole-block check of cu_seqlens: 0-based, non-decreasing, ending at T. Every
 // block of a launch reads the same N + 1 words (they stay in L2) and so comes to
 // the same answer; this costs no launch of its own. All threads must call it.

@@ -9,7 +9,7 @@
 // -expm1(-y) / y on [0, 1/2] are polynomials fitted here (weighted least squares to
 // the minimax relative error at Chebyshev nodes: 1.4e-7 and 5e-8 with fp32
 // evaluation). They run on the fp32 pipe as register pairs, which leaves five
-// special-function results per element (three e^x, one reciprocal, one square root).
+// special-function results per element (three e^x, one reciprocal, one root).
 #pragma once
 
 #include "gdn_common.cuh"
@@ -51,36 +51,39 @@ __device__ __forceinline__ float2 one_minus_exp_small(float2 y) {
     return mul2(y, p);
 }
 
-// Gates of two channels. rate2 = -exp(A_log) log2(e), so that G = log2(alpha).
-struct Gate2 {
-    float2 t;       // e^-|z|
-    float2 z;
-    float2 G;       // log2(alpha), <= 0
-    float2 alpha;
+// Decay of two channels from the gate input a. rate = exp(A_log).
+struct Decay2 {
+    float2 z, t;    // a + dt_bias, e^-|z|
+    float2 sp;      // softplus(z)
+    float2 alpha;   // e^-(rate sp)
     float2 w;       // 1 - alpha^2
-    float2 rs;      // 1 / sqrt(w), 0 where w is 0
-    float2 s;       // sqrt(w)
-    float2 beta;
 };
 
-__device__ __forceinline__ Gate2 gate2(float2 a, float2 b, float2 bias, float2 rate2) {
-    Gate2 r;
+__device__ __forceinline__ Decay2 decay2(float2 a, float2 bias, float2 rate) {
+    Decay2 r;
     r.z = add2(a, bias);
-    const float2 na = make_float2(-fabsf(r.z.x), -fabsf(r.z.y));
-    r.t = ex2_pair(mul2(na, splat2(kLog2e)));
-    const float2 sp = add2(make_float2(fmaxf(r.z.x, 0.f), fmaxf(r.z.y, 0.f)), log1p_unit(r.t));
-    r.G = mul2(rate2, sp);
-    r.alpha = ex2_pair(r.G);
-    const float2 y = mul2(r.G, splat2(-2.f * 0.6931471805599453f));
-    const float2 ws = one_minus_exp_small(y);
-    const float2 wl = fma2(make_float2(-r.alpha.x, -r.alpha.y), r.alpha, splat2(1.f));
-    r.w = make_float2(y.x < 0.5f ? ws.x : wl.x, y.y < 0.5f ? ws.y : wl.y);
-    // below the normal range (where the approximation flushes) s counts as 0; a NaN stays
-    r.rs = make_float2(r.w.x < 1.17549435e-38f ? 0.f : rsqrt_approx(r.w.x),
-                       r.w.y < 1.17549435e-38f ? 0.f : rsqrt_approx(r.w.y));
-    r.s = mul2(r.w, r.rs);
-    r.beta = rcp_pair(add2(ex2_pair(mul2(b, splat2(-kLog2e))), splat2(1.f)));
+    r.t = ex2_pair(make_float2(-fabsf(r.z.x) * kLog2e, -fabsf(r.z.y) * kLog2e));
+    r.sp = add2(make_float2(fmaxf(r.z.x, 0.f), fmaxf(r.z.y, 0.f)), log1p_unit(r.t));
+    const float2 y = mul2(rate, r.sp);   // -log(alpha)
+    // alpha = 1 - em with em = 1 - e^-y from the polynomial where y < 1/2 (the long memories: the
+    // hardware exponential's last bits would pile up over thousands of tokens), else e^-y
+    const float2 es = one_minus_exp_small(y);
+    const float2 al = ex2_pair(mul2(y, splat2(-kLog2e)));
+    const float2 el = fma2(al, splat2(-1.f), splat2(1.f)), as = fma2(es, splat2(-1.f), splat2(1.f));
+    const float2 em = make_float2(y.x < 0.5f ? es.x : el.x, y.y < 0.5f ? es.y : el.y);
+    r.alpha = make_float2(y.x < 0.5f ? as.x : al.x, y.y < 0.5f ? as.y : al.y);
+    r.w = fma2(em, r.alpha, em);
     return r;
+}
+
+// 1 / sqrt(w) for the scale s = w / sqrt(w); a w below the normal range (where the
+// approximation flushes) gives s = 0, a NaN stays one through w.
+__device__ __forceinline__ float2 inv_sqrt2(float2 w) {
+    return make_float2(rsqrt_approx(fmaxf(w.x, 1.17549435e-38f)), rsqrt_approx(fmaxf(w.y, 1.17549435e-38f)));
+}
+
+__device__ __forceinline__ float2 sigmoid2(float2 b) {
+    return rcp_pair(add2(ex2_pair(mul2(b, splat2(-kLog2e))), splat2(1.f)));
 }
 
 // sigmoid(z) from t = e^-|z|

@@ -357,6 +357,14 @@ __device__ __forceinline__ void tma_load_2d(void *smem_dst, const CUtensorMap *m
         :: "r"(smem_u32(smem_dst)), "l"((uint64_t)map), "r"(x), "r"(y), "r"(smem_u32(bar))
         : "memory");
 }
+__device__ __forceinline__ void tma_load_3d(void *smem_dst, const CUtensorMap *map, int x, int y, int z,
+                                            uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];"
+        :: "r"(smem_u32(smem_dst)), "l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
 // 2-D tile store shared -> global through the tensor map's box; completes as a
 // bulk async group (commit with bulk_commit, wait with bulk_wait_read / bulk_wait).
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, int x, int y, const void *smem_src) {
@@ -393,4 +401,8 @@ constexpr uint32_t kPrepOut = kTPTBytes + kXBytes;
 bool encode_tile_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols);
 // the same with a row pitch in bytes (a multiple of 16) other than cols * 2
 bool encode_tile_map_pitch(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint64_t pitch);
+// 3-D map over [batch][tokens][channels] of an activation dtype (GDN_F32, GDN_BF16, GDN_F16) with byte
+// pitches that are multiples of 16, boxes of 1 x box_t x box_c elements, no swizzle, zeros outside
+bool encode_token_map(CUtensorMap *m, int dtype, const void *base, uint64_t batch, uint64_t tokens, uint64_t channels,
+                      uint64_t pitch_b, uint64_t pitch_t, uint32_t box_t, uint32_t box_c);
 }  // namespace gdn

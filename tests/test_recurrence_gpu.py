@@ -165,7 +165,13 @@ def test_gates_at_infinity(dev):
 
 def test_nan_stays_in_its_channel_and_sequence(dev):
     s = make(dev, 1, 0, 64, "bf16", lengths=[100, 100, 100])
-    clean = forward(s).out
+    f = forward(s, want_chunk_states=True)
+    clean, g = f.out.clone(), backward(s, f.chunk_states)
+    s["dout"][0, 160, 9] = float("nan")      # reaches back to its sequence's first token
+    g2 = backward(s, f.chunk_states)
+    bad = torch.isnan(g2.dx)
+    assert bad[0, 100:161, 9].all() and bad.sum() == 61 and torch.equal(g2.dx[~bad], g.dx[~bad])
+    assert torch.isnan(g2.dinitial_state).nonzero().tolist() == [[1, 9]]
     s["x"][0, 130, 7] = float("nan")
     got = forward(s).out
     bad = torch.isnan(got)
@@ -288,18 +294,17 @@ def test_two_calls_at_once(dev):
 
 
 def test_offsets_past_32_bits(dev):
-    """More than 2^32 elements a tensor: the tail of the row, checked from the state carried into its last
-    chunk, and its gradients from a call over the tail alone."""
+    """More than 2^32 elements a tensor: the tail of the row, checked from the state carried into it, and its gradients from a call over the tail alone."""
     T, D = 262144 + 70, 16384
     g = torch.Generator(device=dev).manual_seed(0)
     x = torch.randn((1, T, D), generator=g, dtype=torch.bfloat16, device=dev)
     a = torch.randn((1, T, D), generator=g, dtype=torch.bfloat16, device=dev)
     A_log, bias = torch.full((D,), -1.0, device=dev), torch.full((D,), -4.0, device=dev)
     f = gdn.recurrence_forward(x, a, x, A_log, bias, want_chunk_states=True)
-    t0 = T // 64 * 64
-    assert t0 * D > 2 ** 32
+    t0 = 262144
+    assert t0 * D >= 2 ** 32
     tail = [t[:, t0:].contiguous() for t in (x, a, x)]
-    state = f.chunk_states[:, -1].contiguous()
+    state = f.chunk_states[:, t0 // gdn.GDN_RECURRENCE_CHUNK].contiguous()
     one = gdn.recurrence_forward(*tail, A_log, bias, None, state, want_chunk_states=True)
     r = O.recurrence(*(n64(t).reshape(-1, D)[:, :512] for t in tail), n64(A_log)[:512], n64(bias)[:512], [0, T - t0],
                      n64(state)[:, :512])
@@ -335,3 +340,22 @@ def test_gradient_against_differences(dev):
         diff, want = (ends[0] - ends[1]) / (2 * step), (n64(grad) * n64(v)).sum()
         scale = np.linalg.norm(n64(grad)) * np.sqrt(1.0)   # the derivative along v is of this size
         assert abs(diff - want) <= 2e-2 * scale, (key, diff, want, scale)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_wait_timeout_reported_then_next_call_correct(dev, dtype):
+    """The bounded waits for tiles (gdn_set_wait_test_mode): reported, and the next call is right."""
+    s = make(dev, 1, 1000, 256, dtype)
+    f = forward(s, want_chunk_states=True)
+    g = backward(s, f.chunk_states)
+    assert gdn.gdn_device_status(g.workspace) == gdn.GDN_OK
+    torch.cuda.synchronize()
+    gdn.gdn_set_wait_test_mode(1)
+    try:
+        bad = forward(s)
+        status = gdn.gdn_device_status(bad.workspace), gdn.gdn_device_status(backward(s, f.chunk_states).workspace)
+    finally:
+        gdn.gdn_set_wait_test_mode(0)
+    assert status == (gdn.GDN_ERR_DEVICE_TIMEOUT,) * 2
+    again = forward(s, bufs=bad)
+    assert gdn.gdn_device_status(again.workspace) == gdn.GDN_OK and torch.equal(again.out, f.out)
