@@ -425,7 +425,7 @@ int gdn_backward(const gdn_desc *d,
  * Gates, state and every sum are fp32; out is h rounded once. Results are
  * run-to-run identical.
  */
-#define GDN_RECURRENCE_CHUNK 8 /* tokens between two rows of chunk_states */
+#define GDN_RECURRENCE_CHUNK 4 /* tokens between two rows of chunk_states */
 
 typedef struct {
     int32_t B, T;        /* batch rows, tokens per row; with cu_seqlens: B = 1 and
@@ -458,8 +458,8 @@ int gdn_recurrence_backward_workspace_bytes(const gdn_recurrence_desc *d, size_t
  *   out            [B,T,D] contiguous
  *   final_state    NULL or fp32 [N][D]: h after each sequence's last token, its
  *                  initial state (zeros without one) where it is empty
- *   chunk_states   NULL or fp32 [B][ceil(T/8)][D]: the state carried into tokens
- *                  0, 8, 16, ... of each row, for gdn_recurrence_backward
+ *   chunk_states   NULL or fp32 [B][ceil(T/4)][D]: the state carried into tokens
+ *                  0, 4, 8, ... of each row, for gdn_recurrence_backward
  *   workspace      >= gdn_recurrence_workspace_bytes(), 256-byte aligned;
  *                  gdn_device_status reads its status word
  * x, a, b and out may be NULL when B*T == 0. initial_state and final_state may

@@ -36,7 +36,7 @@ struct RecProblem {
     const int32_t *cu;
     const float *h0;
     void *out;
-    float *hT, *cs;              // final states; states carried into every 8th token
+    float *hT, *cs;              // final states; states carried into every 4th token
     int32_t *status;
     const float *grad_final;
     void *dx, *da, *db;
@@ -48,20 +48,22 @@ struct RecMaps {
     CUtensorMap x, a, b, dy;
 };
 
-constexpr int kR = GDN_RECURRENCE_CHUNK;   // tokens per thread and tile
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxCluster = 16;
-static_assert(kR == 8, "the start and end masks hold one bit per token");
-
-template <typename T> struct Tile {
+// A tile: R tokens for each of the WARPS x G token groups of a CTA by 128 bytes of channels. One more warp
+// carries the state and fetches the tiles.
+template <typename T, int R_, int WARPS_, int STAGES_> struct Tile {
+    using E = T;
+    static constexpr int R = R_, WARPS = WARPS_, STAGES = STAGES_, THREADS = 32 * (WARPS + 1);
     static constexpr int LR = 128 / (4 * (int)sizeof(T));   // lanes per token row, 4 channels each
     static constexpr int G = 32 / LR;                       // token groups per warp
-    static constexpr int NG = kWarps * G;                   // per CTA
-    static constexpr int TT = NG * kR;                      // tokens
+    static constexpr int NG = WARPS * G;                    // per CTA
+    static constexpr int TT = NG * R;                       // tokens
     static constexpr int CH = LR * 4;                       // channels
     static constexpr int kTensor = TT * 128;                // bytes of one tensor's tile
 };
+constexpr int kMaxCluster = 16;   // more than 8 needs an opt-in
+template <typename T> using FwdTile = Tile<T, 4, 4, 4>;
+template <typename T> using BwdTile = Tile<T, GDN_RECURRENCE_CHUNK, 4, 3>;
+constexpr int kBwdLag = 1;   // a tile is done with when the maps of the step this much later are in
 
 struct F4 {          // four channels as two pairs
     float2 lo, hi;
@@ -78,15 +80,23 @@ __device__ __forceinline__ float2 cut2(float2 a, float2 yes, float2 no) {
     return make_float2(__float_as_int(a.x) < 0 ? yes.x : no.x, __float_as_int(a.y) < 0 ? yes.y : no.y);
 }
 // A h + B
-__device__ __forceinline__ F4 apply(const F4 &A, const F4 &B, const F4 &h, bool packed) {
+template <bool PACKED> __device__ __forceinline__ float2 apply2(float2 A, float2 B, float2 h) {
+    const float2 r = fma2(A, h, B);
+    return PACKED ? cut2(A, B, r) : r;
+}
+template <bool PACKED> __device__ __forceinline__ float2 compose2(float2 A, float2 pA) {
+    const float2 r = mul2(A, pA);
+    return PACKED ? cut2(A, A, r) : r;
+}
+template <bool PACKED> __device__ __forceinline__ F4 apply(const F4 &A, const F4 &B, const F4 &h) {
     F4 r = fma4(A, h, B);
-    if (packed) r = {cut2(A.lo, B.lo, r.lo), cut2(A.hi, B.hi, r.hi)};
+    if (PACKED) r = {cut2(A.lo, B.lo, r.lo), cut2(A.hi, B.hi, r.hi)};
     return r;
 }
 // the A of a map after one with pA
-__device__ __forceinline__ F4 compose(const F4 &A, const F4 &pA, bool packed) {
+template <bool PACKED> __device__ __forceinline__ F4 compose(const F4 &A, const F4 &pA) {
     F4 r = mul4(A, pA);
-    if (packed) r = {cut2(A.lo, A.lo, r.lo), cut2(A.hi, A.hi, r.hi)};
+    if (PACKED) r = {cut2(A.lo, A.lo, r.lo), cut2(A.hi, A.hi, r.hi)};
     return r;
 }
 template <bool UP>
@@ -152,77 +162,130 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// 8 bytes into the shared memory of CTA `rank` of the cluster, at this CTA's address `p`
-__device__ __forceinline__ void remote_store(const void *p, uint32_t rank, float a, float b) {
-    asm volatile("{\n\t.reg .b32 ra;\n\tmapa.shared::cluster.u32 ra, %0, %1;\n\t"
-                 "st.shared::cluster.v2.f32 [ra], {%2, %3};\n\t}"
-                 :: "r"(tc::smem_u32(p)), "r"(rank), "f"(a), "f"(b) : "memory");
+// 16 bytes into the shared memory of CTA `rank` of the cluster at this CTA's address `p`, counted by the
+// barrier at this CTA's address `bar` there. Data and signal travel together: a cluster barrier instead
+// would wait for every store to global memory before it.
+__device__ __forceinline__ void remote_store(uint32_t p, uint32_t bar, uint32_t rank, float2 a, float2 b) {
+    asm volatile("{\n\t.reg .b32 ra, rb;\n\tmapa.shared::cluster.u32 ra, %0, %2;\n\tmapa.shared::cluster.u32 rb, %1, %2;\n\t"
+                 "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [ra], {%3, %4, %5, %6}, [rb];\n\t}"
+                 :: "r"(p), "r"(bar), "r"(rank), "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y) : "memory");
 }
 
-// The cross-thread part of a step, for one CTA: composes the maps (A, B) of the token groups in
-// walking order (FWD: rising groups, else falling) and carries the state through them.
-template <typename T, bool FWD> struct Chain {
-    using L = Tile<T>;
-    float4 wA[kWarps][L::LR], wB[kWarps][L::LR];            // maps of the warps
-    float2 agg[2][kMaxCluster][L::CH];                      // maps of the cluster's CTAs, by step parity
+// Waits for an mbarrier's phase; the number of tests is limited, to about a second. `failed` makes every later
+// wait a single test, so that a CTA whose copies do not arrive ends soon.
+__device__ __forceinline__ void bounded_wait(uint64_t *bar, uint32_t phase, bool immediate, bool &failed) {
+    if (tc::mbar_test_now(bar, phase)) return;
+    if (!failed && !immediate)
+#pragma unroll 1
+        for (int i = 0; i < (1 << 24); ++i)
+            if (tc::mbar_test(bar, phase)) return;
+    failed = true;
+}
 
-    // In: this group's map. Out: the state carried into this group; `carry`, the state carried into the
-    // step (the same in all groups of all CTAs), moves on to the next step.
-    __device__ __forceinline__ F4 run(F4 A, F4 B, F4 &carry, int warp, int lane, uint32_t rank, uint32_t cs, int parity,
-                                      bool packed) {
+// Named barriers of the CTA: all its threads arrive, one side without waiting.
+constexpr int kMapsBar = 1, kStatesBar = 3;   // and the next: by step parity
+__device__ __forceinline__ void named_arrive(int id, int threads) {
+    asm volatile("bar.arrive %0, %1;" :: "r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
+}
+
+// The cross-thread part of the walk, for one CTA. The compute warps compose the maps (A, B) of their token
+// groups in walking order (FWD: rising groups, else falling), hand one map per warp to the carry warp, and go on
+// to the next tile; the carry warp composes them to the CTA's map, exchanges it with the cluster, takes the
+// state through it all, and hands back the state carried into each warp. Everything is double-buffered by step
+// parity: a compute warp hands in its map of step k after it has the state of step k - 2, so what it overwrites
+// has been read. The CTA's own signals are named barriers, at which a warp waits without issuing anything
+// (polling mbarriers took up to a third of the issue slots).
+template <typename L, bool FWD, bool PACKED> struct Chain {
+    float4 wA[2][L::WARPS][L::LR], wB[2][L::WARPS][L::LR];   // maps of the warps
+    float4 wc[2][L::WARPS][L::LR];                           // the state carried into each warp
+    uint64_t agg_bar[2];                                     // the cluster's maps have arrived
+    uint64_t full[L::STAGES];                                // a tile has arrived
+
+    __device__ __forceinline__ void init(uint32_t cs) {      // all threads
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < 2; ++i) tc::mbar_init(&agg_bar[i], 1);
+            for (int i = 0; i < L::STAGES; ++i) tc::mbar_init(&full[i], 1);
+            tc::mbar_init_fence();
+        }
+        if (cs > 1) cluster_sync();   // no CTA sends before every barrier is set up
+        else __syncthreads();
+    }
+
+    // Compute warp: composes the groups' maps of step k; (eA, eB) is the map from the state carried into the
+    // warp to the one carried into this group.
+    __device__ __forceinline__ void hand_in(F4 A, F4 B, F4 &eA, F4 &eB, int k, int warp, int lane) {
         const int g = lane / L::LR, q = lane % L::LR;
-        const int og = FWD ? g : L::G - 1 - g, ow = FWD ? warp : kWarps - 1 - warp;   // walking order
+        const int og = FWD ? g : L::G - 1 - g, ow = FWD ? warp : L::WARPS - 1 - warp;   // walking order
 #pragma unroll
         for (int off = 1; off < L::G; off *= 2) {
-            const F4 pA = shfl4<FWD>(A, off * L::LR), pB = shfl4<FWD>(B, off * L::LR);
-            if (og >= off) {
-                B = apply(A, B, pB, packed);
-                A = compose(A, pA, packed);
-            }
+            eA = shfl4<FWD>(A, off * L::LR), eB = shfl4<FWD>(B, off * L::LR);
+            const F4 nB = apply<PACKED>(A, B, eB), nA = compose<PACKED>(A, eA);
+            if (og >= off) B = nB, A = nA;
         }
         if (og == L::G - 1) {
-            wA[ow][q] = to4(A);
-            wB[ow][q] = to4(B);
+            wA[k & 1][ow][q] = to4(A);
+            wB[k & 1][ow][q] = to4(B);
         }
-        F4 eA = shfl4<FWD>(A, L::LR), eB = shfl4<FWD>(B, L::LR);   // of the groups before, in the warp
+        if (L::G > 2) eA = shfl4<FWD>(A, L::LR), eB = shfl4<FWD>(B, L::LR);
         if (og == 0) eA = f4(1.f), eB = f4(0.f);
-        __syncthreads();
-        if (cs > 1) {
-            // the CTA's map to every CTA of the cluster: one channel and a share of the ranks per thread
-            const int c = threadIdx.x % L::CH;
-            float tA = 1.f, tB = 0.f;
+        named_arrive(kMapsBar + (k & 1), L::THREADS);
+    }
+    // Compute warp: the state carried into the group in step k.
+    __device__ __forceinline__ F4 take(const F4 &eA, const F4 &eB, int k, int warp, int lane) {
+        named_sync(kStatesBar + (k & 1), L::THREADS);
+        return apply<PACKED>(eA, eB, f4(wc[k & 1][FWD ? warp : L::WARPS - 1 - warp][lane % L::LR]));
+    }
+
+    // Carry warp, step k, two channels a lane. `carry`: the state carried into the step, the same in all CTAs of
+    // the cluster. agg: [2][cs][CH / 2] of (A, A, B, B), the maps of the cluster's CTAs by step parity. A CTA writes
+    // agg[k % 2] of another only after it has that CTA's map of step k - 1, which that CTA's carry warp sends
+    // after it is done with step k - 2. `lost`: something did not arrive; nothing more is sent or waited for.
+    // This is the latency of a step: everything else is done beside it.
+    __device__ __forceinline__ void carry_step(float2 &carry, int lane, uint32_t rank, uint32_t cs, int k, float4 *agg, bool &lost) {
+        constexpr int kHalf = L::CH / 2;
+        const int c2 = lane % kHalf;
+        named_sync(kMapsBar + (k & 1), L::THREADS);
+        float2 a[L::WARPS], b[L::WARPS];
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float a = ((const float *)wA[w])[c], b = ((const float *)wB[w])[c];
-                const bool cut = packed && __float_as_int(a) < 0;
-                tB = cut ? b : fmaf(a, tB, b);
-                tA = cut ? a : tA * a;
-            }
-            for (uint32_t r = threadIdx.x / L::CH; r < cs; r += kThreads / L::CH) remote_store(&agg[parity][rank][c], r, tA, tB);
+        for (int w = 0; w < L::WARPS; ++w) {
+            a[w] = ((const float2 *)wA[k & 1][w])[c2];
+            b[w] = ((const float2 *)wB[k & 1][w])[c2];
         }
-        F4 c = f4(0.f);   // carried into this CTA's tile
+        float2 c = carry;   // carried into this CTA's tile
         if (cs > 1) {
-            cluster_sync();
-            c = carry;
+            float2 tA = a[0], tB = b[0];
+#pragma unroll
+            for (int w = 1; w < L::WARPS; ++w) {
+                tB = apply2<PACKED>(a[w], b[w], tB);
+                tA = compose2<PACKED>(a[w], tA);
+            }
+            float4 *at = agg + (k & 1) * cs * kHalf;
+            if (!lost) {
+                const uint32_t mine = tc::smem_u32(at + rank * kHalf + c2), bar = tc::smem_u32(&agg_bar[k & 1]);
+                if (lane == 0) tc::mbar_expect_tx(&agg_bar[k & 1], cs * kHalf * 16);
+                if (lane < kHalf)
+#pragma unroll 4
+                    for (uint32_t r = 0; r < cs; ++r) remote_store(mine, bar, r, tA, tB);
+                __syncwarp();
+                bounded_wait(&agg_bar[k & 1], (k >> 1) & 1, false, lost);
+            }
+#pragma unroll 4
             for (uint32_t r = 0; r < cs; ++r) {
+                const float4 m = at[r * kHalf + c2];
                 if (r == rank) c = carry;
-                const float4 *m = (const float4 *)&agg[parity][r][q * 4];
-                const float4 m0 = m[0], m1 = m[1];
-                carry = apply({make_float2(m0.x, m0.z), make_float2(m1.x, m1.z)},
-                              {make_float2(m0.y, m0.w), make_float2(m1.y, m1.w)}, carry, packed);
+                carry = apply2<PACKED>(make_float2(m.x, m.y), make_float2(m.z, m.w), carry);
             }
-        } else {
-            c = carry;
         }
-        // through the warps before this one, and on to the end for a chain of one CTA
-        F4 s = c;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w == ow) c = s;
-            if (w < ow || cs == 1) s = apply(f4(wA[w][q]), f4(wB[w][q]), s, packed);
+        for (int w = 0; w < L::WARPS; ++w) {
+            if (lane < kHalf) ((float2 *)wc[k & 1][w])[c2] = c;
+            c = apply2<PACKED>(a[w], b[w], c);
         }
-        if (cs == 1) carry = s;
-        return apply(eA, eB, c, packed);
+        if (cs == 1) carry = c;
+        named_arrive(kStatesBar + (k & 1), L::THREADS);
     }
 };
 
@@ -261,346 +324,416 @@ __device__ void copy_empty(const RecProblem &p, int row, int ch, int nc, float *
     }
 }
 
-// Waits for a stage (bounded, about a second; see gdn_set_wait_test_mode). `failed` makes every later
-// wait a test, so that a CTA whose copies do not arrive ends soon.
-__device__ __forceinline__ void stage_wait(uint64_t *bar, uint32_t phase, const RecProblem &p, bool &failed) {
-    if (!tc::mbar_wait(bar, phase, failed || p.wait_immediate)) failed = true;
+// exp(A_log) and dt_bias log2(e) of four channels
+__device__ __forceinline__ void channel_params(const RecProblem &p, int ch, int nc, float2 (&rate)[2], float2 (&bias2)[2]) {
+    const F4 l = load_words(p.A_log + ch, nc), b = load_words(p.dt_bias + ch, nc);
+    rate[0] = make_float2(expf(l.lo.x), expf(l.lo.y));
+    rate[1] = make_float2(expf(l.hi.x), expf(l.hi.y));
+    bias2[0] = mul2(b.lo, splat2(kLog2e));
+    bias2[1] = mul2(b.hi, splat2(kLog2e));
 }
 
 // Bound by HBM (8 bytes per 16-bit element) and, near it, by the special-function and issue rates: about
 // 30 instructions and 5 special functions per element.
-template <typename T, bool TMA>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
-rec_forward_kernel(const RecProblem p, const __grid_constant__ RecMaps maps) {
-    using L = Tile<T>;
-    extern __shared__ __align__(128) unsigned char smem[];   // TMA: 2 stages of x, a, b
-    __shared__ Chain<T, true> chain;
-    __shared__ uint64_t full[2];
+// While the carry of tile k - 1 travels, the compute warps work on tile k: its decays and writes need only the
+// inputs. Bound by HBM (8 bytes per 16-bit element) and, near it, by the issue rate.
+template <typename T, bool TMA, bool PACKED>
+__global__ void __launch_bounds__(FwdTile<T>::THREADS, sizeof(T) == 2 ? 3 : 2)
+rec_forward_kernel(const __grid_constant__ RecProblem p, const __grid_constant__ RecMaps maps) {
+    using L = FwdTile<T>;
+    constexpr int kR = L::R;
+    extern __shared__ __align__(128) unsigned char smem[];   // TMA: STAGES tiles of a, b, x; then the cluster's maps
+    __shared__ Chain<L, true, PACKED> chain;
     const gdn_recurrence_desc &d = p.d;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int g = lane / L::LR, q = lane % L::LR;
     uint32_t cs;
     asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cs));
     const uint32_t rank = cluster_rank();
     const int slab = (int)(blockIdx.x / cs) % p.slabs, row = (int)(blockIdx.x / cs) / p.slabs;
-    const bool ok = p.cu == nullptr || seqlens_ok(p.cu, d.N, d.T);
+    const bool ok = !PACKED || seqlens_ok(p.cu, d.N, d.T);
     if (blockIdx.x == 0 && tid == 0) *p.status = ok ? GDN_OK : GDN_ERR_DEVICE_SEQLENS;
     if (!ok) return;   // the same in every CTA
-    const int ch = slab * L::CH + q * 4, nc = min(4, max(0, d.D - ch));
     const int steps = (p.ntiles + (int)cs - 1) / (int)cs;
+    const int mine = (p.ntiles - 1 - (int)rank + (int)cs) / (int)cs;   // steps in which this CTA has a tile
+    chain.init(cs);
+    bool failed = false, lost = false;
 
-    auto issue = [&](int k) {   // thread 0: the tile of step k into stage k % 2
-        const int tile = k * (int)cs + (int)rank;
-        if (tile >= p.ntiles) return;
-        unsigned char *st = smem + (k & 1) * 3 * L::kTensor;
-        tc::mbar_expect_tx(&full[k & 1], 3 * L::kTensor);
-        tc::tma_load_3d(st, &maps.x, slab * L::CH, tile * L::TT, row, &full[k & 1]);
-        tc::tma_load_3d(st + L::kTensor, &maps.a, slab * L::CH, tile * L::TT, row, &full[k & 1]);
-        tc::tma_load_3d(st + 2 * L::kTensor, &maps.b, slab * L::CH, tile * L::TT, row, &full[k & 1]);
-    };
-    if (TMA) {
-        if (tid == 0) {
-            tc::mbar_init(&full[0], 1);
-            tc::mbar_init(&full[1], 1);
-            tc::mbar_init_fence();
-            if (!p.wait_immediate) {
-                issue(0);
-                issue(1);
-            }
+    if (warp == L::WARPS) {   // the carry warp
+        float4 *agg = (float4 *)(smem + (TMA ? L::STAGES * 3 * L::kTensor : 0));
+        auto issue = [&](int k) {
+            if (!TMA || lane != 0 || k >= mine) return;
+            uint64_t *bar = &chain.full[k % L::STAGES];
+            unsigned char *st = smem + k % L::STAGES * 3 * L::kTensor;
+            const int t = (k * (int)cs + (int)rank) * L::TT;
+            tc::mbar_expect_tx(bar, 3 * L::kTensor);
+            tc::tma_load_3d(st, &maps.a, slab * L::CH, t, row, bar);
+            tc::tma_load_3d(st + L::kTensor, &maps.b, slab * L::CH, t, row, bar);
+            tc::tma_load_3d(st + 2 * L::kTensor, &maps.x, slab * L::CH, t, row, bar);
+        };
+        if (p.wait_immediate) __nanosleep(20000);   // the compute warps' first wait cannot be over
+        for (int k = 0; k < L::STAGES; ++k) issue(k);
+        float2 carry = splat2(0.f);
+        for (int k = 0; k < steps; ++k) {
+            chain.carry_step(carry, lane, rank, cs, k, agg, lost);
+            // the maps are in, so every warp has read tile k
+            if (TMA && k < mine) bounded_wait(&chain.full[k % L::STAGES], (k / L::STAGES) & 1, false, lost);   // long since
+            if (!lost) issue(k + L::STAGES);
+            __syncwarp();
         }
-        __syncthreads();
-    }
-    F4 rate = load_words(p.A_log + ch, nc);
-    rate = {make_float2(expf(rate.lo.x), expf(rate.lo.y)), make_float2(expf(rate.hi.x), expf(rate.hi.y))};
-    const F4 bias = load_words(p.dt_bias + ch, nc);
-    if (rank == 0) copy_empty(p, row, ch, nc, p.hT, p.h0, warp * L::G + g, L::NG);
-    Seq seq;
-    seq.init(p, row);
-    F4 carry = f4(0.f);
-    bool failed = false;
-    if (TMA && tid == 0 && p.wait_immediate) {   // so late that the first wait cannot be over
-        issue(0);
-        issue(1);
-    }
-    for (int k = 0; k < steps; ++k) {
-        const int tile = k * (int)cs + (int)rank;
-        const bool real = tile < p.ntiles;
-        const int t0 = tile * L::TT + (warp * L::G + g) * kR;   // this group's first token
-        F4 P[kR], h[kR];
-        if (real) {
-            if (TMA) stage_wait(&full[k & 1], (k >> 1) & 1, p, failed);
-            const unsigned char *st = smem + (k & 1) * 3 * L::kTensor + (t0 - tile * L::TT) * 128 + q * 4 * sizeof(T);
-            seq.up_to(p, t0);
+    } else {
+        const int g = lane / L::LR, q = lane % L::LR;
+        const int ch = slab * L::CH + q * 4, nc = min(4, max(0, d.D - ch));
+        const int tg = (warp * L::G + g) * kR;   // this group's first token in a tile
+        const GateConst C;
+        float2 rate[2], bias2[2];
+        channel_params(p, ch, nc, rate, bias2);
+        if (rank == 0) copy_empty(p, row, ch, nc, p.hT, p.h0, warp * L::G + g, L::NG);
+        Seq seq, seq_out;   // at the tile whose decays are computed, and at the one that is finished
+        seq.init(p, row);
+        seq_out.init(p, row);
+
+        // decay products P and local values h of tile k's tokens, and the map to the carry warp
+        auto begin = [&](int k, F4 (&P)[kR], F4 (&h)[kR], F4 &eA, F4 &eB) {
+            const int tile = k * (int)cs + (int)rank, t0 = tile * L::TT + tg;
+            if (tile < p.ntiles) {
+                auto in = [&](int which, const void *base, int64_t sb, int64_t st, int r) -> F4 {
+                    if (TMA)
+                        return unpack4<T>(smem + (k % L::STAGES * 3 + which) * L::kTensor + (tg + r) * 128 + q * 4 * sizeof(T));
+                    return load_row<T, false>((const T *)base + row * sb + (int64_t)(t0 + r) * st + ch, t0 + r < d.T ? nc : 0);
+                };
+                if (TMA) bounded_wait(&chain.full[k % L::STAGES], (k / L::STAGES) & 1, p.wait_immediate, failed);
+                if (PACKED) seq.up_to(p, t0);
+                constexpr int kB = 4;   // tokens at a time
 #pragma unroll
-            for (int r = 0; r < kR; ++r) {
-                F4 x, a, b;
-                if (TMA) {
-                    x = unpack4<T>(st + r * 128);
-                    a = unpack4<T>(st + L::kTensor + r * 128);
-                    b = unpack4<T>(st + 2 * L::kTensor + r * 128);
-                } else {
-                    const int n = t0 + r < d.T ? nc : 0;
-                    const int64_t t = t0 + r;
-                    x = load_row<T, false>((const T *)p.x + row * d.x_stride_b + t * d.x_stride_t + ch, n);
-                    a = load_row<T, false>((const T *)p.a + row * d.a_stride_b + t * d.a_stride_t + ch, n);
-                    b = load_row<T, false>((const T *)p.b + row * d.b_stride_b + t * d.b_stride_t + ch, n);
-                }
-                const Decay2 e0 = decay2(a.lo, bias.lo, rate.lo), e1 = decay2(a.hi, bias.hi, rate.hi);
-                const F4 s = {mul2(e0.w, inv_sqrt2(e0.w)), mul2(e1.w, inv_sqrt2(e1.w))};
-                P[r] = {e0.alpha, e1.alpha};
-                h[r] = mul4(mul4(s, {sigmoid2(b.lo), sigmoid2(b.hi)}), x);
-            }
-            if (seq.b0 == t0 || (seq.b1 < t0 + kR && seq.b1 < d.T)) {   // a sequence starts here
-                Seq m = seq;
+                for (int r0 = 0; r0 < kR; r0 += kB) {
+                    float2 z[2 * kB], t[2 * kB], Y[2 * kB], al[2 * kB], w[2 * kB];
 #pragma unroll
-                for (int r = 0; r < kR; ++r) {
-                    m.up_to(p, t0 + r);
-                    if (m.b0 == t0 + r && t0 + r < d.T) {
-                        if (p.h0) h[r] = fma4(P[r], load_words(p.h0 + (int64_t)m.n * d.D + ch, nc), h[r]);
-                        P[r] = f4(-0.f);
+                    for (int r = 0; r < kB; ++r) {
+                        const F4 a = in(0, p.a, d.a_stride_b, d.a_stride_t, r0 + r);
+                        z[2 * r] = a.lo;
+                        z[2 * r + 1] = a.hi;
                     }
-                    if (r > 0) {
-                        h[r] = apply(P[r], h[r], h[r - 1], true);
-                        P[r] = compose(P[r], P[r - 1], true);
+                    decays<2 * kB, 2>(C, z, bias2, rate, t, Y, al, w);
+#pragma unroll
+                    for (int r = 0; r < kB; ++r) {
+                        const F4 b = in(1, p.b, d.b_stride_b, d.b_stride_t, r0 + r), x = in(2, p.x, d.x_stride_b, d.x_stride_t, r0 + r);
+                        P[r0 + r] = {al[2 * r], al[2 * r + 1]};
+                        h[r0 + r] = mul4({write_scale2(C, w[2 * r], b.lo), write_scale2(C, w[2 * r + 1], b.hi)}, x);
+                    }
+                }
+                if (seq.b0 == t0 || (PACKED && seq.b1 < t0 + kR && seq.b1 < d.T)) {   // a sequence starts here
+                    Seq m = seq;
+#pragma unroll
+                    for (int r = 0; r < kR; ++r) {
+                        m.up_to(p, t0 + r);
+                        if (m.b0 == t0 + r && t0 + r < d.T) {
+                            if (p.h0) h[r] = fma4(P[r], load_words(p.h0 + (int64_t)m.n * d.D + ch, nc), h[r]);
+                            P[r] = f4(-0.f);
+                        }
+                        if (r > 0) {
+                            h[r] = apply<true>(P[r], h[r], h[r - 1]);
+                            P[r] = compose<true>(P[r], P[r - 1]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int r = 1; r < kR; ++r) {
+                        h[r] = fma4(P[r], h[r - 1], h[r]);
+                        P[r] = mul4(P[r], P[r - 1]);
                     }
                 }
             } else {
 #pragma unroll
-                for (int r = 1; r < kR; ++r) {
-                    h[r] = fma4(P[r], h[r - 1], h[r]);
-                    P[r] = mul4(P[r], P[r - 1]);
-                }
+                for (int r = 0; r < kR; ++r) P[r] = f4(1.f), h[r] = f4(0.f);
             }
-        } else {
+            chain.hand_in(P[kR - 1], h[kR - 1], eA, eB, k, warp, lane);
+        };
+        auto finish = [&](int k, F4 (&P)[kR], F4 (&h)[kR], const F4 &eA, const F4 &eB) {
+            const F4 c = chain.take(eA, eB, k, warp, lane);
+            const int t0 = (k * (int)cs + (int)rank) * L::TT + tg;
+            if (t0 >= d.T) return;
+            if (p.cs && t0 % GDN_RECURRENCE_CHUNK == 0)
+                store_row<float, TMA>(p.cs + ((int64_t)row * ((d.T + GDN_RECURRENCE_CHUNK - 1) / GDN_RECURRENCE_CHUNK) +
+                                              t0 / GDN_RECURRENCE_CHUNK) * d.D + ch, c, nc);
 #pragma unroll
-            for (int r = 0; r < kR; ++r) P[r] = f4(1.f), h[r] = f4(0.f);
-        }
-        const F4 c = chain.run(P[kR - 1], h[kR - 1], carry, warp, lane, rank, cs, k & 1, p.cu != nullptr);
-        // chain.run's barrier: every thread has read this stage
-        if (TMA && tid == 0 && !failed) issue(k + 2);
-        if (real && t0 < d.T) {
-            if (p.cs)
-                store_words(p.cs + ((int64_t)row * ((d.T + kR - 1) / kR) + t0 / kR) * d.D + ch, c, nc);
-#pragma unroll
-            for (int r = 0; r < kR; ++r) h[r] = apply(P[r], h[r], c, p.cu != nullptr);
+            for (int r = 0; r < kR; ++r) h[r] = apply<PACKED>(P[r], h[r], c);
             if (p.out) {
                 T *o = (T *)p.out + ((int64_t)row * d.T + t0) * d.D + ch;
+                if (TMA && nc == 4 && t0 + kR <= d.T) {
 #pragma unroll
-                for (int r = 0; r < kR; ++r)
-                    if (t0 + r < d.T) store_row<T, TMA>(o + (int64_t)r * d.D, h[r], nc);
-            }
-            if (p.hT && seq.b1 <= t0 + kR) {   // a sequence ends here
-                Seq m = seq;
+                    for (int r = 0; r < kR; ++r, o += d.D) pack4<T>(o, h[r]);
+                } else {
 #pragma unroll
-                for (int r = 0; r < kR; ++r) {
-                    m.up_to(p, t0 + r);
-                    if (m.b1 == t0 + r + 1) store_words(p.hT + (int64_t)m.n * d.D + ch, h[r], nc);
+                    for (int r = 0; r < kR; ++r, o += d.D)
+                        if (t0 + r < d.T) store_row<T, TMA>(o, h[r], nc);
                 }
             }
-        }
-        // the warps' maps are read in run() up to here and written again in the next step
-        __syncthreads();
-    }
-    if (failed) *p.status = GDN_ERR_DEVICE_TIMEOUT;
-    if (TMA && tid == 0 && failed)   // copies in flight end before the CTA does
-        for (int k = max(0, steps - 2); k < steps; ++k)
-            if (k * (int)cs + (int)rank < p.ntiles) tc::mbar_wait(&full[k & 1], (k >> 1) & 1);
-}
-
-// The reverse scan: c_t = alpha_t (v_t + c_{t+1}), delta_t = v_t + c_{t+1}, tiles last to first. The
-// states before every 8th token come from the forward, so h_{t-1} is recomputed within a thread.
-template <typename T, bool TMA>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 1)
-rec_backward_kernel(const RecProblem p, const __grid_constant__ RecMaps maps) {
-    using L = Tile<T>;
-    extern __shared__ __align__(128) unsigned char smem[];   // TMA: 2 stages of x, a, b, grad_out
-    __shared__ Chain<T, false> chain;
-    __shared__ uint64_t full[2];
-    const gdn_recurrence_desc &d = p.d;
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int g = lane / L::LR, q = lane % L::LR;
-    uint32_t cs;
-    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cs));
-    const uint32_t rank = cluster_rank();
-    const int chains = (int)(blockIdx.x / cs);
-    const int slab = chains % p.slabs, row = chains / p.slabs;
-    const bool ok = p.cu == nullptr || seqlens_ok(p.cu, d.N, d.T);
-    if (blockIdx.x == 0 && tid == 0) *p.status = ok ? GDN_OK : GDN_ERR_DEVICE_SEQLENS;
-    if (!ok) return;
-    const int ch = slab * L::CH + q * 4, nc = min(4, max(0, d.D - ch));
-    const int steps = (p.ntiles + (int)cs - 1) / (int)cs;
-
-    auto issue = [&](int k) {
-        const int back = k * (int)cs + (int)rank, tile = p.ntiles - 1 - back;
-        if (tile < 0) return;
-        unsigned char *st = smem + (k & 1) * 4 * L::kTensor;
-        tc::mbar_expect_tx(&full[k & 1], 4 * L::kTensor);
-        tc::tma_load_3d(st, &maps.x, slab * L::CH, tile * L::TT, row, &full[k & 1]);
-        tc::tma_load_3d(st + L::kTensor, &maps.a, slab * L::CH, tile * L::TT, row, &full[k & 1]);
-        tc::tma_load_3d(st + 2 * L::kTensor, &maps.b, slab * L::CH, tile * L::TT, row, &full[k & 1]);
-        tc::tma_load_3d(st + 3 * L::kTensor, &maps.dy, slab * L::CH, tile * L::TT, row, &full[k & 1]);
-    };
-    if (TMA) {
-        if (tid == 0) {
-            tc::mbar_init(&full[0], 1);
-            tc::mbar_init(&full[1], 1);
-            tc::mbar_init_fence();
-            if (!p.wait_immediate) issue(0);
-        }
-        __syncthreads();
-    }
-    F4 rate = load_words(p.A_log + ch, nc);
-    rate = {make_float2(expf(rate.lo.x), expf(rate.lo.y)), make_float2(expf(rate.hi.x), expf(rate.hi.y))};
-    const F4 bias = load_words(p.dt_bias + ch, nc);
-    if (rank == 0) copy_empty(p, row, ch, nc, p.dh0, p.grad_final, warp * L::G + g, L::NG);
-    Seq seq;
-    seq.init(p, row);
-    seq.up_to(p, d.T - 1);
-    F4 carry = f4(0.f);
-    // sums of da and of dg g over this thread's tokens: per tile, over 16 tiles, over all
-    F4 sA[2] = {f4(0.f), f4(0.f)}, sb[2] = {f4(0.f), f4(0.f)};
-    bool failed = false;
-    if (TMA && tid == 0 && p.wait_immediate) issue(0);   // so late that the first wait cannot be over
-    for (int k = 0; k < steps; ++k) {
-        const int tile = p.ntiles - 1 - (k * (int)cs + (int)rank);
-        const bool real = tile >= 0;
-        const int t0 = tile * L::TT + (warp * L::G + g) * kR;
-        const bool any = real && t0 < d.T;
-        const unsigned char *st = smem + (k & 1) * 4 * L::kTensor + (warp * L::G + g) * kR * 128 + q * 4 * sizeof(T);
-        auto in = [&](int which, const void *base, int64_t sb_, int64_t st_, int r) -> F4 {
-            if (TMA) return unpack4<T>(st + which * L::kTensor + r * 128);
-            return load_row<T, false>((const T *)base + row * sb_ + (int64_t)(t0 + r) * st_ + ch, t0 + r < d.T ? nc : 0);
-        };
-        auto dy = [&](int r) -> F4 { return in(3, p.grad_out, (int64_t)d.T * d.D, d.D, r); };
-        F4 al[kR], Q = f4(1.f), c = f4(0.f), hs = f4(0.f);
-        uint32_t starts = 0, ends = 0;   // tokens of this group that start or end a sequence
-        if (real) {
-            if (TMA) stage_wait(&full[k & 1], (k >> 1) & 1, p, failed);
-            if (any) {
-                hs = load_words(p.cs + ((int64_t)row * ((d.T + kR - 1) / kR) + t0 / kR) * d.D + ch, nc);
-                seq.down_to(p, t0);
-                if (seq.b0 == t0 || seq.b1 <= t0 + kR) {
-                    Seq m = seq;
-                    for (int r = 0; r < kR && t0 + r < d.T; ++r) {
+            if (p.hT) {
+                if (PACKED) seq_out.up_to(p, t0);
+                if (seq_out.b1 <= t0 + kR) {   // a sequence ends here
+                    Seq m = seq_out;
+#pragma unroll
+                    for (int r = 0; r < kR; ++r) {
                         m.up_to(p, t0 + r);
-                        starts |= (m.b0 == t0 + r ? 1u : 0u) << r;
-                        ends |= (m.b1 == t0 + r + 1 ? 1u : 0u) << r;
+                        if (m.b1 == t0 + r + 1) store_words(p.hT + (int64_t)m.n * d.D + ch, h[r], nc);
                     }
                 }
             }
-#pragma unroll
-            for (int r = 0; r < kR; ++r) {
-                const F4 a = in(1, p.a, d.a_stride_b, d.a_stride_t, r);
-                al[r] = {decay2(a.lo, bias.lo, rate.lo).alpha, decay2(a.hi, bias.hi, rate.hi).alpha};
-                if (starts >> r & 1) al[r] = f4(-0.f);
-            }
-#pragma unroll
-            for (int r = kR - 1; r >= 0; --r) {
-                F4 v = dy(r);
-                if (ends >> r & 1 && p.grad_final) {
-                    Seq m = seq;
-                    m.up_to(p, t0 + r);
-                    v = add4(v, load_words(p.grad_final + (int64_t)m.n * d.D + ch, nc));
-                }
-                c = mul4(al[r], add4(v, c));
-                Q = compose(al[r], Q, p.cu != nullptr);
-                if (starts >> r & 1) c = f4(0.f);
+        };
+        F4 P0[kR], h0[kR], P1[kR], h1[kR], eA0, eB0, eA1, eB1;
+        if (steps > 0) begin(0, P0, h0, eA0, eB0);
+        for (int k = 1; k <= steps; k += 2) {
+            if (k < steps) begin(k, P1, h1, eA1, eB1);
+            finish(k - 1, P0, h0, eA0, eB0);
+            if (k < steps) {
+                if (k + 1 < steps) begin(k + 1, P0, h0, eA0, eB0);
+                finish(k, P1, h1, eA1, eB1);
             }
         }
-        c = chain.run(Q, c, carry, warp, lane, rank, cs, k & 1, p.cu != nullptr);
-        // chain.run's barrier: every thread is done with the stage of step k - 1
-        if (TMA && tid == 0 && !failed) issue(k + 1);
-        if (any) {
-            F4 dl[kR];
-#pragma unroll
-            for (int r = kR - 1; r >= 0; --r) {
-                F4 v = dy(r);
-                if (ends >> r & 1 && p.grad_final) {
-                    Seq m = seq;
-                    m.up_to(p, t0 + r);
-                    v = add4(v, load_words(p.grad_final + (int64_t)m.n * d.D + ch, nc));
-                }
-                dl[r] = add4(v, c);
-                c = mul4(al[r], dl[r]);
-                if (starts >> r & 1) c = f4(0.f);
-            }
-            F4 tA = f4(0.f), tb = f4(0.f);
-            const int64_t o = ((int64_t)row * d.T + t0) * d.D + ch;
-#pragma unroll
-            for (int r = 0; r < kR; ++r) {
-                const F4 x = in(0, p.x, d.x_stride_b, d.x_stride_t, r), a = in(1, p.a, d.a_stride_b, d.a_stride_t, r),
-                         b = in(2, p.b, d.b_stride_b, d.b_stride_t, r);
-                int n0 = 0;
-                if (starts >> r & 1) {
-                    Seq m = seq;
-                    m.up_to(p, t0 + r);
-                    n0 = m.n;
-                    hs = p.h0 ? load_words(p.h0 + (int64_t)n0 * d.D + ch, nc) : f4(0.f);
-                }
-                F4 gx, ga, gb, al1;
-                auto pair = [&](float2 xv, float2 av, float2 bv, float2 bi, float2 ra, float2 de, float2 &hh, float2 &qA,
-                                float2 &qb, float2 &ox, float2 &oa, float2 &ob, float2 &oal) {
-                    const Decay2 e = decay2(av, bi, ra);
-                    const float2 rs = inv_sqrt2(e.w), be = sigmoid2(bv), s = mul2(e.w, rs);
-                    const float2 sg = sigmoid_from_t(e.z, e.t);
-                    const float2 sbx = mul2(mul2(s, be), xv);
-                    ox = mul2(mul2(de, s), be);
-                    ob = mul2(mul2(mul2(de, sbx), fma2(be, splat2(-1.f), splat2(1.f))), splat2(1.f));
-                    // dg = delta (alpha h_{t-1} - beta x alpha^2 / s); 1/s is taken as 0 where s is
-                    const float2 rz = make_float2(e.w.x < 1.17549435e-38f ? 0.f : rs.x, e.w.y < 1.17549435e-38f ? 0.f : rs.y);
-                    const float2 m1 = mul2(e.alpha, hh);
-                    const float2 m2 = mul2(mul2(mul2(be, xv), mul2(e.alpha, e.alpha)), rz);
-                    const float2 ndg = mul2(de, fma2(m1, splat2(-1.f), m2));   // -dg
-                    oa = mul2(mul2(ndg, ra), sg);
-                    qA = fma2(mul2(ndg, ra), e.sp, qA);                        // dg g = -dg rate softplus(z)
-                    qb = add2(qb, oa);
-                    hh = add2(m1, sbx);
-                    oal = e.alpha;
-                };
-                const bool live = t0 + r < d.T;
-                const F4 de = live ? dl[r] : f4(0.f);
-                pair(x.lo, a.lo, b.lo, bias.lo, rate.lo, de.lo, hs.lo, tA.lo, tb.lo, gx.lo, ga.lo, gb.lo, al1.lo);
-                pair(x.hi, a.hi, b.hi, bias.hi, rate.hi, de.hi, hs.hi, tA.hi, tb.hi, gx.hi, ga.hi, gb.hi, al1.hi);
-                if (live) {
-                    store_row<T, TMA>((T *)p.dx + o + (int64_t)r * d.D, gx, nc);
-                    store_row<T, TMA>((T *)p.da + o + (int64_t)r * d.D, ga, nc);
-                    store_row<T, TMA>((T *)p.db + o + (int64_t)r * d.D, gb, nc);
-                    if (starts >> r & 1 && p.dh0) store_words(p.dh0 + (int64_t)n0 * d.D + ch, mul4(al1, dl[r]), nc);
-                }
-            }
-            sA[0] = add4(sA[0], tA);
-            sb[0] = add4(sb[0], tb);
-        }
-        if ((k & 15) == 15) {
-            sA[1] = add4(sA[1], sA[0]);
-            sb[1] = add4(sb[1], sb[0]);
-            sA[0] = sb[0] = f4(0.f);
-        }
-        __syncthreads();
     }
-    // this CTA's sums: over the token groups, in order
-    chain.agg[0][0][0].x = 0.f;   // (the scan's memory is free now)
-    __syncthreads();
-    float *red = (float *)&chain.agg[0][0][0];   // [NG][2][CH]
-    static_assert(sizeof(chain.agg) >= sizeof(float) * Tile<T>::NG * 2 * Tile<T>::CH, "sums fit the scan's memory");
-    {
+    if (failed || lost) *p.status = GDN_ERR_DEVICE_TIMEOUT;
+    // copies in flight end before the CTA does (they have, unless a wait gave up), and no CTA leaves while
+    // another may still write to it
+    if (TMA && warp == L::WARPS && lane == 0)
+        for (int k = max(0, mine - L::STAGES); k < mine; ++k) tc::mbar_wait(&chain.full[k % L::STAGES], (k / L::STAGES) & 1);
+    __syncwarp();
+    if (cs > 1) cluster_sync();
+    else __syncthreads();
+}
+
+// The reverse walk: c_t = alpha_t (v_t + c_{t+1}), delta_t = v_t + c_{t+1} with v = grad_out, tiles last to
+// first. The states before every 4th token come from the forward, so h_{t-1} is recomputed within a thread.
+template <typename T, bool TMA, bool PACKED>
+__global__ void __launch_bounds__(BwdTile<T>::THREADS, sizeof(T) == 2 ? 3 : 2)
+rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant__ RecMaps maps) {
+    using L = BwdTile<T>;
+    constexpr int kR = L::R;
+    static_assert(kR <= 32, "the start and end masks hold one bit per token");
+    extern __shared__ __align__(128) unsigned char smem[];   // TMA: STAGES tiles of x, a, b, grad_out; the cluster's maps
+    __shared__ Chain<L, false, PACKED> chain;
+    __shared__ float red[L::NG][2][L::CH];
+    const gdn_recurrence_desc &d = p.d;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    uint32_t cs;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cs));
+    const uint32_t rank = cluster_rank();
+    const int slab = (int)(blockIdx.x / cs) % p.slabs, row = (int)(blockIdx.x / cs) / p.slabs;
+    const bool ok = !PACKED || seqlens_ok(p.cu, d.N, d.T);
+    if (blockIdx.x == 0 && tid == 0) *p.status = ok ? GDN_OK : GDN_ERR_DEVICE_SEQLENS;
+    if (!ok) return;
+    const int steps = (p.ntiles + (int)cs - 1) / (int)cs;
+    const int mine = (p.ntiles - 1 - (int)rank + (int)cs) / (int)cs;
+    chain.init(cs);
+    bool failed = false, lost = false;
+
+    if (warp == L::WARPS) {
+        float4 *agg = (float4 *)(smem + (TMA ? L::STAGES * 4 * L::kTensor : 0));
+        auto issue = [&](int k) {
+            if (!TMA || lane != 0 || k >= mine) return;
+            uint64_t *bar = &chain.full[k % L::STAGES];
+            unsigned char *st = smem + k % L::STAGES * 4 * L::kTensor;
+            const int t = (p.ntiles - 1 - (k * (int)cs + (int)rank)) * L::TT;
+            tc::mbar_expect_tx(bar, 4 * L::kTensor);
+            tc::tma_load_3d(st + L::kTensor, &maps.a, slab * L::CH, t, row, bar);
+            tc::tma_load_3d(st + 3 * L::kTensor, &maps.dy, slab * L::CH, t, row, bar);
+            tc::tma_load_3d(st, &maps.x, slab * L::CH, t, row, bar);
+            tc::tma_load_3d(st + 2 * L::kTensor, &maps.b, slab * L::CH, t, row, bar);
+        };
+        if (p.wait_immediate) __nanosleep(20000);   // the compute warps' first wait cannot be over
+        for (int k = 0; k < L::STAGES; ++k) issue(k);
+        float2 carry = splat2(0.f);
+        for (int k = 0; k < steps; ++k) {
+            chain.carry_step(carry, lane, rank, cs, k, agg, lost);
+            // the maps are in, so every warp is done with the tile kBwdLag steps before
+            const int was = k - kBwdLag;
+            if (was >= 0) {
+                if (TMA && was < mine) bounded_wait(&chain.full[was % L::STAGES], (was / L::STAGES) & 1, false, lost);
+                if (!lost) issue(was + L::STAGES);
+                __syncwarp();
+            }
+        }
+    } else {
+        const int g = lane / L::LR, q = lane % L::LR;
+        const int ch = slab * L::CH + q * 4, nc = min(4, max(0, d.D - ch));
+        const int tg = (warp * L::G + g) * kR;
+        const GateConst C;
+        float2 rate[2], bias2[2];
+        channel_params(p, ch, nc, rate, bias2);
+        if (rank == 0) copy_empty(p, row, ch, nc, p.dh0, p.grad_final, warp * L::G + g, L::NG);
+        Seq seq;
+        seq.init(p, row);
+        seq.up_to(p, d.T - 1);
+        // sums of da and of dg g over this thread's tokens: over 16 tiles, over all
+        F4 sA[2] = {f4(0.f), f4(0.f)}, sb[2] = {f4(0.f), f4(0.f)};
+
+        auto tile_of = [&](int k) { return p.ntiles - 1 - (k * (int)cs + (int)rank); };
+        auto in = [&](int k, int which, const void *base, int64_t sb_, int64_t st_, int r) -> F4 {
+            const int t0 = tile_of(k) * L::TT + tg;
+            if (TMA) return unpack4<T>(smem + (k % L::STAGES * 4 + which) * L::kTensor + (tg + r) * 128 + q * 4 * sizeof(T));
+            return load_row<T, false>((const T *)base + row * sb_ + (int64_t)(t0 + r) * st_ + ch, t0 + r < d.T ? nc : 0);
+        };
+        // v_t; m: the tile's sequence, ends: the group's tokens that end one
+        auto v_of = [&](int k, int r, uint32_t ends, const Seq &at) -> F4 {
+            F4 v = in(k, 3, p.grad_out, (int64_t)d.T * d.D, d.D, r);
+            if (ends >> r & 1 && p.grad_final) {
+                Seq m = at;
+                const int t0 = tile_of(k) * L::TT + tg;
+                m.up_to(p, t0 + r);
+                v = add4(v, load_words(p.grad_final + (int64_t)m.n * d.D + ch, nc));
+            }
+            return v;
+        };
+        // decays of tile k's tokens (-0 at a sequence's first), and the map to the carry warp
+        auto begin = [&](int k, F4 (&al)[kR], uint32_t &starts, uint32_t &ends, Seq &at, F4 &eA, F4 &eB) {
+            const int tile = tile_of(k), t0 = tile * L::TT + tg;
+            F4 Q = f4(1.f), c = f4(0.f);
+            starts = ends = 0;
+            if (tile >= 0) {
+                if (TMA) bounded_wait(&chain.full[k % L::STAGES], (k / L::STAGES) & 1, p.wait_immediate, failed);
+                if (t0 < d.T) {
+                    seq.down_to(p, t0);
+                    if (seq.b0 == t0 || seq.b1 <= t0 + kR) {
+                        Seq m = seq;
+                        for (int r = 0; r < kR && t0 + r < d.T; ++r) {
+                            m.up_to(p, t0 + r);
+                            starts |= (m.b0 == t0 + r ? 1u : 0u) << r;
+                            ends |= (m.b1 == t0 + r + 1 ? 1u : 0u) << r;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int r0 = 0; r0 < kR; r0 += 2) {
+                    float2 z[4], t[4], Y[4], av[4], w[4];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const F4 a = in(k, 1, p.a, d.a_stride_b, d.a_stride_t, r0 + r);
+                        z[2 * r] = a.lo;
+                        z[2 * r + 1] = a.hi;
+                    }
+                    decays<4, 2>(C, z, bias2, rate, t, Y, av, w);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        al[r0 + r] = {av[2 * r], av[2 * r + 1]};
+                        if (starts >> (r0 + r) & 1) al[r0 + r] = f4(-0.f);
+                    }
+                }
+#pragma unroll
+                for (int r = kR - 1; r >= 0; --r) {
+                    c = mul4(al[r], add4(v_of(k, r, ends, seq), c));
+                    Q = compose<PACKED>(al[r], Q);
+                    if (starts >> r & 1) c = f4(0.f);
+                }
+            }
+            at = seq;
+            chain.hand_in(Q, c, eA, eB, k, warp, lane);
+        };
+        auto finish = [&](int k, F4 (&al)[kR], uint32_t starts, uint32_t ends, const Seq &at, const F4 &eA, const F4 &eB) {
+            const int tile = tile_of(k), t0 = tile * L::TT + tg;
+            const bool any = tile >= 0 && t0 < d.T;
+            F4 hs = f4(0.f);
+            if (any)
+                hs = load_row<float, TMA>(p.cs + ((int64_t)row * ((d.T + kR - 1) / kR) + t0 / kR) * d.D + ch, nc);
+            F4 c = chain.take(eA, eB, k, warp, lane);
+            if (any) {
+#pragma unroll
+                for (int r = kR - 1; r >= 0; --r) {   // al becomes delta
+                    const F4 dl = add4(v_of(k, r, ends, at), c);
+                    c = mul4(al[r], dl);
+                    if (starts >> r & 1) c = f4(0.f);
+                    al[r] = dl;
+                }
+                F4 tA = f4(0.f), tb = f4(0.f);
+                const int64_t o = ((int64_t)row * d.T + t0) * d.D + ch;
+#pragma unroll
+                for (int h0 = 0; h0 < kR; h0 += 2) {
+                    float2 z[4], t[4], Y[4], av[4], w[4];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const F4 a = in(k, 1, p.a, d.a_stride_b, d.a_stride_t, h0 + r);
+                        z[2 * r] = a.lo;
+                        z[2 * r + 1] = a.hi;
+                    }
+                    decays<4, 2>(C, z, bias2, rate, t, Y, av, w);
+#pragma unroll
+                    for (int r2 = 0; r2 < 2; ++r2) {
+                        const int r = h0 + r2;
+                        const F4 x = in(k, 0, p.x, d.x_stride_b, d.x_stride_t, r), b = in(k, 2, p.b, d.b_stride_b, d.b_stride_t, r);
+                        int n0 = 0;
+                        if (starts >> r & 1) {
+                            Seq m = at;
+                            m.up_to(p, t0 + r);
+                            n0 = m.n;
+                            hs = p.h0 ? load_words(p.h0 + (int64_t)n0 * d.D + ch, nc) : f4(0.f);
+                        }
+                        const bool live = t0 + r < d.T;
+                        const F4 de = live ? al[r] : f4(0.f);
+                        F4 gx, ga, gb;
+                        auto pair = [&](int i, float2 xv, float2 bv, float2 dv, float2 &hh, float2 &qA, float2 &qb, float2 &ox,
+                                        float2 &oa, float2 &ob) {
+                            const float2 rs = inv_sqrt2(w[i]), be = sigmoid2(C, bv), s = mul2(w[i], rs);
+                            const float2 sg = sigmoid_from_t(C, z[i], t[i]);
+                            const float2 sbx = mul2(mul2(s, be), xv);
+                            ox = mul2(mul2(dv, s), be);
+                            ob = mul2(mul2(dv, sbx), one_minus(C, be));
+                            // dg = delta (alpha h_{t-1} - beta x alpha^2 / s); 1/s is taken as 0 where s is
+                            const float2 rz = make_float2(w[i].x < kLeastNormal ? 0.f : rs.x, w[i].y < kLeastNormal ? 0.f : rs.y);
+                            const float2 m1 = mul2(av[i], hh);
+                            const float2 m2 = mul2(mul2(mul2(be, xv), mul2(av[i], av[i])), rz);
+                            const float2 ndg = mul2(dv, fma2(m1, C.neg, m2));   // -dg
+                            oa = mul2(mul2(ndg, rate[i % 2]), sg);
+                            qA = fma2(ndg, Y[i], qA);                                    // dg g log2(e)
+                            qb = add2(qb, oa);
+                            hh = add2(m1, sbx);
+                        };
+                        pair(2 * r2, x.lo, b.lo, de.lo, hs.lo, tA.lo, tb.lo, gx.lo, ga.lo, gb.lo);
+                        pair(2 * r2 + 1, x.hi, b.hi, de.hi, hs.hi, tA.hi, tb.hi, gx.hi, ga.hi, gb.hi);
+                        if (live) {
+                            store_row<T, TMA>((T *)p.dx + o + (int64_t)r * d.D, gx, nc);
+                            store_row<T, TMA>((T *)p.da + o + (int64_t)r * d.D, ga, nc);
+                            store_row<T, TMA>((T *)p.db + o + (int64_t)r * d.D, gb, nc);
+                            if (starts >> r & 1 && p.dh0)
+                                store_words(p.dh0 + (int64_t)n0 * d.D + ch, mul4({av[2 * r2], av[2 * r2 + 1]}, al[r]), nc);
+                        }
+                    }
+                }
+                sA[0] = add4(sA[0], tA);
+                sb[0] = add4(sb[0], tb);
+            }
+            if ((k & 15) == 15) {
+                sA[1] = add4(sA[1], sA[0]);
+                sb[1] = add4(sb[1], sb[0]);
+                sA[0] = sb[0] = f4(0.f);
+            }
+        };
+        F4 al[kR], eA, eB;
+        uint32_t starts, ends;
+        Seq at;
+        for (int k = 0; k < steps; ++k) {
+            begin(k, al, starts, ends, at, eA, eB);
+            finish(k, al, starts, ends, at, eA, eB);
+        }
+        // this CTA's sums: over the token groups, in order
         const int gi = warp * L::G + g;
-        *(float4 *)&red[(gi * 2) * L::CH + q * 4] = to4(add4(sA[1], sA[0]));
-        *(float4 *)&red[(gi * 2 + 1) * L::CH + q * 4] = to4(add4(sb[1], sb[0]));
+        *(float4 *)&red[gi][0][q * 4] = to4(mul4(add4(sA[1], sA[0]), f4(kLn2)));
+        *(float4 *)&red[gi][1][q * 4] = to4(add4(sb[1], sb[0]));
     }
     __syncthreads();
-    for (int i = tid; i < 2 * L::CH; i += kThreads) {
+    for (int i = tid; i < 2 * L::CH; i += L::THREADS) {
         const int which = i / L::CH, c = i % L::CH;
         if (slab * L::CH + c >= d.D) continue;
         float s = 0.f;
 #pragma unroll
-        for (int j = 0; j < L::NG; ++j) s += red[(j * 2 + which) * L::CH + c];
+        for (int j = 0; j < L::NG; ++j) s += red[j][which][c];
         p.part[(((int64_t)row * cs + rank) * 2 + which) * d.D + slab * L::CH + c] = s;
     }
-    if (failed) *p.status = GDN_ERR_DEVICE_TIMEOUT;
-    if (TMA && tid == 0 && failed)
-        for (int k = max(0, steps - 2); k < steps; ++k)
-            if (k * (int)cs + (int)rank < p.ntiles) tc::mbar_wait(&full[k & 1], (k >> 1) & 1);
+    if (failed || lost) *p.status = GDN_ERR_DEVICE_TIMEOUT;
+    // copies in flight end before the CTA does (they have, unless a wait gave up), and no CTA leaves while
+    // another may still write to it
+    if (TMA && warp == L::WARPS && lane == 0)
+        for (int k = max(0, mine - L::STAGES); k < mine; ++k) tc::mbar_wait(&chain.full[k % L::STAGES], (k / L::STAGES) & 1);
+    __syncwarp();
+    if (cs > 1) cluster_sync();
+    else __syncthreads();
 }
 
 // The parameter gradients: part[parts][2][D] over its rows, 8 strided partial sums per channel.
@@ -636,49 +769,46 @@ __global__ void __launch_bounds__(128) rec_step_kernel(const RecProblem p, float
     const F4 b = load_row<T, VEC>((const T *)p.b + n * d.b_stride_b + ch, nc);
     const F4 x = load_row<T, VEC>((const T *)p.x + n * d.x_stride_b + ch, nc);
     const F4 h0 = load_row<float, VEC>(state + n * d.D + ch, nc);
-    const F4 bias = load_row<float, VEC>(p.dt_bias + ch, nc);
-    F4 rate = load_row<float, VEC>(p.A_log + ch, nc);
-    rate = {make_float2(expf(rate.lo.x), expf(rate.lo.y)), make_float2(expf(rate.hi.x), expf(rate.hi.y))};
-    const Decay2 e0 = decay2(a.lo, bias.lo, rate.lo), e1 = decay2(a.hi, bias.hi, rate.hi);
-    const F4 s = {mul2(e0.w, inv_sqrt2(e0.w)), mul2(e1.w, inv_sqrt2(e1.w))};
-    const F4 h = fma4({e0.alpha, e1.alpha}, h0, mul4(mul4(s, {sigmoid2(b.lo), sigmoid2(b.hi)}), x));
+    const F4 bias = load_row<float, VEC>(p.dt_bias + ch, nc), l = load_row<float, VEC>(p.A_log + ch, nc);
+    const float2 rate[2] = {make_float2(expf(l.lo.x), expf(l.lo.y)), make_float2(expf(l.hi.x), expf(l.hi.y))};
+    const float2 bias2[2] = {mul2(bias.lo, splat2(kLog2e)), mul2(bias.hi, splat2(kLog2e))};
+    const GateConst C;
+    float2 z[2] = {a.lo, a.hi}, t[2], Y[2], al[2], w[2];
+    decays<2, 2>(C, z, bias2, rate, t, Y, al, w);
+    const F4 h = fma4({al[0], al[1]}, h0, mul4({write_scale2(C, w[0], b.lo), write_scale2(C, w[1], b.hi)}, x));
     store_row<float, VEC>(state + n * d.D + ch, h, nc);
     store_row<T, VEC>((T *)p.out + n * d.D + ch, h, nc);
 }
 
 // ===================================================================== host
-// CTAs per chain: as many as keep the chip filled (four CTAs per SM) and have a tile each. Clusters
-// of 16 need an opt-in and are only used where 8 leave more than half of the SMs idle.
-int cluster_size(int64_t chains, int64_t ntiles) {
-    int cs = 1;
-    while (cs < 8 && chains * cs * 2 <= 4 * kSms && cs < ntiles) cs *= 2;
-    if (cs == 8 && chains * 16 <= kSms && ntiles > 8) cs = 16;
-    return cs;
+// CTAs per chain: as many as fill the chip once at per_sm CTAs per SM, of those that have a tile.
+int cluster_size(int64_t chains, int64_t ntiles, int per_sm) {
+    int64_t fill = (int64_t)per_sm * kSms / chains;
+    if (fill > 6) fill = fill < 8 ? 6 : 8;
+    return (int)std::max<int64_t>(1, std::min<int64_t>({fill, ntiles, kMaxCluster}));
 }
-int tile_tokens(int dtype) { return dtype == GDN_F32 ? Tile<float>::TT : Tile<__half>::TT; }
-int tile_channels(int dtype) { return dtype == GDN_F32 ? Tile<float>::CH : Tile<__half>::CH; }
 
 struct RecPlan {
     int slabs, ntiles, cs;
     int64_t chains;
 };
-RecPlan make_plan(const gdn_recurrence_desc &d) {
+template <typename L> RecPlan make_plan(const gdn_recurrence_desc &d, int per_sm) {
     RecPlan r;
-    r.slabs = (int)cdiv64(d.D, tile_channels(d.dtype));
-    r.ntiles = (int)cdiv64(d.T, tile_tokens(d.dtype));
+    r.slabs = (int)cdiv64(d.D, L::CH);
+    r.ntiles = (int)cdiv64(d.T, L::TT);
     r.chains = (int64_t)d.B * r.slabs;
-    r.cs = cluster_size(r.chains, r.ntiles);
+    r.cs = cluster_size(r.chains, r.ntiles, per_sm);
     return r;
 }
 
 template <typename K>
-cudaError_t launch_chains(K kernel, const RecPlan &pl, size_t smem, cudaStream_t s, const RecProblem &p, const RecMaps &m) {
+cudaError_t launch_chains(K kernel, int threads, const RecPlan &pl, size_t smem, cudaStream_t s, const RecProblem &p, const RecMaps &m) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess && pl.cs > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(pl.chains * pl.cs));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -696,44 +826,51 @@ bool tma_ok(const gdn_recurrence_desc &d, const void *p, int64_t sb, int64_t st)
     return ptr_aligned(p, 16) && (st * es) % 16 == 0 && (d.B == 1 || (sb > 0 && (sb * es) % 16 == 0)) &&
            st * es < (1ll << 40) && sb * es < (1ll << 40);
 }
+template <typename L>
 bool tma_map(CUtensorMap *m, const gdn_recurrence_desc &d, const void *p, int64_t sb, int64_t st) {
     const uint64_t es = act_size(d.dtype);
     const uint64_t pt = (uint64_t)st * es, pb = d.B == 1 ? (uint64_t)d.T * pt : (uint64_t)sb * es;
-    return encode_token_map(m, d.dtype, p, d.B, d.T, d.D, pb, pt, tile_tokens(d.dtype), tile_channels(d.dtype));
+    return encode_token_map(m, d.dtype, p, d.B, d.T, d.D, pb, pt, L::TT, L::CH);
 }
 
 template <typename T>
-cudaError_t launch_forward(const RecProblem &p, const RecPlan &pl, cudaStream_t s) {
+cudaError_t launch_forward(RecProblem p, cudaStream_t s) {
+    using L = FwdTile<T>;
     const gdn_recurrence_desc &d = p.d;
+    const RecPlan pl = make_plan<L>(d, sizeof(T) == 2 ? 3 : 2);
+    p.slabs = pl.slabs;
+    p.ntiles = pl.ntiles;
     RecMaps m;
     memset(&m, 0, sizeof(m));
-    const bool tma = d.T > 0 && (d.D * sizeof(T)) % 16 == 0 && ptr_aligned(p.out, 16) &&
+    const bool tma = d.T > 0 && (d.D * sizeof(T)) % 16 == 0 && ptr_aligned(p.out, 16) && ptr_aligned(p.cs, 16) &&
                      tma_ok(d, p.x, d.x_stride_b, d.x_stride_t) && tma_ok(d, p.a, d.a_stride_b, d.a_stride_t) &&
                      tma_ok(d, p.b, d.b_stride_b, d.b_stride_t);
-    if (!tma) return launch_chains(rec_forward_kernel<T, false>, pl, 0, s, p, m);
-    if (!tma_map(&m.x, d, p.x, d.x_stride_b, d.x_stride_t) || !tma_map(&m.a, d, p.a, d.a_stride_b, d.a_stride_t) ||
-        !tma_map(&m.b, d, p.b, d.b_stride_b, d.b_stride_t))
+    if (tma && (!tma_map<L>(&m.x, d, p.x, d.x_stride_b, d.x_stride_t) || !tma_map<L>(&m.a, d, p.a, d.a_stride_b, d.a_stride_t) ||
+                !tma_map<L>(&m.b, d, p.b, d.b_stride_b, d.b_stride_t)))
         return cudaErrorInvalidValue;
-    return launch_chains(rec_forward_kernel<T, true>, pl, 2 * 3 * Tile<T>::kTensor, s, p, m);
+    auto kernel = p.cu ? (tma ? rec_forward_kernel<T, true, true> : rec_forward_kernel<T, false, true>)
+                       : (tma ? rec_forward_kernel<T, true, false> : rec_forward_kernel<T, false, false>);
+    return launch_chains(kernel, L::THREADS, pl, (tma ? L::STAGES * 3 * L::kTensor : 0) + 2 * (size_t)pl.cs * 2 * L::CH * 4, s, p, m);
 }
 
 template <typename T>
-cudaError_t launch_backward_rec(const RecProblem &p, const RecPlan &pl, cudaStream_t s) {
+cudaError_t launch_backward_rec(RecProblem p, cudaStream_t s) {
+    using L = BwdTile<T>;
     const gdn_recurrence_desc &d = p.d;
+    const RecPlan pl = make_plan<L>(d, sizeof(T) == 2 ? 3 : 2);
+    p.slabs = pl.slabs;
+    p.ntiles = pl.ntiles;
     RecMaps m;
     memset(&m, 0, sizeof(m));
     const bool tma = d.T > 0 && (d.D * sizeof(T)) % 16 == 0 && ptr_aligned(p.dx, 16) && ptr_aligned(p.da, 16) &&
                      ptr_aligned(p.db, 16) && ptr_aligned(p.grad_out, 16) && tma_ok(d, p.x, d.x_stride_b, d.x_stride_t) &&
                      tma_ok(d, p.a, d.a_stride_b, d.a_stride_t) && tma_ok(d, p.b, d.b_stride_b, d.b_stride_t);
-    cudaError_t e;
-    if (tma) {
-        if (!tma_map(&m.x, d, p.x, d.x_stride_b, d.x_stride_t) || !tma_map(&m.a, d, p.a, d.a_stride_b, d.a_stride_t) ||
-            !tma_map(&m.b, d, p.b, d.b_stride_b, d.b_stride_t) || !tma_map(&m.dy, d, p.grad_out, (int64_t)d.T * d.D, d.D))
-            return cudaErrorInvalidValue;
-        e = launch_chains(rec_backward_kernel<T, true>, pl, 2 * 4 * Tile<T>::kTensor, s, p, m);
-    } else {
-        e = launch_chains(rec_backward_kernel<T, false>, pl, 0, s, p, m);
-    }
+    if (tma && (!tma_map<L>(&m.x, d, p.x, d.x_stride_b, d.x_stride_t) || !tma_map<L>(&m.a, d, p.a, d.a_stride_b, d.a_stride_t) ||
+                !tma_map<L>(&m.b, d, p.b, d.b_stride_b, d.b_stride_t) || !tma_map<L>(&m.dy, d, p.grad_out, (int64_t)d.T * d.D, d.D)))
+        return cudaErrorInvalidValue;
+    auto kernel = p.cu ? (tma ? rec_backward_kernel<T, true, true> : rec_backward_kernel<T, false, true>)
+                       : (tma ? rec_backward_kernel<T, true, false> : rec_backward_kernel<T, false, false>);
+    const cudaError_t e = launch_chains(kernel, L::THREADS, pl, (tma ? L::STAGES * 4 * L::kTensor : 0) + 2 * (size_t)pl.cs * 2 * L::CH * 4, s, p, m);
     if (e != cudaSuccess) return e;
     rec_params_kernel<<<(unsigned)cdiv64(d.D, 32), 256, 0, s>>>(p, d.B * pl.cs);
     return cudaGetLastError();
@@ -770,7 +907,7 @@ RecLayout bwd_layout(const gdn_recurrence_desc &d) {
     size_t off = 0;
     const size_t chunks = ((size_t)d.T + GDN_RECURRENCE_CHUNK - 1) / GDN_RECURRENCE_CHUNK;
     L.status = off; off += kStatusBytes;
-    L.part = off;   off = align_up(off + (size_t)d.B * make_plan(d).cs * 2 * d.D * 4, 256);
+    L.part = off;   off = align_up(off + (size_t)d.B * kMaxCluster * 2 * d.D * 4, 256);
     L.cs = off;     off = align_up(off + (size_t)d.B * chunks * d.D * 4, 256);
     L.total = off;
     return L;
@@ -843,11 +980,8 @@ int gdn_recurrence_forward(const gdn_recurrence_desc *d, const void *x, const vo
     p.cs = chunk_states;
     p.status = (int32_t *)workspace;
     p.wait_immediate = wait_test_mode();
-    const RecPlan pl = make_plan(*d);
-    p.slabs = pl.slabs;
-    p.ntiles = pl.ntiles;
     return by_dtype(d->dtype, [&](auto t) {
-        return layer_status(launch_forward<decltype(t)>(p, pl, (cudaStream_t)stream));
+        return layer_status(launch_forward<decltype(t)>(p, (cudaStream_t)stream));
     });
 }
 
@@ -893,14 +1027,11 @@ int gdn_recurrence_backward(const gdn_recurrence_desc *d, const void *x, const v
     p.dh0 = dinitial_state;
     const cudaStream_t s = (cudaStream_t)stream;
     p.wait_immediate = wait_test_mode();
-    const RecPlan pl = make_plan(*d);
-    p.slabs = pl.slabs;
-    p.ntiles = pl.ntiles;
     return by_dtype(d->dtype, [&](auto t) {
         using T = decltype(t);
         cudaError_t e = cudaSuccess;
-        if (!chunk_states && d->T > 0) e = launch_forward<T>(p, pl, s);   // chunk states only
-        return layer_status(e != cudaSuccess ? e : launch_backward_rec<T>(p, pl, s));
+        if (!chunk_states && d->T > 0) e = launch_forward<T>(p, s);   // chunk states only
+        return layer_status(e != cudaSuccess ? e : launch_backward_rec<T>(p, s));
     });
 }
 

@@ -2,14 +2,16 @@
 // on pairs of channels.
 //
 //   t = e^-|z|, softplus(z) = max(z, 0) + log1p(t), g = -E softplus(z), alpha = e^g
-//   w = 1 - alpha^2 = -expm1(2g), s = sqrt(w), beta = 1 / (1 + e^-b)
+//   em = 1 - alpha, w = 1 - alpha^2 = em + em alpha, s = sqrt(w), beta = 1 / (1 + e^-b)
 //
-// Long memory lives where softplus(z) is small and alpha close to 1, so neither
-// log(1 + t) nor 1 - alpha^2 may be taken literally: log1p(t) / t on [0, 1] and
-// -expm1(-y) / y on [0, 1/2] are polynomials fitted here (weighted least squares to
-// the minimax relative error at Chebyshev nodes: 1.4e-7 and 5e-8 with fp32
-// evaluation). They run on the fp32 pipe as register pairs, which leaves five
-// special-function results per element (three e^x, one reciprocal, one root).
+// Everything is kept in powers of two: z, softplus and -g carry a factor log2(e), so
+// the exponentials are the hardware's. Long memory lives where softplus(z) is small
+// and alpha close to 1, so neither log(1 + t) nor 1 - alpha may be taken literally:
+// log2(1 + t) / t on [0, 1] and (1 - 2^-Y) / Y on [0, 1/4] are polynomials fitted here
+// (weighted least squares to the minimax relative error at Chebyshev nodes; 3.5e-7 and
+// 1.3e-7 in fp32 evaluation). They run on the fp32 pipe as register pairs, which
+// leaves five special-function results per element: three exponentials (32 a clock
+// and SM), a reciprocal and a root (16).
 #pragma once
 
 #include "gdn_common.cuh"
@@ -17,78 +19,104 @@
 namespace gdn {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLeastNormal = 1.17549435e-38f;
+
+// The constants of the pair operations, in registers: a pair operation takes no literal and no constant bank, and
+// left to itself the compiler moves each constant into place before each use (6 of 42 instructions per element).
+struct GateConst {
+    float2 sp[8], om[4], log2e, one, neg;
+    __device__ __forceinline__ static float2 pin(float v) {
+        float2 r;
+        asm volatile("mov.f32 %0, %1;" : "=f"(r.x) : "f"(v));
+        asm volatile("mov.f32 %0, %1;" : "=f"(r.y) : "f"(v));
+        return r;
+    }
+    __device__ __forceinline__ GateConst() {
+        const float s[8] = {1.4426947832107544f, -0.7213100790977478f, 0.48006370663642883f, -0.3533948063850403f,
+                            0.25600969791412354f, -0.15535184741020203f, 0.06360787153244019f, -0.012319467030465603f};
+        const float o[4] = {0.6931471228599548f, -0.24022150039672852f, 0.055404357612133026f, -0.008974975906312466f};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sp[i] = pin(s[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) om[i] = pin(o[i]);
+        log2e = pin(kLog2e);
+        one = pin(1.f);
+        neg = pin(-1.f);
+    }
+};
 
 __device__ __forceinline__ float rsqrt_approx(float x) {
     float y;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float sqrt_approx(float x) {
+    float y;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ float2 ex2_pair(float2 x) { return make_float2(ex2_approx(x.x), ex2_approx(x.y)); }
 __device__ __forceinline__ float2 rcp_pair(float2 x) { return make_float2(rcp_approx(x.x), rcp_approx(x.y)); }
+__device__ __forceinline__ float2 one_minus(const GateConst &k, float2 x) { return fma2(x, k.neg, k.one); }
 
-// log(1 + t) for t in [0, 1]
-__device__ __forceinline__ float2 log1p_unit(float2 t) {
-    float2 p = splat2(0.005232691299170256f);
-    p = fma2(p, t, splat2(-0.029505228623747826f));
-    p = fma2(p, t, splat2(0.07822593301534653f));
-    p = fma2(p, t, splat2(-0.13663244247436523f));
-    p = fma2(p, t, splat2(0.19106006622314453f));
-    p = fma2(p, t, splat2(-0.2484298199415207f));
-    p = fma2(p, t, splat2(0.3331909775733948f));
-    p = fma2(p, t, splat2(-0.4999949336051941f));
-    p = fma2(p, t, splat2(0.9999999403953552f));
-    return mul2(t, p);
+// Decays of N pairs of channels from the gate input a. Step by step over all pairs: each coefficient is
+// then fetched once for all of them.
+//   z: (a + dt_bias) log2(e), t: e^-|a + dt_bias|, Y: -log2(alpha) = exp(A_log) softplus(a + dt_bias) log2(e),
+//   w: 1 - alpha^2
+// In: z holds a. bias2 = dt_bias log2(e) and rate = exp(A_log) of pair i are bias2[i % M], rate[i % M].
+template <int N, int M>
+__device__ __forceinline__ void decays(const GateConst &C, float2 (&z)[N], const float2 (&bias2)[M], const float2 (&rate)[M], float2 (&t)[N],
+                                       float2 (&Y)[N], float2 (&alpha)[N], float2 (&w)[N]) {
+    float2 q[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = fma2(z[i], C.log2e, bias2[i % M]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) t[i] = ex2_pair(make_float2(-fabsf(z[i].x), -fabsf(z[i].y)));
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = fma2(C.sp[7], t[i], C.sp[6]);
+#pragma unroll
+    for (int k = 5; k >= 0; --k)
+#pragma unroll
+        for (int i = 0; i < N; ++i) q[i] = fma2(q[i], t[i], C.sp[k]);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        Y[i] = mul2(rate[i % M], fma2(q[i], t[i], make_float2(fmaxf(z[i].x, 0.f), fmaxf(z[i].y, 0.f))));
+    // alpha = 1 - em, with em from the polynomial for slow decays (the hardware exponential's last bits would
+    // pile up over thousands of tokens), and the exponential beyond
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = fma2(C.om[3], Y[i], C.om[2]);
+#pragma unroll
+    for (int k = 1; k >= 0; --k)
+#pragma unroll
+        for (int i = 0; i < N; ++i) q[i] = fma2(q[i], Y[i], C.om[k]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float2 es = mul2(q[i], Y[i]), al = ex2_pair(make_float2(-Y[i].x, -Y[i].y));
+        const float2 as = one_minus(C, es), el = one_minus(C, al);
+        const bool s0 = Y[i].x < 0.25f, s1 = Y[i].y < 0.25f;
+        const float2 em = make_float2(s0 ? es.x : el.x, s1 ? es.y : el.y);
+        alpha[i] = make_float2(s0 ? as.x : al.x, s1 ? as.y : al.y);
+        w[i] = fma2(em, alpha[i], em);
+    }
 }
 
-// 1 - e^-y for y in [0, 1/2]
-__device__ __forceinline__ float2 one_minus_exp_small(float2 y) {
-    float2 p = splat2(-0.0011216348502784967f);
-    p = fma2(p, y, splat2(0.008187386207282543f));
-    p = fma2(p, y, splat2(-0.041629090905189514f));
-    p = fma2(p, y, splat2(0.16666224598884583f));
-    p = fma2(p, y, splat2(-0.4999998211860657f));
-    p = fma2(p, y, splat2(1.0f));
-    return mul2(y, p);
+__device__ __forceinline__ float2 sigmoid2(const GateConst &C, float2 b) {
+    const float2 m = mul2(b, C.log2e);
+    return rcp_pair(add2(ex2_pair(make_float2(-m.x, -m.y)), C.one));
 }
-
-// Decay of two channels from the gate input a. rate = exp(A_log).
-struct Decay2 {
-    float2 z, t;    // a + dt_bias, e^-|z|
-    float2 sp;      // softplus(z)
-    float2 alpha;   // e^-(rate sp)
-    float2 w;       // 1 - alpha^2
-};
-
-__device__ __forceinline__ Decay2 decay2(float2 a, float2 bias, float2 rate) {
-    Decay2 r;
-    r.z = add2(a, bias);
-    r.t = ex2_pair(make_float2(-fabsf(r.z.x) * kLog2e, -fabsf(r.z.y) * kLog2e));
-    r.sp = add2(make_float2(fmaxf(r.z.x, 0.f), fmaxf(r.z.y, 0.f)), log1p_unit(r.t));
-    const float2 y = mul2(rate, r.sp);   // -log(alpha)
-    // alpha = 1 - em with em = 1 - e^-y from the polynomial where y < 1/2 (the long memories: the
-    // hardware exponential's last bits would pile up over thousands of tokens), else e^-y
-    const float2 es = one_minus_exp_small(y);
-    const float2 al = ex2_pair(mul2(y, splat2(-kLog2e)));
-    const float2 el = fma2(al, splat2(-1.f), splat2(1.f)), as = fma2(es, splat2(-1.f), splat2(1.f));
-    const float2 em = make_float2(y.x < 0.5f ? es.x : el.x, y.y < 0.5f ? es.y : el.y);
-    r.alpha = make_float2(y.x < 0.5f ? as.x : al.x, y.y < 0.5f ? as.y : al.y);
-    r.w = fma2(em, r.alpha, em);
-    return r;
+// sqrt(w) sigmoid(b); a w below the normal range counts as 0
+__device__ __forceinline__ float2 write_scale2(const GateConst &C, float2 w, float2 b) {
+    return mul2(make_float2(sqrt_approx(w.x), sqrt_approx(w.y)), sigmoid2(C, b));
 }
-
-// 1 / sqrt(w) for the scale s = w / sqrt(w); a w below the normal range (where the
-// approximation flushes) gives s = 0, a NaN stays one through w.
+// 1 / sqrt(w), finite for w = 0; a NaN stays one through w
 __device__ __forceinline__ float2 inv_sqrt2(float2 w) {
-    return make_float2(rsqrt_approx(fmaxf(w.x, 1.17549435e-38f)), rsqrt_approx(fmaxf(w.y, 1.17549435e-38f)));
-}
-
-__device__ __forceinline__ float2 sigmoid2(float2 b) {
-    return rcp_pair(add2(ex2_pair(mul2(b, splat2(-kLog2e))), splat2(1.f)));
+    return make_float2(rsqrt_approx(fmaxf(w.x, kLeastNormal)), rsqrt_approx(fmaxf(w.y, kLeastNormal)));
 }
 
 // sigmoid(z) from t = e^-|z|
-__device__ __forceinline__ float2 sigmoid_from_t(float2 z, float2 t) {
-    const float2 r = rcp_pair(add2(t, splat2(1.f)));
+__device__ __forceinline__ float2 sigmoid_from_t(const GateConst &C, float2 z, float2 t) {
+    const float2 r = rcp_pair(add2(t, C.one));
     const float2 q = mul2(t, r);
     return make_float2(z.x >= 0.f ? r.x : q.x, z.y >= 0.f ? r.y : q.y);
 }

@@ -46,7 +46,7 @@ EXPORTS = ("gdn_desc_init", "gdn_workspace_bytes", "gdn_workspace_offsets", "gdn
            "gdn_group_norm_backward_workspace_bytes", "gdn_group_norm_forward",
            "gdn_group_norm_backward")
 
-GDN_RECURRENCE_CHUNK = 8
+GDN_RECURRENCE_CHUNK = 4
 ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
 ROTARY_SCALINGS = {"plain": 0, "linear": 1, "by_parts": 2}
 ACTIVATIONS = {"none": 0, "silu": 1}
