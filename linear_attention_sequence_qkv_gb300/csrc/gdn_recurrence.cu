@@ -62,7 +62,8 @@ template <typename T, int R_, int WARPS_, int STAGES_> struct Tile {
 };
 constexpr int kMaxCluster = 16;   // more than 8 needs an opt-in
 template <typename T> using FwdTile = Tile<T, 4, 4, 4>;
-template <typename T> using BwdTile = Tile<T, GDN_RECURRENCE_CHUNK, 4, 3>;
+template <typename T> using BwdTile = Tile<T, GDN_RECURRENCE_CHUNK, 4, 2>;
+template <typename T> constexpr int kBwdStash = 3 * BwdTile<T>::R * 32 * BwdTile<T>::WARPS * 16;   // bytes
 constexpr int kBwdLag = 1;   // a tile is done with when the maps of the step this much later are in
 
 struct F4 {          // four channels as two pairs
@@ -406,19 +407,19 @@ rec_forward_kernel(const __grid_constant__ RecProblem p, const __grid_constant__
                 constexpr int kB = 4;   // tokens at a time
 #pragma unroll
                 for (int r0 = 0; r0 < kR; r0 += kB) {
-                    float2 z[2 * kB], t[2 * kB], Y[2 * kB], al[2 * kB], w[2 * kB];
+                    float2 z[2 * kB], t[2 * kB], Y[2 * kB], al[2 * kB], em[2 * kB];
 #pragma unroll
                     for (int r = 0; r < kB; ++r) {
                         const F4 a = in(0, p.a, d.a_stride_b, d.a_stride_t, r0 + r);
                         z[2 * r] = a.lo;
                         z[2 * r + 1] = a.hi;
                     }
-                    decays<2 * kB, 2>(C, z, bias2, rate, t, Y, al, w);
+                    decays<2 * kB, 2>(C, z, bias2, rate, t, Y, al, em);
 #pragma unroll
                     for (int r = 0; r < kB; ++r) {
                         const F4 b = in(1, p.b, d.b_stride_b, d.b_stride_t, r0 + r), x = in(2, p.x, d.x_stride_b, d.x_stride_t, r0 + r);
                         P[r0 + r] = {al[2 * r], al[2 * r + 1]};
-                        h[r0 + r] = mul4({write_scale2(C, w[2 * r], b.lo), write_scale2(C, w[2 * r + 1], b.hi)}, x);
+                        h[r0 + r] = mul4({write_scale2(C, em[2 * r], al[2 * r], b.lo), write_scale2(C, em[2 * r + 1], al[2 * r + 1], b.hi)}, x);
                     }
                 }
                 if (seq.b0 == t0 || (PACKED && seq.b1 < t0 + kR && seq.b1 < d.T)) {   // a sequence starts here
@@ -508,7 +509,7 @@ __global__ void __launch_bounds__(BwdTile<T>::THREADS, sizeof(T) == 2 ? 3 : 2)
 rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant__ RecMaps maps) {
     using L = BwdTile<T>;
     constexpr int kR = L::R;
-    static_assert(kR <= 32, "the start and end masks hold one bit per token");
+    static_assert(kR <= 32, "the start mask holds one bit per token");
     extern __shared__ __align__(128) unsigned char smem[];   // TMA: STAGES tiles of x, a, b, grad_out; the cluster's maps
     __shared__ Chain<L, false, PACKED> chain;
     __shared__ float red[L::NG][2][L::CH];
@@ -527,7 +528,7 @@ rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant_
     bool failed = false, lost = false;
 
     if (warp == L::WARPS) {
-        float4 *agg = (float4 *)(smem + (TMA ? L::STAGES * 4 * L::kTensor : 0));
+        float4 *agg = (float4 *)(smem + (TMA ? L::STAGES * 4 * L::kTensor : 0) + kBwdStash<T>);
         auto issue = [&](int k) {
             if (!TMA || lane != 0 || k >= mine) return;
             uint64_t *bar = &chain.full[k % L::STAGES];
@@ -572,62 +573,61 @@ rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant_
             if (TMA) return unpack4<T>(smem + (k % L::STAGES * 4 + which) * L::kTensor + (tg + r) * 128 + q * 4 * sizeof(T));
             return load_row<T, false>((const T *)base + row * sb_ + (int64_t)(t0 + r) * st_ + ch, t0 + r < d.T ? nc : 0);
         };
-        // v_t; m: the tile's sequence, ends: the group's tokens that end one
-        auto v_of = [&](int k, int r, uint32_t ends, const Seq &at) -> F4 {
-            F4 v = in(k, 3, p.grad_out, (int64_t)d.T * d.D, d.D, r);
-            if (ends >> r & 1 && p.grad_final) {
-                Seq m = at;
-                const int t0 = tile_of(k) * L::TT + tg;
-                m.up_to(p, t0 + r);
-                v = add4(v, load_words(p.grad_final + (int64_t)m.n * d.D + ch, nc));
-            }
-            return v;
-        };
-        // decays of tile k's tokens (-0 at a sequence's first), and the map to the carry warp
-        auto begin = [&](int k, F4 (&al)[kR], uint32_t &starts, uint32_t &ends, Seq &at, F4 &eA, F4 &eB) {
+        // Between begin and finish a thread keeps three values per token and channel in its own slots of shared
+        // memory: em, Y and rate sigmoid(z) (half of the work of recomputing them).
+        float4 *stash = (float4 *)(smem + (TMA ? L::STAGES * 4 * L::kTensor : 0)) + tid;
+        constexpr int kSlot = 32 * L::WARPS;
+        // decays of tile k's tokens (-0 at a sequence's first), their v_t, and the map to the carry warp
+        auto begin = [&](int k, F4 (&al)[kR], F4 (&v)[kR], uint32_t &starts, F4 &eA, F4 &eB) {
             const int tile = tile_of(k), t0 = tile * L::TT + tg;
             F4 Q = f4(1.f), c = f4(0.f);
-            starts = ends = 0;
+            starts = 0;
             if (tile >= 0) {
                 if (TMA) bounded_wait(&chain.full[k % L::STAGES], (k / L::STAGES) & 1, p.wait_immediate, failed);
+                float2 z[2 * kR], t[2 * kR], Y[2 * kR], av[2 * kR], em[2 * kR];
+#pragma unroll
+                for (int r = 0; r < kR; ++r) {
+                    const F4 a = in(k, 1, p.a, d.a_stride_b, d.a_stride_t, r);
+                    z[2 * r] = a.lo;
+                    z[2 * r + 1] = a.hi;
+                }
+                decays<2 * kR, 2>(C, z, bias2, rate, t, Y, av, em);
+#pragma unroll
+                for (int r = 0; r < kR; ++r) {
+                    const float2 s0 = mul2(rate[0], sigmoid_from_t(C, z[2 * r], t[2 * r]));
+                    const float2 s1 = mul2(rate[1], sigmoid_from_t(C, z[2 * r + 1], t[2 * r + 1]));
+                    stash[(3 * r) * kSlot] = to4({em[2 * r], em[2 * r + 1]});
+                    stash[(3 * r + 1) * kSlot] = to4({Y[2 * r], Y[2 * r + 1]});
+                    stash[(3 * r + 2) * kSlot] = to4({s0, s1});
+                    al[r] = {av[2 * r], av[2 * r + 1]};
+                    v[r] = in(k, 3, p.grad_out, (int64_t)d.T * d.D, d.D, r);
+                }
                 if (t0 < d.T) {
-                    seq.down_to(p, t0);
-                    if (seq.b0 == t0 || seq.b1 <= t0 + kR) {
+                    if (PACKED) seq.down_to(p, t0);
+                    if (seq.b0 == t0 || seq.b1 <= t0 + kR) {   // a sequence starts or ends here
                         Seq m = seq;
-                        for (int r = 0; r < kR && t0 + r < d.T; ++r) {
+#pragma unroll
+                        for (int r = 0; r < kR; ++r) {
                             m.up_to(p, t0 + r);
-                            starts |= (m.b0 == t0 + r ? 1u : 0u) << r;
-                            ends |= (m.b1 == t0 + r + 1 ? 1u : 0u) << r;
+                            if (t0 + r < d.T && m.b0 == t0 + r) {
+                                starts |= 1u << r;
+                                al[r] = f4(-0.f);
+                            }
+                            if (m.b1 == t0 + r + 1 && p.grad_final)
+                                v[r] = add4(v[r], load_words(p.grad_final + (int64_t)m.n * d.D + ch, nc));
                         }
                     }
                 }
 #pragma unroll
-                for (int r0 = 0; r0 < kR; r0 += 2) {
-                    float2 z[4], t[4], Y[4], av[4], w[4];
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const F4 a = in(k, 1, p.a, d.a_stride_b, d.a_stride_t, r0 + r);
-                        z[2 * r] = a.lo;
-                        z[2 * r + 1] = a.hi;
-                    }
-                    decays<4, 2>(C, z, bias2, rate, t, Y, av, w);
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        al[r0 + r] = {av[2 * r], av[2 * r + 1]};
-                        if (starts >> (r0 + r) & 1) al[r0 + r] = f4(-0.f);
-                    }
-                }
-#pragma unroll
                 for (int r = kR - 1; r >= 0; --r) {
-                    c = mul4(al[r], add4(v_of(k, r, ends, seq), c));
+                    c = mul4(al[r], add4(v[r], c));
                     Q = compose<PACKED>(al[r], Q);
-                    if (starts >> r & 1) c = f4(0.f);
+                    if (PACKED) c = {cut2(al[r].lo, splat2(0.f), c.lo), cut2(al[r].hi, splat2(0.f), c.hi)};
                 }
             }
-            at = seq;
             chain.hand_in(Q, c, eA, eB, k, warp, lane);
         };
-        auto finish = [&](int k, F4 (&al)[kR], uint32_t starts, uint32_t ends, const Seq &at, const F4 &eA, const F4 &eB) {
+        auto finish = [&](int k, F4 (&al)[kR], F4 (&v)[kR], uint32_t starts, const F4 &eA, const F4 &eB) {
             const int tile = tile_of(k), t0 = tile * L::TT + tg;
             const bool any = tile >= 0 && t0 < d.T;
             F4 hs = f4(0.f);
@@ -636,65 +636,56 @@ rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant_
             F4 c = chain.take(eA, eB, k, warp, lane);
             if (any) {
 #pragma unroll
-                for (int r = kR - 1; r >= 0; --r) {   // al becomes delta
-                    const F4 dl = add4(v_of(k, r, ends, at), c);
-                    c = mul4(al[r], dl);
-                    if (starts >> r & 1) c = f4(0.f);
-                    al[r] = dl;
+                for (int r = kR - 1; r >= 0; --r) {   // v becomes delta; behind the row's end both are 0
+                    v[r] = add4(v[r], c);
+                    c = mul4(al[r], v[r]);
+                    if (PACKED) c = {cut2(al[r].lo, splat2(0.f), c.lo), cut2(al[r].hi, splat2(0.f), c.hi)};
                 }
                 F4 tA = f4(0.f), tb = f4(0.f);
                 const int64_t o = ((int64_t)row * d.T + t0) * d.D + ch;
+                T *dx = (T *)p.dx + o, *da = (T *)p.da + o, *db = (T *)p.db + o;
+                const bool whole = nc == 4 && t0 + kR <= d.T;
 #pragma unroll
-                for (int h0 = 0; h0 < kR; h0 += 2) {
-                    float2 z[4], t[4], Y[4], av[4], w[4];
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const F4 a = in(k, 1, p.a, d.a_stride_b, d.a_stride_t, h0 + r);
-                        z[2 * r] = a.lo;
-                        z[2 * r + 1] = a.hi;
+                for (int r = 0; r < kR; ++r) {
+                    const F4 x = in(k, 0, p.x, d.x_stride_b, d.x_stride_t, r), b = in(k, 2, p.b, d.b_stride_b, d.b_stride_t, r);
+                    const F4 em = f4(stash[(3 * r) * kSlot]), Y = f4(stash[(3 * r + 1) * kSlot]), rsg = f4(stash[(3 * r + 2) * kSlot]);
+                    if (starts >> r & 1) {   // the decay itself again, the state before, and the state's gradient
+                        al[r] = {decay_of(em.lo, Y.lo), decay_of(em.hi, Y.hi)};
+                        Seq m = seq;
+                        m.up_to(p, t0 + r);
+                        hs = p.h0 ? load_words(p.h0 + (int64_t)m.n * d.D + ch, nc) : f4(0.f);
+                        if (p.dh0) store_words(p.dh0 + (int64_t)m.n * d.D + ch, mul4(al[r], v[r]), nc);
                     }
-                    decays<4, 2>(C, z, bias2, rate, t, Y, av, w);
-#pragma unroll
-                    for (int r2 = 0; r2 < 2; ++r2) {
-                        const int r = h0 + r2;
-                        const F4 x = in(k, 0, p.x, d.x_stride_b, d.x_stride_t, r), b = in(k, 2, p.b, d.b_stride_b, d.b_stride_t, r);
-                        int n0 = 0;
-                        if (starts >> r & 1) {
-                            Seq m = at;
-                            m.up_to(p, t0 + r);
-                            n0 = m.n;
-                            hs = p.h0 ? load_words(p.h0 + (int64_t)n0 * d.D + ch, nc) : f4(0.f);
-                        }
-                        const bool live = t0 + r < d.T;
-                        const F4 de = live ? al[r] : f4(0.f);
-                        F4 gx, ga, gb;
-                        auto pair = [&](int i, float2 xv, float2 bv, float2 dv, float2 &hh, float2 &qA, float2 &qb, float2 &ox,
-                                        float2 &oa, float2 &ob) {
-                            const float2 rs = inv_sqrt2(w[i]), be = sigmoid2(C, bv), s = mul2(w[i], rs);
-                            const float2 sg = sigmoid_from_t(C, z[i], t[i]);
-                            const float2 sbx = mul2(mul2(s, be), xv);
-                            ox = mul2(mul2(dv, s), be);
-                            ob = mul2(mul2(dv, sbx), one_minus(C, be));
-                            // dg = delta (alpha h_{t-1} - beta x alpha^2 / s); 1/s is taken as 0 where s is
-                            const float2 rz = make_float2(w[i].x < kLeastNormal ? 0.f : rs.x, w[i].y < kLeastNormal ? 0.f : rs.y);
-                            const float2 m1 = mul2(av[i], hh);
-                            const float2 m2 = mul2(mul2(mul2(be, xv), mul2(av[i], av[i])), rz);
-                            const float2 ndg = mul2(dv, fma2(m1, C.neg, m2));   // -dg
-                            oa = mul2(mul2(ndg, rate[i % 2]), sg);
-                            qA = fma2(ndg, Y[i], qA);                                    // dg g log2(e)
-                            qb = add2(qb, oa);
-                            hh = add2(m1, sbx);
-                        };
-                        pair(2 * r2, x.lo, b.lo, de.lo, hs.lo, tA.lo, tb.lo, gx.lo, ga.lo, gb.lo);
-                        pair(2 * r2 + 1, x.hi, b.hi, de.hi, hs.hi, tA.hi, tb.hi, gx.hi, ga.hi, gb.hi);
-                        if (live) {
-                            store_row<T, TMA>((T *)p.dx + o + (int64_t)r * d.D, gx, nc);
-                            store_row<T, TMA>((T *)p.da + o + (int64_t)r * d.D, ga, nc);
-                            store_row<T, TMA>((T *)p.db + o + (int64_t)r * d.D, gb, nc);
-                            if (starts >> r & 1 && p.dh0)
-                                store_words(p.dh0 + (int64_t)n0 * d.D + ch, mul4({av[2 * r2], av[2 * r2 + 1]}, al[r]), nc);
-                        }
+                    F4 gx, ga, gb;
+                    auto pair = [&](float2 em, float2 Y, float2 rsg, float2 al, float2 xv, float2 bv, float2 dv, float2 &hh,
+                                    float2 &qA, float2 &qb, float2 &ox, float2 &oa, float2 &ob) {
+                        const float2 w = fma2(em, al, em), rs = inv_sqrt2(w), be = sigmoid2(C, bv);
+                        const float2 bx = mul2(be, xv), s = mul2(w, rs), sbx = mul2(s, bx);
+                        ox = mul2(mul2(dv, s), be);
+                        ob = mul2(mul2(dv, sbx), one_minus(C, be));
+                        // dg = delta (alpha h_{t-1} - beta x alpha^2 / s). Where w counts as 0, so do rate
+                        // sigmoid(z) and Y, below 2^-126, and 1/s is kept below 2^63: the product vanishes
+                        const float2 m1 = mul2(al, hh), m2 = mul2(mul2(mul2(al, al), rs), bx);
+                        const float2 ndg = mul2(dv, fma2(m1, C.neg, m2));   // -dg
+                        oa = mul2(ndg, rsg);
+                        qA = fma2(ndg, Y, qA);                              // dg g log2(e)
+                        qb = add2(qb, oa);
+                        hh = add2(m1, sbx);
+                    };
+                    pair(em.lo, Y.lo, rsg.lo, al[r].lo, x.lo, b.lo, v[r].lo, hs.lo, tA.lo, tb.lo, gx.lo, ga.lo, gb.lo);
+                    pair(em.hi, Y.hi, rsg.hi, al[r].hi, x.hi, b.hi, v[r].hi, hs.hi, tA.hi, tb.hi, gx.hi, ga.hi, gb.hi);
+                    if (TMA && whole) {
+                        pack4<T>(dx, gx);
+                        pack4<T>(da, ga);
+                        pack4<T>(db, gb);
+                    } else if (t0 + r < d.T) {
+                        store_row<T, TMA>(dx, gx, nc);
+                        store_row<T, TMA>(da, ga, nc);
+                        store_row<T, TMA>(db, gb, nc);
                     }
+                    dx += d.D;
+                    da += d.D;
+                    db += d.D;
                 }
                 sA[0] = add4(sA[0], tA);
                 sb[0] = add4(sb[0], tb);
@@ -705,12 +696,11 @@ rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant_
                 sA[0] = sb[0] = f4(0.f);
             }
         };
-        F4 al[kR], eA, eB;
-        uint32_t starts, ends;
-        Seq at;
+        F4 al[kR], v[kR], eA, eB;
+        uint32_t starts;
         for (int k = 0; k < steps; ++k) {
-            begin(k, al, starts, ends, at, eA, eB);
-            finish(k, al, starts, ends, at, eA, eB);
+            begin(k, al, v, starts, eA, eB);
+            finish(k, al, v, starts, eA, eB);
         }
         // this CTA's sums: over the token groups, in order
         const int gi = warp * L::G + g;
@@ -773,9 +763,9 @@ __global__ void __launch_bounds__(128) rec_step_kernel(const RecProblem p, float
     const float2 rate[2] = {make_float2(expf(l.lo.x), expf(l.lo.y)), make_float2(expf(l.hi.x), expf(l.hi.y))};
     const float2 bias2[2] = {mul2(bias.lo, splat2(kLog2e)), mul2(bias.hi, splat2(kLog2e))};
     const GateConst C;
-    float2 z[2] = {a.lo, a.hi}, t[2], Y[2], al[2], w[2];
-    decays<2, 2>(C, z, bias2, rate, t, Y, al, w);
-    const F4 h = fma4({al[0], al[1]}, h0, mul4({write_scale2(C, w[0], b.lo), write_scale2(C, w[1], b.hi)}, x));
+    float2 z[2] = {a.lo, a.hi}, t[2], Y[2], al[2], em[2];
+    decays<2, 2>(C, z, bias2, rate, t, Y, al, em);
+    const F4 h = fma4({al[0], al[1]}, h0, mul4({write_scale2(C, em[0], al[0], b.lo), write_scale2(C, em[1], al[1], b.hi)}, x));
     store_row<float, VEC>(state + n * d.D + ch, h, nc);
     store_row<T, VEC>((T *)p.out + n * d.D + ch, h, nc);
 }
@@ -870,7 +860,7 @@ cudaError_t launch_backward_rec(RecProblem p, cudaStream_t s) {
         return cudaErrorInvalidValue;
     auto kernel = p.cu ? (tma ? rec_backward_kernel<T, true, true> : rec_backward_kernel<T, false, true>)
                        : (tma ? rec_backward_kernel<T, true, false> : rec_backward_kernel<T, false, false>);
-    const cudaError_t e = launch_chains(kernel, L::THREADS, pl, (tma ? L::STAGES * 4 * L::kTensor : 0) + 2 * (size_t)pl.cs * 2 * L::CH * 4, s, p, m);
+    const cudaError_t e = launch_chains(kernel, L::THREADS, pl, (tma ? L::STAGES * 4 * L::kTensor : 0) + kBwdStash<T> + 2 * (size_t)pl.cs * 2 * L::CH * 4, s, p, m);
     if (e != cudaSuccess) return e;
     rec_params_kernel<<<(unsigned)cdiv64(d.D, 32), 256, 0, s>>>(p, d.B * pl.cs);
     return cudaGetLastError();

@@ -63,11 +63,11 @@ __device__ __forceinline__ float2 one_minus(const GateConst &k, float2 x) { retu
 // Decays of N pairs of channels from the gate input a. Step by step over all pairs: each coefficient is
 // then fetched once for all of them.
 //   z: (a + dt_bias) log2(e), t: e^-|a + dt_bias|, Y: -log2(alpha) = exp(A_log) softplus(a + dt_bias) log2(e),
-//   w: 1 - alpha^2
+//   em: 1 - alpha
 // In: z holds a. bias2 = dt_bias log2(e) and rate = exp(A_log) of pair i are bias2[i % M], rate[i % M].
 template <int N, int M>
 __device__ __forceinline__ void decays(const GateConst &C, float2 (&z)[N], const float2 (&bias2)[M], const float2 (&rate)[M], float2 (&t)[N],
-                                       float2 (&Y)[N], float2 (&alpha)[N], float2 (&w)[N]) {
+                                       float2 (&Y)[N], float2 (&alpha)[N], float2 (&em)[N]) {
     float2 q[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) z[i] = fma2(z[i], C.log2e, bias2[i % M]);
@@ -95,9 +95,8 @@ __device__ __forceinline__ void decays(const GateConst &C, float2 (&z)[N], const
         const float2 es = mul2(q[i], Y[i]), al = ex2_pair(make_float2(-Y[i].x, -Y[i].y));
         const float2 as = one_minus(C, es), el = one_minus(C, al);
         const bool s0 = Y[i].x < 0.25f, s1 = Y[i].y < 0.25f;
-        const float2 em = make_float2(s0 ? es.x : el.x, s1 ? es.y : el.y);
+        em[i] = make_float2(s0 ? es.x : el.x, s1 ? es.y : el.y);
         alpha[i] = make_float2(s0 ? as.x : al.x, s1 ? as.y : al.y);
-        w[i] = fma2(em, alpha[i], em);
     }
 }
 
@@ -105,8 +104,13 @@ __device__ __forceinline__ float2 sigmoid2(const GateConst &C, float2 b) {
     const float2 m = mul2(b, C.log2e);
     return rcp_pair(add2(ex2_pair(make_float2(-m.x, -m.y)), C.one));
 }
-// sqrt(w) sigmoid(b); a w below the normal range counts as 0
-__device__ __forceinline__ float2 write_scale2(const GateConst &C, float2 w, float2 b) {
+// alpha from em and Y
+__device__ __forceinline__ float2 decay_of(float2 em, float2 Y) {
+    return make_float2(Y.x < 0.25f ? 1.f - em.x : ex2_approx(-Y.x), Y.y < 0.25f ? 1.f - em.y : ex2_approx(-Y.y));
+}
+// sqrt(1 - alpha^2) sigmoid(b); a 1 - alpha^2 below the normal range counts as 0
+__device__ __forceinline__ float2 write_scale2(const GateConst &C, float2 em, float2 alpha, float2 b) {
+    const float2 w = fma2(em, alpha, em);
     return mul2(make_float2(sqrt_approx(w.x), sqrt_approx(w.y)), sigmoid2(C, b));
 }
 // 1 / sqrt(w), finite for w = 0; a NaN stays one through w
