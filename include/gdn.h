@@ -526,7 +526,8 @@ typedef struct {
     int32_t B, T, N;     /* as in gdn_recurrence_desc */
     int32_t Hq, Hk;      /* heads of q and of k; Hk = 0: no k */
     int32_t d;           /* channels per head */
-    int32_t rot;         /* rotated channels per head: even, 2..d */
+    int32_t rot;         /* rotated channels per head: even, 2..d (at most 32768; a token's
+                            channels, (Hq + Hk) d, at most 2^24, tokens below 2^31) */
     int32_t layout;      /* gdn_rotary_layout */
     int32_t inverse;     /* 0 or 1 */
     int32_t dtype;       /* gdn_dtype of q, k and their outputs */
@@ -583,7 +584,7 @@ typedef enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 } gdn_activation;
 
 typedef struct {
     int32_t N, L;          /* instances, positions per instance (either may be 0) */
-    int32_t C, G;          /* channels, groups (C % G == 0) */
+    int32_t C, G;          /* channels (at most 2^24), groups (C % G == 0) */
     int32_t dtype;         /* gdn_dtype of x, out, grad_out, dx */
     int32_t weight_dtype;  /* of weight and bias: dtype, or GDN_F32 */
     int32_t act;           /* gdn_activation */

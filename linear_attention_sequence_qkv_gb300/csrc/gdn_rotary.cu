@@ -1,7 +1,16 @@
 // gdn_rotary.cu -- rotary positions (include/gdn.h): the table of turns on the host
 // and the rotation of q and k.
+//
+// A streaming kernel, bound by HBM: every channel is read and written once (in place,
+// the channels behind the rotated ones are not touched at all). The angle depends on
+// the token and the pair alone, so a CTA computes the cosines and sines of its few
+// tokens once, into shared memory, for all heads. A unit of work is one vector per
+// half of a rotated head (half layout), one vector of whole pairs (interleaved), or one
+// copied vector; a thread has several in flight.
 #include <math.h>
 #include <string.h>
+
+#include <algorithm>
 
 #include "gdn_layer_ops.cuh"
 
@@ -15,6 +24,11 @@ struct RotaryProblem {
     const int32_t *pos, *cu, *off;
     void *qo, *ko;
     int32_t *status;
+    int tokens;             // per CTA
+    int u_rot;              // units of a head's rotated channels
+    int u_q, u_k;           // units of q's and of k's rotated channels per token
+    int c_q, c_k;           // units of their copied channels (0 in place)
+    int u_copy;             // units of a head's copied channels
 };
 
 // Position of token t of row `row` (see gdn_rotary in include/gdn.h)
@@ -39,37 +53,164 @@ __device__ __forceinline__ float2 cos_sin(int64_t position, uint64_t turn) {
     return make_float2(c, s);
 }
 
-// One thread per pair or copied channel of a token.
-template <typename T>
-__global__ void __launch_bounds__(128) rotary_kernel(const RotaryProblem p) {
+template <int BYTES> struct Raw;
+template <> struct Raw<16> { using type = uint4; };
+template <> struct Raw<8> { using type = uint2; };
+template <> struct Raw<4> { using type = uint32_t; };
+template <> struct Raw<2> { using type = uint16_t; };
+template <typename T, int V> union Vec {
+    typename Raw<V * sizeof(T)>::type raw;
+    T e[V];
+};
+
+constexpr int kThreads = 256;
+constexpr int kBatch = 4;              // units in flight per thread
+constexpr int kTableBytes = 32768;     // cosines and sines of a CTA's tokens
+
+// V: elements per vector. HALF: a unit is the vectors at u V and rot/2 + u V; else the V elements from u V (two
+// single elements for V = 1).
+template <typename T, int V, bool HALF>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryProblem p) {
+    constexpr int NP = HALF ? V : (V > 1 ? V / 2 : 1);   // pairs per unit
+    constexpr int W = NP < 4 ? NP : 4;                   // floats per table entry
+    constexpr int Q = NP / W;                            // entries of cosines (and of sines) per unit
+    extern __shared__ __align__(16) float tab[];         // [token][2 Q][unit][W]
     const gdn_rotary_desc &d = p.d;
     const bool ok = p.cu == nullptr || seqlens_ok(p.cu, d.N, d.T);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = ok ? GDN_OK : GDN_ERR_DEVICE_SEQLENS;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.status = ok ? GDN_OK : GDN_ERR_DEVICE_SEQLENS;
     if (!ok) return;
-    const int half = d.rot / 2, units = half + d.d - d.rot, H = d.Hq + d.Hk;
-    for (int64_t tok = blockIdx.x; tok < (int64_t)d.B * d.T; tok += gridDim.x) {
-        const int row = (int)(tok / d.T), t = (int)(tok - (int64_t)row * d.T);
-        const int64_t position = token_position(p, row, t);
-        for (int i = threadIdx.x; i < H * units; i += 128) {
-            const int h = i / units, u = i - h * units;
-            const bool isk = h >= d.Hq;
-            const T *src = (const T *)(isk ? p.k : p.q) + row * (isk ? d.k_stride_b : d.q_stride_b) +
-                           t * (isk ? d.k_stride_t : d.q_stride_t) + (int64_t)(isk ? h - d.Hq : h) * d.d;
-            T *dst = (T *)(isk ? p.ko : p.qo) + row * (isk ? d.k_out_stride_b : d.q_out_stride_b) +
-                     t * (isk ? d.k_out_stride_t : d.q_out_stride_t) + (int64_t)(isk ? h - d.Hq : h) * d.d;
-            if (u >= half) {
-                dst[d.rot + u - half] = src[d.rot + u - half];
+    const int64_t tok0 = (int64_t)blockIdx.x * p.tokens;
+    const int nt = (int)min((int64_t)p.tokens, (int64_t)d.B * d.T - tok0);
+    const int half = d.rot / 2;
+    for (int i = threadIdx.x; i < nt * half; i += kThreads) {
+        const int t = i / half, pr = i - t * half;
+        const uint32_t row = (uint32_t)(tok0 + t) / (uint32_t)d.T;
+        const float2 cs = cos_sin(token_position(p, row, (int)((uint32_t)(tok0 + t) - row * d.T)), p.turns[pr]);
+        const int u = pr / NP, e = pr % NP;
+        float *at = tab + ((t * 2 * Q + e / W) * p.u_rot + u) * W + e % W;
+        at[0] = cs.x * d.scale;
+        at[Q * p.u_rot * W] = cs.y * (d.inverse ? -d.scale : d.scale);
+    }
+    __syncthreads();
+    const int per = p.u_q + p.u_k + p.c_q + p.c_k;       // units per token
+    const int total = nt * per, step = kThreads * gridDim.y;
+    for (int i0 = blockIdx.y * kThreads + threadIdx.x; i0 < total; i0 += kBatch * step) {
+        const T *src[kBatch];
+        T *dst[kBatch];
+        const float *tb[kBatch];                          // the unit's table entries; null: copy
+        Vec<T, V> a[kBatch], b[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int i = i0 + j * step;
+            if (i >= total) continue;
+            const int t = i / per;
+            int r = i - t * per;
+            const uint32_t tok = (uint32_t)(tok0 + t), row = tok / (uint32_t)d.T, tt = tok - row * d.T;   // below 2^31
+            const bool rot = r < p.u_q + p.u_k;
+            if (!rot) r -= p.u_q + p.u_k;
+            const bool isk = r >= (rot ? p.u_q : p.c_q);
+            if (isk) r -= rot ? p.u_q : p.c_q;
+            const int uh = rot ? p.u_rot : p.u_copy, h = r / uh, u = r - h * uh;
+            const int64_t off = (int64_t)h * d.d + (rot ? (HALF ? u * V : u * 2 * NP) : d.rot + u * V);
+            src[j] = (const T *)(isk ? p.k : p.q) + row * (isk ? d.k_stride_b : d.q_stride_b) + tt * (isk ? d.k_stride_t : d.q_stride_t) + off;
+            dst[j] = (T *)(isk ? p.ko : p.qo) + row * (isk ? d.k_out_stride_b : d.q_out_stride_b) +
+                     tt * (isk ? d.k_out_stride_t : d.q_out_stride_t) + off;
+            tb[j] = rot ? tab + (t * 2 * Q * p.u_rot + u) * W : nullptr;
+            a[j].raw = *(const decltype(a[j].raw) *)src[j];
+            if (rot && (HALF || V == 1)) b[j].raw = *(const decltype(b[j].raw) *)(src[j] + (HALF ? half : 1));
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            if (i0 + j * step >= total) continue;
+            if (tb[j] == nullptr) {
+                *(decltype(a[j].raw) *)dst[j] = a[j].raw;
                 continue;
             }
-            float2 cs = cos_sin(position, p.turns[u]);
-            cs.x *= d.scale;
-            cs.y *= d.inverse ? -d.scale : d.scale;
-            const int i1 = d.layout == GDN_ROTARY_HALF ? u : 2 * u, i2 = d.layout == GDN_ROTARY_HALF ? u + half : 2 * u + 1;
-            const float x1 = to_f<T>(src[i1]), x2 = to_f<T>(src[i2]);
-            dst[i1] = from_f<T>(x1 * cs.x - x2 * cs.y);
-            dst[i2] = from_f<T>(x2 * cs.x + x1 * cs.y);
+            float c[NP], s[NP];
+#pragma unroll
+            for (int e = 0; e < NP; e += W) {
+                const float *tc = tb[j] + e / W * p.u_rot * W, *ts = tc + Q * p.u_rot * W;
+                if (W == 4) {
+                    const float4 c4 = *(const float4 *)tc, s4 = *(const float4 *)ts;
+                    c[e] = c4.x, c[e + 1 < NP ? e + 1 : e] = c4.y, c[e + 2 < NP ? e + 2 : e] = c4.z, c[e + 3 < NP ? e + 3 : e] = c4.w;
+                    s[e] = s4.x, s[e + 1 < NP ? e + 1 : e] = s4.y, s[e + 2 < NP ? e + 2 : e] = s4.z, s[e + 3 < NP ? e + 3 : e] = s4.w;
+                } else {
+#pragma unroll
+                    for (int w = 0; w < W; ++w) c[e + w] = tc[w], s[e + w] = ts[w];
+                }
+            }
+            if (HALF || V == 1) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float x1 = to_f<T>(a[j].e[e]), x2 = to_f<T>(b[j].e[e]);
+                    a[j].e[e] = from_f<T>(x1 * c[e] - x2 * s[e]);
+                    b[j].e[e] = from_f<T>(x2 * c[e] + x1 * s[e]);
+                }
+                *(decltype(a[j].raw) *)dst[j] = a[j].raw;
+                *(decltype(b[j].raw) *)(dst[j] + (HALF ? half : 1)) = b[j].raw;
+            } else {
+#pragma unroll
+                for (int e = 0; e < V / 2; ++e) {
+                    const float x1 = to_f<T>(a[j].e[2 * e]), x2 = to_f<T>(a[j].e[V > 1 ? 2 * e + 1 : 0]);
+                    a[j].e[2 * e] = from_f<T>(x1 * c[e] - x2 * s[e]);
+                    a[j].e[V > 1 ? 2 * e + 1 : 0] = from_f<T>(x2 * c[e] + x1 * s[e]);
+                }
+                *(decltype(a[j].raw) *)dst[j] = a[j].raw;
+            }
         }
     }
+}
+
+// The widest vector that divides the rotated part, the rest of the head, and every base and stride.
+bool fits(const gdn_rotary_desc &d, int v, const void *q, const void *k, const void *qo, const void *ko) {
+    const size_t bytes = v * act_size(d.dtype);
+    const int rot = d.layout == GDN_ROTARY_HALF ? d.rot / 2 : d.rot;
+    if (bytes > 16 || rot % v || d.d % v || (d.rot < d.d && d.rot % v)) return false;
+    const void *ptrs[] = {q, qo, d.Hk ? k : nullptr, d.Hk ? ko : nullptr};
+    const int64_t st[] = {d.q_stride_t, d.q_out_stride_t, d.Hk ? d.k_stride_t : 0, d.Hk ? d.k_out_stride_t : 0};
+    const int64_t sb[] = {d.q_stride_b, d.q_out_stride_b, d.Hk ? d.k_stride_b : 0, d.Hk ? d.k_out_stride_b : 0};
+    for (int i = 0; i < 4; ++i)
+        if (!ptr_aligned(ptrs[i], bytes) || (d.T > 1 && st[i] % v) || (d.B > 1 && sb[i] % v)) return false;
+    return true;
+}
+
+template <typename T, int V, bool HALF>
+cudaError_t launch_rotary(RotaryProblem p, cudaStream_t s) {
+    constexpr int NP = HALF ? V : (V > 1 ? V / 2 : 1);
+    const gdn_rotary_desc &d = p.d;
+    const int64_t ntok = (int64_t)d.B * d.T;
+    p.u_rot = d.rot / 2 / NP;
+    p.u_copy = (d.d - d.rot) / V;
+    p.u_q = d.Hq * p.u_rot;
+    p.u_k = d.Hk * p.u_rot;
+    p.c_q = p.q == p.qo ? 0 : d.Hq * p.u_copy;
+    p.c_k = p.k == p.ko ? 0 : d.Hk * p.u_copy;
+    // tokens per CTA: about one batch of units for every thread, as long as that leaves four CTAs per SM and the
+    // table fits; few tokens are split over the heads instead
+    const int64_t per = (int64_t)p.u_q + p.u_k + p.c_q + p.c_k;
+    int64_t tokens = std::max<int64_t>(1, std::min<int64_t>(kBatch * kThreads / per, ntok / (4 * kSms)));
+    tokens = std::max<int64_t>(1, std::min<int64_t>(tokens, kTableBytes / (4 * (int64_t)d.rot)));
+    p.tokens = (int)tokens;
+    const int64_t blocks = cdiv64(ntok, tokens);
+    const int64_t split = std::max<int64_t>(1, std::min<int64_t>(cdiv64(tokens * per, kThreads), 4 * kSms / std::max<int64_t>(blocks, 1)));
+    const size_t smem = (size_t)tokens * d.rot * 4;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(rotary_kernel<T, V, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    rotary_kernel<T, V, HALF><<<dim3((unsigned)std::max<int64_t>(blocks, 1), (unsigned)split), kThreads, smem, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T, bool HALF>
+cudaError_t launch_by_vector(const RotaryProblem &p, cudaStream_t s) {
+    const auto can = [&](int v) { return fits(p.d, v, p.q, p.k, p.qo, p.ko); };
+    if constexpr (sizeof(T) == 2)
+        if (can(8)) return launch_rotary<T, 8, HALF>(p, s);
+    if (can(4)) return launch_rotary<T, 4, HALF>(p, s);
+    if (can(2)) return launch_rotary<T, 2, HALF>(p, s);
+    return launch_rotary<T, 1, HALF>(p, s);
 }
 
 int check_desc(const gdn_rotary_desc *d, bool packed) {
@@ -80,7 +221,9 @@ int check_desc(const gdn_rotary_desc *d, bool packed) {
     if (d->layout != GDN_ROTARY_HALF && d->layout != GDN_ROTARY_INTERLEAVED) return GDN_ERR_INVALID_ARG;
     if (d->inverse != 0 && d->inverse != 1) return GDN_ERR_INVALID_ARG;
     if (!dtype_ok(d->dtype)) return GDN_ERR_UNSUPPORTED;
-    if ((int64_t)d->d * ((int64_t)d->Hq + d->Hk) > (1 << 30)) return GDN_ERR_UNSUPPORTED;
+    if ((int64_t)d->d * ((int64_t)d->Hq + d->Hk) > (1 << 24)) return GDN_ERR_UNSUPPORTED;
+    if (d->rot > 32768) return GDN_ERR_UNSUPPORTED;   // one token's cosines and sines in shared memory
+    if ((int64_t)d->B * d->T > 0x7fffffff) return GDN_ERR_UNSUPPORTED;
     const int64_t strides[] = {d->q_stride_b, d->q_stride_t, d->q_out_stride_b, d->q_out_stride_t,
                                d->k_stride_b, d->k_stride_t, d->k_out_stride_b, d->k_out_stride_t};
     for (int i = 0; i < (d->Hk ? 8 : 4); ++i)
@@ -169,16 +312,26 @@ int gdn_rotary(const gdn_rotary_desc *d, const void *q, const void *k, const uin
         (d->Hk && k == k_out && (d->k_stride_b != d->k_out_stride_b || d->k_stride_t != d->k_out_stride_t)))
         return GDN_ERR_INVALID_ARG;
     if ((rc = check_workspace(workspace, workspace_bytes, kStatusBytes)) != GDN_OK) return rc;
-    RotaryProblem p = {*d, q, k, turns, positions, cu_seqlens, offsets, q_out, k_out, (int32_t *)workspace};
-    const int64_t ntok = (int64_t)d->B * d->T;
-    const unsigned grid = (unsigned)(ntok < 1 ? 1 : ntok < 65536 ? ntok : 65536);
+    RotaryProblem p;
+    memset(&p, 0, sizeof(p));
+    p.d = *d;
+    p.q = q;
+    p.k = k;
+    p.turns = turns;
+    p.pos = positions;
+    p.cu = cu_seqlens;
+    p.off = offsets;
+    p.qo = q_out;
+    p.ko = k_out;
+    p.status = (int32_t *)workspace;
+    const bool half = d->layout == GDN_ROTARY_HALF;
     const cudaStream_t s = (cudaStream_t)stream;
     switch (d->dtype) {
-    case GDN_F32: rotary_kernel<float><<<grid, 128, 0, s>>>(p); break;
-    case GDN_BF16: rotary_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>(p); break;
-    default: rotary_kernel<__half><<<grid, 128, 0, s>>>(p); break;
+    case GDN_F32: return layer_status(half ? launch_by_vector<float, true>(p, s) : launch_by_vector<float, false>(p, s));
+    case GDN_BF16:
+        return layer_status(half ? launch_by_vector<__nv_bfloat16, true>(p, s) : launch_by_vector<__nv_bfloat16, false>(p, s));
+    default: return layer_status(half ? launch_by_vector<__half, true>(p, s) : launch_by_vector<__half, false>(p, s));
     }
-    return layer_status(cudaGetLastError());
 }
 
 }  // extern "C"
