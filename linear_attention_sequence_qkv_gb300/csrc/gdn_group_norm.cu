@@ -42,26 +42,33 @@ struct NormProblem {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kBlocksForward = 3, kBlocksBackward = 2, kBlocksGeneral = 4;   // per SM, resident at once
+constexpr int kRowsForward = 2;   // rows a warp works on at a time (two reductions in flight); as many are on their way
+constexpr int kAheadBackward = 3; // rows on their way while a warp works on one
+constexpr int kBatch = 8, kBatchBackward = 4;   // rows in flight per warp in the general form
 
 template <typename T> struct VecN { static constexpr int value = 16 / sizeof(T); };
 
-// V elements of T as fp32 (V = 1, or 16 bytes)
+// V elements of T as they stand in memory (V = 1, or 16 bytes), and as pairs of fp32 values: sm_100-class
+// SMs run add, multiply and fma on a pair as one instruction. V = 1 fills the first half of one pair.
+template <typename T, int V> struct RawV { using type = uint4; };
+template <typename T> struct RawV<T, 1> { using type = T; };
+template <int V> constexpr int kPairs = V > 1 ? V / 2 : 1;
 template <typename T, int V>
-__device__ __forceinline__ void load_v(const T *p, float *v) {
-    if constexpr (V == 1) v[0] = to_f<T>(*p);
-    else unpack16<T>(*reinterpret_cast<const uint4 *>(p), v);
+__device__ __forceinline__ typename RawV<T, V>::type load_raw(const T *p) {
+    return *reinterpret_cast<const typename RawV<T, V>::type *>(p);
 }
 template <typename T, int V>
-__device__ __forceinline__ void store_v(T *p, const float *v) {
-    if constexpr (V == 1) *p = from_f<T>(v[0]);
-    else *reinterpret_cast<uint4 *>(p) = pack16<T>(v);
+__device__ __forceinline__ void unpack_v(const typename RawV<T, V>::type &r, float2 *v) {
+    if constexpr (V == 1) v[0] = make_float2(to_f<T>(r), 0.f);
+    else Pairs<T>::unpack(r, v);
 }
-
-__device__ __forceinline__ float param(const void *p, int dtype, int c, float none) {
-    if (!p) return none;
-    return dtype == GDN_F32 ? ((const float *)p)[c]
-           : dtype == GDN_BF16 ? __bfloat162float(((const __nv_bfloat16 *)p)[c]) : __half2float(((const __half *)p)[c]);
+template <typename T, int V>
+__device__ __forceinline__ void store_v(T *p, const float2 *v) {
+    if constexpr (V == 1) *p = from_f<T>(v[0].x);
+    else *reinterpret_cast<uint4 *>(p) = Pairs<T>::pack(v);
 }
+// the sum over a pair's elements that exist
+template <int V> __device__ __forceinline__ float total(float2 v) { return V == 1 ? v.x : v.x + v.y; }
 
 __device__ __forceinline__ float lane_sum(float v, int lg) {   // over lg adjacent lanes, the same in all of them
 #pragma unroll
@@ -72,12 +79,25 @@ __device__ __forceinline__ float lane_sum(float v, int lg) {   // over lg adjace
     return v;
 }
 
-__device__ __forceinline__ float sigmoid_fast(float z) { return rcp_approx(1.f + ex2_approx(-1.4426950408889634f * z)); }
-__device__ __forceinline__ float act_f(float z, int act) { return act == GDN_ACT_SILU ? z * sigmoid_fast(z) : z; }
-__device__ __forceinline__ float act_grad(float z, int act) {   // d act(z) / dz
-    if (act == GDN_ACT_NONE) return 1.f;
-    const float s = sigmoid_fast(z), zc = fminf(fmaxf(z, -3e38f), 3e38f);   // no 0 times inf
-    return s * fmaf(zc, 1.f - s, 1.f);
+__device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
+__device__ __forceinline__ float2 sigmoid2(float2 z) {
+    const float2 m = mul2(z, splat2(-1.4426950408889634f));
+    const float2 c = add2(make_float2(ex2_approx(m.x), ex2_approx(m.y)), splat2(1.f));
+    return make_float2(rcp_approx(c.x), rcp_approx(c.y));
+}
+template <int ACT> __device__ __forceinline__ float2 act2(float2 z) { return ACT == GDN_ACT_SILU ? silu2_acc(z) : z; }
+template <int ACT> __device__ __forceinline__ float2 act_grad2(float2 z) {   // d act(z) / dz
+    if (ACT == GDN_ACT_NONE) return splat2(1.f);
+    const float2 s = sigmoid2(z);
+    return mul2(s, fma2(z, fma2(s, splat2(-1.f), splat2(1.f)), splat2(1.f)));
+}
+
+// The same with the number of lanes known (LG), or in lg (LG = 0)
+template <int LG> __device__ __forceinline__ float lane_sum_t(float v, int lg) {
+    if (LG == 0) return lane_sum(v, lg);
+#pragma unroll
+    for (int off = LG / 2; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
 }
 
 // The warp's place: its set, its lane's first channel, and whether the lane has channels.
@@ -109,61 +129,94 @@ __device__ __forceinline__ Place place(const NormProblem &p) {
     return q;
 }
 
-// ------------------------------------------------------------------ rows
-constexpr int kRows = 4;   // vectors in flight per lane
+// One of weight and bias for the lane's V channels from c on; the loads are independent of one another.
+template <typename W, int V>
+__device__ __forceinline__ void load_param(const void *p, bool any, int c, float none, float2 *v) {
+    const W *at = (const W *)p + c;
+#pragma unroll
+    for (int e = 0; e < kPairs<V>; ++e) {
+        v[e] = splat2(any ? none : 0.f);
+        if (any && p) {
+            v[e].x = to_f<W>(at[2 * e]);
+            if (V > 1) v[e].y = to_f<W>(at[2 * e + 1]);
+        }
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void load_params(const NormProblem &p, bool any, int c, float2 *w, float2 *b) {
+    if (sizeof(T) == 4 || p.d.weight_dtype == GDN_F32) {
+        load_param<float, V>(p.w, any, c, 1.f, w);
+        load_param<float, V>(p.b, any, c, 0.f, b);
+    } else {
+        load_param<T, V>(p.w, any, c, 1.f, w);
+        load_param<T, V>(p.b, any, c, 0.f, b);
+    }
+    // as fp32 values from here on: the compiler would keep the 16-bit ones and convert them for every row
+#pragma unroll
+    for (int e = 0; e < kPairs<V>; ++e)
+        asm volatile("" : "+f"(w[e].x), "+f"(w[e].y), "+f"(b[e].x), "+f"(b[e].y));
+}
 
-template <typename T, int V, int NV>
+// ------------------------------------------------------------------ rows
+template <typename T, int V, int NV, int ACT, int LG>
 __global__ void __launch_bounds__(kThreads, NV == 1 ? kBlocksForward : 1) norm_rows_forward(const __grid_constant__ NormProblem p) {
     const gdn_group_norm_desc &d = p.d;
     const Place q = place<V>(p);
     if (q.slice >= p.slices) return;
+    constexpr int NP = kPairs<V>;
+    constexpr int kR = NV == 1 ? kRowsForward : 1;
     const int cg = d.C / d.G;
     const float inv = 1.f / (float)cg;
-    constexpr int kR = kRows / NV;
     bool has[NV];
-    float w[NV][V], b[NV][V];
+    float2 w[NV][NP], b[NV][NP];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         has[i] = q.any && (q.sub + i * p.lg) * V < cg;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            w[i][e] = has[i] ? param(p.w, d.weight_dtype, q.c + i * p.lg * V + e, 1.f) : 0.f;
-            b[i][e] = has[i] ? param(p.b, d.weight_dtype, q.c + i * p.lg * V + e, 0.f) : 0.f;
-        }
+        load_params<T, V>(p, has[i], q.c + i * p.lg * V, w[i], b[i]);
     }
-    for (int64_t n0 = q.slice; n0 < p.items; n0 += (int64_t)kR * p.slices) {
-        float x[kR][NV][V], mean[kR], rstd[kR];
+    // the next rows are on their way while these are worked on
+    typename RawV<T, V>::type raw[kR][NV] = {};
+    auto fetch = [&](int64_t n0) {
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
             const int64_t n = n0 + (int64_t)r * p.slices;
 #pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (n < p.items && has[i]) raw[r][i] = load_raw<T, V>((const T *)p.x + n * d.x_stride_n + q.c + i * p.lg * V);
+        }
+    };
+    fetch(q.slice);
+    for (int64_t n0 = q.slice; n0 < p.items; n0 += (int64_t)kR * p.slices) {
+        float2 x[kR][NV][NP];
+        float mean[kR], rstd[kR];
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            float2 s = splat2(0.f);
+#pragma unroll
             for (int i = 0; i < NV; ++i) {
-                if (n < p.items && has[i]) load_v<T, V>((const T *)p.x + n * d.x_stride_n + q.c + i * p.lg * V, x[r][i]);
-                else
+                unpack_v<T, V>(raw[r][i], x[r][i]);
 #pragma unroll
-                    for (int e = 0; e < V; ++e) x[r][i][e] = 0.f;
+                for (int e = 0; e < NP; ++e) s = add2(s, x[r][i][e]);   // a lane without channels holds zeros
             }
+            mean[r] = total<V>(s);
         }
+        fetch(n0 + (int64_t)kR * p.slices);
+#pragma unroll
+        for (int r = 0; r < kR; ++r) mean[r] = lane_sum_t<LG>(mean[r], p.lg) * inv;
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
-            float s = 0.f;
+            float t = 0.f;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+            for (int i = 0; i < NV; ++i) {
+                float2 s = splat2(0.f);
 #pragma unroll
-                for (int e = 0; e < V; ++e) s += x[r][i][e];
-            mean[r] = lane_sum(s, p.lg) * inv;
-        }
-#pragma unroll
-        for (int r = 0; r < kR; ++r) {
-            float s = 0.f;
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    x[r][i][e] -= mean[r];
-                    if (has[i]) s = fmaf(x[r][i][e], x[r][i][e], s);
+                for (int e = 0; e < NP; ++e) {
+                    x[r][i][e] = add2(x[r][i][e], splat2(-mean[r]));
+                    s = fma2(x[r][i][e], x[r][i][e], s);
                 }
-            rstd[r] = rsqrtf(fmaf(lane_sum(s, p.lg), inv, d.eps));
+                if (has[i]) t += total<V>(s);
+            }
+            rstd[r] = rsqrtf(fmaf(lane_sum_t<LG>(t, p.lg), inv, d.eps));
         }
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
@@ -177,148 +230,159 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? kBlocksForward : 1) norm_r
             for (int i = 0; i < NV; ++i) {
                 if (!has[i]) continue;
 #pragma unroll
-                for (int e = 0; e < V; ++e) x[r][i][e] = act_f(fmaf(x[r][i][e] * rstd[r], w[i][e], b[i][e]), d.act);
+                for (int e = 0; e < NP; ++e) x[r][i][e] = act2<ACT>(fma2(mul2(x[r][i][e], splat2(rstd[r])), w[i][e], b[i][e]));
                 store_v<T, V>((T *)p.out + n * d.C + q.c + i * p.lg * V, x[r][i]);
             }
         }
     }
 }
 
-// The element's part of the backward: xh, dz = dout act'(z), t = dz w.
-struct Grad {
-    float xh, dz, t;
+// The backward's part of an element: xh, dz = dout act'(z), t = dz w.
+struct Grad2 {
+    float2 xh, dz, t;
 };
-__device__ __forceinline__ Grad grad_of(float x, float dy, float mean, float rstd, float w, float b, int act) {
-    Grad g;
-    g.xh = (x - mean) * rstd;
-    g.dz = dy * act_grad(fmaf(g.xh, w, b), act);
-    g.t = g.dz * w;
+template <int ACT>
+__device__ __forceinline__ Grad2 grad_of(float2 x, float2 dy, float mean, float rstd, float2 w, float2 b) {
+    Grad2 g;
+    g.xh = mul2(add2(x, splat2(-mean)), splat2(rstd));
+    g.dz = mul2(dy, act_grad2<ACT>(fma2(g.xh, w, b)));
+    g.t = mul2(g.dz, w);
     return g;
 }
 
 // Sums of dweight and dbias of a warp's channels: over 16 rows, over all (the second level keeps the
 // rounding of long sums down), then into its partial row.
 template <int N> struct ParamSums {
-    float w[2][N], b[2][N];
+    float2 w[2][N], b[2][N];
     int rows;
     __device__ __forceinline__ ParamSums() {
 #pragma unroll
-        for (int i = 0; i < N; ++i) w[0][i] = w[1][i] = b[0][i] = b[1][i] = 0.f;
+        for (int i = 0; i < N; ++i) w[0][i] = w[1][i] = b[0][i] = b[1][i] = splat2(0.f);
         rows = 0;
     }
     __device__ __forceinline__ void row_done() {
         if (++rows & 15) return;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            w[1][i] += w[0][i];
-            b[1][i] += b[0][i];
-            w[0][i] = b[0][i] = 0.f;
+            w[1][i] = add2(w[1][i], w[0][i]);
+            b[1][i] = add2(b[1][i], b[0][i]);
+            w[0][i] = b[0][i] = splat2(0.f);
+        }
+    }
+    template <int V> __device__ __forceinline__ void write(const NormProblem &p, int slice, int c, int i) const {
+        float *pw = p.part + (int64_t)slice * 2 * p.d.C + c, *pb = pw + p.d.C;
+#pragma unroll
+        for (int e = 0; e < kPairs<V>; ++e) {
+            const float2 sw = add2(w[1][i + e], w[0][i + e]), sb = add2(b[1][i + e], b[0][i + e]);
+            pw[2 * e] = sw.x;
+            pb[2 * e] = sb.x;
+            if (V > 1) {
+                pw[2 * e + 1] = sw.y;
+                pb[2 * e + 1] = sb.y;
+            }
         }
     }
 };
 
-template <typename T, int V, int NV>
+template <typename T, int V, int NV, int ACT, int LG>
 __global__ void __launch_bounds__(kThreads, NV == 1 ? kBlocksBackward : 1) norm_rows_backward(const __grid_constant__ NormProblem p) {
     const gdn_group_norm_desc &d = p.d;
     const Place q = place<V>(p);
+    pdl_trigger();
     if (q.slice >= p.slices) return;
+    constexpr int NP = kPairs<V>;
     const int cg = d.C / d.G;
     const float inv = 1.f / (float)cg;
-    constexpr int kR = 2 / NV;
     bool has[NV];
-    float w[NV][V], b[NV][V];
-    ParamSums<NV * V> sums;
+    float2 w[NV][NP], b[NV][NP];
+    ParamSums<NV * NP> sums;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         has[i] = q.any && (q.sub + i * p.lg) * V < cg;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            w[i][e] = has[i] ? param(p.w, d.weight_dtype, q.c + i * p.lg * V + e, 1.f) : 0.f;
-            b[i][e] = has[i] ? param(p.b, d.weight_dtype, q.c + i * p.lg * V + e, 0.f) : 0.f;
-        }
+        load_params<T, V>(p, has[i], q.c + i * p.lg * V, w[i], b[i]);
     }
-    for (int64_t n0 = q.slice; n0 < p.items; n0 += (int64_t)kR * p.slices) {
-        float x[kR][NV][V], y[kR][NV][V], mean[kR], rstd[kR];
+    constexpr int kA = NV == 1 ? kAheadBackward : 1;
+    typename RawV<T, V>::type rx[kA][NV] = {}, ry[kA][NV] = {};
+    float rm[kA] = {}, rr[kA] = {};
+    auto fetch = [&](int j, int64_t n) {
+        if (n >= p.items) return;
+        rm[j] = p.mean[n * d.G + q.g];
+        rr[j] = p.rstd[n * d.G + q.g];
 #pragma unroll
-        for (int r = 0; r < kR; ++r) {
-            const int64_t n = n0 + (int64_t)r * p.slices;
-            mean[r] = n < p.items ? p.mean[n * d.G + q.g] : 0.f;
-            rstd[r] = n < p.items ? p.rstd[n * d.G + q.g] : 0.f;
+        for (int i = 0; i < NV; ++i)
+            if (has[i]) {
+                rx[j][i] = load_raw<T, V>((const T *)p.x + n * d.x_stride_n + q.c + i * p.lg * V);
+                ry[j][i] = load_raw<T, V>((const T *)p.dy + n * d.C + q.c + i * p.lg * V);
+            }
+    };
+#pragma unroll
+    for (int j = 0; j < kA; ++j) fetch(j, q.slice + (int64_t)j * p.slices);
+    for (int64_t n0 = q.slice; n0 < p.items; n0 += (int64_t)kA * p.slices) {
+#pragma unroll
+        for (int j = 0; j < kA; ++j) {
+            const int64_t n = n0 + (int64_t)j * p.slices;
+            if (n >= p.items) break;
+            float2 x[NV][NP], y[NV][NP];
+            const float mean = rm[j], rstd = rr[j];
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                if (n < p.items && has[i]) {
-                    load_v<T, V>((const T *)p.x + n * d.x_stride_n + q.c + i * p.lg * V, x[r][i]);
-                    load_v<T, V>((const T *)p.dy + n * d.C + q.c + i * p.lg * V, y[r][i]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < V; ++e) x[r][i][e] = mean[r], y[r][i][e] = 0.f;
-                }
+                unpack_v<T, V>(rx[j][i], x[i]);
+                unpack_v<T, V>(ry[j][i], y[i]);   // zeros for a lane without channels: no part in any sum
             }
-        }
-#pragma unroll
-        for (int r = 0; r < kR; ++r) {
-            const int64_t n = n0 + (int64_t)r * p.slices;
-            float s1 = 0.f, s2 = 0.f;
+            fetch(j, n + (int64_t)kA * p.slices);
+            float2 s1 = splat2(0.f), s2 = splat2(0.f);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const Grad g = grad_of(x[r][i][e], y[r][i][e], mean[r], rstd[r], w[i][e], b[i][e], d.act);
-                    x[r][i][e] = g.xh;
-                    y[r][i][e] = g.t;
-                    if (n < p.items) {
-                        sums.w[0][i * V + e] = fmaf(g.dz, g.xh, sums.w[0][i * V + e]);
-                        sums.b[0][i * V + e] += g.dz;
+                for (int e = 0; e < NP; ++e) {
+                    const Grad2 g = grad_of<ACT>(x[i][e], y[i][e], mean, rstd, w[i][e], b[i][e]);
+                    x[i][e] = g.xh;
+                    y[i][e] = g.t;
+                    sums.w[0][i * NP + e] = fma2(g.dz, g.xh, sums.w[0][i * NP + e]);
+                    sums.b[0][i * NP + e] = add2(sums.b[0][i * NP + e], g.dz);
+                    if (has[i]) {
+                        s1 = add2(s1, g.t);
+                        s2 = fma2(g.t, g.xh, s2);
                     }
-                    s1 += g.t;
-                    s2 = fmaf(g.t, g.xh, s2);
                 }
-            if (n < p.items) sums.row_done();
-            const float m1 = lane_sum(s1, p.lg) * inv, m2 = lane_sum(s2, p.lg) * inv;
-            if (n >= p.items) continue;
+            sums.row_done();
+            const float m1 = lane_sum_t<LG>(total<V>(s1), p.lg) * inv, m2 = lane_sum_t<LG>(total<V>(s2), p.lg) * inv;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 if (!has[i]) continue;
 #pragma unroll
-                for (int e = 0; e < V; ++e) y[r][i][e] = rstd[r] * fmaf(-x[r][i][e], m2, y[r][i][e] - m1);
-                store_v<T, V>((T *)p.dx + n * d.C + q.c + i * p.lg * V, y[r][i]);
+                for (int e = 0; e < NP; ++e)
+                    y[i][e] = mul2(fma2(x[i][e], splat2(-m2), add2(y[i][e], splat2(-m1))), splat2(rstd));
+                store_v<T, V>((T *)p.dx + n * d.C + q.c + i * p.lg * V, y[i]);
             }
         }
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-            if (has[i]) {
-                const int c = q.c + i * p.lg * V + e;
-                p.part[((int64_t)q.slice * 2) * d.C + c] = sums.w[1][i * V + e] + sums.w[0][i * V + e];
-                p.part[((int64_t)q.slice * 2 + 1) * d.C + c] = sums.b[1][i * V + e] + sums.b[0][i * V + e];
-            }
+        if (has[i]) sums.template write<V>(p, q.slice, q.c + i * p.lg * V, i * NP);
 }
 
 // --------------------------------------------------------------- general
-// Mean and centred sum of squares of n elements, and their union (n may be 0).
+// Mean and centred sum of squares of n elements, and their union.
 struct Stat {
     float n, mean, m2;
 };
-__device__ __forceinline__ Stat merge(const Stat &a, const Stat &b) {
+__device__ __forceinline__ Stat merge(const Stat &a, const Stat &b) {   // b.n > 0
     Stat r;
     r.n = a.n + b.n;
-    if (r.n == 0.f) return {0.f, 0.f, 0.f};
-    const float dl = b.mean - a.mean, f = b.n / r.n;
+    const float dl = b.mean - a.mean, f = __fdividef(b.n, r.n);
     r.mean = fmaf(dl, f, a.mean);
     r.m2 = a.m2 + b.m2 + dl * dl * a.n * f;
     return r;
 }
-__device__ __forceinline__ Stat lane_merge(Stat s, int lg) {   // over lg adjacent lanes, in the same order in all
-    const int lane = threadIdx.x % 32;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const Stat o = {__shfl_xor_sync(0xffffffffu, s.n, off), __shfl_xor_sync(0xffffffffu, s.mean, off),
-                        __shfl_xor_sync(0xffffffffu, s.m2, off)};
-        if (off < lg) s = (lane & off) ? merge(o, s) : merge(s, o);
-    }
-    return s;
+// The union over lg adjacent lanes: the mean of the means, then the squares about it.
+__device__ __forceinline__ Stat lane_union(const Stat &s, int lg) {
+    Stat r;
+    r.n = lane_sum(s.n, lg);
+    r.mean = lane_sum(s.n * s.mean, lg) / r.n;
+    const float dl = s.mean - r.mean;
+    r.m2 = lane_sum(s.n > 0.f ? fmaf(s.n * dl, dl, s.m2) : 0.f, lg);
+    return r;
 }
 
 // (instance, positions) of an item
@@ -333,90 +397,113 @@ __device__ __forceinline__ int64_t stat_at(const NormProblem &p, int64_t item, c
     return item * parts + (p.slabs == 1 ? q.g : q.set);
 }
 
-constexpr int kStatRows = 4;
-
 template <typename T, int V>
 __device__ __forceinline__ Stat chunk_stat(const NormProblem &p, const Place &q, int64_t n, int l0, int l1) {
     const gdn_group_norm_desc &d = p.d;
+    constexpr int NP = kPairs<V>;
     Stat s = {0.f, 0.f, 0.f};
     const T *at = (const T *)p.x + n * d.x_stride_n + q.c;
-    for (int l = l0; l < l1; l += kStatRows) {
-        float v[kStatRows][V];
-        const int rows = min(kStatRows, l1 - l);
+    if (q.any)
+        for (int l = l0; l < l1; l += kBatch) {
+            typename RawV<T, V>::type raw[kBatch] = {};
+            const int rows = min(kBatch, l1 - l);
 #pragma unroll
-        for (int r = 0; r < kStatRows; ++r) {
-            if (q.any && r < rows) load_v<T, V>(at + (int64_t)(l + r) * d.x_stride_l, v[r]);
-            else
+            for (int r = 0; r < kBatch; ++r)
+                if (r < rows) raw[r] = load_raw<T, V>(at + (int64_t)(l + r) * d.x_stride_l);
+            float2 sum = splat2(0.f), sq = splat2(0.f), v[NP];
 #pragma unroll
-                for (int e = 0; e < V; ++e) v[r][e] = 0.f;
+            for (int r = 0; r < kBatch; ++r) {
+                unpack_v<T, V>(raw[r], v);
+#pragma unroll
+                for (int e = 0; e < NP; ++e) sum = add2(sum, v[e]);
+            }
+            const float cnt = (float)(rows * V), mean = __fdividef(total<V>(sum), cnt);
+#pragma unroll
+            for (int r = 0; r < kBatch; ++r) {
+                if (r >= rows) break;
+                unpack_v<T, V>(raw[r], v);
+#pragma unroll
+                for (int e = 0; e < NP; ++e) {
+                    v[e] = add2(v[e], splat2(-mean));
+                    sq = fma2(v[e], v[e], sq);
+                }
+            }
+            s = merge(s, {cnt, mean, total<V>(sq)});
         }
-        float sum = 0.f, m2 = 0.f;
-#pragma unroll
-        for (int r = 0; r < kStatRows; ++r)
-#pragma unroll
-            for (int e = 0; e < V; ++e) sum += v[r][e];
-        const float cnt = (float)(rows * V), mean = sum / cnt;
-#pragma unroll
-        for (int r = 0; r < kStatRows; ++r)
-            if (r < rows)
-#pragma unroll
-                for (int e = 0; e < V; ++e) m2 = fmaf(v[r][e] - mean, v[r][e] - mean, m2);
-        s = merge(s, {cnt, mean, m2});
-    }
-    if (!q.any) s = {0.f, 0.f, 0.f};
-    return lane_merge(s, p.lg);
+    return lane_union(s, p.lg);
 }
 
-template <typename T, int V>
+// Rows l .. l + B - 1 (below l1) of a [.., C] tensor at the lane's channels
+template <typename T, int V, int B>
+__device__ __forceinline__ void fetch_rows(const T *at, int64_t stride, bool any, int l, int l1, typename RawV<T, V>::type (&raw)[B]) {
+#pragma unroll
+    for (int r = 0; r < B; ++r)
+        if (any && l + r < l1) raw[r] = load_raw<T, V>(at + (int64_t)(l + r) * stride);
+}
+
+// raw: the first batch, fetched already
+template <typename T, int V, int ACT>
 __device__ __forceinline__ void normalise(const NormProblem &p, const Place &q, int64_t n, int l0, int l1, float mean, float rstd,
-                                          const float *w, const float *b) {
+                                          const float2 *w, const float2 *b, typename RawV<T, V>::type (&raw)[kBatch]) {
     const gdn_group_norm_desc &d = p.d;
     if (!q.any) return;
     const T *at = (const T *)p.x + n * d.x_stride_n + q.c;
     T *to = (T *)p.out + n * d.L * d.C + q.c;
-#pragma unroll 4
-    for (int l = l0; l < l1; ++l) {
-        float v[V];
-        load_v<T, V>(at + (int64_t)l * d.x_stride_l, v);
+    for (int l = l0; l < l1; l += kBatch) {   // loads first: a store could change what is loaded after it
+        if (l > l0) fetch_rows<T, V>(at, d.x_stride_l, true, l, l1, raw);
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = act_f(fmaf((v[e] - mean) * rstd, w[e], b[e]), d.act);
-        store_v<T, V>(to + (int64_t)l * d.C, v);
+        for (int r = 0; r < kBatch; ++r) {
+            if (l + r >= l1) break;
+            float2 v[kPairs<V>];
+            unpack_v<T, V>(raw[r], v);
+#pragma unroll
+            for (int e = 0; e < kPairs<V>; ++e)
+                v[e] = act2<ACT>(fma2(mul2(add2(v[e], splat2(-mean)), splat2(rstd)), w[e], b[e]));
+            store_v<T, V>(to + (int64_t)(l + r) * d.C, v);
+        }
     }
 }
 
-// The whole group's statistics from the partials of its chunks and slabs
+// Visits the partials of the group's chunks and slabs that fall to this lane, loads in batches: f(part, value)
+template <typename F>
+__device__ __forceinline__ void each_partial(const NormProblem &p, const Place &q, int64_t n, F &&f) {
+    const int parts = p.chunks * p.slabs;
+    for (int i0 = q.sub; i0 < parts; i0 += 8 * p.lg) {
+        float2 m[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + j * p.lg, k = p.slabs == 1 ? i : i / p.slabs;
+            if (i < parts) m[j] = p.stat[((n * p.chunks + k) * p.d.G + q.g) * p.slabs + i - k * p.slabs];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (i0 + j * p.lg < parts) f(i0 + j * p.lg, m[j]);
+    }
+}
+// The whole group's statistics
 template <int V>
 __device__ __forceinline__ Stat group_stat(const NormProblem &p, const Place &q, int64_t n) {
     const gdn_group_norm_desc &d = p.d;
-    const int cg = d.C / d.G, parts = p.chunks * p.slabs;
+    const int cg = d.C / d.G;
     Stat s = {0.f, 0.f, 0.f};
-    for (int i = q.sub; i < parts; i += p.lg) {
-        const int k = i / p.slabs, sl = i - k * p.slabs;
-        const float2 m = p.stat[((n * p.chunks + k) * d.G + q.g) * p.slabs + sl];
+    each_partial(p, q, n, [&](int i, float2 m) {
+        const int k = p.slabs == 1 ? i : i / p.slabs, sl = i - k * p.slabs;
         const int rows = min(d.L, (k + 1) * p.chunk_rows) - k * p.chunk_rows;
         const int width = p.slabs == 1 ? cg : min(cg, (sl + 1) * 32 * V) - sl * 32 * V;
         s = merge(s, {(float)rows * (float)width, m.x, m.y});
-    }
-    return lane_merge(s, p.lg);
-}
-
-template <int V>
-__device__ __forceinline__ void load_params(const NormProblem &p, const Place &q, float *w, float *b) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-        w[e] = q.any ? param(p.w, p.d.weight_dtype, q.c + e, 1.f) : 0.f;
-        b[e] = q.any ? param(p.b, p.d.weight_dtype, q.c + e, 0.f) : 0.f;
-    }
+    });
+    return lane_union(s, p.lg);
 }
 
 // FUSED: one chunk and one slab, so the warp has the whole group and writes it too
-template <typename T, int V, bool FUSED>
+template <typename T, int V, int ACT, bool FUSED>
 __global__ void __launch_bounds__(kThreads) norm_stat_kernel(const __grid_constant__ NormProblem p) {
     const gdn_group_norm_desc &d = p.d;
     const Place q = place<V>(p);
+    if (!FUSED) pdl_trigger();
     if (q.slice >= p.slices) return;
-    float w[V], b[V];
-    if (FUSED) load_params<V>(p, q, w, b);
+    float2 w[kPairs<V>], b[kPairs<V>];
+    if (FUSED) load_params<T, V>(p, q.any, q.c, w, b);
     for (int64_t it = q.slice; it < p.items; it += p.slices) {
         int64_t n;
         int l0, l1;
@@ -428,138 +515,166 @@ __global__ void __launch_bounds__(kThreads) norm_stat_kernel(const __grid_consta
                 if (p.mean) p.mean[n * d.G + q.g] = s.mean;
                 if (p.rstd) p.rstd[n * d.G + q.g] = rstd;
             }
-            normalise<T, V>(p, q, n, l0, l1, s.mean, rstd, w, b);
+            typename RawV<T, V>::type raw[kBatch];
+            fetch_rows<T, V>((const T *)p.x + n * d.x_stride_n + q.c, d.x_stride_l, q.any, l0, l1, raw);
+            normalise<T, V, ACT>(p, q, n, l0, l1, s.mean, rstd, w, b, raw);
         } else if (q.any && q.sub == 0) {
             p.stat[stat_at(p, it, q)] = make_float2(s.mean, s.m2);
         }
     }
 }
 
-template <typename T, int V>
+// A programmatic dependent of norm_stat_kernel
+template <typename T, int V, int ACT>
 __global__ void __launch_bounds__(kThreads) norm_apply_kernel(const __grid_constant__ NormProblem p) {
     const gdn_group_norm_desc &d = p.d;
     const Place q = place<V>(p);
-    if (q.slice >= p.slices) return;
-    float w[V], b[V];
-    load_params<V>(p, q, w, b);
-    for (int64_t it = q.slice; it < p.items; it += p.slices) {
+    float2 w[kPairs<V>], b[kPairs<V>];
+    load_params<T, V>(p, q.any, q.c, w, b);
+    bool waited = false;
+    for (int64_t it = q.slice; it < (q.slice < p.slices ? p.items : 0); it += p.slices) {
         int64_t n;
         int l0, l1;
         item_rows(p, it, n, l0, l1);
+        typename RawV<T, V>::type raw[kBatch];
+        fetch_rows<T, V>((const T *)p.x + n * d.x_stride_n + q.c, d.x_stride_l, q.any, l0, l1, raw);
+        if (!waited) pdl_wait();
+        waited = true;
         const Stat s = group_stat<V>(p, q, n);
         const float rstd = rsqrtf(s.m2 / s.n + d.eps);
         if (q.any && q.sub == 0 && l0 == 0 && q.c == q.g * (d.C / d.G)) {
             if (p.mean) p.mean[n * d.G + q.g] = s.mean;
             if (p.rstd) p.rstd[n * d.G + q.g] = rstd;
         }
-        normalise<T, V>(p, q, n, l0, l1, s.mean, rstd, w, b);
+        normalise<T, V, ACT>(p, q, n, l0, l1, s.mean, rstd, w, b, raw);
     }
+    if (!waited) pdl_wait();
 }
 
-template <typename T, int V>
+template <typename T, int V, int ACT>
 __global__ void __launch_bounds__(kThreads) norm_sums_kernel(const __grid_constant__ NormProblem p) {
     const gdn_group_norm_desc &d = p.d;
     const Place q = place<V>(p);
+    constexpr int NP = kPairs<V>;
+    pdl_trigger();
     if (q.slice >= p.slices) return;
-    float w[V], b[V];
-    load_params<V>(p, q, w, b);
-    ParamSums<V> sums;
+    float2 w[NP], b[NP];
+    load_params<T, V>(p, q.any, q.c, w, b);
+    ParamSums<NP> sums;
     for (int64_t it = q.slice; it < p.items; it += p.slices) {
         int64_t n;
         int l0, l1;
         item_rows(p, it, n, l0, l1);
         const float mean = p.mean[n * d.G + q.g], rstd = p.rstd[n * d.G + q.g];
-        float s1 = 0.f, s2 = 0.f;
+        float2 s1 = splat2(0.f), s2 = splat2(0.f);
         if (q.any) {
             const T *at = (const T *)p.x + n * d.x_stride_n + q.c, *dy = (const T *)p.dy + n * d.L * d.C + q.c;
-#pragma unroll 2
-            for (int l = l0; l < l1; ++l) {
-                float x[V], y[V], r1 = 0.f, r2 = 0.f;
-                load_v<T, V>(at + (int64_t)l * d.x_stride_l, x);
-                load_v<T, V>(dy + (int64_t)l * d.C, y);
+            for (int l = l0; l < l1; l += kBatchBackward) {
+                typename RawV<T, V>::type rx[kBatchBackward], ry[kBatchBackward];
+                fetch_rows<T, V>(at, d.x_stride_l, true, l, l1, rx);
+                fetch_rows<T, V>(dy, d.C, true, l, l1, ry);
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const Grad g = grad_of(x[e], y[e], mean, rstd, w[e], b[e], d.act);
-                    sums.w[0][e] = fmaf(g.dz, g.xh, sums.w[0][e]);
-                    sums.b[0][e] += g.dz;
-                    r1 += g.t;
-                    r2 = fmaf(g.t, g.xh, r2);
+                for (int r = 0; r < kBatchBackward; ++r) {
+                    if (l + r >= l1) break;
+                    float2 x[NP], y[NP], r1 = splat2(0.f), r2 = splat2(0.f);
+                    unpack_v<T, V>(rx[r], x);
+                    unpack_v<T, V>(ry[r], y);
+#pragma unroll
+                    for (int e = 0; e < NP; ++e) {
+                        const Grad2 g = grad_of<ACT>(x[e], y[e], mean, rstd, w[e], b[e]);
+                        sums.w[0][e] = fma2(g.dz, g.xh, sums.w[0][e]);
+                        sums.b[0][e] = add2(sums.b[0][e], g.dz);
+                        r1 = add2(r1, g.t);
+                        r2 = fma2(g.t, g.xh, r2);
+                    }
+                    s1 = add2(s1, r1);
+                    s2 = add2(s2, r2);
+                    sums.row_done();
                 }
-                s1 += r1;
-                s2 += r2;
-                sums.row_done();
             }
         }
-        s1 = lane_sum(s1, p.lg);
-        s2 = lane_sum(s2, p.lg);
-        if (q.any && q.sub == 0) p.stat[stat_at(p, it, q)] = make_float2(s1, s2);
+        const float t1 = lane_sum(total<V>(s1), p.lg), t2 = lane_sum(total<V>(s2), p.lg);
+        if (q.any && q.sub == 0) p.stat[stat_at(p, it, q)] = make_float2(t1, t2);
     }
-#pragma unroll
-    for (int e = 0; e < V; ++e)
-        if (q.any) {
-            p.part[((int64_t)q.slice * 2) * d.C + q.c + e] = sums.w[1][e] + sums.w[0][e];
-            p.part[((int64_t)q.slice * 2 + 1) * d.C + q.c + e] = sums.b[1][e] + sums.b[0][e];
-        }
+    if (q.any) sums.template write<V>(p, q.slice, q.c, 0);
 }
 
-template <typename T, int V>
+// A programmatic dependent of norm_sums_kernel
+template <typename T, int V, int ACT>
 __global__ void __launch_bounds__(kThreads) norm_dx_kernel(const __grid_constant__ NormProblem p) {
     const gdn_group_norm_desc &d = p.d;
     const Place q = place<V>(p);
-    if (q.slice >= p.slices) return;
+    constexpr int NP = kPairs<V>;
     const float count = (float)d.L * (float)(d.C / d.G);
-    float w[V], b[V];
-    load_params<V>(p, q, w, b);
-    for (int64_t it = q.slice; it < p.items; it += p.slices) {
+    float2 w[NP], b[NP];
+    load_params<T, V>(p, q.any, q.c, w, b);
+    bool waited = false;
+    for (int64_t it = q.slice; it < (q.slice < p.slices ? p.items : 0); it += p.slices) {
         int64_t n;
         int l0, l1;
         item_rows(p, it, n, l0, l1);
+        const T *at = (const T *)p.x + n * d.x_stride_n + q.c, *dy = (const T *)p.dy + n * d.L * d.C + q.c;
+        typename RawV<T, V>::type rx[kBatchBackward], ry[kBatchBackward];
+        fetch_rows<T, V>(at, d.x_stride_l, q.any, l0, l1, rx);
+        fetch_rows<T, V>(dy, d.C, q.any, l0, l1, ry);
+        const float mean = p.mean[n * d.G + q.g], rstd = p.rstd[n * d.G + q.g];
+        if (!waited) pdl_wait();
+        waited = true;
         float s1 = 0.f, s2 = 0.f;
-        const int parts = p.chunks * p.slabs;
-        for (int i = q.sub; i < parts; i += p.lg) {
-            const int k = i / p.slabs, sl = i - k * p.slabs;
-            const float2 m = p.stat[((n * p.chunks + k) * d.G + q.g) * p.slabs + sl];
+        each_partial(p, q, n, [&](int, float2 m) {
             s1 += m.x;
             s2 += m.y;
-        }
+        });
         const float m1 = lane_sum(s1, p.lg) / count, m2 = lane_sum(s2, p.lg) / count;
         if (!q.any) continue;
-        const float mean = p.mean[n * d.G + q.g], rstd = p.rstd[n * d.G + q.g];
-        const T *at = (const T *)p.x + n * d.x_stride_n + q.c, *dy = (const T *)p.dy + n * d.L * d.C + q.c;
         T *dx = (T *)p.dx + n * d.L * d.C + q.c;
-#pragma unroll 2
-        for (int l = l0; l < l1; ++l) {
-            float x[V], y[V];
-            load_v<T, V>(at + (int64_t)l * d.x_stride_l, x);
-            load_v<T, V>(dy + (int64_t)l * d.C, y);
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const Grad g = grad_of(x[e], y[e], mean, rstd, w[e], b[e], d.act);
-                y[e] = rstd * fmaf(-g.xh, m2, g.t - m1);
+        for (int l = l0; l < l1; l += kBatchBackward) {
+            if (l > l0) {
+                fetch_rows<T, V>(at, d.x_stride_l, true, l, l1, rx);
+                fetch_rows<T, V>(dy, d.C, true, l, l1, ry);
             }
-            store_v<T, V>(dx + (int64_t)l * d.C, y);
+#pragma unroll
+            for (int r = 0; r < kBatchBackward; ++r) {
+                if (l + r >= l1) break;
+                float2 x[NP], y[NP];
+                unpack_v<T, V>(rx[r], x);
+                unpack_v<T, V>(ry[r], y);
+#pragma unroll
+                for (int e = 0; e < NP; ++e) {
+                    const Grad2 g = grad_of<ACT>(x[e], y[e], mean, rstd, w[e], b[e]);
+                    y[e] = mul2(fma2(g.xh, splat2(-m2), add2(g.t, splat2(-m1))), splat2(rstd));
+                }
+                store_v<T, V>(dx + (int64_t)(l + r) * d.C, y);
+            }
         }
     }
+    // only after the wait: its dependent relies on norm_sums_kernel, too
+    if (!waited) pdl_wait();
+    pdl_trigger();
 }
 
-// dweight and dbias from part[slices][2][C]: 32 channels a block, 8 strided partial sums each
-__global__ void __launch_bounds__(256) norm_params_kernel(const __grid_constant__ NormProblem p) {
-    __shared__ float red[2][8][32];
+// dweight and dbias from part[slices][2][C]: 32 channels a block, 32 strided partial sums each. A
+// programmatic dependent of the kernel before it.
+constexpr int kParamThreads = 1024;
+__global__ void __launch_bounds__(kParamThreads) norm_params_kernel(const __grid_constant__ NormProblem p) {
+    __shared__ float red[2][32][33];
     const int ch = threadIdx.x % 32, c = blockIdx.x * 32 + ch, s = threadIdx.x / 32;
     float v[2] = {0.f, 0.f};
+    pdl_wait();
     if (c < p.d.C)
-        for (int i = s; i < p.slices; i += 8) {
+#pragma unroll 4
+        for (int i = s; i < p.slices; i += 32) {
             v[0] += p.part[((int64_t)i * 2) * p.d.C + c];
             v[1] += p.part[((int64_t)i * 2 + 1) * p.d.C + c];
         }
     red[0][s][ch] = v[0];
     red[1][s][ch] = v[1];
     __syncthreads();
-    if (s < 2 && c < p.d.C) {
-        float t = 0.f;
-        for (int i = 0; i < 8; ++i) t += red[s][i][ch];
-        float *to = s ? p.db : p.dw;
-        if (to) to[c] = t;
+    // warp s sums channel s of the block over the 32 partial sums
+    const float t0 = lane_sum(red[0][ch][s], 32), t1 = lane_sum(red[1][ch][s], 32);
+    if (ch == 0 && blockIdx.x * 32 + s < p.d.C) {
+        if (p.dw) p.dw[blockIdx.x * 32 + s] = t0;
+        if (p.db) p.db[blockIdx.x * 32 + s] = t1;
     }
 }
 
@@ -588,9 +703,9 @@ Plan make_plan(const gdn_group_norm_desc &d, int v, int nv_most) {
     r.slabs = r.rows ? 1 : (int)cdiv64(cgv, r.lg);
     r.sets = r.slabs == 1 ? (int)cdiv64(d.G, 32 / r.lg) : d.G * r.slabs;
     r.chunks = 1;
-    if (!r.rows) {   // enough chunks of positions to fill the chip, of at least 8 positions
+    if (!r.rows) {   // enough chunks of positions to fill the chip, of at least a batch each
         const int64_t want = cdiv64((int64_t)kSms * kBlocksGeneral * kWarps, std::max<int64_t>(1, (int64_t)d.N * r.sets));
-        r.chunks = (int)std::max<int64_t>(1, std::min<int64_t>(want, d.L / 8));
+        r.chunks = (int)std::max<int64_t>(1, std::min<int64_t>(want, d.L / kBatch));
     }
     r.chunk_rows = (int)cdiv64(d.L, r.chunks);
     r.chunks = (int)cdiv64(d.L, std::max(1, r.chunk_rows));
@@ -635,46 +750,62 @@ void apply_plan(NormProblem &p, const Plan &pl, void *ws, bool backward) {
 }
 unsigned grid_of(const Plan &pl) { return (unsigned)cdiv64((int64_t)pl.sets * pl.slices, kWarps); }
 
-template <typename T, int V>
+template <typename T, int V, int ACT>
 cudaError_t run_forward(NormProblem p, void *ws, cudaStream_t s) {
     const Plan pl = make_plan(p.d, V, kNvForward);
     apply_plan(p, pl, ws, false);
-    const unsigned grid = grid_of(pl);
+    const dim3 grid = grid_of(pl), block = kThreads;
     if (pl.rows) {
-        if (pl.nv == 1) norm_rows_forward<T, V, 1><<<grid, kThreads, 0, s>>>(p);
-        else if (pl.nv == 2) norm_rows_forward<T, V, 2><<<grid, kThreads, 0, s>>>(p);
-        else norm_rows_forward<T, V, 4><<<grid, kThreads, 0, s>>>(p);
-    } else if (pl.chunks * pl.slabs == 1) {
-        norm_stat_kernel<T, V, true><<<grid, kThreads, 0, s>>>(p);
-    } else {
-        norm_stat_kernel<T, V, false><<<grid, kThreads, 0, s>>>(p);
-        norm_apply_kernel<T, V><<<grid, kThreads, 0, s>>>(p);
+        // more than one vector a lane: all 32 lanes; for one, the usual heads have an instance of their own
+        auto kernel = pl.nv == 2   ? norm_rows_forward<T, V, 2, ACT, 32>
+                      : pl.nv == 4 ? norm_rows_forward<T, V, 4, ACT, 32>
+                                   : norm_rows_forward<T, V, 1, ACT, 0>;
+        if constexpr (V > 1) {
+            if (pl.nv == 1 && pl.lg == 8) kernel = norm_rows_forward<T, V, 1, ACT, 8>;
+            if (pl.nv == 1 && pl.lg == 16) kernel = norm_rows_forward<T, V, 1, ACT, 16>;
+            if (pl.nv == 1 && pl.lg == 32) kernel = norm_rows_forward<T, V, 1, ACT, 32>;
+        }
+        return launch_kernel(false, kernel, grid, block, 0, s, p);
     }
-    return cudaGetLastError();
+    if (pl.chunks * pl.slabs == 1) return launch_kernel(false, norm_stat_kernel<T, V, ACT, true>, grid, block, 0, s, p);
+    const cudaError_t e = launch_kernel(false, norm_stat_kernel<T, V, ACT, false>, grid, block, 0, s, p);
+    return e != cudaSuccess ? e : launch_kernel(true, norm_apply_kernel<T, V, ACT>, grid, block, 0, s, p);
 }
 
-template <typename T, int V>
+template <typename T, int V, int ACT>
 cudaError_t run_backward(NormProblem p, void *ws, cudaStream_t s) {
     const Plan pl = make_plan(p.d, V, kNvBackward);
     apply_plan(p, pl, ws, true);
-    const unsigned grid = grid_of(pl);
+    const dim3 grid = grid_of(pl), block = kThreads;
+    cudaError_t e;
     if (pl.rows) {
-        if (pl.nv == 1) norm_rows_backward<T, V, 1><<<grid, kThreads, 0, s>>>(p);
-        else norm_rows_backward<T, V, 2><<<grid, kThreads, 0, s>>>(p);
+        auto kernel = pl.nv == 2 ? norm_rows_backward<T, V, 2, ACT, 32> : norm_rows_backward<T, V, 1, ACT, 0>;
+        if constexpr (V > 1) {
+            if (pl.nv == 1 && pl.lg == 8) kernel = norm_rows_backward<T, V, 1, ACT, 8>;
+            if (pl.nv == 1 && pl.lg == 16) kernel = norm_rows_backward<T, V, 1, ACT, 16>;
+            if (pl.nv == 1 && pl.lg == 32) kernel = norm_rows_backward<T, V, 1, ACT, 32>;
+        }
+        e = launch_kernel(false, kernel, grid, block, 0, s, p);
     } else {
-        norm_sums_kernel<T, V><<<grid, kThreads, 0, s>>>(p);
-        norm_dx_kernel<T, V><<<grid, kThreads, 0, s>>>(p);
+        e = launch_kernel(false, norm_sums_kernel<T, V, ACT>, grid, block, 0, s, p);
+        if (e == cudaSuccess) e = launch_kernel(true, norm_dx_kernel<T, V, ACT>, grid, block, 0, s, p);
     }
-    if (p.dw || p.db) norm_params_kernel<<<(unsigned)cdiv64(p.d.C, 32), 256, 0, s>>>(p);
-    return cudaGetLastError();
+    if (e != cudaSuccess || (!p.dw && !p.db)) return e;
+    return launch_kernel(true, norm_params_kernel, dim3((unsigned)cdiv64(p.d.C, 32)), dim3(kParamThreads), 0, s, p);
+}
+
+template <typename T, int V>
+cudaError_t run_act(const NormProblem &p, bool backward, void *ws, cudaStream_t s) {
+    if (p.d.act == GDN_ACT_SILU)
+        return backward ? run_backward<T, V, GDN_ACT_SILU>(p, ws, s) : run_forward<T, V, GDN_ACT_SILU>(p, ws, s);
+    return backward ? run_backward<T, V, GDN_ACT_NONE>(p, ws, s) : run_forward<T, V, GDN_ACT_NONE>(p, ws, s);
 }
 
 template <typename T>
 cudaError_t run(const NormProblem &p, bool backward, void *ws, cudaStream_t s) {
     constexpr int V = VecN<T>::value;
     const bool vec = vectors_fit(p.d, p.x, p.dy, backward ? p.dx : p.out);
-    if (backward) return vec ? run_backward<T, V>(p, ws, s) : run_backward<T, 1>(p, ws, s);
-    return vec ? run_forward<T, V>(p, ws, s) : run_forward<T, 1>(p, ws, s);
+    return vec ? run_act<T, V>(p, backward, ws, s) : run_act<T, 1>(p, backward, ws, s);
 }
 
 int run_any(const NormProblem &p, bool backward, void *ws, cudaStream_t s) {

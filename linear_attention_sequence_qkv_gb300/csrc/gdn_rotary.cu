@@ -64,13 +64,13 @@ template <typename T, int V> union Vec {
 };
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;              // units in flight per thread
+constexpr int kBatch = 2;              // units in flight per thread
 constexpr int kTableBytes = 32768;     // cosines and sines of a CTA's tokens
 
 // V: elements per vector. HALF: a unit is the vectors at u V and rot/2 + u V; else the V elements from u V (two
 // single elements for V = 1).
 template <typename T, int V, bool HALF>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryProblem p) {
+__global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_constant__ RotaryProblem p) {
     constexpr int NP = HALF ? V : (V > 1 ? V / 2 : 1);   // pairs per unit
     constexpr int W = NP < 4 ? NP : 4;                   // floats per table entry
     constexpr int Q = NP / W;                            // entries of cosines (and of sines) per unit
@@ -82,23 +82,13 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     const int64_t tok0 = (int64_t)blockIdx.x * p.tokens;
     const int nt = (int)min((int64_t)p.tokens, (int64_t)d.B * d.T - tok0);
     const int half = d.rot / 2;
-    for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-        const int t = i / half, pr = i - t * half;
-        const uint32_t row = (uint32_t)(tok0 + t) / (uint32_t)d.T;
-        const float2 cs = cos_sin(token_position(p, row, (int)((uint32_t)(tok0 + t) - row * d.T)), p.turns[pr]);
-        const int u = pr / NP, e = pr % NP;
-        float *at = tab + ((t * 2 * Q + e / W) * p.u_rot + u) * W + e % W;
-        at[0] = cs.x * d.scale;
-        at[Q * p.u_rot * W] = cs.y * (d.inverse ? -d.scale : d.scale);
-    }
-    __syncthreads();
     const int per = p.u_q + p.u_k + p.c_q + p.c_k;       // units per token
     const int total = nt * per, step = kThreads * gridDim.y;
-    for (int i0 = blockIdx.y * kThreads + threadIdx.x; i0 < total; i0 += kBatch * step) {
-        const T *src[kBatch];
-        T *dst[kBatch];
-        const float *tb[kBatch];                          // the unit's table entries; null: copy
-        Vec<T, V> a[kBatch], b[kBatch];
+    const T *src[kBatch];
+    T *dst[kBatch];
+    const float *tb[kBatch];                              // the unit's table entries; null: copy
+    Vec<T, V> a[kBatch], b[kBatch];
+    auto fetch = [&](int i0) {
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             const int i = i0 + j * step;
@@ -119,6 +109,20 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
             a[j].raw = *(const decltype(a[j].raw) *)src[j];
             if (rot && (HALF || V == 1)) b[j].raw = *(const decltype(b[j].raw) *)(src[j] + (HALF ? half : 1));
         }
+    };
+    int i0 = blockIdx.y * kThreads + threadIdx.x;
+    fetch(i0);   // on their way while the table is computed
+    for (int i = threadIdx.x; i < nt * half; i += kThreads) {
+        const int t = i / half, pr = i - t * half;
+        const uint32_t row = (uint32_t)(tok0 + t) / (uint32_t)d.T;
+        const float2 cs = cos_sin(token_position(p, row, (int)((uint32_t)(tok0 + t) - row * d.T)), p.turns[pr]);
+        const int u = pr / NP, e = pr % NP;
+        float *at = tab + ((t * 2 * Q + e / W) * p.u_rot + u) * W + e % W;
+        at[0] = cs.x * d.scale;
+        at[Q * p.u_rot * W] = cs.y * (d.inverse ? -d.scale : d.scale);
+    }
+    __syncthreads();
+    for (; i0 < total; i0 += kBatch * step, fetch(i0)) {
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             if (i0 + j * step >= total) continue;
