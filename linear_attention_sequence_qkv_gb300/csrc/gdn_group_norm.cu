@@ -43,7 +43,7 @@ struct NormProblem {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kBlocksForward = 3, kBlocksBackward = 2, kBlocksGeneral = 4;   // per SM, resident at once
 constexpr int kRowsForward = 2;   // rows a warp works on at a time (two reductions in flight); as many are on their way
-constexpr int kAheadBackward = 3; // rows on their way while a warp works on one
+constexpr int kAheadBackward = 6; // rows on their way in the backward
 constexpr int kBatch = 8, kBatchBackward = 4;   // rows in flight per warp in the general form
 
 template <typename T> struct VecN { static constexpr int value = 16 / sizeof(T); };
@@ -156,6 +156,23 @@ __device__ __forceinline__ void load_params(const NormProblem &p, bool any, int 
     for (int e = 0; e < kPairs<V>; ++e)
         asm volatile("" : "+f"(w[e].x), "+f"(w[e].y), "+f"(b[e].x), "+f"(b[e].y));
 }
+
+// A warp's rows on their way into shared memory: DEPTH rows of NT tensors, 16 bytes per lane and vector. A lane
+// reads only what it copied itself, so its own wait is enough.
+template <int NT, int NV, int DEPTH> struct RowRing {
+    uint4 *base;   // the lane's first slot
+    __device__ __forceinline__ RowRing(uint4 *smem) {
+        base = smem + (threadIdx.x / 32) * (DEPTH * NT * NV * 32) + threadIdx.x % 32;
+    }
+    __device__ __forceinline__ uint4 *slot(int j, int t, int i) const { return base + ((j * NT + t) * NV + i) * 32; }
+    __device__ __forceinline__ void copy(int j, int t, int i, const void *src) const {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                     :: "r"((uint32_t)__cvta_generic_to_shared(slot(j, t, i))), "l"(src) : "memory");
+    }
+    static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    static __device__ __forceinline__ void wait_oldest() { asm volatile("cp.async.wait_group %0;" :: "n"(DEPTH - 1) : "memory"); }
+};
+template <int NT, int NV, int DEPTH> constexpr size_t kRingBytes = (size_t)kWarps * DEPTH * NT * NV * 512;
 
 // ------------------------------------------------------------------ rows
 template <typename T, int V, int NV, int ACT, int LG>
@@ -301,60 +318,76 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? kBlocksBackward : 1) norm_
         has[i] = q.any && (q.sub + i * p.lg) * V < cg;
         load_params<T, V>(p, has[i], q.c + i * p.lg * V, w[i], b[i]);
     }
-    constexpr int kA = NV == 1 ? kAheadBackward : 1;
-    typename RawV<T, V>::type rx[kA][NV] = {}, ry[kA][NV] = {};
-    float rm[kA] = {}, rr[kA] = {};
+    constexpr int kSteps = kAheadBackward / NV;
+    extern __shared__ uint4 ring_smem[];
+    const RowRing<2, NV, kSteps> ring(ring_smem);
+    T single[2][NV];
     auto fetch = [&](int j, int64_t n) {
-        if (n >= p.items) return;
-        rm[j] = p.mean[n * d.G + q.g];
-        rr[j] = p.rstd[n * d.G + q.g];
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (has[i]) {
-                rx[j][i] = load_raw<T, V>((const T *)p.x + n * d.x_stride_n + q.c + i * p.lg * V);
-                ry[j][i] = load_raw<T, V>((const T *)p.dy + n * d.C + q.c + i * p.lg * V);
-            }
-    };
-#pragma unroll
-    for (int j = 0; j < kA; ++j) fetch(j, q.slice + (int64_t)j * p.slices);
-    for (int64_t n0 = q.slice; n0 < p.items; n0 += (int64_t)kA * p.slices) {
-#pragma unroll
-        for (int j = 0; j < kA; ++j) {
-            const int64_t n = n0 + (int64_t)j * p.slices;
-            if (n >= p.items) break;
-            float2 x[NV][NP], y[NV][NP];
-            const float mean = rm[j], rstd = rr[j];
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                unpack_v<T, V>(rx[j][i], x[i]);
-                unpack_v<T, V>(ry[j][i], y[i]);   // zeros for a lane without channels: no part in any sum
-            }
-            fetch(j, n + (int64_t)kA * p.slices);
-            float2 s1 = splat2(0.f), s2 = splat2(0.f);
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int e = 0; e < NP; ++e) {
-                    const Grad2 g = grad_of<ACT>(x[i][e], y[i][e], mean, rstd, w[i][e], b[i][e]);
-                    x[i][e] = g.xh;
-                    y[i][e] = g.t;
-                    sums.w[0][i * NP + e] = fma2(g.dz, g.xh, sums.w[0][i * NP + e]);
-                    sums.b[0][i * NP + e] = add2(sums.b[0][i * NP + e], g.dz);
-                    if (has[i]) {
-                        s1 = add2(s1, g.t);
-                        s2 = fma2(g.t, g.xh, s2);
-                    }
+            if (n < p.items && has[i]) {
+                const T *x = (const T *)p.x + n * d.x_stride_n + q.c + i * p.lg * V, *y = (const T *)p.dy + n * d.C + q.c + i * p.lg * V;
+                if (V > 1) {
+                    ring.copy(j, 0, i, x);
+                    ring.copy(j, 1, i, y);
+                } else {
+                    single[0][i] = *x;
+                    single[1][i] = *y;
                 }
-            sums.row_done();
-            const float m1 = lane_sum_t<LG>(total<V>(s1), p.lg) * inv, m2 = lane_sum_t<LG>(total<V>(s2), p.lg) * inv;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (!has[i]) continue;
-#pragma unroll
-                for (int e = 0; e < NP; ++e)
-                    y[i][e] = mul2(fma2(x[i][e], splat2(-m2), add2(y[i][e], splat2(-m1))), splat2(rstd));
-                store_v<T, V>((T *)p.dx + n * d.C + q.c + i * p.lg * V, y[i]);
             }
+        if (V > 1) ring.commit();
+    };
+    // (mean, rstd) of this row and the next two
+    auto stats = [&](int64_t n) {
+        return n < p.items ? make_float2(p.mean[n * d.G + q.g], p.rstd[n * d.G + q.g]) : make_float2(0.f, 0.f);
+    };
+    if (V > 1)
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) fetch(j, q.slice + (int64_t)j * p.slices);
+    float2 st0 = stats(q.slice), st1 = stats(q.slice + (int64_t)p.slices);
+    int j = 0;
+    for (int64_t n = q.slice; n < p.items; n += p.slices) {
+        const float2 st2 = stats(n + 2 * (int64_t)p.slices);
+        const float mean = st0.x, rstd = st0.y;
+        st0 = st1;
+        st1 = st2;
+        if (V > 1) ring.wait_oldest();
+        else fetch(0, n);
+        float2 x[NV][NP], y[NV][NP], s1 = splat2(0.f), s2 = splat2(0.f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!has[i]) continue;   // no part in any sum
+            if constexpr (V > 1) {
+                unpack_v<T, V>(*ring.slot(j, 0, i), x[i]);
+                unpack_v<T, V>(*ring.slot(j, 1, i), y[i]);
+            } else {
+                unpack_v<T, V>(single[0][i], x[i]);
+                unpack_v<T, V>(single[1][i], y[i]);
+            }
+#pragma unroll
+            for (int e = 0; e < NP; ++e) {
+                const Grad2 g = grad_of<ACT>(x[i][e], y[i][e], mean, rstd, w[i][e], b[i][e]);
+                x[i][e] = g.xh;
+                y[i][e] = g.t;
+                sums.w[0][i * NP + e] = fma2(g.dz, g.xh, sums.w[0][i * NP + e]);
+                sums.b[0][i * NP + e] = add2(sums.b[0][i * NP + e], g.dz);
+                s1 = add2(s1, g.t);
+                s2 = fma2(g.t, g.xh, s2);
+            }
+        }
+        sums.row_done();
+        const float m1 = lane_sum_t<LG>(total<V>(s1), p.lg) * inv, m2 = lane_sum_t<LG>(total<V>(s2), p.lg) * inv;
+        if (V > 1) {   // this row's slots have been read
+            fetch(j, n + (int64_t)kSteps * p.slices);
+            j = j + 1 < kSteps ? j + 1 : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!has[i]) continue;
+#pragma unroll
+            for (int e = 0; e < NP; ++e)
+                y[i][e] = mul2(fma2(x[i][e], splat2(-m2), add2(y[i][e], splat2(-m1))), splat2(rstd));
+            store_v<T, V>((T *)p.dx + n * d.C + q.c + i * p.lg * V, y[i]);
         }
     }
 #pragma unroll
@@ -785,7 +818,9 @@ cudaError_t run_backward(NormProblem p, void *ws, cudaStream_t s) {
             if (pl.nv == 1 && pl.lg == 16) kernel = norm_rows_backward<T, V, 1, ACT, 16>;
             if (pl.nv == 1 && pl.lg == 32) kernel = norm_rows_backward<T, V, 1, ACT, 32>;
         }
-        e = launch_kernel(false, kernel, grid, block, 0, s, p);
+        const size_t ring = V > 1 ? kRingBytes<2, 1, kAheadBackward> : 0;   // NV vectors of 1 / NV as many rows
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring);
+        if (e == cudaSuccess) e = launch_kernel(false, kernel, grid, block, ring, s, p);
     } else {
         e = launch_kernel(false, norm_sums_kernel<T, V, ACT>, grid, block, 0, s, p);
         if (e == cudaSuccess) e = launch_kernel(true, norm_dx_kernel<T, V, ACT>, grid, block, 0, s, p);
