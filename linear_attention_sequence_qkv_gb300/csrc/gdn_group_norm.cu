@@ -2,7 +2,8 @@
 // forward and backward. Bound by HBM.
 //
 // A warp works on a fixed set of adjacent channels: 32 / LG groups of LG lanes each
-// (LG, a power of two, covers a group's vectors), or a 32-lane slab of a larger group.
+// (LG, a power of two, covers a group's vectors), or a 32-lane slab of a larger group
+// (in the rows form a block takes a larger group).
 // Weights stay in registers, sums cross lanes by shuffles, and rows stream past.
 //
 //   rows     L = 1 and a group fits LG lanes x NV vectors: a row is read once, its mean
@@ -32,7 +33,7 @@ struct NormProblem {
     float *mean, *rstd, *dw, *db;
     float2 *stat;      // general: [item][part] partial (mean, centred sum of squares), or (sum t, sum t xh)
     float *part;       // [slices][2][C] partial sums of dweight, dbias
-    int lg;            // lanes per group or slab
+    int lg;            // lanes per group or slab; kThreads: a block per group
     int sets;          // sets of channels, one per warp
     int slabs;         // slabs per group (1 where a warp holds whole groups)
     int slices;        // warps that share a set
@@ -92,9 +93,20 @@ template <int ACT> __device__ __forceinline__ float2 act_grad2(float2 z) {   // 
     return mul2(s, fma2(z, fma2(s, splat2(-1.f), splat2(1.f)), splat2(1.f)));
 }
 
-// The same with the number of lanes known (LG), or in lg (LG = 0)
+// The same with the number of lanes known (LG), in lg (LG = 0), or over the block (LG = kThreads: all threads call it)
 template <int LG> __device__ __forceinline__ float lane_sum_t(float v, int lg) {
     if (LG == 0) return lane_sum(v, lg);
+    if constexpr (LG == kThreads) {
+        __shared__ float part[kWarps];
+        v = lane_sum_t<32>(v, lg);
+        float t = 0.f;
+        __syncthreads();   // the sum before has been read
+        if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) t += part[i];
+        return t;
+    }
 #pragma unroll
     for (int off = LG / 2; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     return v;
@@ -112,6 +124,14 @@ __device__ __forceinline__ Place place(const NormProblem &p) {
     const int w = blockIdx.x * kWarps + threadIdx.x / 32, lane = threadIdx.x % 32;
     const int cg = p.d.C / p.d.G;
     Place q;
+    if (p.lg == kThreads) {   // a block per group
+        q.g = q.set = blockIdx.x % p.sets;
+        q.slice = blockIdx.x / p.sets;
+        q.sub = threadIdx.x;
+        q.any = q.slice < p.slices && q.sub * V < cg;
+        q.c = q.g * cg + q.sub * V;
+        return q;
+    }
     q.set = w % p.sets;
     q.slice = w / p.sets;
     q.sub = lane % p.lg;
@@ -318,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? kBlocksBackward : 1) norm_
         has[i] = q.any && (q.sub + i * p.lg) * V < cg;
         load_params<T, V>(p, has[i], q.c + i * p.lg * V, w[i], b[i]);
     }
-    constexpr int kSteps = kAheadBackward / NV;
+    constexpr int kSteps = V > 1 ? kAheadBackward / NV : 1;
     extern __shared__ uint4 ring_smem[];
     const RowRing<2, NV, kSteps> ring(ring_smem);
     T single[2][NV];
@@ -724,17 +744,24 @@ int pow2_at_least(int x) {
     while (r < x) r *= 2;
     return r;
 }
-constexpr int kNvForward = 4, kNvBackward = 2;
-// v: elements per vector; nv_most: vectors a lane of the rows form may hold
-Plan make_plan(const gdn_group_norm_desc &d, int v, int nv_most) {
+// vectors a lane of the rows form may hold (registers)
+int most_vectors(int v, bool backward) { return backward && v > 1 ? 2 : 4; }
+// v: elements per vector
+Plan make_plan(const gdn_group_norm_desc &d, int v, bool backward) {
     Plan r;
-    const int cg = d.C / d.G, cgv = cg / v;
+    const int cg = d.C / d.G, cgv = cg / v, most = most_vectors(v, backward);
     r.v = v;
     r.lg = std::min(32, pow2_at_least(cgv));
     r.nv = pow2_at_least((int)cdiv64(cgv, r.lg));
-    r.rows = d.L == 1 && r.nv <= nv_most;
+    // rows: a warp where its lanes hold the group, else a block (two vectors or more a lane: 32 lanes)
+    if (r.nv > (v > 1 ? 2 : most)) {
+        r.lg = kThreads;
+        r.nv = pow2_at_least((int)cdiv64(cgv, r.lg));
+    }
+    r.rows = d.L == 1 && r.nv <= most;
+    if (!r.rows) r.lg = std::min(32, pow2_at_least(cgv));
     r.slabs = r.rows ? 1 : (int)cdiv64(cgv, r.lg);
-    r.sets = r.slabs == 1 ? (int)cdiv64(d.G, 32 / r.lg) : d.G * r.slabs;
+    r.sets = r.lg == kThreads ? d.G : r.slabs == 1 ? (int)cdiv64(d.G, 32 / r.lg) : d.G * r.slabs;
     r.chunks = 1;
     if (!r.rows) {   // enough chunks of positions to fill the chip, of at least a batch each
         const int64_t want = cdiv64((int64_t)kSms * kBlocksGeneral * kWarps, std::max<int64_t>(1, (int64_t)d.N * r.sets));
@@ -743,8 +770,9 @@ Plan make_plan(const gdn_group_norm_desc &d, int v, int nv_most) {
     r.chunk_rows = (int)cdiv64(d.L, r.chunks);
     r.chunks = (int)cdiv64(d.L, std::max(1, r.chunk_rows));
     r.items = (int64_t)d.N * r.chunks;
-    const int64_t warps = (int64_t)kSms * kWarps * (!r.rows ? kBlocksGeneral : nv_most == kNvForward ? kBlocksForward : kBlocksBackward);
-    r.slices = (int)std::max<int64_t>(1, std::min<int64_t>(warps / r.sets, r.items));
+    const int64_t teams = (int64_t)kSms * (!r.rows ? kBlocksGeneral : !backward ? kBlocksForward : kBlocksBackward) *
+                          (r.lg == kThreads ? 1 : kWarps);
+    r.slices = (int)std::max<int64_t>(1, std::min<int64_t>(teams / r.sets, r.items));
     return r;
 }
 int vector_of(const gdn_group_norm_desc &d) { return 16 / (int)act_size(d.dtype); }
@@ -763,7 +791,7 @@ size_t workspace_need(const gdn_group_norm_desc &d, bool backward) {
     if ((int64_t)d.N * d.L == 0) return kStatusBytes;
     for (int v : {1, vector_of(d)}) {
         if (d.C / d.G % v) continue;
-        const Plan pl = make_plan(d, v, backward ? kNvBackward : kNvForward);
+        const Plan pl = make_plan(d, v, backward);
         most = std::max(most, stat_bytes(d, pl) + (backward ? part_bytes(d, pl) : 0));
     }
     return kStatusBytes + most;
@@ -781,18 +809,25 @@ void apply_plan(NormProblem &p, const Plan &pl, void *ws, bool backward) {
     p.stat = (float2 *)w;
     if (backward) p.part = (float *)(w + stat_bytes(p.d, pl));
 }
-unsigned grid_of(const Plan &pl) { return (unsigned)cdiv64((int64_t)pl.sets * pl.slices, kWarps); }
+unsigned grid_of(const Plan &pl) {
+    return (unsigned)cdiv64((int64_t)pl.sets * pl.slices, pl.lg == kThreads ? 1 : kWarps);
+}
 
 template <typename T, int V, int ACT>
 cudaError_t run_forward(NormProblem p, void *ws, cudaStream_t s) {
-    const Plan pl = make_plan(p.d, V, kNvForward);
+    const Plan pl = make_plan(p.d, V, false);
     apply_plan(p, pl, ws, false);
     const dim3 grid = grid_of(pl), block = kThreads;
     if (pl.rows) {
-        // more than one vector a lane: all 32 lanes; for one, the usual heads have an instance of their own
-        auto kernel = pl.nv == 2   ? norm_rows_forward<T, V, 2, ACT, 32>
-                      : pl.nv == 4 ? norm_rows_forward<T, V, 4, ACT, 32>
-                                   : norm_rows_forward<T, V, 1, ACT, 0>;
+        // several vectors a lane: all 32 lanes, or the block; for one, the usual heads have an instance of their own
+        auto kernel = norm_rows_forward<T, V, 1, ACT, 0>;
+        if (pl.lg == kThreads)
+            kernel = pl.nv == 1   ? norm_rows_forward<T, V, 1, ACT, kThreads>
+                     : pl.nv == 2 ? norm_rows_forward<T, V, 2, ACT, kThreads>
+                                  : norm_rows_forward<T, V, 4, ACT, kThreads>;
+        else if (pl.nv == 2) kernel = norm_rows_forward<T, V, 2, ACT, 32>;
+        if constexpr (V == 1)
+            if (pl.lg == 32 && pl.nv == 4) kernel = norm_rows_forward<T, V, 4, ACT, 32>;
         if constexpr (V > 1) {
             if (pl.nv == 1 && pl.lg == 8) kernel = norm_rows_forward<T, V, 1, ACT, 8>;
             if (pl.nv == 1 && pl.lg == 16) kernel = norm_rows_forward<T, V, 1, ACT, 16>;
@@ -807,12 +842,17 @@ cudaError_t run_forward(NormProblem p, void *ws, cudaStream_t s) {
 
 template <typename T, int V, int ACT>
 cudaError_t run_backward(NormProblem p, void *ws, cudaStream_t s) {
-    const Plan pl = make_plan(p.d, V, kNvBackward);
+    const Plan pl = make_plan(p.d, V, true);
     apply_plan(p, pl, ws, true);
     const dim3 grid = grid_of(pl), block = kThreads;
     cudaError_t e;
     if (pl.rows) {
-        auto kernel = pl.nv == 2 ? norm_rows_backward<T, V, 2, ACT, 32> : norm_rows_backward<T, V, 1, ACT, 0>;
+        auto kernel = norm_rows_backward<T, V, 1, ACT, 0>;
+        if (pl.lg == kThreads)
+            kernel = pl.nv == 1 ? norm_rows_backward<T, V, 1, ACT, kThreads> : norm_rows_backward<T, V, 2, ACT, kThreads>;
+        else if (pl.nv == 2) kernel = norm_rows_backward<T, V, 2, ACT, 32>;
+        if constexpr (V == 1)
+            if (pl.nv == 4) kernel = pl.lg == 32 ? norm_rows_backward<T, V, 4, ACT, 32> : norm_rows_backward<T, V, 4, ACT, kThreads>;
         if constexpr (V > 1) {
             if (pl.nv == 1 && pl.lg == 8) kernel = norm_rows_backward<T, V, 1, ACT, 8>;
             if (pl.nv == 1 && pl.lg == 16) kernel = norm_rows_backward<T, V, 1, ACT, 16>;

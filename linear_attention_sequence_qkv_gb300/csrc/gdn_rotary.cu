@@ -28,7 +28,7 @@ struct RotaryProblem {
     int u_rot;              // units of a head's rotated channels
     int u_q, u_k;           // units of q's and of k's rotated channels per token
     int c_q, c_k;           // units of their copied channels (0 in place)
-    int u_copy;             // units of a head's copied channels
+    int u_copy, copy_bytes; // units of a head's copied channels, and their size
 };
 
 // Position of token t of row `row` (see gdn_rotary in include/gdn.h)
@@ -45,9 +45,17 @@ __device__ __forceinline__ int64_t token_position(const RotaryProblem &p, int ro
 }
 
 // cos and sin of 2 pi frac(position * turn / 2^64): the 64-bit product wraps at whole
-// turns, and its upper half as a signed fraction has 32 bits of the remaining angle.
+// turns, and its upper half as a signed fraction has 32 bits of the remaining angle. For
+// 16-bit outputs the hardware's functions on [-pi, pi] are exact enough (absolute error about
+// 2^-21, against a rounding of 2^-9 or 2^-12), and where a token has few heads they are what
+// bounds the kernel (one head of 64: 656 us with sincospif, 64 x 60000 tokens).
+template <bool FAST>
 __device__ __forceinline__ float2 cos_sin(int64_t position, uint64_t turn) {
     const uint64_t phase = (uint64_t)position * turn;
+    if (FAST) {
+        const float a = (float)(int32_t)(phase >> 32) * 1.4629180792671596e-9f;   // 2 pi 2^-32
+        return make_float2(__cosf(a), __sinf(a));
+    }
     float c, s;
     sincospif((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31: in half turns
     return make_float2(c, s);
@@ -68,6 +76,52 @@ constexpr int kBatch = 2;              // units in flight per thread
 constexpr int kBatches = 4;
 constexpr int kTableBytes = 32768;     // cosines and sines of a CTA's tokens
 
+// A head of a token, and the unit u of it, from the index r of a unit among a token's: units_q of them q's, per
+// head `per`.
+template <typename T> struct Head {
+    const T *src;
+    T *dst;
+    int u;
+};
+template <typename T>
+__device__ __forceinline__ Head<T> head_of(const RotaryProblem &p, uint32_t tok, int r, int units_q, int per) {
+    const gdn_rotary_desc &d = p.d;
+    const uint32_t row = tok / (uint32_t)d.T, t = tok - row * d.T;   // tok is below 2^31
+    const bool isk = r >= units_q;
+    if (isk) r -= units_q;
+    const int h = r / per;
+    Head<T> x;
+    x.u = r - h * per;
+    x.src = (const T *)(isk ? p.k : p.q) + row * (isk ? d.k_stride_b : d.q_stride_b) + t * (isk ? d.k_stride_t : d.q_stride_t) +
+            (int64_t)h * d.d;
+    x.dst = (T *)(isk ? p.ko : p.qo) + row * (isk ? d.k_out_stride_b : d.q_out_stride_b) +
+            t * (isk ? d.k_out_stride_t : d.q_out_stride_t) + (int64_t)h * d.d;
+    return x;
+}
+
+// The channels behind the rotated ones, in vectors of R
+template <typename T, typename R>
+__device__ __forceinline__ void copy_rest(const RotaryProblem &p, int64_t tok0, int nt) {
+    constexpr int kB = 4;
+    const int per = p.c_q + p.c_k, total = nt * per, step = kThreads * gridDim.y;
+    for (int i0 = blockIdx.y * kThreads + threadIdx.x; i0 < total; i0 += kB * step) {
+        R v[kB], *to[kB];
+#pragma unroll
+        for (int j = 0; j < kB; ++j) {
+            const int i = i0 + j * step;
+            if (i >= total) continue;
+            const int t = i / per;
+            // without q's copies (q in place) the first of them are k's
+            const Head<T> hd = head_of<T>(p, (uint32_t)(tok0 + t), i - t * per, p.c_q, p.u_copy);
+            v[j] = ((const R *)(hd.src + p.d.rot))[hd.u];
+            to[j] = (R *)(hd.dst + p.d.rot) + hd.u;
+        }
+#pragma unroll
+        for (int j = 0; j < kB; ++j)
+            if (i0 + j * step < total) *to[j] = v[j];
+    }
+}
+
 // V: elements per vector. HALF: a unit is the vectors at u V and rot/2 + u V; else the V elements from u V (two
 // single elements for V = 1).
 template <typename T, int V, bool HALF>
@@ -83,11 +137,11 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
     const int64_t tok0 = (int64_t)blockIdx.x * p.tokens;
     const int nt = (int)min((int64_t)p.tokens, (int64_t)d.B * d.T - tok0);
     const int half = d.rot / 2;
-    const int per = p.u_q + p.u_k + p.c_q + p.c_k;       // units per token
+    const int per = p.u_q + p.u_k;                        // units per token
     const int total = nt * per, step = kThreads * gridDim.y;
     const T *src[kBatch];
     T *dst[kBatch];
-    const float *tb[kBatch];                              // the unit's table entries; null: copy
+    const float *tb[kBatch];                              // the unit's table entries
     Vec<T, V> a[kBatch], b[kBatch];
     auto fetch = [&](int i0) {
 #pragma unroll
@@ -96,19 +150,13 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
             if (i >= total) continue;
             const int t = i / per;
             int r = i - t * per;
-            const uint32_t tok = (uint32_t)(tok0 + t), row = tok / (uint32_t)d.T, tt = tok - row * d.T;   // below 2^31
-            const bool rot = r < p.u_q + p.u_k;
-            if (!rot) r -= p.u_q + p.u_k;
-            const bool isk = r >= (rot ? p.u_q : p.c_q);
-            if (isk) r -= rot ? p.u_q : p.c_q;
-            const int uh = rot ? p.u_rot : p.u_copy, h = r / uh, u = r - h * uh;
-            const int64_t off = (int64_t)h * d.d + (rot ? (HALF ? u * V : u * 2 * NP) : d.rot + u * V);
-            src[j] = (const T *)(isk ? p.k : p.q) + row * (isk ? d.k_stride_b : d.q_stride_b) + tt * (isk ? d.k_stride_t : d.q_stride_t) + off;
-            dst[j] = (T *)(isk ? p.ko : p.qo) + row * (isk ? d.k_out_stride_b : d.q_out_stride_b) +
-                     tt * (isk ? d.k_out_stride_t : d.q_out_stride_t) + off;
-            tb[j] = rot ? tab + (t * 2 * Q * p.u_rot + u) * W : nullptr;
+            const Head<T> hd = head_of<T>(p, (uint32_t)(tok0 + t), r, p.u_q, p.u_rot);
+            const int off = HALF ? hd.u * V : hd.u * 2 * NP;
+            src[j] = hd.src + off;
+            dst[j] = hd.dst + off;
+            tb[j] = tab + (t * 2 * Q * p.u_rot + hd.u) * W;
             a[j].raw = *(const decltype(a[j].raw) *)src[j];
-            if (rot && (HALF || V == 1)) b[j].raw = *(const decltype(b[j].raw) *)(src[j] + (HALF ? half : 1));
+            if (HALF || V == 1) b[j].raw = *(const decltype(b[j].raw) *)(src[j] + (HALF ? half : 1));
         }
     };
     int i0 = blockIdx.y * kThreads + threadIdx.x;
@@ -116,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
     for (int i = threadIdx.x; i < nt * half; i += kThreads) {
         const int t = i / half, pr = i - t * half;
         const uint32_t row = (uint32_t)(tok0 + t) / (uint32_t)d.T;
-        const float2 cs = cos_sin(token_position(p, row, (int)((uint32_t)(tok0 + t) - row * d.T)), p.turns[pr]);
+        const float2 cs = cos_sin<sizeof(T) == 2>(token_position(p, row, (int)((uint32_t)(tok0 + t) - row * d.T)), p.turns[pr]);
         const int u = pr / NP, e = pr % NP;
         float *at = tab + ((t * 2 * Q + e / W) * p.u_rot + u) * W + e % W;
         at[0] = cs.x * d.scale;
@@ -127,10 +175,6 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             if (i0 + j * step >= total) continue;
-            if (tb[j] == nullptr) {
-                *(decltype(a[j].raw) *)dst[j] = a[j].raw;
-                continue;
-            }
             float c[NP], s[NP];
 #pragma unroll
             for (int e = 0; e < NP; e += W) {
@@ -164,14 +208,21 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
             }
         }
     }
+    if (p.c_q + p.c_k == 0) return;
+    switch (p.copy_bytes) {
+    case 16: copy_rest<T, uint4>(p, tok0, nt); break;
+    case 8: copy_rest<T, uint2>(p, tok0, nt); break;
+    case 4: copy_rest<T, uint32_t>(p, tok0, nt); break;
+    default: copy_rest<T, uint16_t>(p, tok0, nt); break;
+    }
 }
 
-// The widest vector that divides the rotated part, the rest of the head, and every base and stride.
-bool fits(const gdn_rotary_desc &d, int v, const void *q, const void *k, const void *qo, const void *ko) {
+// Whether vectors of v elements divide `width` channels (and a head) and fit every base and stride
+bool fits(const RotaryProblem &p, int v, int width) {
+    const gdn_rotary_desc &d = p.d;
     const size_t bytes = v * act_size(d.dtype);
-    const int rot = d.layout == GDN_ROTARY_HALF ? d.rot / 2 : d.rot;
-    if (bytes > 16 || rot % v || d.d % v || (d.rot < d.d && d.rot % v)) return false;
-    const void *ptrs[] = {q, qo, d.Hk ? k : nullptr, d.Hk ? ko : nullptr};
+    if (bytes > 16 || width % v || d.d % v) return false;
+    const void *ptrs[] = {p.q, p.qo, d.Hk ? p.k : nullptr, d.Hk ? p.ko : nullptr};
     const int64_t st[] = {d.q_stride_t, d.q_out_stride_t, d.Hk ? d.k_stride_t : 0, d.Hk ? d.k_out_stride_t : 0};
     const int64_t sb[] = {d.q_stride_b, d.q_out_stride_b, d.Hk ? d.k_stride_b : 0, d.Hk ? d.k_out_stride_b : 0};
     for (int i = 0; i < 4; ++i)
@@ -185,7 +236,10 @@ cudaError_t launch_rotary(RotaryProblem p, cudaStream_t s) {
     const gdn_rotary_desc &d = p.d;
     const int64_t ntok = (int64_t)d.B * d.T;
     p.u_rot = d.rot / 2 / NP;
-    p.u_copy = (d.d - d.rot) / V;
+    int vc = 16 / (int)sizeof(T);   // a head's start, the rotated part and the rest: multiples of the copy's vector
+    while (vc > 1 && !fits(p, vc, d.rot)) vc /= 2;
+    p.copy_bytes = vc * (int)sizeof(T);
+    p.u_copy = (d.d - d.rot) / vc;
     p.u_q = d.Hq * p.u_rot;
     p.u_k = d.Hk * p.u_rot;
     p.c_q = p.q == p.qo ? 0 : d.Hq * p.u_copy;
@@ -211,7 +265,8 @@ cudaError_t launch_rotary(RotaryProblem p, cudaStream_t s) {
 
 template <typename T, bool HALF>
 cudaError_t launch_by_vector(const RotaryProblem &p, cudaStream_t s) {
-    const auto can = [&](int v) { return fits(p.d, v, p.q, p.k, p.qo, p.ko); };
+    const int width = HALF ? p.d.rot / 2 : p.d.rot;
+    const auto can = [&](int v) { return fits(p, v, width); };
     if constexpr (sizeof(T) == 2)
         if (can(8)) return launch_rotary<T, 8, HALF>(p, s);
     if (can(4)) return launch_rotary<T, 4, HALF>(p, s);
