@@ -161,14 +161,25 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
     };
     int i0 = blockIdx.y * kThreads + threadIdx.x;
     fetch(i0);   // on their way while the table is computed
-    for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-        const int t = i / half, pr = i - t * half;
+    // a thread keeps its pair where the pairs fit the block, and steps over the tokens
+    int t = 0, pr0 = threadIdx.x, tstep = 1, pstep = kThreads;
+    if (half <= kThreads) {
+        tstep = kThreads / half;
+        t = threadIdx.x / half;
+        pr0 -= t * half;
+        pstep = half;
+        if (t >= tstep) t = nt;
+    }
+    for (; t < nt; t += tstep) {
         const uint32_t row = (uint32_t)(tok0 + t) / (uint32_t)d.T;
-        const float2 cs = cos_sin<sizeof(T) == 2>(token_position(p, row, (int)((uint32_t)(tok0 + t) - row * d.T)), p.turns[pr]);
-        const int u = pr / NP, e = pr % NP;
-        float *at = tab + ((t * 2 * Q + e / W) * p.u_rot + u) * W + e % W;
-        at[0] = cs.x * d.scale;
-        at[Q * p.u_rot * W] = cs.y * (d.inverse ? -d.scale : d.scale);
+        const int64_t position = token_position(p, row, (int)((uint32_t)(tok0 + t) - row * d.T));
+        for (int pr = pr0; pr < half; pr += pstep) {
+            const float2 cs = cos_sin<sizeof(T) == 2>(position, p.turns[pr]);
+            const int u = pr / NP, e = pr % NP;
+            float *at = tab + ((t * 2 * Q + e / W) * p.u_rot + u) * W + e % W;
+            at[0] = cs.x * d.scale;
+            at[Q * p.u_rot * W] = cs.y * (d.inverse ? -d.scale : d.scale);
+        }
     }
     __syncthreads();
     for (; i0 < total; i0 += kBatch * step, fetch(i0)) {
