@@ -428,8 +428,8 @@ int gdn_backward(const gdn_desc *d,
 #define GDN_RECURRENCE_CHUNK 4 /* tokens between two rows of chunk_states */
 
 typedef struct {
-    int32_t B, T;        /* batch rows, tokens per row; with cu_seqlens: B = 1 and
-                            T = total packed tokens */
+    int32_t B, T;        /* batch rows, tokens per row (at most 2^31 - 2^16); with
+                            cu_seqlens: B = 1 and T = total packed tokens */
     int32_t N;           /* sequences: B without cu_seqlens, else cu_seqlens has N+1 entries */
     int32_t D;           /* channels */
     int32_t dtype;       /* gdn_dtype of x, a, b, out and their gradients */
@@ -583,7 +583,8 @@ int gdn_rotary(const gdn_rotary_desc *d, const void *q, const void *k, const uin
 typedef enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 } gdn_activation;
 
 typedef struct {
-    int32_t N, L;          /* instances, positions per instance (either may be 0) */
+    int32_t N, L;          /* instances, positions per instance (either may be 0; L at
+                              most 2^31 - 2^16) */
     int32_t C, G;          /* channels (at most 2^24), groups (C % G == 0) */
     int32_t dtype;         /* gdn_dtype of x, out, grad_out, dx */
     int32_t weight_dtype;  /* of weight and bias: dtype, or GDN_F32 */

@@ -898,7 +898,7 @@ int check_desc(const gdn_group_norm_desc *d) {
     if (!dtype_ok(d->dtype) || (d->weight_dtype != d->dtype && d->weight_dtype != GDN_F32)) return GDN_ERR_UNSUPPORTED;
     if (!(d->eps >= 0.f) || d->x_stride_n < 0 || d->x_stride_l < 0) return GDN_ERR_INVALID_ARG;
     if (d->L > 1 && d->x_stride_l < d->C) return GDN_ERR_INVALID_ARG;
-    if (d->C > (1 << 24)) return GDN_ERR_UNSUPPORTED;
+    if (d->C > (1 << 24) || d->L > 0x7fff0000) return GDN_ERR_UNSUPPORTED;   // 32-bit loops over both
     if ((double)d->N * d->L * d->C > 4.0e12 || (int64_t)d->N * d->G > 0x7fffffff) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }

@@ -325,6 +325,19 @@ __device__ void copy_empty(const RecProblem &p, int row, int ch, int nc, float *
     }
 }
 
+// Without TMA: R tokens by four channels of a tensor, element by element, zeros where there is nothing. The loads
+// of the next tile are issued while this one is worked on.
+template <typename T, int R>
+__device__ __forceinline__ void fetch_elements(T (&v)[R][4], const T *p, int64_t stride, int tokens, int nc) {
+#pragma unroll
+    for (int r = 0; r < R; ++r, p += stride)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[r][c] = r < tokens && c < nc ? p[c] : from_f<T>(0.f);
+}
+template <typename T> __device__ __forceinline__ F4 of_elements(const T (&v)[4]) {
+    return {make_float2(to_f<T>(v[0]), to_f<T>(v[1])), make_float2(to_f<T>(v[2]), to_f<T>(v[3]))};
+}
+
 // exp(A_log) and dt_bias log2(e) of four channels
 __device__ __forceinline__ void channel_params(const RecProblem &p, int ch, int nc, float2 (&rate)[2], float2 (&bias2)[2]) {
     const F4 l = load_words(p.A_log + ch, nc), b = load_words(p.dt_bias + ch, nc);
@@ -334,12 +347,10 @@ __device__ __forceinline__ void channel_params(const RecProblem &p, int ch, int 
     bias2[1] = mul2(b.hi, splat2(kLog2e));
 }
 
-// Bound by HBM (8 bytes per 16-bit element) and, near it, by the special-function and issue rates: about
-// 30 instructions and 5 special functions per element.
 // While the carry of tile k - 1 travels, the compute warps work on tile k: its decays and writes need only the
 // inputs. Bound by HBM (8 bytes per 16-bit element) and, near it, by the issue rate.
 template <typename T, bool TMA, bool PACKED>
-__global__ void __launch_bounds__(FwdTile<T>::THREADS, sizeof(T) == 2 ? 3 : 2)
+__global__ void __launch_bounds__(FwdTile<T>::THREADS, sizeof(T) == 2 && TMA ? 3 : 2)
 rec_forward_kernel(const __grid_constant__ RecProblem p, const __grid_constant__ RecMaps maps) {
     using L = FwdTile<T>;
     constexpr int kR = L::R;
@@ -393,14 +404,23 @@ rec_forward_kernel(const __grid_constant__ RecProblem p, const __grid_constant__
         seq.init(p, row);
         seq_out.init(p, row);
 
+        T ea[kR][4], eb[kR][4], ex[kR][4];   // without TMA: the next tile's elements
+        auto fetch = [&](int k) {
+            const int tile = k * (int)cs + (int)rank, t0 = tile * L::TT + tg;
+            if (TMA || tile >= p.ntiles) return;
+            fetch_elements<T, kR>(ea, (const T *)p.a + row * d.a_stride_b + t0 * d.a_stride_t + ch, d.a_stride_t, d.T - t0, nc);
+            fetch_elements<T, kR>(eb, (const T *)p.b + row * d.b_stride_b + t0 * d.b_stride_t + ch, d.b_stride_t, d.T - t0, nc);
+            fetch_elements<T, kR>(ex, (const T *)p.x + row * d.x_stride_b + t0 * d.x_stride_t + ch, d.x_stride_t, d.T - t0, nc);
+        };
+        fetch(0);
         // decay products P and local values h of tile k's tokens, and the map to the carry warp
         auto begin = [&](int k, F4 (&P)[kR], F4 (&h)[kR], F4 &eA, F4 &eB) {
             const int tile = k * (int)cs + (int)rank, t0 = tile * L::TT + tg;
             if (tile < p.ntiles) {
-                auto in = [&](int which, const void *base, int64_t sb, int64_t st, int r) -> F4 {
+                auto in = [&](int which, const T (&e)[kR][4], int r) -> F4 {
                     if (TMA)
                         return unpack4<T>(smem + (k % L::STAGES * 3 + which) * L::kTensor + (tg + r) * 128 + q * 4 * sizeof(T));
-                    return load_row<T, false>((const T *)base + row * sb + (int64_t)(t0 + r) * st + ch, t0 + r < d.T ? nc : 0);
+                    return of_elements<T>(e[r]);
                 };
                 if (TMA) bounded_wait(&chain.full[k % L::STAGES], (k / L::STAGES) & 1, p.wait_immediate, failed);
                 if (PACKED) seq.up_to(p, t0);
@@ -410,18 +430,19 @@ rec_forward_kernel(const __grid_constant__ RecProblem p, const __grid_constant__
                     float2 z[2 * kB], t[2 * kB], Y[2 * kB], al[2 * kB], em[2 * kB];
 #pragma unroll
                     for (int r = 0; r < kB; ++r) {
-                        const F4 a = in(0, p.a, d.a_stride_b, d.a_stride_t, r0 + r);
+                        const F4 a = in(0, ea, r0 + r);
                         z[2 * r] = a.lo;
                         z[2 * r + 1] = a.hi;
                     }
                     decays<2 * kB, 2>(C, z, bias2, rate, t, Y, al, em);
 #pragma unroll
                     for (int r = 0; r < kB; ++r) {
-                        const F4 b = in(1, p.b, d.b_stride_b, d.b_stride_t, r0 + r), x = in(2, p.x, d.x_stride_b, d.x_stride_t, r0 + r);
+                        const F4 b = in(1, eb, r0 + r), x = in(2, ex, r0 + r);
                         P[r0 + r] = {al[2 * r], al[2 * r + 1]};
                         h[r0 + r] = mul4({write_scale2(C, em[2 * r], al[2 * r], b.lo), write_scale2(C, em[2 * r + 1], al[2 * r + 1], b.hi)}, x);
                     }
                 }
+                fetch(k + 1);
                 if (seq.b0 == t0 || (PACKED && seq.b1 < t0 + kR && seq.b1 < d.T)) {   // a sequence starts here
                     Seq m = seq;
 #pragma unroll
@@ -505,7 +526,7 @@ rec_forward_kernel(const __grid_constant__ RecProblem p, const __grid_constant__
 // The reverse walk: c_t = alpha_t (v_t + c_{t+1}), delta_t = v_t + c_{t+1} with v = grad_out, tiles last to
 // first. The states before every 4th token come from the forward, so h_{t-1} is recomputed within a thread.
 template <typename T, bool TMA, bool PACKED>
-__global__ void __launch_bounds__(BwdTile<T>::THREADS, sizeof(T) == 2 ? 3 : 2)
+__global__ void __launch_bounds__(BwdTile<T>::THREADS, sizeof(T) == 2 && TMA ? 3 : 2)
 rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant__ RecMaps maps) {
     using L = BwdTile<T>;
     constexpr int kR = L::R;
@@ -567,12 +588,25 @@ rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant_
         // sums of da and of dg g over this thread's tokens: over 16 tiles, over all
         F4 sA[2] = {f4(0.f), f4(0.f)}, sb[2] = {f4(0.f), f4(0.f)};
 
+        T ea[kR][4], ey[kR][4], ex[kR][4], eb[kR][4];   // without TMA: the next tile's a and grad_out, this one's x and b
         auto tile_of = [&](int k) { return p.ntiles - 1 - (k * (int)cs + (int)rank); };
-        auto in = [&](int k, int which, const void *base, int64_t sb_, int64_t st_, int r) -> F4 {
-            const int t0 = tile_of(k) * L::TT + tg;
+        auto in = [&](int k, int which, const T (&e)[kR][4], int r) -> F4 {
             if (TMA) return unpack4<T>(smem + (k % L::STAGES * 4 + which) * L::kTensor + (tg + r) * 128 + q * 4 * sizeof(T));
-            return load_row<T, false>((const T *)base + row * sb_ + (int64_t)(t0 + r) * st_ + ch, t0 + r < d.T ? nc : 0);
+            return of_elements<T>(e[r]);
         };
+        auto fetch_ay = [&](int k) {
+            const int tile = tile_of(k), t0 = tile * L::TT + tg;
+            if (TMA || tile < 0) return;
+            fetch_elements<T, kR>(ea, (const T *)p.a + row * d.a_stride_b + t0 * d.a_stride_t + ch, d.a_stride_t, d.T - t0, nc);
+            fetch_elements<T, kR>(ey, (const T *)p.grad_out + ((int64_t)row * d.T + t0) * d.D + ch, d.D, d.T - t0, nc);
+        };
+        auto fetch_xb = [&](int k) {
+            const int tile = tile_of(k), t0 = tile * L::TT + tg;
+            if (TMA || tile < 0) return;
+            fetch_elements<T, kR>(ex, (const T *)p.x + row * d.x_stride_b + t0 * d.x_stride_t + ch, d.x_stride_t, d.T - t0, nc);
+            fetch_elements<T, kR>(eb, (const T *)p.b + row * d.b_stride_b + t0 * d.b_stride_t + ch, d.b_stride_t, d.T - t0, nc);
+        };
+        fetch_ay(0);
         // Between begin and finish a thread keeps three values per token and channel in its own slots of shared
         // memory: em, Y and rate sigmoid(z) (half of the work of recomputing them).
         float4 *stash = (float4 *)(smem + (TMA ? L::STAGES * 4 * L::kTensor : 0)) + tid;
@@ -587,7 +621,7 @@ rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant_
                 float2 z[2 * kR], t[2 * kR], Y[2 * kR], av[2 * kR], em[2 * kR];
 #pragma unroll
                 for (int r = 0; r < kR; ++r) {
-                    const F4 a = in(k, 1, p.a, d.a_stride_b, d.a_stride_t, r);
+                    const F4 a = in(k, 1, ea, r);
                     z[2 * r] = a.lo;
                     z[2 * r + 1] = a.hi;
                 }
@@ -600,8 +634,10 @@ rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant_
                     stash[(3 * r + 1) * kSlot] = to4({Y[2 * r], Y[2 * r + 1]});
                     stash[(3 * r + 2) * kSlot] = to4({s0, s1});
                     al[r] = {av[2 * r], av[2 * r + 1]};
-                    v[r] = in(k, 3, p.grad_out, (int64_t)d.T * d.D, d.D, r);
+                    v[r] = in(k, 3, ey, r);
                 }
+                fetch_xb(k);
+                fetch_ay(k + 1);
                 if (t0 < d.T) {
                     if (PACKED) seq.down_to(p, t0);
                     if (seq.b0 == t0 || seq.b1 <= t0 + kR) {   // a sequence starts or ends here
@@ -647,7 +683,7 @@ rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant_
                 const bool whole = nc == 4 && t0 + kR <= d.T;
 #pragma unroll
                 for (int r = 0; r < kR; ++r) {
-                    const F4 x = in(k, 0, p.x, d.x_stride_b, d.x_stride_t, r), b = in(k, 2, p.b, d.b_stride_b, d.b_stride_t, r);
+                    const F4 x = in(k, 0, ex, r), b = in(k, 2, eb, r);
                     const F4 em = f4(stash[(3 * r) * kSlot]), Y = f4(stash[(3 * r + 1) * kSlot]), rsg = f4(stash[(3 * r + 2) * kSlot]);
                     if (starts >> r & 1) {   // the decay itself again, the state before, and the state's gradient
                         al[r] = {decay_of(em.lo, Y.lo), decay_of(em.hi, Y.hi)};
@@ -827,14 +863,14 @@ template <typename T>
 cudaError_t launch_forward(RecProblem p, cudaStream_t s) {
     using L = FwdTile<T>;
     const gdn_recurrence_desc &d = p.d;
-    const RecPlan pl = make_plan<L>(d, sizeof(T) == 2 ? 3 : 2);
-    p.slabs = pl.slabs;
-    p.ntiles = pl.ntiles;
     RecMaps m;
     memset(&m, 0, sizeof(m));
     const bool tma = d.T > 0 && (d.D * sizeof(T)) % 16 == 0 && ptr_aligned(p.out, 16) && ptr_aligned(p.cs, 16) &&
                      tma_ok(d, p.x, d.x_stride_b, d.x_stride_t) && tma_ok(d, p.a, d.a_stride_b, d.a_stride_t) &&
                      tma_ok(d, p.b, d.b_stride_b, d.b_stride_t);
+    const RecPlan pl = make_plan<L>(d, sizeof(T) == 2 && tma ? 3 : 2);
+    p.slabs = pl.slabs;
+    p.ntiles = pl.ntiles;
     if (tma && (!tma_map<L>(&m.x, d, p.x, d.x_stride_b, d.x_stride_t) || !tma_map<L>(&m.a, d, p.a, d.a_stride_b, d.a_stride_t) ||
                 !tma_map<L>(&m.b, d, p.b, d.b_stride_b, d.b_stride_t)))
         return cudaErrorInvalidValue;
@@ -847,14 +883,14 @@ template <typename T>
 cudaError_t launch_backward_rec(RecProblem p, cudaStream_t s) {
     using L = BwdTile<T>;
     const gdn_recurrence_desc &d = p.d;
-    const RecPlan pl = make_plan<L>(d, sizeof(T) == 2 ? 3 : 2);
-    p.slabs = pl.slabs;
-    p.ntiles = pl.ntiles;
     RecMaps m;
     memset(&m, 0, sizeof(m));
     const bool tma = d.T > 0 && (d.D * sizeof(T)) % 16 == 0 && ptr_aligned(p.dx, 16) && ptr_aligned(p.da, 16) &&
                      ptr_aligned(p.db, 16) && ptr_aligned(p.grad_out, 16) && tma_ok(d, p.x, d.x_stride_b, d.x_stride_t) &&
                      tma_ok(d, p.a, d.a_stride_b, d.a_stride_t) && tma_ok(d, p.b, d.b_stride_b, d.b_stride_t);
+    const RecPlan pl = make_plan<L>(d, sizeof(T) == 2 && tma ? 3 : 2);
+    p.slabs = pl.slabs;
+    p.ntiles = pl.ntiles;
     if (tma && (!tma_map<L>(&m.x, d, p.x, d.x_stride_b, d.x_stride_t) || !tma_map<L>(&m.a, d, p.a, d.a_stride_b, d.a_stride_t) ||
                 !tma_map<L>(&m.b, d, p.b, d.b_stride_b, d.b_stride_t) || !tma_map<L>(&m.dy, d, p.grad_out, (int64_t)d.T * d.D, d.D)))
         return cudaErrorInvalidValue;
@@ -878,6 +914,7 @@ int by_dtype(int dtype, F &&f) {
 int check_desc(const gdn_recurrence_desc *d, bool packed) {
     if (!d) return GDN_ERR_INVALID_ARG;
     if (d->B < 1 || d->T < 0 || d->N < 1 || d->D < 1) return GDN_ERR_INVALID_ARG;
+    if (d->T > 0x7fff0000) return GDN_ERR_UNSUPPORTED;   // tile arithmetic in 32 bits
     if (packed ? d->B != 1 : d->N != d->B) return GDN_ERR_INVALID_ARG;
     if (!dtype_ok(d->dtype)) return GDN_ERR_UNSUPPORTED;
     const int64_t strides[] = {d->x_stride_b, d->x_stride_t, d->a_stride_b, d->a_stride_t, d->b_stride_b, d->b_stride_t};
