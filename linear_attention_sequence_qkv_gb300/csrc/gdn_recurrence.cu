@@ -807,11 +807,17 @@ __global__ void __launch_bounds__(128) rec_step_kernel(const RecProblem p, float
 }
 
 // ===================================================================== host
-// CTAs per chain: as many as fill the chip once at per_sm CTAs per SM, of those that have a tile.
+// CTAs per chain. With few chains a step's latency is what counts (0.9 us, forward), so a chain takes as many CTAs
+// as it can while all clusters are resident: a cluster stays within one of the chip's 8 processing clusters of up
+// to 20 SMs, which leaves room for 12 clusters of 16, 20 of 12, 28 of 10. With its gradient over 32768 bf16 tokens:
+//     4 chains  16 CTAs 221 us, 12 277, 8 386        20 chains  12 CTAs 366 us, 16 461, 8 490
+//    12 chains  16 CTAs 274 us, 12 342, 8 406        28 chains  10 CTAs 452 us, 12 607, 8 513
+// With more chains, as many as fill the chip once at per_sm CTAs per SM; clusters of 7 fit no better than those
+// of 8 (59 against 51 at 3 CTAs per SM), so 6 (74) serves for both.
 int cluster_size(int64_t chains, int64_t ntiles, int per_sm) {
-    int64_t fill = (int64_t)per_sm * kSms / chains;
-    if (fill > 6) fill = fill < 8 ? 6 : 8;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({fill, ntiles, kMaxCluster}));
+    int64_t cs = chains <= 12 ? kMaxCluster : chains <= 20 ? 12 : chains <= 28 ? 10 : (int64_t)per_sm * kSms / chains;
+    if (chains > 28 && cs > 6) cs = cs < 8 ? 6 : 8;
+    return (int)std::max<int64_t>(1, std::min<int64_t>({cs, ntiles, kMaxCluster}));
 }
 
 struct RecPlan {
