@@ -322,7 +322,7 @@ template <int N> struct ParamSums {
 };
 
 template <typename T, int V, int NV, int ACT, int LG>
-__global__ void __launch_bounds__(kThreads, NV == 1 ? kBlocksBackward : 1) norm_rows_backward(const __grid_constant__ NormProblem p) {
+__global__ void __launch_bounds__(kThreads, NV == 1 || V == 1 ? kBlocksBackward : 1) norm_rows_backward(const __grid_constant__ NormProblem p) {
     const gdn_group_norm_desc &d = p.d;
     const Place q = place<V>(p);
     pdl_trigger();
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? kBlocksBackward : 1) norm_
     constexpr int kSteps = V > 1 ? kAheadBackward / NV : 1;
     extern __shared__ uint4 ring_smem[];
     const RowRing<2, NV, kSteps> ring(ring_smem);
-    T single[2][NV];
+    T single[2][NV] = {};   // element by element: the next row's
     auto fetch = [&](int j, int64_t n) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
@@ -361,9 +361,8 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? kBlocksBackward : 1) norm_
     auto stats = [&](int64_t n) {
         return n < p.items ? make_float2(p.mean[n * d.G + q.g], p.rstd[n * d.G + q.g]) : make_float2(0.f, 0.f);
     };
-    if (V > 1)
 #pragma unroll
-        for (int j = 0; j < kSteps; ++j) fetch(j, q.slice + (int64_t)j * p.slices);
+    for (int j = 0; j < kSteps; ++j) fetch(j, q.slice + (int64_t)j * p.slices);
     float2 st0 = stats(q.slice), st1 = stats(q.slice + (int64_t)p.slices);
     int j = 0;
     for (int64_t n = q.slice; n < p.items; n += p.slices) {
@@ -372,7 +371,6 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? kBlocksBackward : 1) norm_
         st0 = st1;
         st1 = st2;
         if (V > 1) ring.wait_oldest();
-        else fetch(0, n);
         float2 x[NV][NP], y[NV][NP], s1 = splat2(0.f), s2 = splat2(0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -395,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? kBlocksBackward : 1) norm_
                 s2 = fma2(g.t, g.xh, s2);
             }
         }
+        if (V == 1) fetch(0, n + p.slices);
         sums.row_done();
         const float m1 = lane_sum_t<LG>(total<V>(s1), p.lg) * inv, m2 = lane_sum_t<LG>(total<V>(s2), p.lg) * inv;
         if (V > 1) {   // this row's slots have been read
