@@ -32,11 +32,13 @@ struct NormProblem {
     void *out, *dx;
     float *mean, *rstd, *dw, *db;
     float2 *stat;      // general: [item][part] partial (mean, centred sum of squares), or (sum t, sum t xh)
-    float *part;       // [slices][2][C] partial sums of dweight, dbias
+    float *part;       // [part_rows][2][C] partial sums of dweight, dbias
     int lg;            // lanes per group or slab; kThreads: a block per group
     int sets;          // sets of channels, one per warp
     int slabs;         // slabs per group (1 where a warp holds whole groups)
     int slices;        // warps that share a set
+    int by_block;      // general backward: the warps of a block share a set, and write one partial row
+    int part_rows;
     int chunks, chunk_rows;   // general: chunks of positions per instance
     int64_t items;     // rows, or (instance, chunk) pairs
 };
@@ -134,6 +136,10 @@ __device__ __forceinline__ Place place(const NormProblem &p) {
     }
     q.set = w % p.sets;
     q.slice = w / p.sets;
+    if (p.by_block) {
+        q.set = blockIdx.x % p.sets;
+        q.slice = blockIdx.x / p.sets * kWarps + threadIdx.x / 32;
+    }
     q.sub = lane % p.lg;
     int in;                // the lane's first element within the group
     if (p.slabs == 1) {
@@ -143,7 +149,7 @@ __device__ __forceinline__ Place place(const NormProblem &p) {
         q.g = q.set / p.slabs;
         in = (q.set % p.slabs * 32 + lane) * V;
     }
-    q.any = q.slice < p.slices && q.g < p.d.G && in < cg;
+    q.any = (p.by_block || q.slice < p.slices) && q.g < p.d.G && in < cg;
     if (q.g >= p.d.G) q.g = p.d.G - 1;
     q.c = q.g * cg + in;
     return q;
@@ -609,11 +615,10 @@ __global__ void __launch_bounds__(kThreads) norm_sums_kernel(const __grid_consta
     const Place q = place<V>(p);
     constexpr int NP = kPairs<V>;
     pdl_trigger();
-    if (q.slice >= p.slices) return;
     float2 w[NP], b[NP];
     load_params<T, V>(p, q.any, q.c, w, b);
     ParamSums<NP> sums;
-    for (int64_t it = q.slice; it < p.items; it += p.slices) {
+    for (int64_t it = q.slice; it < (q.slice < p.slices ? p.items : 0); it += p.slices) {
         int64_t n;
         int l0, l1;
         item_rows(p, it, n, l0, l1);
@@ -648,7 +653,28 @@ __global__ void __launch_bounds__(kThreads) norm_sums_kernel(const __grid_consta
         const float t1 = lane_sum(total<V>(s1), p.lg), t2 = lane_sum(total<V>(s2), p.lg);
         if (q.any && q.sub == 0) p.stat[stat_at(p, it, q)] = make_float2(t1, t2);
     }
-    if (q.any) sums.template write<V>(p, q.slice, q.c, 0);
+    if (!p.by_block) {
+        if (q.any) sums.template write<V>(p, q.slice, q.c, 0);
+        return;
+    }
+    // the block's warps hold the same channels: warp i sums pair i over them
+    __shared__ float2 red[kWarps][2 * NP][32];
+    static_assert(2 * NP <= kWarps, "a warp per pair");
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+#pragma unroll
+    for (int e = 0; e < NP; ++e) {
+        red[warp][e][lane] = add2(sums.w[1][e], sums.w[0][e]);
+        red[warp][NP + e][lane] = add2(sums.b[1][e], sums.b[0][e]);
+    }
+    __syncthreads();
+    if (warp < 2 * NP && q.any) {
+        float2 t = splat2(0.f);
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) t = add2(t, red[i][warp][lane]);
+        float *to = p.part + ((int64_t)(blockIdx.x / p.sets) * 2 + warp / NP) * d.C + q.c + warp % NP * 2;
+        to[0] = t.x;
+        if (V > 1) to[1] = t.y;
+    }
 }
 
 // A programmatic dependent of norm_sums_kernel
@@ -705,7 +731,7 @@ __global__ void __launch_bounds__(kThreads) norm_dx_kernel(const __grid_constant
     pdl_trigger();
 }
 
-// dweight and dbias from part[slices][2][C]: 32 channels a block, 32 strided partial sums each. A
+// dweight and dbias from part[part_rows][2][C]: 32 channels a block, 32 strided partial sums each. A
 // programmatic dependent of the kernel before it.
 constexpr int kParamThreads = 1024;
 __global__ void __launch_bounds__(kParamThreads) norm_params_kernel(const __grid_constant__ NormProblem p) {
@@ -715,7 +741,7 @@ __global__ void __launch_bounds__(kParamThreads) norm_params_kernel(const __grid
     pdl_wait();
     if (c < p.d.C)
 #pragma unroll 4
-        for (int i = s; i < p.slices; i += 32) {
+        for (int i = s; i < p.part_rows; i += 32) {
             v[0] += p.part[((int64_t)i * 2) * p.d.C + c];
             v[1] += p.part[((int64_t)i * 2 + 1) * p.d.C + c];
         }
@@ -734,7 +760,7 @@ __global__ void __launch_bounds__(kParamThreads) norm_params_kernel(const __grid
 // Which form serves a problem, and its launch: a function of sizes and alignment alone. `general` also
 // bounds the workspace, whatever the alignment of a later call.
 struct Plan {
-    bool rows;
+    bool rows, by_block;
     int v, nv, lg, sets, slabs, slices, chunks, chunk_rows;
     int64_t items;
 };
@@ -772,8 +798,12 @@ Plan make_plan(const gdn_group_norm_desc &d, int v, bool backward) {
     const int64_t teams = (int64_t)kSms * (!r.rows ? kBlocksGeneral : !backward ? kBlocksForward : kBlocksBackward) *
                           (r.lg == kThreads ? 1 : kWarps);
     r.slices = (int)std::max<int64_t>(1, std::min<int64_t>(teams / r.sets, r.items));
+    // With eight slices or more, a block of one set: an eighth of the partial rows, which weigh as much as the tensors
+    // where there are few sets (2 x 2048 x 1536 in 6 groups: 810 rows of 12 KB, against 12.6 MB each of x and grad_out)
+    r.by_block = backward && !r.rows && r.slices >= kWarps;
     return r;
 }
+int part_rows(const Plan &pl) { return pl.by_block ? (int)cdiv64(pl.slices, kWarps) : pl.slices; }
 int vector_of(const gdn_group_norm_desc &d) { return 16 / (int)act_size(d.dtype); }
 bool vectors_fit(const gdn_group_norm_desc &d, const void *x, const void *dy, const void *out) {
     const int v = vector_of(d);
@@ -783,7 +813,7 @@ bool vectors_fit(const gdn_group_norm_desc &d, const void *x, const void *dy, co
 size_t stat_bytes(const gdn_group_norm_desc &d, const Plan &pl) {
     return pl.rows ? 0 : align_up((size_t)pl.items * d.G * pl.slabs * sizeof(float2), 256);
 }
-size_t part_bytes(const gdn_group_norm_desc &d, const Plan &pl) { return align_up((size_t)pl.slices * 2 * d.C * 4, 256); }
+size_t part_bytes(const gdn_group_norm_desc &d, const Plan &pl) { return align_up((size_t)part_rows(pl) * 2 * d.C * 4, 256); }
 // both vector widths, since a call's alignment decides
 size_t workspace_need(const gdn_group_norm_desc &d, bool backward) {
     size_t most = 0;
@@ -801,6 +831,8 @@ void apply_plan(NormProblem &p, const Plan &pl, void *ws, bool backward) {
     p.sets = pl.sets;
     p.slabs = pl.slabs;
     p.slices = pl.slices;
+    p.by_block = pl.by_block;
+    p.part_rows = part_rows(pl);
     p.chunks = pl.chunks;
     p.chunk_rows = pl.chunk_rows;
     p.items = pl.items;
@@ -809,6 +841,7 @@ void apply_plan(NormProblem &p, const Plan &pl, void *ws, bool backward) {
     if (backward) p.part = (float *)(w + stat_bytes(p.d, pl));
 }
 unsigned grid_of(const Plan &pl) {
+    if (pl.by_block) return (unsigned)(pl.sets * part_rows(pl));
     return (unsigned)cdiv64((int64_t)pl.sets * pl.slices, pl.lg == kThreads ? 1 : kWarps);
 }
 
