@@ -44,7 +44,10 @@ struct NormProblem {
 };
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kBlocksForward = 3, kBlocksBackward = 2, kBlocksGeneral = 4;   // per SM, resident at once
+// Blocks per SM, resident at once: rows forward and backward, general forward and backward. Three for the last is
+// slower (2 x 2048 x 1536 in 6 groups 24.9 against 20.7 us, 60 x 2000 x 2048 in 16 540 against 464 us): registers
+// hold two.
+constexpr int kBlocksForward = 3, kBlocksBackward = 2, kBlocksGeneral = 4, kBlocksSums = 2;
 constexpr int kRowsForward = 2;   // rows a warp works on at a time (two reductions in flight); as many are on their way
 constexpr int kAheadBackward = 6; // rows on their way in the backward
 constexpr int kBatch = 8, kBatchBackward = 4;   // rows in flight per warp in the general form
@@ -787,17 +790,26 @@ Plan make_plan(const gdn_group_norm_desc &d, int v, bool backward) {
     if (!r.rows) r.lg = std::min(32, pow2_at_least(cgv));
     r.slabs = r.rows ? 1 : (int)cdiv64(cgv, r.lg);
     r.sets = r.lg == kThreads ? d.G : r.slabs == 1 ? (int)cdiv64(d.G, 32 / r.lg) : d.G * r.slabs;
+    const int64_t per_sm = !r.rows ? (backward ? kBlocksSums : kBlocksGeneral) : !backward ? kBlocksForward : kBlocksBackward;
+    const int64_t teams = std::max<int64_t>(1, kSms * per_sm * (r.lg == kThreads ? 1 : kWarps) / r.sets);   // that share a set
     r.chunks = 1;
-    if (!r.rows) {   // enough chunks of positions to fill the chip, of at least a batch each
-        const int64_t want = cdiv64((int64_t)kSms * kBlocksGeneral * kWarps, std::max<int64_t>(1, (int64_t)d.N * r.sets));
-        r.chunks = (int)std::max<int64_t>(1, std::min<int64_t>(want, d.L / kBatch));
+    r.chunk_rows = d.L;
+    if (!r.rows && d.L > 1) {
+        // Chunks of positions, of at least a batch each: as many as give every team k of them, for the k (1 to 8) that
+        // keeps the busiest team's positions fewest; a chunk costs about four more (its partials, its last batch).
+        int64_t least = INT64_MAX;
+        for (int k = 1; k <= 8; ++k) {
+            const int64_t want = std::max<int64_t>(1, std::min<int64_t>(k * teams / std::max(1, d.N), d.L / kBatch));
+            const int64_t rows = cdiv64(d.L, want), chunks = cdiv64(d.L, rows);
+            const int64_t cost = cdiv64(d.N * chunks, teams) * (rows + 4);
+            if (cost >= least) continue;
+            least = cost;
+            r.chunks = (int)chunks;
+            r.chunk_rows = (int)rows;
+        }
     }
-    r.chunk_rows = (int)cdiv64(d.L, r.chunks);
-    r.chunks = (int)cdiv64(d.L, std::max(1, r.chunk_rows));
     r.items = (int64_t)d.N * r.chunks;
-    const int64_t teams = (int64_t)kSms * (!r.rows ? kBlocksGeneral : !backward ? kBlocksForward : kBlocksBackward) *
-                          (r.lg == kThreads ? 1 : kWarps);
-    r.slices = (int)std::max<int64_t>(1, std::min<int64_t>(teams / r.sets, r.items));
+    r.slices = (int)std::max<int64_t>(1, std::min<int64_t>(teams, r.items));
     // With eight slices or more, a block of one set: an eighth of the partial rows, which weigh as much as the tensors
     // where there are few sets (2 x 2048 x 1536 in 6 groups: 810 rows of 12 KB, against 12.6 MB each of x and grad_out)
     r.by_block = backward && !r.rows && r.slices >= kWarps;
