@@ -431,7 +431,7 @@ typedef struct {
     int32_t B, T;        /* batch rows, tokens per row (at most 2^31 - 2^16); with
                             cu_seqlens: B = 1 and T = total packed tokens */
     int32_t N;           /* sequences: B without cu_seqlens, else cu_seqlens has N+1 entries */
-    int32_t D;           /* channels */
+    int32_t D;           /* channels (at most 2^30) */
     int32_t dtype;       /* gdn_dtype of x, a, b, out and their gradients */
     int32_t reserved0;
     /* (batch, token) element strides; channel stride is 1 */

@@ -176,3 +176,16 @@ def test_gradient_against_differences(dev):
             ends.append((n64(gdn.group_norm_forward(*moved, groups=3).out) * n64(dy)).sum())
         diff, want = (ends[0] - ends[1]) / (2 * step), (n64(grad) * n64(v)).sum()
         assert abs(diff - want) <= 2e-2 * np.linalg.norm(n64(grad)), i
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("N,L,C,G", [(3, 1, 1032, 1), (2, 1, 4112, 2), (2, 1, 1003, 1), (3, 1, 2050, 2), (2, 1, 8208, 1), (1, 1, 70, 1),
+                                     (5, 1, 388, 4), (2500, 1, 64, 1), (1300, 1, 33, 1)])
+def test_wide_odd_and_many_rows(dev, N, L, C, G, dtype):
+    check_all(*make(dev, N, L, C, dtype, seed=N + C), G, "silu", dtype)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("N,L,C,G", [(3, 1000, 8, 1), (70, 41, 512, 64), (2, 2047, 48, 6), (700, 3, 16, 2), (1, 9, 16400, 1), (5, 333, 130, 2)])
+def test_chunks_of_positions(dev, N, L, C, G, dtype):
+    check_all(*make(dev, N, L, C, dtype, seed=N + L), G, "silu", dtype)

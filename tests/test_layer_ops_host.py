@@ -208,3 +208,19 @@ def test_strides_of_single_elements(lib):
     wide = torch.zeros(1, 5, 20)[:, :, 4:12]
     d = gdn.recurrence_desc_for(wide, wide, wide)
     assert d.x_stride_t == 20
+
+
+@pytest.mark.parametrize("args", [(1, 2 ** 31 - 1, 0, 8, 1), (1, 2 ** 31 - 2 ** 16 + 1, 0, 8, 1), (1, 1, 0, 2 ** 30 + 1, 1),
+                                  (1, 1, 0, 2 ** 31 - 1, 1)])
+def test_sizes_whose_indices_would_wrap_are_refused(lib, args):
+    assert lib.gdn_recurrence_desc_init(ctypes.byref(gdn.gdn_recurrence_desc()), *args) == UNSUPPORTED
+    edge = (1, min(args[1], 2 ** 31 - 2 ** 16), 0, min(args[3], 2 ** 30), 1)
+    assert lib.gdn_recurrence_desc_init(ctypes.byref(gdn.gdn_recurrence_desc()), *edge) == gdn.GDN_OK
+
+
+@pytest.mark.parametrize("N,L,C,G", [(1, 2 ** 31 - 1, 8, 1), (1, 1, 2 ** 24 + 1, 1)])
+def test_group_norm_sizes_whose_indices_would_wrap_are_refused(lib, N, L, C, G):
+    assert lib.gdn_group_norm_desc_init(ctypes.byref(gdn.gdn_group_norm_desc()), N, L, C, G, gdn.GDN_F32) == UNSUPPORTED
+    edge = (N, min(L, 2 ** 31 - 2 ** 16), min(C, 2 ** 24), G)
+    d = gdn.gdn_group_norm_desc_init(*edge, gdn.GDN_F32)
+    assert gdn.gdn_group_norm_workspace_bytes(d) >= 256 and gdn.gdn_group_norm_backward_workspace_bytes(d) >= 256

@@ -359,3 +359,35 @@ def test_wait_timeout_reported_then_next_call_correct(dev, dtype):
     assert status == (gdn.GDN_ERR_DEVICE_TIMEOUT,) * 2
     again = forward(s, bufs=bad)
     assert gdn.gdn_device_status(again.workspace) == gdn.GDN_OK and torch.equal(again.out, f.out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,T,D", [(1, 1000, 64), (12, 530, 32), (13, 530, 30), (20, 420, 32), (21, 420, 31), (28, 400, 32),
+                                   (29, 400, 32), (1, 513, 832), (1, 513, 835)])
+def test_every_number_of_ctas_per_row(dev, B, T, D, dtype):
+    """Rows by channel slabs around the counts where the number of CTAs per row changes, rows long enough to use them."""
+    check_all(make(dev, B, T, D, dtype, seed=B + T + D))
+
+
+@pytest.mark.parametrize("D", [64, 63])
+def test_long_packed_row_of_few_channels(dev, D):
+    lengths = [700, 0, 1, 31, 32, 33, 1, 900, 511, 0]
+    check_all(make(dev, 1, sum(lengths), D, "bf16", seed=D, lengths=lengths))
+
+
+def test_elements_next_to_unmapped_rows_are_not_needed(dev):
+    """Odd rows at the very start and end of their own buffers, guarded by NaN: nothing outside the rows counts."""
+    B, T, D = 2, 75, 37
+    s = make(dev, B, T, D, "fp16", seed=5)
+    whole = forward(s, want_chunk_states=True)
+    grads = backward(s, whole.chunk_states)
+    for name in ("x", "a", "b"):
+        buf = torch.full((B * T * D + 2 * D,), float("nan"), dtype=s[name].dtype, device=dev)
+        view = buf[D:D + B * T * D].view(B, T, D)
+        view.copy_(s[name])
+        s[name] = view
+    again = forward(s, want_chunk_states=True)
+    assert torch.equal(again.out, whole.out) and torch.equal(again.final_state, whole.final_state)
+    after = backward(s, again.chunk_states)
+    for name in ("dx", "da", "db", "dA_log", "ddt_bias", "dinitial_state"):
+        assert torch.equal(getattr(after, name), getattr(grads, name)), name

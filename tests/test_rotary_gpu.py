@@ -167,3 +167,19 @@ def test_captured_and_replayed(dev):
         graph.replay()
         torch.cuda.synchronize()
         held(out, q, np.full((4, 1), step), O.frequencies(64), 64, 64, "half", "bf16")
+
+
+@pytest.mark.parametrize("d,rot", [(192, 48), (80, 20), (66, 66), (64, 2)])
+def test_one_of_the_tensors_in_place(dev, d, rot):
+    B, T, H = 2, 37, 3
+    g = torch.Generator().manual_seed(d)
+    q, k = (torch.randn((B, T, h * d), generator=g).to(torch.bfloat16).to(dev) for h in (H, 1))
+    table = gdn.rotary_table(rot, device=dev)
+    want_q, want_k = gdn.rotary(q, k, table, d=d, rot=rot)
+    held(want_q, q, np.broadcast_to(np.arange(T), (B, T)), O.frequencies(rot), d, rot, "half", "bf16")
+    in_place, kept = q.clone(), k.clone()
+    _, ko = gdn.rotary(in_place, kept, table, d=d, rot=rot, q_out=in_place)
+    assert torch.equal(in_place, want_q) and torch.equal(ko, want_k) and torch.equal(kept, k)
+    in_place, kept = k.clone(), q.clone()
+    qo, _ = gdn.rotary(kept, in_place, table, d=d, rot=rot, k_out=in_place)
+    assert torch.equal(in_place, want_k) and torch.equal(qo, want_q) and torch.equal(kept, q)
