@@ -140,27 +140,41 @@ template <typename T> __device__ __forceinline__ void pack4(void *p, const F4 &v
 }
 template <> __device__ __forceinline__ void pack4<float>(void *p, const F4 &v) { *(float4 *)p = to4(v); }
 
-// Up to four channels of a row in global memory; nc of them exist. VEC: rows are aligned and nc is 4 or 0.
-template <typename T, bool VEC>
+// Up to four channels of a row in global memory, STEP apart; nc of them exist. VEC: adjacent ones of an aligned row,
+// and nc is 4 or 0.
+template <typename T, bool VEC, int STEP = 1>
 __device__ __forceinline__ F4 load_row(const T *p, int nc) {
     if (VEC) return nc > 0 ? unpack4<T>(p) : f4(0.f);
-    return {make_float2(nc > 0 ? to_f<T>(p[0]) : 0.f, nc > 1 ? to_f<T>(p[1]) : 0.f),
-            make_float2(nc > 2 ? to_f<T>(p[2]) : 0.f, nc > 3 ? to_f<T>(p[3]) : 0.f)};
+    return {make_float2(nc > 0 ? to_f<T>(p[0]) : 0.f, nc > 1 ? to_f<T>(p[STEP]) : 0.f),
+            make_float2(nc > 2 ? to_f<T>(p[2 * STEP]) : 0.f, nc > 3 ? to_f<T>(p[3 * STEP]) : 0.f)};
 }
-template <typename T, bool VEC>
+template <typename T, bool VEC, int STEP = 1>
 __device__ __forceinline__ void store_row(T *p, const F4 &v, int nc) {
     if (VEC) {
         if (nc > 0) pack4<T>(p, v);
         return;
     }
     if (nc > 0) p[0] = from_f<T>(v.lo.x);
-    if (nc > 1) p[1] = from_f<T>(v.lo.y);
-    if (nc > 2) p[2] = from_f<T>(v.hi.x);
-    if (nc > 3) p[3] = from_f<T>(v.hi.y);
+    if (nc > 1) p[STEP] = from_f<T>(v.lo.y);
+    if (nc > 2) p[2 * STEP] = from_f<T>(v.hi.x);
+    if (nc > 3) p[3 * STEP] = from_f<T>(v.hi.y);
 }
 // four fp32 values of a row whose alignment is not known
-__device__ __forceinline__ F4 load_words(const float *p, int nc) { return load_row<float, false>(p, nc); }
-__device__ __forceinline__ void store_words(float *p, const F4 &v, int nc) { store_row<float, false>(p, v, nc); }
+template <int STEP> __device__ __forceinline__ F4 load_words(const float *p, int nc) { return load_row<float, false, STEP>(p, nc); }
+template <int STEP> __device__ __forceinline__ void store_words(float *p, const F4 &v, int nc) { store_row<float, false, STEP>(p, v, nc); }
+
+// The channels of lane q of a token's LR lanes, from a slab's first channel on: four adjacent ones, or without TMA
+// every LR-th, so that the lanes of an element-wise access are neighbours in memory (3 x 19422 x 1147 fp32 with its
+// gradient 919 us, with adjacent ones 1028).
+template <typename L, bool TMA> struct Columns {
+    static constexpr int STEP = TMA ? 1 : L::LR;
+    int ch, nc;   // the first, and how many exist
+    __device__ __forceinline__ Columns(int slab, int q, int D) {
+        ch = slab * L::CH + (TMA ? q * 4 : q);
+        nc = min(4, max(0, (D - ch + STEP - 1) / STEP));
+    }
+    static __device__ __forceinline__ int of(int i) { return TMA ? i : i / 4 + i % 4 * L::LR; }   // value i of a slab's 4 LR
+};
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -324,30 +338,30 @@ struct Seq {
 };
 
 // Sequences without tokens: their final state is their initial state (dst, src), zeros without one.
-__device__ void copy_empty(const RecProblem &p, int row, int ch, int nc, float *dst, const float *src, int group, int groups) {
+template <int STEP> __device__ void copy_empty(const RecProblem &p, int row, int ch, int nc, float *dst, const float *src, int group, int groups) {
     if (dst == nullptr) return;
     for (int n = (p.cu ? 0 : row) + group; n < (p.cu ? p.d.N : row + 1); n += groups) {
         if (p.cu ? p.cu[n] != p.cu[n + 1] : p.d.T != 0) continue;
-        store_words(dst + (int64_t)n * p.d.D + ch, src ? load_words(src + (int64_t)n * p.d.D + ch, nc) : f4(0.f), nc);
+        store_words<STEP>(dst + (int64_t)n * p.d.D + ch, src ? load_words<STEP>(src + (int64_t)n * p.d.D + ch, nc) : f4(0.f), nc);
     }
 }
 
-// Without TMA: R tokens by four channels of a tensor, element by element, zeros where there is nothing. The loads
+// Without TMA: R tokens by a lane's four channels of a tensor, element by element, zeros where there is nothing. The loads
 // of the next tile are issued while this one is worked on.
-template <typename T, int R>
+template <int STEP, typename T, int R>
 __device__ __forceinline__ void fetch_elements(T (&v)[R][4], const T *p, int64_t stride, int tokens, int nc) {
 #pragma unroll
     for (int r = 0; r < R; ++r, p += stride)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) v[r][c] = r < tokens && c < nc ? p[c] : from_f<T>(0.f);
+        for (int c = 0; c < 4; ++c) v[r][c] = r < tokens && c < nc ? p[c * STEP] : from_f<T>(0.f);
 }
 template <typename T> __device__ __forceinline__ F4 of_elements(const T (&v)[4]) {
     return {make_float2(to_f<T>(v[0]), to_f<T>(v[1])), make_float2(to_f<T>(v[2]), to_f<T>(v[3]))};
 }
 
 // exp(A_log) and dt_bias log2(e) of four channels
-__device__ __forceinline__ void channel_params(const RecProblem &p, int ch, int nc, float2 (&rate)[2], float2 (&bias2)[2]) {
-    const F4 l = load_words(p.A_log + ch, nc), b = load_words(p.dt_bias + ch, nc);
+template <int STEP> __device__ __forceinline__ void channel_params(const RecProblem &p, int ch, int nc, float2 (&rate)[2], float2 (&bias2)[2]) {
+    const F4 l = load_words<STEP>(p.A_log + ch, nc), b = load_words<STEP>(p.dt_bias + ch, nc);
     rate[0] = make_float2(expf(l.lo.x), expf(l.lo.y));
     rate[1] = make_float2(expf(l.hi.x), expf(l.hi.y));
     bias2[0] = mul2(b.lo, splat2(kLog2e));
@@ -402,12 +416,14 @@ rec_forward_kernel(const __grid_constant__ RecProblem p, const __grid_constant__
         }
     } else {
         const int g = lane / L::LR, q = lane % L::LR;
-        const int ch = slab * L::CH + q * 4, nc = min(4, max(0, d.D - ch));
+        const Columns<L, TMA> col(slab, q, d.D);
+        const int ch = col.ch, nc = col.nc;
+        constexpr int kStep = Columns<L, TMA>::STEP;
         const int tg = (warp * L::G + g) * kR;   // this group's first token in a tile
         const GateConst C;
         float2 rate[2], bias2[2];
-        channel_params(p, ch, nc, rate, bias2);
-        if (rank == 0) copy_empty(p, row, ch, nc, p.hT, p.h0, warp * L::G + g, L::NG);
+        channel_params<kStep>(p, ch, nc, rate, bias2);
+        if (rank == 0) copy_empty<kStep>(p, row, ch, nc, p.hT, p.h0, warp * L::G + g, L::NG);
         Seq seq, seq_out;   // at the tile whose decays are computed, and at the one that is finished
         seq.init(p, row);
         seq_out.init(p, row);
@@ -416,9 +432,9 @@ rec_forward_kernel(const __grid_constant__ RecProblem p, const __grid_constant__
         auto fetch = [&](int k) {
             const int tile = k * (int)cs + (int)rank, t0 = tile * L::TT + tg;
             if (TMA || tile >= p.ntiles) return;
-            fetch_elements<T, kR>(ea, (const T *)p.a + row * d.a_stride_b + t0 * d.a_stride_t + ch, d.a_stride_t, d.T - t0, nc);
-            fetch_elements<T, kR>(eb, (const T *)p.b + row * d.b_stride_b + t0 * d.b_stride_t + ch, d.b_stride_t, d.T - t0, nc);
-            fetch_elements<T, kR>(ex, (const T *)p.x + row * d.x_stride_b + t0 * d.x_stride_t + ch, d.x_stride_t, d.T - t0, nc);
+            fetch_elements<kStep, T, kR>(ea, (const T *)p.a + row * d.a_stride_b + t0 * d.a_stride_t + ch, d.a_stride_t, d.T - t0, nc);
+            fetch_elements<kStep, T, kR>(eb, (const T *)p.b + row * d.b_stride_b + t0 * d.b_stride_t + ch, d.b_stride_t, d.T - t0, nc);
+            fetch_elements<kStep, T, kR>(ex, (const T *)p.x + row * d.x_stride_b + t0 * d.x_stride_t + ch, d.x_stride_t, d.T - t0, nc);
         };
         fetch(0);
         // decay products P and local values h of tile k's tokens, and the map to the carry warp
@@ -457,7 +473,7 @@ rec_forward_kernel(const __grid_constant__ RecProblem p, const __grid_constant__
                     for (int r = 0; r < kR; ++r) {
                         m.up_to(p, t0 + r);
                         if (m.b0 == t0 + r && t0 + r < d.T) {
-                            if (p.h0) h[r] = fma4(P[r], load_words(p.h0 + (int64_t)m.n * d.D + ch, nc), h[r]);
+                            if (p.h0) h[r] = fma4(P[r], load_words<kStep>(p.h0 + (int64_t)m.n * d.D + ch, nc), h[r]);
                             P[r] = f4(-0.f);
                         }
                         if (r > 0) {
@@ -483,7 +499,7 @@ rec_forward_kernel(const __grid_constant__ RecProblem p, const __grid_constant__
             const int t0 = (k * (int)cs + (int)rank) * L::TT + tg;
             if (t0 >= d.T) return;
             if (p.cs && t0 % GDN_RECURRENCE_CHUNK == 0)
-                store_row<float, TMA>(p.cs + ((int64_t)row * ((d.T + GDN_RECURRENCE_CHUNK - 1) / GDN_RECURRENCE_CHUNK) +
+                store_row<float, TMA, kStep>(p.cs + ((int64_t)row * ((d.T + GDN_RECURRENCE_CHUNK - 1) / GDN_RECURRENCE_CHUNK) +
                                               t0 / GDN_RECURRENCE_CHUNK) * d.D + ch, c, nc);
 #pragma unroll
             for (int r = 0; r < kR; ++r) h[r] = apply<PACKED>(P[r], h[r], c);
@@ -495,7 +511,7 @@ rec_forward_kernel(const __grid_constant__ RecProblem p, const __grid_constant__
                 } else {
 #pragma unroll
                     for (int r = 0; r < kR; ++r, o += d.D)
-                        if (t0 + r < d.T) store_row<T, TMA>(o, h[r], nc);
+                        if (t0 + r < d.T) store_row<T, TMA, kStep>(o, h[r], nc);
                 }
             }
             if (p.hT) {
@@ -505,7 +521,7 @@ rec_forward_kernel(const __grid_constant__ RecProblem p, const __grid_constant__
 #pragma unroll
                     for (int r = 0; r < kR; ++r) {
                         m.up_to(p, t0 + r);
-                        if (m.b1 == t0 + r + 1) store_words(p.hT + (int64_t)m.n * d.D + ch, h[r], nc);
+                        if (m.b1 == t0 + r + 1) store_words<kStep>(p.hT + (int64_t)m.n * d.D + ch, h[r], nc);
                     }
                 }
             }
@@ -586,12 +602,14 @@ rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant_
         }
     } else {
         const int g = lane / L::LR, q = lane % L::LR;
-        const int ch = slab * L::CH + q * 4, nc = min(4, max(0, d.D - ch));
+        const Columns<L, TMA> col(slab, q, d.D);
+        const int ch = col.ch, nc = col.nc;
+        constexpr int kStep = Columns<L, TMA>::STEP;
         const int tg = (warp * L::G + g) * kR;
         const GateConst C;
         float2 rate[2], bias2[2];
-        channel_params(p, ch, nc, rate, bias2);
-        if (rank == 0) copy_empty(p, row, ch, nc, p.dh0, p.grad_final, warp * L::G + g, L::NG);
+        channel_params<kStep>(p, ch, nc, rate, bias2);
+        if (rank == 0) copy_empty<kStep>(p, row, ch, nc, p.dh0, p.grad_final, warp * L::G + g, L::NG);
         Seq seq;
         seq.init(p, row);
         seq.up_to(p, d.T - 1);
@@ -607,14 +625,14 @@ rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant_
         auto fetch_ay = [&](int k) {
             const int tile = tile_of(k), t0 = tile * L::TT + tg;
             if (TMA || tile < 0) return;
-            fetch_elements<T, kR>(ea, (const T *)p.a + row * d.a_stride_b + t0 * d.a_stride_t + ch, d.a_stride_t, d.T - t0, nc);
-            fetch_elements<T, kR>(ey, (const T *)p.grad_out + ((int64_t)row * d.T + t0) * d.D + ch, d.D, d.T - t0, nc);
+            fetch_elements<kStep, T, kR>(ea, (const T *)p.a + row * d.a_stride_b + t0 * d.a_stride_t + ch, d.a_stride_t, d.T - t0, nc);
+            fetch_elements<kStep, T, kR>(ey, (const T *)p.grad_out + ((int64_t)row * d.T + t0) * d.D + ch, d.D, d.T - t0, nc);
         };
         auto fetch_xb = [&](int k) {
             const int tile = tile_of(k), t0 = tile * L::TT + tg;
             if (TMA || tile < 0) return;
-            fetch_elements<T, kR>(ex, (const T *)p.x + row * d.x_stride_b + t0 * d.x_stride_t + ch, d.x_stride_t, d.T - t0, nc);
-            fetch_elements<T, kR>(eb, (const T *)p.b + row * d.b_stride_b + t0 * d.b_stride_t + ch, d.b_stride_t, d.T - t0, nc);
+            fetch_elements<kStep, T, kR>(ex, (const T *)p.x + row * d.x_stride_b + t0 * d.x_stride_t + ch, d.x_stride_t, d.T - t0, nc);
+            fetch_elements<kStep, T, kR>(eb, (const T *)p.b + row * d.b_stride_b + t0 * d.b_stride_t + ch, d.b_stride_t, d.T - t0, nc);
         };
         fetch_ay(0);
         // Between begin and finish a thread keeps three values per token and channel in its own slots of shared
@@ -660,7 +678,7 @@ rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant_
                                 al[r] = f4(-0.f);
                             }
                             if (m.b1 == t0 + r + 1 && p.grad_final)
-                                v[r] = add4(v[r], load_words(p.grad_final + (int64_t)m.n * d.D + ch, nc));
+                                v[r] = add4(v[r], load_words<kStep>(p.grad_final + (int64_t)m.n * d.D + ch, nc));
                         }
                     }
                 }
@@ -678,7 +696,7 @@ rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant_
             const bool any = tile >= 0 && t0 < d.T;
             F4 hs = f4(0.f);
             if (any)
-                hs = load_row<float, TMA>(p.cs + ((int64_t)row * ((d.T + kR - 1) / kR) + t0 / kR) * d.D + ch, nc);
+                hs = load_row<float, TMA, kStep>(p.cs + ((int64_t)row * ((d.T + kR - 1) / kR) + t0 / kR) * d.D + ch, nc);
             F4 c = chain.take(eA, eB, k, warp, lane);
             if (any) {
 #pragma unroll
@@ -699,8 +717,8 @@ rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant_
                         al[r] = {decay_of(em.lo, Y.lo), decay_of(em.hi, Y.hi)};
                         Seq m = seq;
                         m.up_to(p, t0 + r);
-                        hs = p.h0 ? load_words(p.h0 + (int64_t)m.n * d.D + ch, nc) : f4(0.f);
-                        if (p.dh0) store_words(p.dh0 + (int64_t)m.n * d.D + ch, mul4(al[r], v[r]), nc);
+                        hs = p.h0 ? load_words<kStep>(p.h0 + (int64_t)m.n * d.D + ch, nc) : f4(0.f);
+                        if (p.dh0) store_words<kStep>(p.dh0 + (int64_t)m.n * d.D + ch, mul4(al[r], v[r]), nc);
                     }
                     F4 gx, ga, gb;
                     auto pair = [&](float2 em, float2 Y, float2 rsg, float2 al, float2 xv, float2 bv, float2 dv, float2 &hh,
@@ -725,9 +743,9 @@ rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant_
                         pack4<T>(da, ga);
                         pack4<T>(db, gb);
                     } else if (t0 + r < d.T) {
-                        store_row<T, TMA>(dx, gx, nc);
-                        store_row<T, TMA>(da, ga, nc);
-                        store_row<T, TMA>(db, gb, nc);
+                        store_row<T, TMA, kStep>(dx, gx, nc);
+                        store_row<T, TMA, kStep>(da, ga, nc);
+                        store_row<T, TMA, kStep>(db, gb, nc);
                     }
                     dx += d.D;
                     da += d.D;
@@ -755,12 +773,12 @@ rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant_
     }
     __syncthreads();
     for (int i = tid; i < 2 * L::CH; i += L::THREADS) {
-        const int which = i / L::CH, c = i % L::CH;
-        if (slab * L::CH + c >= d.D) continue;
+        const int which = i / L::CH, v = i % L::CH, c = slab * L::CH + Columns<L, TMA>::of(v);
+        if (c >= d.D) continue;
         float s = 0.f;
 #pragma unroll
-        for (int j = 0; j < L::NG; ++j) s += red[j][which][c];
-        p.part[(((int64_t)row * cs + rank) * 2 + which) * d.D + slab * L::CH + c] = s;
+        for (int j = 0; j < L::NG; ++j) s += red[j][which][v];
+        p.part[(((int64_t)row * cs + rank) * 2 + which) * d.D + c] = s;
     }
     if (failed || lost) *p.status = GDN_ERR_DEVICE_TIMEOUT;
     // copies in flight end before the CTA does (they have, unless a wait gave up), and no CTA leaves while
@@ -817,17 +835,22 @@ __global__ void __launch_bounds__(128) rec_step_kernel(const RecProblem p, float
 }
 
 // ===================================================================== host
-// CTAs per chain. With few chains a step's latency is what counts (0.9 us, forward), so a chain takes as many CTAs
-// as it can while all clusters are resident: a cluster stays within one of the chip's 8 processing clusters of up
-// to 20 SMs, which leaves room for 12 clusters of 16, 20 of 12, 28 of 10. With its gradient over 32768 bf16 tokens:
-//     4 chains  16 CTAs 221 us, 12 277, 8 386        20 chains  12 CTAs 366 us, 16 461, 8 490
-//    12 chains  16 CTAs 274 us, 12 342, 8 406        28 chains  10 CTAs 452 us, 12 607, 8 513
-// With more chains, as many as fill the chip once at per_sm CTAs per SM; clusters of 7 fit no better than those
-// of 8 (59 against 51 at 3 CTAs per SM), so 6 (74) serves for both.
+// CTAs per chain: as many as leave all clusters resident, since a cluster that waits for another's end costs its whole
+// time again (a cluster stays within one of the chip's processing clusters, so larger ones fit worse than their sum of
+// CTAs says: the counts here are the occupancy calculator's). At two CTAs per SM up to 16, at three, where registers
+// allow that, up to 8: with more than two, larger clusters wait for the slowest SM. Backward over 16384 bf16 tokens:
+//     24 chains  10 CTAs 153 us, 8 168, 12 221      72 chains  6 CTAs 286 us, 5 325, 7 412
+//     36 chains   8 CTAs 191 us, 7 210, 10 277      84 chains  5 CTAs 332 us, 4 393, 6 449
+//     50 chains   8 CTAs 212 us, 7 238,  9 316     100 chains  4 CTAs 399 us, 3 514, 5 536
+//     56 chains   7 CTAs 244 us, 6 271,  8 340     128 chains  3 CTAs 528 us, 2 635, 4 637
+// (the forward's order is the same but for 24 to 43 chains, where 10 to 14 CTAs gain it up to 13 %).
 int cluster_size(int64_t chains, int64_t ntiles, int per_sm) {
-    int64_t cs = chains <= 12 ? kMaxCluster : chains <= 20 ? 12 : chains <= 28 ? 10 : (int64_t)per_sm * kSms / chains;
-    if (chains > 28 && cs > 6) cs = cs < 8 ? 6 : 8;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({cs, ntiles, kMaxCluster}));
+    constexpr int kResident2[kMaxCluster] = {304, 152, 97, 74, 58, 46, 38, 36, 30, 28, 23, 23, 19, 14, 14, 14};
+    constexpr int kResident3[8] = {456, 228, 148, 110, 87, 74, 59, 51};
+    int cs = 1;
+    for (int i = 1; i <= kMaxCluster; ++i)
+        if (kResident2[i - 1] >= chains || (per_sm > 2 && i <= 8 && kResident3[i - 1] >= chains)) cs = i;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(cs, ntiles));
 }
 
 struct RecPlan {
