@@ -795,13 +795,15 @@ Plan make_plan(const gdn_group_norm_desc &d, int v, bool backward) {
     r.chunks = 1;
     r.chunk_rows = d.L;
     if (!r.rows && d.L > 1) {
-        // Chunks of positions, of at least a batch each: as many as give every team k of them, for the k (1 to 8) that
-        // keeps the busiest team's positions fewest; a chunk costs about four more (its partials, its last batch).
+        // Chunks of positions, of at least a batch each: as many as give every team m / 64 of them, for the m that keeps
+        // the busiest team's time least, counted in positions: those of its chunks, and for each chunk four more (its
+        // last batch, its own partial) and the partials that a lane reads in the second pass (3 x 2176 x 176 in 22
+        // groups of one lane each: 272 chunks 43.7 us, so 22.0 us).
         int64_t least = INT64_MAX;
-        for (int k = 1; k <= 8; ++k) {
-            const int64_t want = std::max<int64_t>(1, std::min<int64_t>(k * teams / std::max(1, d.N), d.L / kBatch));
+        for (int m = 1; m <= 512; m += m < 64 ? m : 64) {
+            const int64_t want = std::max<int64_t>(1, std::min<int64_t>(m * teams / (64ll * std::max(1, d.N)), d.L / kBatch));
             const int64_t rows = cdiv64(d.L, want), chunks = cdiv64(d.L, rows);
-            const int64_t cost = cdiv64(d.N * chunks, teams) * (rows + 4);
+            const int64_t cost = cdiv64(d.N * chunks, teams) * (rows + 4 + chunks * r.slabs / r.lg);
             if (cost >= least) continue;
             least = cost;
             r.chunks = (int)chunks;
