@@ -547,7 +547,7 @@ int gdn_rotary_desc_init(gdn_rotary_desc *d, int B, int T, int packed, int Hq, i
  * of 2^-64 turns, from fp64 arithmetic, into the HOST array `turns`. factor, low,
  * high and original are read by the scalings that use them. Returns
  * GDN_ERR_INVALID_ARG for an odd or non-positive rot, theta <= 0, factor <= 0,
- * high <= low or original <= 0. */
+ * high <= low, original <= 0, or values that leave a frequency not finite. */
 int gdn_rotary_table(int rot, double theta, int scaling, double factor, double low, double high,
                      double original, uint64_t *turns);
 

@@ -6,9 +6,10 @@
 // (in the rows form a block takes a larger group).
 // Weights stay in registers, sums cross lanes by shuffles, and rows stream past.
 //
-//   rows     L = 1 and a group fits LG lanes x NV vectors: a row is read once, its mean
-//            and its centred squares are summed from registers, and it is written. Four
-//            rows are in flight per warp.
+//   rows     L = 1 and a group fits LG lanes x NV vectors, or a block's: a row is read once,
+//            its mean and its centred squares are summed from registers, and it is written.
+//            Two rows are worked on per warp and two are on their way; the backward's come
+//            through shared memory, six ahead.
 //   general  several positions, or larger groups: partial means and centred sums of
 //            squares per (instance, chunk of positions), merged pairwise; a second pass
 //            normalises (one kernel where a warp holds a whole group, else two). The
@@ -17,6 +18,14 @@
 // The backward has the same two forms, with the sums of t and t xh in the statistics'
 // place. Parameter gradients are summed per warp over its rows, written as partial rows
 // and added up by a last small kernel. Every order is fixed by the sizes.
+//
+// Measured, of the copy rate: rows of 4096 in 32 groups, bf16, 131072 forward 380 us (83 %),
+// 65536 fp16 forward 193 us (82 %) and backward 347 us (68 %: 110 registers, two blocks per SM,
+// issue slots 58 % used); in one group, 131072 forward, 510 us (62 %: two block-wide sums a
+// row). Over positions: 60 x 16384 x 512 in 8 groups, forward, 473 us (63 %; 94 % counting the
+// second read); 2 x 2048 x 1536 in 6 groups 10 us and 17 us backward, launches and latency. Groups
+// that are no multiple of 16 bytes go element by element: 100000 rows of 4160 in 64 groups
+// 1060 us (23 %), issue-bound.
 #include <string.h>
 
 #include <algorithm>

@@ -6,7 +6,9 @@
 // the token and the pair alone, so a CTA computes the cosines and sines of its few
 // tokens once, into shared memory, for all heads. A unit of work is one vector per
 // half of a rotated head (half layout), one vector of whole pairs (interleaved), or one
-// copied vector; a thread has several in flight.
+// copied vector; a thread has several in flight. 131072 tokens of 32 heads of 128 in bf16
+// take 308 us (2.1 GB, 103 % of the copy rate). With few heads per token the table counts: one
+// head of 64 for 64 x 60000 tokens takes 470 us, 31 % of it.
 #include <math.h>
 #include <string.h>
 
@@ -48,7 +50,7 @@ __device__ __forceinline__ int64_t token_position(const RotaryProblem &p, int ro
 // turns, and its upper half as a signed fraction has 32 bits of the remaining angle. For
 // 16-bit outputs the hardware's functions on [-pi, pi] are exact enough (absolute error about
 // 2^-21, against a rounding of 2^-9 or 2^-12), and where a token has few heads they are what
-// bounds the kernel (one head of 64: 656 us with sincospif, 64 x 60000 tokens).
+// bounds the kernel (one head of 64 for 64 x 60000 tokens: 470 us, 656 with sincospif).
 template <bool FAST>
 __device__ __forceinline__ float2 cos_sin(int64_t position, uint64_t turn) {
     const uint64_t phase = (uint64_t)position * turn;
@@ -353,6 +355,7 @@ int gdn_rotary_table(int rot, double theta, int scaling, double factor, double l
             f = keep * f + (1.0 - keep) * f / factor;
         }
         const double t = f / two_pi;
+        if (!isfinite(t)) return GDN_ERR_INVALID_ARG;
         // whole turns drop out; 1 - 2^-53 is the largest fraction, so the product stays below 2^64
         turns[i] = (uint64_t)ldexp(t - floor(t), 64);
     }

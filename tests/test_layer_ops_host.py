@@ -224,3 +224,10 @@ def test_group_norm_sizes_whose_indices_would_wrap_are_refused(lib, N, L, C, G):
     edge = (N, min(L, 2 ** 31 - 2 ** 16), min(C, 2 ** 24), G)
     d = gdn.gdn_group_norm_desc_init(*edge, gdn.GDN_F32)
     assert gdn.gdn_group_norm_workspace_bytes(d) >= 256 and gdn.gdn_group_norm_backward_workspace_bytes(d) >= 256
+
+
+@pytest.mark.parametrize("args", [(128, 5e-324, 0, 1.0, 1.0, 2.0, 1.0), (128, 10000.0, 1, 5e-324, 1.0, 2.0, 1.0),
+                                  (64, 1e-300, 2, 1e-20, 1e305, 1e306, 1.0)])
+def test_rotary_table_of_infinite_frequencies_is_refused(lib, args):
+    out = torch.zeros(64, dtype=torch.int64)
+    assert lib.gdn_rotary_table(*args, out.data_ptr()) == INVALID
