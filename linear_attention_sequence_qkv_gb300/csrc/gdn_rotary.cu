@@ -8,7 +8,7 @@
 // half of a rotated head (half layout), one vector of whole pairs (interleaved), or one
 // copied vector; a thread has several in flight. 131072 tokens of 32 heads of 128 in bf16
 // take 308 us (2.1 GB, 103 % of the copy rate). With few heads per token the table counts: one
-// head of 64 for 64 x 60000 tokens takes 470 us, 31 % of it.
+// head of 64 for 64 x 60000 tokens takes 390 us, 37 % of it.
 #include <math.h>
 #include <string.h>
 
@@ -50,7 +50,7 @@ __device__ __forceinline__ int64_t token_position(const RotaryProblem &p, int ro
 // turns, and its upper half as a signed fraction has 32 bits of the remaining angle. For
 // 16-bit outputs the hardware's functions on [-pi, pi] are exact enough (absolute error about
 // 2^-21, against a rounding of 2^-9 or 2^-12), and where a token has few heads they are what
-// bounds the kernel (one head of 64 for 64 x 60000 tokens: 470 us, 656 with sincospif).
+// bounds the kernel (one head of 64 for 64 x 60000 tokens: 545 us, 656 with sincospif).
 template <bool FAST>
 __device__ __forceinline__ float2 cos_sin(int64_t position, uint64_t turn) {
     const uint64_t phase = (uint64_t)position * turn;
@@ -163,24 +163,28 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
     };
     int i0 = blockIdx.y * kThreads + threadIdx.x;
     fetch(i0);   // on their way while the table is computed
-    // a thread keeps its pair where the pairs fit the block, and steps over the tokens
-    int t = 0, pr0 = threadIdx.x, tstep = 1, pstep = kThreads;
-    if (half <= kThreads) {
-        tstep = kThreads / half;
-        t = threadIdx.x / half;
-        pr0 -= t * half;
-        pstep = half;
-        if (t >= tstep) t = nt;
-    }
-    for (; t < nt; t += tstep) {
+    auto position_of = [&](int t) {
         const uint32_t row = (uint32_t)(tok0 + t) / (uint32_t)d.T;
-        const int64_t position = token_position(p, row, (int)((uint32_t)(tok0 + t) - row * d.T));
-        for (int pr = pr0; pr < half; pr += pstep) {
-            const float2 cs = cos_sin<sizeof(T) == 2>(position, p.turns[pr]);
-            const int u = pr / NP, e = pr % NP;
-            float *at = tab + ((t * 2 * Q + e / W) * p.u_rot + u) * W + e % W;
-            at[0] = cs.x * d.scale;
-            at[Q * p.u_rot * W] = cs.y * (d.inverse ? -d.scale : d.scale);
+        return token_position(p, row, (int)((uint32_t)(tok0 + t) - row * d.T));
+    };
+    auto entry = [&](int t, int64_t position, int pr, uint64_t turn) {
+        const float2 cs = cos_sin<sizeof(T) == 2>(position, turn);
+        const int u = pr / NP, e = pr % NP;
+        float *at = tab + ((t * 2 * Q + e / W) * p.u_rot + u) * W + e % W;
+        at[0] = cs.x * d.scale;
+        at[Q * p.u_rot * W] = cs.y * (d.inverse ? -d.scale : d.scale);
+    };
+    if (half <= kThreads && nt * half > 8 * kThreads) {
+        // Long tables (few heads): a thread keeps its pair and steps over the tokens. 64 x 60000 tokens of one head
+        // of 64: 390 us, 545 with the loop below, which is the faster one for short tables (32 heads of 128: 305
+        // against 311 us, 4096 tokens of 12 heads of 256 with 64 rotated: 11.5 against 12.3).
+        const int tstep = kThreads / half, t0 = threadIdx.x / half, pr = threadIdx.x - t0 * half;
+        const uint64_t turn = p.turns[pr];
+        for (int t = t0 < tstep ? t0 : nt; t < nt; t += tstep) entry(t, position_of(t), pr, turn);
+    } else {
+        for (int i = threadIdx.x; i < nt * half; i += kThreads) {
+            const int t = i / half, pr = i - t * half;
+            entry(t, position_of(t), pr, p.turns[pr]);
         }
     }
     __syncthreads();
