@@ -8,6 +8,7 @@ library is missing or fails to load, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -625,6 +626,18 @@ def _on_current(t):
         raise ValueError(f"tensors on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
 
 
+def _allocating(stream):
+    """Where a function below allocates: on the stream that it launches on, whose order then also guards the
+    memory's former and next use."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
+def _expect_workspace(t, device):
+    _expect(t, "workspace", (t.numel(),), torch.uint8, device)
+
+
 def recurrence_desc_for(x, a, b, cu_seqlens=None) -> gdn_recurrence_desc:
     """Descriptor of the gated linear recurrence over [B, T, D] views x, a, b."""
     B, T, D = x.shape
@@ -703,12 +716,14 @@ def recurrence_forward(x, a, b, A_log, dt_bias, cu_seqlens=None, initial_state=N
     d = recurrence_desc_for(x, a, b, cu_seqlens)
     _check_recurrence(d, x, A_log, dt_bias, cu_seqlens, initial_state)
     if bufs is None:
-        bufs = alloc_recurrence(d, x.device, want_final_state, want_chunk_states)
+        with _allocating(stream):
+            bufs = alloc_recurrence(d, x.device, want_final_state, want_chunk_states)
     else:
         _expect(bufs.out, "bufs.out", (d.B, d.T, d.D), x.dtype, x.device)
         _expect(bufs.final_state, "bufs.final_state", (d.N, d.D), torch.float32, x.device)
         _expect(bufs.chunk_states, "bufs.chunk_states", (d.B, -(-d.T // GDN_RECURRENCE_CHUNK), d.D), torch.float32,
                 x.device)
+        _expect_workspace(bufs.workspace, x.device)
         bufs.desc = d
     gdn_recurrence_forward(d, x, a, b, A_log, dt_bias, cu_seqlens, initial_state, bufs.out, bufs.final_state,
                            bufs.chunk_states, bufs.workspace, bufs.ws_bytes, stream)
@@ -725,13 +740,15 @@ def recurrence_backward(x, a, b, A_log, dt_bias, grad_out, grad_final=None, chun
     _expect(grad_final, "grad_final", (d.N, d.D), torch.float32, x.device)
     _expect(chunk_states, "chunk_states", (d.B, -(-d.T // GDN_RECURRENCE_CHUNK), d.D), torch.float32, x.device)
     if grads is None:
-        grads = alloc_recurrence_grads(d, x.device)
+        with _allocating(stream):
+            grads = alloc_recurrence_grads(d, x.device)
     else:
         for name in ("dx", "da", "db"):
             _expect(getattr(grads, name), f"grads.{name}", (d.B, d.T, d.D), x.dtype, x.device)
         for name in ("dA_log", "ddt_bias"):
             _expect(getattr(grads, name), f"grads.{name}", (d.D,), torch.float32, x.device)
         _expect(grads.dinitial_state, "grads.dinitial_state", (d.N, d.D), torch.float32, x.device)
+        _expect_workspace(grads.workspace, x.device)
     gdn_recurrence_backward(d, x, a, b, A_log, dt_bias, cu_seqlens, initial_state, chunk_states, grad_out, grad_final,
                             grads.dx, grads.da, grads.db, grads.dA_log, grads.ddt_bias, grads.dinitial_state,
                             grads.workspace, grads.ws_bytes, stream)
@@ -744,7 +761,8 @@ def recurrence_step(x, a, b, A_log, dt_bias, state, out=None, stream=None) -> to
     _check_recurrence(d, x, A_log, dt_bias, None, None)
     _expect(state, "state", (d.B, d.D), torch.float32, x.device)
     if out is None:
-        out = torch.empty((d.B, d.T, d.D), dtype=x.dtype, device=x.device)
+        with _allocating(stream):
+            out = torch.empty((d.B, d.T, d.D), dtype=x.dtype, device=x.device)
     _expect(out, "out", (d.B, 1, d.D), x.dtype, x.device)
     gdn_recurrence_step(d, x, a, b, A_log, dt_bias, state, out, stream)
     return out
@@ -796,10 +814,11 @@ def rotary(q, k, table, *, d, rot=None, layout="half", inverse=False, scale=1.0,
     k themselves to rotate in place. inverse=True is the gradient. positions int32 [B, T], or offsets
     int32 [N] added to the positions counted from each sequence's start."""
     _on_current(q)
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    with _allocating(stream):
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
     r = rotary_desc_for(q, k, q_out, k_out, d=d, rot=rot, layout=layout, inverse=inverse, scale=scale,
                         cu_seqlens=cu_seqlens)
     _expect(table, "table", (r.rot // 2,), torch.int64, q.device)
@@ -807,7 +826,9 @@ def rotary(q, k, table, *, d, rot=None, layout="half", inverse=False, scale=1.0,
     _expect(cu_seqlens, "cu_seqlens", (r.N + 1,), torch.int32, q.device)
     _expect(offsets, "offsets", (r.N,), torch.int32, q.device)
     if workspace is None:
-        workspace = torch.empty(gdn_rotary_workspace_bytes(r), dtype=torch.uint8, device=q.device)
+        with _allocating(stream):
+            workspace = torch.empty(gdn_rotary_workspace_bytes(r), dtype=torch.uint8, device=q.device)
+    _expect_workspace(workspace, q.device)
     gdn_rotary(r, q, k, table, positions, cu_seqlens, offsets, q_out, k_out, workspace, workspace.numel(), stream)
     return q_out, k_out
 
@@ -878,11 +899,13 @@ def group_norm_forward(x, weight=None, bias=None, *, groups, act="silu", eps=1e-
     d = group_norm_desc_for(x, weight if weight is not None else bias, groups=groups, act=act, eps=eps)
     _check_group_norm(d, x, weight, bias)
     if bufs is None:
-        bufs = alloc_group_norm(d, x.device)
+        with _allocating(stream):
+            bufs = alloc_group_norm(d, x.device)
     else:
         _expect(bufs.out, "bufs.out", x.shape, x.dtype, x.device)
         for name in ("mean", "rstd"):
             _expect(getattr(bufs, name), f"bufs.{name}", (d.N, d.G), torch.float32, x.device)
+        _expect_workspace(bufs.workspace, x.device)
         bufs.desc = d
     gdn_group_norm_forward(d, x, weight, bias, bufs.out, bufs.mean, bufs.rstd, bufs.workspace, bufs.ws_bytes, stream)
     return bufs
@@ -897,11 +920,13 @@ def group_norm_backward(x, weight, bias, mean, rstd, grad_out, *, groups, act="s
     for t, name in ((mean, "mean"), (rstd, "rstd")):
         _expect(t, name, (d.N, d.G), torch.float32, x.device)
     if grads is None:
-        grads = alloc_group_norm_grads(d, x.device)
+        with _allocating(stream):
+            grads = alloc_group_norm_grads(d, x.device)
     else:
         _expect(grads.dx, "grads.dx", x.shape, x.dtype, x.device)
         for name in ("dweight", "dbias"):
             _expect(getattr(grads, name), f"grads.{name}", (d.C,), torch.float32, x.device)
+        _expect_workspace(grads.workspace, x.device)
     gdn_group_norm_backward(d, x, weight, bias, mean, rstd, grad_out, grads.dx, grads.dweight, grads.dbias,
                             grads.workspace, grads.ws_bytes, stream)
     return grads

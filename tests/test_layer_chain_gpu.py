@@ -123,3 +123,48 @@ def test_norm_of_the_delta_rule_output(dev):
     r = O.group_norm(x.double().cpu().numpy(), None, None, w.Hv, "none", 1e-5)
     got = f.out.double().cpu().numpy()
     assert (np.abs(got - r["out"]) <= O.bound(r["out"], r["out_err"], "fp16")).all()
+
+
+def test_memory_of_a_call_on_another_stream_is_that_streams_own(dev):
+    """A function given a stream allocates on it: memory that the current stream may still be using is not written."""
+    B, T, D = 2, 256, 512
+    g = torch.Generator().manual_seed(4)
+    x, a, b, dy = (torch.randn((B, T, D), generator=g).to(torch.bfloat16).to(dev) for _ in range(4))
+    A_log, bias, state = torch.zeros(D, device=dev), torch.full((D,), -2.0, device=dev), torch.zeros((B, D), device=dev)
+    table = gdn.rotary_table(64, device=dev)
+    mean, rstd = (lambda f: (f.mean, f.rstd))(gdn.group_norm_forward(x, groups=8))
+    one = [t[:, :1] for t in (x, a, b)]
+    calls = {
+        "forward": lambda s: gdn.recurrence_forward(x, a, b, A_log, bias, stream=s).out,
+        "backward": lambda s: gdn.recurrence_backward(x, a, b, A_log, bias, dy, stream=s).dx,
+        "step": lambda s: gdn.recurrence_step(*one, A_log, bias, state.clone() if s is None else steps, stream=s),
+        "rotary": lambda s: gdn.rotary(x, None, table, d=64, stream=s)[0],
+        "norm": lambda s: gdn.group_norm_forward(x, groups=8, stream=s).out,
+        "norm backward": lambda s: gdn.group_norm_backward(x, None, None, mean, rstd, dy, groups=8, stream=s).dx,
+    }
+    side = torch.cuda.Stream()
+    for as_handle in (False, True):
+        for name, call in calls.items():
+            steps = state.clone()
+            want = call(None).clone()
+            torch.cuda.synchronize()
+            used = torch.empty_like(want)
+            at = used.data_ptr()
+            del used   # the current stream's next tensor of this size would be here
+            got = call(side.cuda_stream if as_handle else side)
+            assert got.data_ptr() != at, name
+            torch.cuda.synchronize()
+            assert torch.equal(got, want), name
+
+
+def test_workspaces_of_the_wrong_kind_are_refused(dev):
+    x = torch.zeros((1, 4, 64), device=dev)
+    table = gdn.rotary_table(64, device=dev)
+    for ws in (torch.zeros(256, dtype=torch.uint8), torch.zeros(256, device=dev),
+               torch.zeros((16, 16), dtype=torch.uint8, device=dev)):
+        with pytest.raises(ValueError):
+            gdn.rotary(x, None, table, d=64, workspace=ws)
+    f = gdn.group_norm_forward(x, groups=2)
+    f.workspace = torch.zeros(4096, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        gdn.group_norm_forward(x, groups=2, bufs=f)
