@@ -482,8 +482,10 @@ int gdn_recurrence_forward(const gdn_recurrence_desc *d, const void *x, const vo
  *   dA_log, ddt_bias  fp32 [D], sums over all tokens in a fixed order
  *   dinitial_state NULL or fp32 [N][D]; grad_final's row where a sequence is empty
  *   workspace      >= gdn_recurrence_backward_workspace_bytes(), 256-byte aligned
- * Outputs are written in full. Where g_t = 0 in fp32 (no decay, so no write), the
- * derivative of sqrt(1 - alpha^2) is taken as its limit in a, 0.
+ * Outputs are written in full and must not overlap the inputs or each other. A
+ * malformed cu_seqlens and a wait that runs out are reported as in the forward.
+ * Where g_t = 0 in fp32 (no decay, so no write), the derivative of
+ * sqrt(1 - alpha^2) is taken as its limit in a, 0.
  */
 int gdn_recurrence_backward(const gdn_recurrence_desc *d, const void *x, const void *a, const void *b,
                             const float *A_log, const float *dt_bias, const int32_t *cu_seqlens,
@@ -494,7 +496,8 @@ int gdn_recurrence_backward(const gdn_recurrence_desc *d, const void *x, const v
 
 /*
  * One more token of each of B sequences (d->T == 1, N == B): the state, fp32
- * [B][D], is read and overwritten with h; out [B,1,D] contiguous. No workspace.
+ * [B][D], is read and overwritten with h; out [B,1,D] contiguous, which must not
+ * overlap the state or the inputs. No workspace.
  */
 int gdn_recurrence_step(const gdn_recurrence_desc *d, const void *x, const void *a, const void *b,
                         const float *A_log, const float *dt_bias, float *state, void *out,
@@ -618,6 +621,7 @@ int gdn_group_norm_forward(const gdn_group_norm_desc *d, const void *x, const vo
  *   dweight, dbias NULL, or fp32 [C] (written also when weight or bias is NULL; zeros
  *                  when N*L == 0)
  *   workspace      >= gdn_group_norm_backward_workspace_bytes(), 256-byte aligned
+ * dx must not overlap x or grad_out.
  */
 int gdn_group_norm_backward(const gdn_group_norm_desc *d, const void *x, const void *weight,
                             const void *bias, const float *mean, const float *rstd,

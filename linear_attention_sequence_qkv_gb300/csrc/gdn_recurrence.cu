@@ -50,6 +50,7 @@ struct RecProblem {
     void *dx, *da, *db;
     float *dA_log, *ddt_bias, *dh0, *part;
     int slabs, ntiles, wait_immediate;
+    int recomputed;              // backward: the states come from a forward of the same call
 };
 
 struct RecMaps {
@@ -567,7 +568,8 @@ rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant_
     const uint32_t rank = cluster_rank();
     const int slab = (int)(blockIdx.x / cs) % p.slabs, row = (int)(blockIdx.x / cs) / p.slabs;
     const bool ok = !PACKED || seqlens_ok(p.cu, d.N, d.T);
-    if (blockIdx.x == 0 && tid == 0) *p.status = ok ? GDN_OK : GDN_ERR_DEVICE_SEQLENS;
+    // after a forward of this call, which may have reported a wait that ran out, only what is worse
+    if (blockIdx.x == 0 && tid == 0 && !(ok && p.recomputed)) *p.status = ok ? GDN_OK : GDN_ERR_DEVICE_SEQLENS;
     if (!ok) return;
     const int steps = (p.ntiles + (int)cs - 1) / (int)cs;
     const int mine = (p.ntiles - 1 - (int)rank + (int)cs) / (int)cs;
@@ -925,7 +927,7 @@ cudaError_t launch_backward_rec(RecProblem p, cudaStream_t s) {
     RecMaps m;
     memset(&m, 0, sizeof(m));
     const bool tma = d.T > 0 && (d.D * sizeof(T)) % 16 == 0 && ptr_aligned(p.dx, 16) && ptr_aligned(p.da, 16) &&
-                     ptr_aligned(p.db, 16) && ptr_aligned(p.grad_out, 16) && tma_ok(d, p.x, d.x_stride_b, d.x_stride_t) &&
+                     ptr_aligned(p.db, 16) && ptr_aligned(p.grad_out, 16) && ptr_aligned(p.cs, 16) && tma_ok(d, p.x, d.x_stride_b, d.x_stride_t) &&
                      tma_ok(d, p.a, d.a_stride_b, d.a_stride_t) && tma_ok(d, p.b, d.b_stride_b, d.b_stride_t);
     const RecPlan pl = make_plan<L>(d, sizeof(T) == 2 && tma ? 3 : 2);
     p.slabs = pl.slabs;
@@ -1096,7 +1098,8 @@ int gdn_recurrence_backward(const gdn_recurrence_desc *d, const void *x, const v
     return by_dtype(d->dtype, [&](auto t) {
         using T = decltype(t);
         cudaError_t e = cudaSuccess;
-        if (!chunk_states && d->T > 0) e = launch_forward<T>(p, s);   // chunk states only
+        p.recomputed = !chunk_states && d->T > 0;
+        if (p.recomputed) e = launch_forward<T>(p, s);   // chunk states only
         return layer_status(e != cudaSuccess ? e : launch_backward_rec<T>(p, s));
     });
 }

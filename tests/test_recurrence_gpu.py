@@ -391,3 +391,49 @@ def test_elements_next_to_unmapped_rows_are_not_needed(dev):
     after = backward(s, again.chunk_states)
     for name in ("dx", "da", "db", "dA_log", "ddt_bias", "dinitial_state"):
         assert torch.equal(getattr(after, name), getattr(grads, name)), name
+
+
+@pytest.mark.parametrize("which", ["chunk_states", "dout", "x", "A_log", "dt_bias", "h0", "dfinal"])
+def test_tensors_aligned_to_their_elements_only(dev, which):
+    """Each tensor in turn starts one element behind a 16-byte boundary: the same values, or to rounding."""
+    s = make(dev, 2, 70, 64, "bf16", seed=3)
+    r = oracle(s)
+    chunk = forward(s, want_chunk_states=True).chunk_states
+
+    def shifted(t):
+        buf = torch.zeros(t.numel() + 8, dtype=t.dtype, device=dev)
+        view = buf[1:1 + t.numel()].view(t.shape)
+        view.copy_(t)
+        assert view.data_ptr() % 16 == t.element_size() and view.is_contiguous()
+        return view
+
+    if which == "chunk_states":
+        chunk = shifted(chunk)
+    else:
+        s[which] = shifted(s[which])
+    f = forward(s)
+    held(f.out, r, "out", "bf16")
+    g = backward(s, chunk)
+    assert gdn.gdn_device_status(g.workspace) == gdn.GDN_OK
+    for name, t in zip(GRADS, (g.dx, g.da, g.db, g.dA_log, g.ddt_bias, g.dinitial_state)):
+        held(t, r, name, "bf16" if name in ("dx", "da", "db") else "fp32")
+
+
+def test_timeout_of_the_recomputed_states_is_reported(dev):
+    """A backward that recomputes the states and itself waits for no copy still reports the forward's timeout."""
+    s = make(dev, 1, 1000, 256, "bf16")
+    want = backward(s, None)
+    buf = torch.zeros(s["dout"].numel() + 8, dtype=torch.bfloat16, device=dev)
+    view = buf[1:1 + s["dout"].numel()].view(s["dout"].shape)   # no copies into shared memory from here
+    view.copy_(s["dout"])
+    s["dout"] = view
+    torch.cuda.synchronize()
+    gdn.gdn_set_wait_test_mode(1)
+    try:
+        status = gdn.gdn_device_status(backward(s, None).workspace)
+    finally:
+        gdn.gdn_set_wait_test_mode(0)
+    assert status == gdn.GDN_ERR_DEVICE_TIMEOUT
+    g = backward(s, None)
+    assert gdn.gdn_device_status(g.workspace) == gdn.GDN_OK
+    assert torch.allclose(g.dx.float(), want.dx.float(), rtol=1e-2, atol=1e-2)
