@@ -24,9 +24,9 @@
 //
 // What bounds them, measured: fp32 the bandwidth (65536 x 4096 forward 642 us, 99 % of the
 // copy rate); 16-bit types the issue rate and the latency of a step, 42 instructions per
-// element forward and 70 backward (131072 x 4096 bf16 forward 1091 us, 58 % of the copy
-// rate; 65536 x 4096 in 16 sequences 670 us forward, which also writes the states, and
-// 1180 us backward). With few chains a step's latency alone.
+// element forward and 67 backward (131072 x 4096 bf16 forward 1038 us, 61 % of the copy
+// rate; 65536 x 4096 in 16 sequences 613 us forward, which also writes the states, and
+// 1141 us backward). With few chains a step's latency alone.
 #include <algorithm>
 #include <string.h>
 
@@ -370,7 +370,7 @@ template <int STEP> __device__ __forceinline__ void channel_params(const RecProb
 }
 
 // While the carry of tile k - 1 travels, the compute warps work on tile k: its decays and writes need only the
-// inputs (unpipelined, 131072 x 4096 bf16 took 2377 us against 1091). Three CTAs an SM: fp32 and element-by-element
+// inputs (unpipelined, 131072 x 4096 bf16 took 2377 us against 1038). Three CTAs an SM: fp32 and element-by-element
 // reads hold more in registers and run two.
 template <typename T, bool TMA, bool PACKED>
 __global__ void __launch_bounds__(FwdTile<T>::THREADS, sizeof(T) == 2 && TMA ? 3 : 2)
@@ -421,7 +421,7 @@ rec_forward_kernel(const __grid_constant__ RecProblem p, const __grid_constant__
         const int ch = col.ch, nc = col.nc;
         constexpr int kStep = Columns<L, TMA>::STEP;
         const int tg = (warp * L::G + g) * kR;   // this group's first token in a tile
-        const GateConst C;
+        const GateConst C(!TMA && sizeof(T) == 2);
         float2 rate[2], bias2[2];
         channel_params<kStep>(p, ch, nc, rate, bias2);
         if (rank == 0) copy_empty<kStep>(p, row, ch, nc, p.hT, p.h0, warp * L::G + g, L::NG);
@@ -551,7 +551,7 @@ rec_forward_kernel(const __grid_constant__ RecProblem p, const __grid_constant__
 // The reverse walk: c_t = alpha_t (v_t + c_{t+1}), delta_t = v_t + c_{t+1} with v = grad_out, tiles last to
 // first. The states before every 4th token come from the forward, so h_{t-1} is recomputed within a thread: 4 bytes
 // per 4 elements more to write and to read, against a second scan. With a state every 8 tokens and their values in
-// registers two CTAs an SM are left, and 65536 x 4096 bf16 takes 1621 us against 1180.
+// registers two CTAs an SM are left, and 65536 x 4096 bf16 takes 1621 us against 1141.
 template <typename T, bool TMA, bool PACKED>
 __global__ void __launch_bounds__(BwdTile<T>::THREADS, sizeof(T) == 2 && TMA ? 3 : 2)
 rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant__ RecMaps maps) {
@@ -608,7 +608,7 @@ rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant_
         const int ch = col.ch, nc = col.nc;
         constexpr int kStep = Columns<L, TMA>::STEP;
         const int tg = (warp * L::G + g) * kR;
-        const GateConst C;
+        const GateConst C(!TMA && sizeof(T) == 2);
         float2 rate[2], bias2[2];
         channel_params<kStep>(p, ch, nc, rate, bias2);
         if (rank == 0) copy_empty<kStep>(p, row, ch, nc, p.dh0, p.grad_final, warp * L::G + g, L::NG);
@@ -828,7 +828,7 @@ __global__ void __launch_bounds__(128) rec_step_kernel(const RecProblem p, float
     const F4 bias = load_row<float, VEC>(p.dt_bias + ch, nc), l = load_row<float, VEC>(p.A_log + ch, nc);
     const float2 rate[2] = {make_float2(expf(l.lo.x), expf(l.lo.y)), make_float2(expf(l.hi.x), expf(l.hi.y))};
     const float2 bias2[2] = {mul2(bias.lo, splat2(kLog2e)), mul2(bias.hi, splat2(kLog2e))};
-    const GateConst C;
+    const GateConst C(false);
     float2 z[2] = {a.lo, a.hi}, t[2], Y[2], al[2], em[2];
     decays<2, 2>(C, z, bias2, rate, t, Y, al, em);
     const F4 h = fma4({al[0], al[1]}, h0, mul4({write_scale2(C, em[0], al[0], b.lo), write_scale2(C, em[1], al[1], b.hi)}, x));
