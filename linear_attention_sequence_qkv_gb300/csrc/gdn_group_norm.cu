@@ -53,10 +53,14 @@ struct NormProblem {
 };
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-// Blocks per SM, resident at once: rows forward and backward, general forward and backward. Three for the last is
+// Blocks per SM, resident at once: rows forward, general forward and backward. Three for the last is
 // slower (2 x 2048 x 1536 in 6 groups 24.9 against 20.7 us, 60 x 2000 x 2048 in 16 540 against 464 us): registers
 // hold two.
-constexpr int kBlocksForward = 3, kBlocksBackward = 2, kBlocksGeneral = 4, kBlocksSums = 2;
+constexpr int kBlocksForward = 3, kBlocksGeneral = 4, kBlocksSums = 2;
+// The rows backward: three where their registers fit (vectors of four fp32, or no activation's derivative: 65536 x 4096
+// in 32 groups fp32 526 against 625 us with two, in 64 without activation bf16 301 against 323), else two (in 32 with
+// SiLU fp16 346 against 454 us with three, spilling).
+constexpr int blocks_backward(bool vectors, bool fp32, int act) { return vectors && (fp32 || act == GDN_ACT_NONE) ? 3 : 2; }
 constexpr int kRowsForward = 2;   // rows a warp works on at a time (two reductions in flight); as many are on their way
 constexpr int kAheadBackward = 6; // rows on their way in the backward
 constexpr int kBatch = 8, kBatchBackward = 4;   // rows in flight per warp in the general form
@@ -340,7 +344,7 @@ template <int N> struct ParamSums {
 };
 
 template <typename T, int V, int NV, int ACT, int LG>
-__global__ void __launch_bounds__(kThreads, NV == 1 || V == 1 ? kBlocksBackward : 1) norm_rows_backward(const __grid_constant__ NormProblem p) {
+__global__ void __launch_bounds__(kThreads, NV == 1 || V == 1 ? blocks_backward(V > 1, sizeof(T) == 4, ACT) : 1) norm_rows_backward(const __grid_constant__ NormProblem p) {
     const gdn_group_norm_desc &d = p.d;
     const Place q = place<V>(p);
     pdl_trigger();
@@ -799,7 +803,9 @@ Plan make_plan(const gdn_group_norm_desc &d, int v, bool backward) {
     if (!r.rows) r.lg = std::min(32, pow2_at_least(cgv));
     r.slabs = r.rows ? 1 : (int)cdiv64(cgv, r.lg);
     r.sets = r.lg == kThreads ? d.G : r.slabs == 1 ? (int)cdiv64(d.G, 32 / r.lg) : d.G * r.slabs;
-    const int64_t per_sm = !r.rows ? (backward ? kBlocksSums : kBlocksGeneral) : !backward ? kBlocksForward : kBlocksBackward;
+    const int64_t per_sm = !r.rows    ? (backward ? kBlocksSums : kBlocksGeneral)
+                           : backward ? blocks_backward(v > 1, d.dtype == GDN_F32, d.act)
+                                      : kBlocksForward;
     const int64_t teams = std::max<int64_t>(1, kSms * per_sm * (r.lg == kThreads ? 1 : kWarps) / r.sets);   // that share a set
     r.chunks = 1;
     r.chunk_rows = d.L;
