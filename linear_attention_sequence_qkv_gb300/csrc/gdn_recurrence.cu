@@ -975,7 +975,9 @@ RecLayout bwd_layout(const gdn_recurrence_desc &d) {
     size_t off = 0;
     const size_t chunks = ((size_t)d.T + GDN_RECURRENCE_CHUNK - 1) / GDN_RECURRENCE_CHUNK;
     L.status = off; off += kStatusBytes;
-    L.part = off;   off = align_up(off + (size_t)d.B * kMaxCluster * 2 * d.D * 4, 256);
+    // at three CTAs per SM a chain has no fewer of them than at two
+    const int cs = d.dtype == GDN_F32 ? make_plan<BwdTile<float>>(d, 3).cs : make_plan<BwdTile<__half>>(d, 3).cs;
+    L.part = off;   off = align_up(off + (size_t)d.B * cs * 2 * d.D * 4, 256);
     L.cs = off;     off = align_up(off + (size_t)d.B * chunks * d.D * 4, 256);
     L.total = off;
     return L;

@@ -231,3 +231,11 @@ def test_group_norm_sizes_whose_indices_would_wrap_are_refused(lib, N, L, C, G):
 def test_rotary_table_of_infinite_frequencies_is_refused(lib, args):
     out = torch.zeros(64, dtype=torch.int64)
     assert lib.gdn_rotary_table(*args, out.data_ptr()) == INVALID
+
+
+@pytest.mark.parametrize("dtype", [gdn.GDN_F32, gdn.GDN_BF16])
+def test_backward_workspace_of_many_rows_is_small(lib, dtype):
+    """Partial sums of one CTA per row and channel slab where rows fill the chip, beside the states of every 4th token."""
+    B, T, D = 20000, 8, 512
+    need = gdn.gdn_recurrence_backward_workspace_bytes(gdn.gdn_recurrence_desc_init(B, T, 0, D, dtype))
+    assert need <= 1024 + B * 2 * D * 4 + B * (T // 4) * D * 4
