@@ -180,7 +180,7 @@ def test_gradient_against_differences(dev):
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("N,L,C,G", [(3, 1, 1032, 1), (2, 1, 4112, 2), (2, 1, 1003, 1), (3, 1, 2050, 2), (2, 1, 8208, 1), (1, 1, 70, 1),
-                                     (5, 1, 388, 4), (2500, 1, 64, 1), (1300, 1, 33, 1)])
+                                     (5, 1, 388, 4), (2500, 1, 64, 1), (1300, 1, 33, 1), (2, 1, 16400, 1), (3, 1, 40001, 1)])
 def test_wide_odd_and_many_rows(dev, N, L, C, G, dtype):
     check_all(*make(dev, N, L, C, dtype, seed=N + C), G, "silu", dtype)
 

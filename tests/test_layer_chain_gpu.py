@@ -168,3 +168,38 @@ def test_workspaces_of_the_wrong_kind_are_refused(dev):
     f.workspace = torch.zeros(4096, dtype=torch.uint8)
     with pytest.raises(ValueError):
         gdn.group_norm_forward(x, groups=2, bufs=f)
+
+
+def test_captured_chain_with_a_live_eager_result(dev):
+    """The layer forward and backward captured into one graph while eager results of the same inputs live; replays
+    on new inputs equal eager calls on them, and leave the earlier results alone."""
+    B, T, D, d = 2, 96, 256, 64
+    g = torch.Generator().manual_seed(9)
+    x, a, b, dy = (torch.randn((B, T, D), generator=g).to(torch.bfloat16).to(dev) for _ in range(4))
+    A_log, bias, table = torch.zeros(D, device=dev), torch.full((D,), -2.0, device=dev), gdn.rotary_table(d, device=dev)
+
+    def layer():
+        q, _ = gdn.rotary(x, None, table, d=d)
+        f = gdn.recurrence_forward(q, a, b, A_log, bias, want_chunk_states=True)
+        n = gdn.group_norm_forward(f.out, groups=4)
+        gn = gdn.group_norm_backward(f.out, None, None, n.mean, n.rstd, dy, groups=4)
+        gr = gdn.recurrence_backward(q, a, b, A_log, bias, gn.dx, None, f.chunk_states)
+        dx, _ = gdn.rotary(gr.dx, None, table, d=d, inverse=True)
+        return n.out, dx, gr.da, gr.dA_log
+
+    eager = layer()
+    kept = [t.clone() for t in eager]
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer()
+    torch.cuda.current_stream().wait_stream(side)
+    with torch.cuda.graph(graph):
+        out = layer()
+    for seed in (1, 2):
+        x.copy_(torch.randn((B, T, D), generator=torch.Generator().manual_seed(seed)).to(torch.bfloat16))
+        graph.replay()
+        for got, want in zip(out, layer()):
+            assert torch.equal(got, want)
+    for t, k in zip(eager, kept):
+        assert torch.equal(t, k)
