@@ -868,15 +868,21 @@ template <typename L> RecPlan make_plan(const gdn_recurrence_desc &d, int per_sm
     return r;
 }
 
-template <typename K>
-cudaError_t launch_chains(K kernel, int threads, const RecPlan &pl, size_t smem, cudaStream_t s, const RecProblem &p, const RecMaps &m) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+// Shared memory that the maps of a chain's CTAs take, by step parity
+template <typename L> constexpr size_t exchange_bytes(int cs) { return 2 * (size_t)cs * 2 * L::CH * sizeof(float); }
+
+// fixed: bytes of shared memory beside the exchanged maps. A kernel's limit is state of the whole process: set to what
+// the call at hand needs, it could be lowered by another host thread's call between this one's setting and its launch,
+// so it is what the largest cluster needs, whatever the call.
+template <typename L, typename K>
+cudaError_t launch_chains(K kernel, const RecPlan &pl, size_t fixed, cudaStream_t s, const RecProblem &p, const RecMaps &m) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(fixed + exchange_bytes<L>(kMaxCluster)));
     if (e == cudaSuccess && pl.cs > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(pl.chains * pl.cs));
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.blockDim = dim3(L::THREADS);
+    cfg.dynamicSmemBytes = fixed + exchange_bytes<L>(pl.cs);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -917,7 +923,7 @@ cudaError_t launch_forward(RecProblem p, cudaStream_t s) {
         return cudaErrorInvalidValue;
     auto kernel = p.cu ? (tma ? rec_forward_kernel<T, true, true> : rec_forward_kernel<T, false, true>)
                        : (tma ? rec_forward_kernel<T, true, false> : rec_forward_kernel<T, false, false>);
-    return launch_chains(kernel, L::THREADS, pl, (tma ? L::STAGES * 3 * L::kTensor : 0) + 2 * (size_t)pl.cs * 2 * L::CH * 4, s, p, m);
+    return launch_chains<L>(kernel, pl, tma ? L::STAGES * 3 * L::kTensor : 0, s, p, m);
 }
 
 template <typename T>
@@ -937,7 +943,7 @@ cudaError_t launch_backward_rec(RecProblem p, cudaStream_t s) {
         return cudaErrorInvalidValue;
     auto kernel = p.cu ? (tma ? rec_backward_kernel<T, true, true> : rec_backward_kernel<T, false, true>)
                        : (tma ? rec_backward_kernel<T, true, false> : rec_backward_kernel<T, false, false>);
-    const cudaError_t e = launch_chains(kernel, L::THREADS, pl, (tma ? L::STAGES * 4 * L::kTensor : 0) + kBwdStash<T> + 2 * (size_t)pl.cs * 2 * L::CH * 4, s, p, m);
+    const cudaError_t e = launch_chains<L>(kernel, pl, (tma ? L::STAGES * 4 * L::kTensor : 0) + kBwdStash<T>, s, p, m);
     if (e != cudaSuccess) return e;
     rec_params_kernel<<<(unsigned)cdiv64(d.D, 32), 256, 0, s>>>(p, d.B * pl.cs);
     return cudaGetLastError();

@@ -77,6 +77,7 @@ constexpr int kThreads = 256;
 constexpr int kBatch = 2;              // units in flight per thread
 constexpr int kBatches = 4;
 constexpr int kTableBytes = 32768;     // cosines and sines of a CTA's tokens
+constexpr int kMostRotated = 32768;    // channels of a head: one token's cosines and sines have to fit
 
 // A head of a token, and the unit u of it, from the index r of a unit among a token's: units_q of them q's, per
 // head `per`.
@@ -273,7 +274,8 @@ cudaError_t launch_rotary(RotaryProblem p, cudaStream_t s) {
     const size_t smem = (size_t)tokens * d.rot * 4;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(rotary_kernel<T, V, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        // the limit is the whole process's: the same for all calls, so that none lowers another's before its launch
+        const cudaError_t e = cudaFuncSetAttribute(rotary_kernel<T, V, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kMostRotated);
         if (e != cudaSuccess) return e;
     }
     rotary_kernel<T, V, HALF><<<dim3((unsigned)std::max<int64_t>(blocks, 1), (unsigned)split), kThreads, smem, s>>>(p);
@@ -300,7 +302,7 @@ int check_desc(const gdn_rotary_desc *d, bool packed) {
     if (d->inverse != 0 && d->inverse != 1) return GDN_ERR_INVALID_ARG;
     if (!dtype_ok(d->dtype)) return GDN_ERR_UNSUPPORTED;
     if ((int64_t)d->d * ((int64_t)d->Hq + d->Hk) > (1 << 24)) return GDN_ERR_UNSUPPORTED;
-    if (d->rot > 32768) return GDN_ERR_UNSUPPORTED;   // one token's cosines and sines in shared memory
+    if (d->rot > kMostRotated) return GDN_ERR_UNSUPPORTED;
     if ((int64_t)d->B * d->T > 0x7fffffff) return GDN_ERR_UNSUPPORTED;
     const int64_t strides[] = {d->q_stride_b, d->q_stride_t, d->q_out_stride_b, d->q_out_stride_t,
                                d->k_stride_b, d->k_stride_t, d->k_out_stride_b, d->k_out_stride_t};

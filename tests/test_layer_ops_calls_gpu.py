@@ -1,0 +1,92 @@
+"""Calls of the operators beside the gated delta rule from several host threads at once."""
+import threading
+
+import pytest
+import torch
+
+from linear_attention_sequence_qkv_gb300 import build, gdn
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    build.build()
+    gdn.load()
+    return torch.device("cuda:0")
+
+
+def at_once(calls, reps):
+    """Each of `calls` (a function that launches on the stream it is given and returns a status) in a host thread
+    and on a stream of its own, `reps` times; the statuses that were not GDN_OK."""
+    torch.cuda.synchronize()
+    bad, start = [], threading.Barrier(len(calls))
+
+    def work(call, stream):
+        stream.synchronize()
+        start.wait()
+        for i in range(reps):
+            rc = call(stream)
+            if rc != gdn.GDN_OK:
+                bad.append(rc)
+            if i % 64 == 63:
+                stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(c, torch.cuda.Stream())) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    return bad
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_recurrences_of_different_clusters_from_two_threads(dev, dtype):
+    """One chain of a row of many tiles (the largest cluster, and the most shared memory) beside rows of one tile (clusters of
+    one CTA): neither call changes what the other may launch with."""
+    calls, checks = [], []
+    for B, T in ((1, 600), (40, 1)):
+        D = 128 // dtype.itemsize
+        x, a, b, dout = (torch.randn(B, T, D, device=dev).to(dtype) for _ in range(4))
+        A_log, bias = torch.zeros(D, device=dev), torch.zeros(D, device=dev)
+        d = gdn.recurrence_desc_for(x, a, b)
+        f, g = gdn.alloc_recurrence(d, dev, want_chunk_states=True), gdn.alloc_recurrence_grads(d, dev)
+
+        def call(stream, d=d, x=x, a=a, b=b, A_log=A_log, bias=bias, f=f, g=g, dout=dout):
+            rc = gdn.gdn_recurrence_forward(d, x, a, b, A_log, bias, None, None, f.out, f.final_state, f.chunk_states,
+                                            f.workspace, f.ws_bytes, stream, check=False)
+            return rc or gdn.gdn_recurrence_backward(d, x, a, b, A_log, bias, None, None, f.chunk_states, dout, None, g.dx,
+                                                     g.da, g.db, g.dA_log, g.ddt_bias, g.dinitial_state, g.workspace,
+                                                     g.ws_bytes, stream, check=False)
+
+        assert call(torch.cuda.current_stream()) == gdn.GDN_OK
+        torch.cuda.synchronize()
+        checks.append((f, g, f.out.clone(), g.da.clone(), g.dA_log.clone()))
+        calls.append(call)
+    assert at_once(calls, 4000) == []
+    for f, g, out, da, dA_log in checks:
+        assert gdn.gdn_device_status(f.workspace) == gdn.GDN_OK and gdn.gdn_device_status(g.workspace) == gdn.GDN_OK
+        assert torch.equal(f.out, out) and torch.equal(g.da, da) and torch.equal(g.dA_log, dA_log)
+
+
+def test_rotations_of_different_widths_from_two_threads(dev):
+    """Heads wide enough that their tables need more shared memory than every kernel may have, of two widths."""
+    calls, checks = [], []
+    for d in (32768, 16384):
+        q = torch.randn(1, 2, d, device=dev).to(torch.bfloat16)
+        table, out = gdn.rotary_table(d, device=dev), torch.empty_like(q)
+        r = gdn.rotary_desc_for(q, None, out, None, d=d)
+        ws = torch.empty(gdn.gdn_rotary_workspace_bytes(r), dtype=torch.uint8, device=dev)
+
+        def call(stream, r=r, q=q, table=table, out=out, ws=ws):
+            return gdn.gdn_rotary(r, q, None, table, None, None, None, out, None, ws, ws.numel(), stream, check=False)
+
+        assert call(torch.cuda.current_stream()) == gdn.GDN_OK
+        torch.cuda.synchronize()
+        checks.append((out, out.clone()))
+        calls.append(call)
+    assert at_once(calls, 8000) == []
+    for out, want in checks:
+        assert torch.equal(out, want)
