@@ -920,6 +920,18 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
+// The driver call behind the tensor maps needs a context, which a host thread has only after its first call of the
+// runtime that binds one: then the map is encoded again.
+template <typename... A>
+bool encode(A... args) {
+    const auto fn = encode_fn();
+    if (!fn) return false;
+    CUresult r = fn(args...);
+    int device;
+    if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&device) == cudaSuccess && cudaSetDevice(device) == cudaSuccess)
+        r = fn(args...);
+    return r == CUDA_SUCCESS;
+}
 
 // Segmented schedule of a long single sequence: one high-priority stream per
 // device for the chain segments and the events that order them against the
@@ -975,21 +987,17 @@ bool encode_tile_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t c
 }
 
 bool encode_tile_map_pitch(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint64_t pitch) {
-    auto fn = encode_fn();
-    if (!fn) return false;
     cuuint64_t dims[2] = {cols, rows};
     cuuint64_t strides[1] = {pitch};
     cuuint32_t box[2] = {64, 64};
     cuuint32_t es[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void *>(base), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void *>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 bool encode_token_map(CUtensorMap *m, int dtype, const void *base, uint64_t batch, uint64_t tokens, uint64_t channels,
                       uint64_t pitch_b, uint64_t pitch_t, uint32_t box_t, uint32_t box_c) {
-    auto fn = encode_fn();
-    if (!fn) return false;
     const cuuint64_t dims[3] = {channels, tokens, batch};
     const cuuint64_t strides[2] = {pitch_t, pitch_b};
     const cuuint32_t box[3] = {box_c, box_t, 1};
@@ -997,9 +1005,8 @@ bool encode_token_map(CUtensorMap *m, int dtype, const void *base, uint64_t batc
     const CUtensorMapDataType type = dtype == GDN_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                      : dtype == GDN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    return fn(m, type, 3, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(m, type, 3, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 bool chunk_tc_supports(const gdn_desc &d) {

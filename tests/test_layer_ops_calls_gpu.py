@@ -90,3 +90,32 @@ def test_rotations_of_different_widths_from_two_threads(dev):
     assert at_once(calls, 8000) == []
     for out, want in checks:
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_first_call_of_a_host_thread(dev, backward):
+    """A thread whose first use of CUDA is the call itself: no context is bound to it yet."""
+    x, a, b, dout = (torch.randn(2, 50, 64, device=dev).to(torch.bfloat16) for _ in range(4))
+    A_log, bias = torch.zeros(64, device=dev), torch.zeros(64, device=dev)
+    d = gdn.recurrence_desc_for(x, a, b)
+    f, g = gdn.alloc_recurrence(d, dev, want_chunk_states=True), gdn.alloc_recurrence_grads(d, dev)
+
+    def call(stream):
+        if backward:
+            return gdn.gdn_recurrence_backward(d, x, a, b, A_log, bias, None, None, f.chunk_states, dout, None, g.dx, g.da,
+                                               g.db, g.dA_log, g.ddt_bias, g.dinitial_state, g.workspace, g.ws_bytes, stream,
+                                               check=False)
+        return gdn.gdn_recurrence_forward(d, x, a, b, A_log, bias, None, None, f.out, f.final_state, f.chunk_states,
+                                          f.workspace, f.ws_bytes, stream, check=False)
+
+    want = gdn.recurrence_forward(x, a, b, A_log, bias, want_chunk_states=True)
+    want_g = gdn.recurrence_backward(x, a, b, A_log, bias, dout, None, want.chunk_states)
+    f.out.zero_(), g.dx.zero_(), f.chunk_states.copy_(want.chunk_states)
+    stream, got = torch.cuda.Stream().cuda_stream, []
+    torch.cuda.synchronize()
+    t = threading.Thread(target=lambda: got.append(call(stream)))
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert got == [gdn.GDN_OK]
+    assert torch.equal(g.dx, want_g.dx) if backward else torch.equal(f.out, want.out)
