@@ -193,16 +193,22 @@ __device__ __forceinline__ void remote_store(uint32_t p, uint32_t bar, uint32_t 
                  "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [ra], {%3, %4, %5, %6}, [rb];\n\t}"
                  :: "r"(p), "r"(bar), "r"(rank), "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y) : "memory");
 }
+// A word into the shared memory of CTA `rank`, seen there after the next cluster barrier
+__device__ __forceinline__ void remote_word(uint32_t p, uint32_t rank, uint32_t v) {
+    asm volatile("{\n\t.reg .b32 ra;\n\tmapa.shared::cluster.u32 ra, %0, %1;\n\tst.shared::cluster.u32 [ra], %2;\n\t}"
+                 :: "r"(p), "r"(rank), "r"(v) : "memory");
+}
+// Counts bytes that an mbarrier expects and nobody sends as arrived
+__device__ __forceinline__ void never_sent(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" :: "r"(tc::smem_u32(bar)), "r"(bytes) : "memory");
+}
 
-// Waits for an mbarrier's phase; the number of tests is limited, to about a second. `failed` makes every later
-// wait a single test, so that a CTA whose copies do not arrive ends soon.
+// A warp's wait for an mbarrier's phase, a second at most (the library's mbar_wait); all lanes call it and leave it with
+// the same answer, since what follows are instructions of the whole warp. `failed` makes every later wait a single test,
+// so that a CTA whose copies do not arrive ends soon.
 __device__ __forceinline__ void bounded_wait(uint64_t *bar, uint32_t phase, bool immediate, bool &failed) {
-    if (tc::mbar_test_now(bar, phase)) return;
-    if (!failed && !immediate)
-#pragma unroll 1
-        for (int i = 0; i < (1 << 24); ++i)
-            if (tc::mbar_test(bar, phase)) return;
-    failed = true;
+    if (__all_sync(0xffffffffu, tc::mbar_test_now(bar, phase))) return;
+    if (failed || immediate || !__all_sync(0xffffffffu, tc::mbar_wait(bar, phase))) failed = true;
 }
 
 // Named barriers of the CTA: all its threads arrive, one side without waiting.
@@ -226,9 +232,14 @@ template <typename L, bool FWD, bool PACKED> struct Chain {
     float4 wc[2][L::WARPS][L::LR];                           // the state carried into each warp
     uint64_t agg_bar[2];                                     // the cluster's maps have arrived
     uint64_t full[L::STAGES];                                // a tile has arrived
+    uint32_t sent[kMaxCluster];                              // steps whose maps each CTA of the cluster has sent
+    uint32_t gave_up;                                        // the carry warp lost something
+    static constexpr uint32_t kMapBytes = L::CH / 2 * 16;    // of one CTA
 
-    __device__ __forceinline__ void init(uint32_t cs) {      // all threads
+    __device__ __forceinline__ void init(uint32_t cs, int steps) {      // all threads
+        if (threadIdx.x < kMaxCluster) sent[threadIdx.x] = steps;
         if (threadIdx.x == 0) {
+            gave_up = 0;
             for (int i = 0; i < 2; ++i) tc::mbar_init(&agg_bar[i], 1);
             for (int i = 0; i < L::STAGES; ++i) tc::mbar_init(&full[i], 1);
             tc::mbar_init_fence();
@@ -266,8 +277,8 @@ template <typename L, bool FWD, bool PACKED> struct Chain {
     // the cluster. agg: [2][cs][CH / 2] of (A, A, B, B), the maps of the cluster's CTAs by step parity. A CTA writes
     // agg[k % 2] of another only after it has that CTA's map of step k - 1, which that CTA's carry warp sends
     // after it is done with step k - 2. `lost`: something did not arrive; nothing more is sent or waited for.
-    // This is the latency of a step: everything else is done beside it.
-    __device__ __forceinline__ void carry_step(float2 &carry, int lane, uint32_t rank, uint32_t cs, int k, float4 *agg, bool &lost) {
+    // immediate: the test mode of the waits. This is the latency of a step: everything else is done beside it.
+    __device__ __forceinline__ void carry_step(float2 &carry, int lane, uint32_t rank, uint32_t cs, int k, float4 *agg, bool immediate, bool &lost) {
         constexpr int kHalf = L::CH / 2;
         const int c2 = lane % kHalf;
         named_sync(kMapsBar + (k & 1), L::THREADS);
@@ -288,12 +299,12 @@ template <typename L, bool FWD, bool PACKED> struct Chain {
             float4 *at = agg + (k & 1) * cs * kHalf;
             if (!lost) {
                 const uint32_t mine = tc::smem_u32(at + rank * kHalf + c2), bar = tc::smem_u32(&agg_bar[k & 1]);
-                if (lane == 0) tc::mbar_expect_tx(&agg_bar[k & 1], cs * kHalf * 16);
+                if (lane == 0) tc::mbar_expect_tx(&agg_bar[k & 1], cs * kMapBytes);
                 if (lane < kHalf)
 #pragma unroll 4
                     for (uint32_t r = 0; r < cs; ++r) remote_store(mine, bar, r, tA, tB);
                 __syncwarp();
-                bounded_wait(&agg_bar[k & 1], (k >> 1) & 1, false, lost);
+                bounded_wait(&agg_bar[k & 1], (k >> 1) & 1, immediate, lost);
             }
 #pragma unroll 4
             for (uint32_t r = 0; r < cs; ++r) {
@@ -309,6 +320,41 @@ template <typename L, bool FWD, bool PACKED> struct Chain {
         }
         if (cs == 1) carry = c;
         named_arrive(kStatesBar + (k & 1), L::THREADS);
+    }
+
+    // The carry warp after its last step: it has issued the copies of `issued` tiles (first lane), of which the last ones
+    // may not have been waited for, and sent its maps of `steps_sent` steps.
+    __device__ __forceinline__ void end_carry(bool copies, int issued, int steps_sent, bool lost, int lane, uint32_t rank, uint32_t cs, int32_t *status) {
+        if (copies && lane == 0)
+            for (int k = max(0, issued - L::STAGES); k < issued; ++k) tc::mbar_wait(&full[k % L::STAGES], (k / L::STAGES) & 1);
+        if (lost) {
+            if (lane == 0) gave_up = 1, *status = GDN_ERR_DEVICE_TIMEOUT;
+            if (lane < (int)cs) remote_word(tc::smem_u32(&sent[rank]), lane, steps_sent);
+        }
+        __syncwarp();
+    }
+
+    // The end of a CTA; all threads. No map may be on its way to it when it leaves. A CTA that lost nothing has had them
+    // all. One that did, and so sent its own of s steps, may not have all of step s - 1 (those of the CTAs that sent
+    // theirs are still waited for), nor any of step s, which it does not expect and a CTA that had all of step s - 1
+    // sends. Nothing later: step s + 1 is sent only with this CTA's map of step s.
+    __device__ __forceinline__ void leave(uint32_t rank, uint32_t cs) {
+        __syncwarp();
+        if (cs == 1) {
+            __syncthreads();
+            return;
+        }
+        cluster_sync();   // nobody sends any more, and everyone's `sent` is known
+        if (!gave_up || threadIdx.x != 0) return;
+        const int s = (int)sent[rank];
+        for (int k = s - 1; k <= s; ++k) {
+            uint32_t n = 0;
+            for (uint32_t r = 0; r < cs; ++r) n += (int)sent[r] > k;
+            if (k == s && n == 0) break;
+            if (k == s) tc::mbar_expect_tx(&agg_bar[k & 1], n * kMapBytes);
+            else if (n < cs) never_sent(&agg_bar[k & 1], (cs - n) * kMapBytes);
+            tc::mbar_wait(&agg_bar[k & 1], (k >> 1) & 1);
+        }
     }
 };
 
@@ -390,13 +436,16 @@ rec_forward_kernel(const __grid_constant__ RecProblem p, const __grid_constant__
     if (!ok) return;   // the same in every CTA
     const int steps = (p.ntiles + (int)cs - 1) / (int)cs;
     const int mine = (p.ntiles - 1 - (int)rank + (int)cs) / (int)cs;   // steps in which this CTA has a tile
-    chain.init(cs);
-    bool failed = false, lost = false;
+    chain.init(cs, steps);
+    bool failed = false;
 
     if (warp == L::WARPS) {   // the carry warp
         float4 *agg = (float4 *)(smem + (TMA ? L::STAGES * 3 * L::kTensor : 0));
+        bool lost = false;
+        int issued = 0;
         auto issue = [&](int k) {
             if (!TMA || lane != 0 || k >= mine) return;
+            issued = k + 1;
             uint64_t *bar = &chain.full[k % L::STAGES];
             unsigned char *st = smem + k % L::STAGES * 3 * L::kTensor;
             const int t = (k * (int)cs + (int)rank) * L::TT;
@@ -408,13 +457,16 @@ rec_forward_kernel(const __grid_constant__ RecProblem p, const __grid_constant__
         if (p.wait_immediate) __nanosleep(20000);   // the compute warps' first wait cannot be over
         for (int k = 0; k < L::STAGES; ++k) issue(k);
         float2 carry = splat2(0.f);
+        int sent = 0;
         for (int k = 0; k < steps; ++k) {
-            chain.carry_step(carry, lane, rank, cs, k, agg, lost);
+            if (!lost) sent = k + 1;
+            chain.carry_step(carry, lane, rank, cs, k, agg, p.wait_immediate, lost);
             // the maps are in, so every warp has read tile k
             if (TMA && k < mine) bounded_wait(&chain.full[k % L::STAGES], (k / L::STAGES) & 1, false, lost);   // long since
             if (!lost) issue(k + L::STAGES);
             __syncwarp();
         }
+        chain.end_carry(TMA, issued, sent, lost, lane, rank, cs, p.status);
     } else {
         const int g = lane / L::LR, q = lane % L::LR;
         const Columns<L, TMA> col(slab, q, d.D);
@@ -538,14 +590,8 @@ rec_forward_kernel(const __grid_constant__ RecProblem p, const __grid_constant__
             }
         }
     }
-    if (failed || lost) *p.status = GDN_ERR_DEVICE_TIMEOUT;
-    // copies in flight end before the CTA does (they have, unless a wait gave up), and no CTA leaves while
-    // another may still write to it
-    if (TMA && warp == L::WARPS && lane == 0)
-        for (int k = max(0, mine - L::STAGES); k < mine; ++k) tc::mbar_wait(&chain.full[k % L::STAGES], (k / L::STAGES) & 1);
-    __syncwarp();
-    if (cs > 1) cluster_sync();
-    else __syncthreads();
+    if (failed) *p.status = GDN_ERR_DEVICE_TIMEOUT;
+    chain.leave(rank, cs);
 }
 
 // The reverse walk: c_t = alpha_t (v_t + c_{t+1}), delta_t = v_t + c_{t+1} with v = grad_out, tiles last to
@@ -573,13 +619,16 @@ rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant_
     if (!ok) return;
     const int steps = (p.ntiles + (int)cs - 1) / (int)cs;
     const int mine = (p.ntiles - 1 - (int)rank + (int)cs) / (int)cs;
-    chain.init(cs);
-    bool failed = false, lost = false;
+    chain.init(cs, steps);
+    bool failed = false;
 
     if (warp == L::WARPS) {
         float4 *agg = (float4 *)(smem + (TMA ? L::STAGES * 4 * L::kTensor : 0) + kBwdStash<T>);
+        bool lost = false;
+        int issued = 0;
         auto issue = [&](int k) {
             if (!TMA || lane != 0 || k >= mine) return;
+            issued = k + 1;
             uint64_t *bar = &chain.full[k % L::STAGES];
             unsigned char *st = smem + k % L::STAGES * 4 * L::kTensor;
             const int t = (p.ntiles - 1 - (k * (int)cs + (int)rank)) * L::TT;
@@ -592,8 +641,10 @@ rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant_
         if (p.wait_immediate) __nanosleep(20000);   // the compute warps' first wait cannot be over
         for (int k = 0; k < L::STAGES; ++k) issue(k);
         float2 carry = splat2(0.f);
+        int sent = 0;
         for (int k = 0; k < steps; ++k) {
-            chain.carry_step(carry, lane, rank, cs, k, agg, lost);
+            if (!lost) sent = k + 1;
+            chain.carry_step(carry, lane, rank, cs, k, agg, p.wait_immediate, lost);
             // the maps are in, so every warp is done with the tile before
             const int was = k - 1;
             if (was >= 0) {
@@ -602,6 +653,7 @@ rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant_
                 __syncwarp();
             }
         }
+        chain.end_carry(TMA, issued, sent, lost, lane, rank, cs, p.status);
     } else {
         const int g = lane / L::LR, q = lane % L::LR;
         const Columns<L, TMA> col(slab, q, d.D);
@@ -782,14 +834,8 @@ rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant_
         for (int j = 0; j < L::NG; ++j) s += red[j][which][v];
         p.part[(((int64_t)row * cs + rank) * 2 + which) * d.D + c] = s;
     }
-    if (failed || lost) *p.status = GDN_ERR_DEVICE_TIMEOUT;
-    // copies in flight end before the CTA does (they have, unless a wait gave up), and no CTA leaves while
-    // another may still write to it
-    if (TMA && warp == L::WARPS && lane == 0)
-        for (int k = max(0, mine - L::STAGES); k < mine; ++k) tc::mbar_wait(&chain.full[k % L::STAGES], (k / L::STAGES) & 1);
-    __syncwarp();
-    if (cs > 1) cluster_sync();
-    else __syncthreads();
+    if (failed) *p.status = GDN_ERR_DEVICE_TIMEOUT;
+    chain.leave(rank, cs);
 }
 
 // The parameter gradients: part[parts][2][D] over its rows, 8 strided partial sums per channel.

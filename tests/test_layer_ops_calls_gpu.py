@@ -1,5 +1,7 @@
-"""Calls of the operators beside the gated delta rule from several host threads at once."""
+"""Calls of the operators beside the gated delta rule that are not one after the other from one host thread: several threads
+at once, a thread's first call, and calls whose waits run out."""
 import threading
+import time
 
 import pytest
 import torch
@@ -119,3 +121,41 @@ def test_first_call_of_a_host_thread(dev, backward):
     torch.cuda.synchronize()
     assert got == [gdn.GDN_OK]
     assert torch.equal(g.dx, want_g.dx) if backward else torch.equal(f.out, want.out)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("B,T,D,waits", [(1, 1000, 63, True), (1, 1000, 64, True), (3, 530, 99, True), (1, 130, 24, True),
+                                         (2, 31, 5, False)])
+def test_maps_that_do_not_arrive_are_reported(dev, B, T, D, waits, packed, dtype):
+    """gdn_set_wait_test_mode where CTAs of a cluster wait for one another, also without copies into shared memory to wait
+    for (D odd): the CTAs give up, report it, and wait for what is on its way to them but not for what nobody
+    issued (a second each), and the next calls are right. One CTA per row without copies (31 tokens of 5 channels) waits
+    for nothing."""
+    B = 1 if packed else B
+    x, a, b, dout = (torch.randn(B, T, D, device=dev).to(dtype) for _ in range(4))
+    A_log, bias = torch.zeros(D, device=dev), torch.full((D,), -2.0, device=dev)
+    cu = torch.tensor([0, T // 3, T // 3, T // 2 + 1, T], dtype=torch.int32, device=dev) if packed else None
+    fwd = lambda: gdn.recurrence_forward(x, a, b, A_log, bias, cu, want_chunk_states=True)  # noqa: E731
+    bwd = lambda cs: gdn.recurrence_backward(x, a, b, A_log, bias, dout, None, cs, cu)  # noqa: E731
+    want = fwd()
+    want_g = bwd(want.chunk_states)
+    assert gdn.gdn_device_status(want_g.workspace) == gdn.GDN_OK
+    torch.cuda.synchronize()
+    gdn.gdn_set_wait_test_mode(1)
+    try:
+        start = time.perf_counter()
+        for _ in range(10):
+            got = [gdn.gdn_device_status(f.workspace) for f in (fwd(), bwd(want.chunk_states), bwd(None))]
+            assert got == [gdn.GDN_ERR_DEVICE_TIMEOUT if waits else gdn.GDN_OK] * 3
+        took = time.perf_counter() - start
+    finally:
+        gdn.gdn_set_wait_test_mode(0)
+    assert took < 0.5
+    for _ in range(2):
+        again = fwd()
+        again_g = bwd(again.chunk_states)
+        assert gdn.gdn_device_status(again.workspace) == gdn.GDN_OK and gdn.gdn_device_status(again_g.workspace) == gdn.GDN_OK
+        assert torch.equal(again.out, want.out) and torch.equal(again.final_state, want.final_state)
+        for name in ("dx", "da", "db", "dA_log", "ddt_bias", "dinitial_state"):
+            assert torch.equal(getattr(again_g, name), getattr(want_g, name)), name
