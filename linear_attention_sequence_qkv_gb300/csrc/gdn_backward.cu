@@ -1455,6 +1455,14 @@ int serial_tile(const gdn_desc &d) {
     return 16;
 }
 
+// the most that any dk asks of a tile's kernel: its limit, whatever the call (see allow_shared)
+template <int NV>
+size_t serial_smem_most() {
+    int dk = 512;
+    while (serial_smem_bytes<NV>(dk) > 227 * 1024) dk /= 2;
+    return serial_smem_bytes<NV>(dk);
+}
+
 template <typename T, int NV>
 cudaError_t launch_serial(const BwdProblem &bp, bool reverse, cudaStream_t s) {
     const gdn_desc &d = bp.f.d;
@@ -1464,12 +1472,12 @@ cudaError_t launch_serial(const BwdProblem &bp, bool reverse, cudaStream_t s) {
     cudaError_t e;
     if (!reverse) {
         const size_t bytes = serial_smem_bytes<NV>(d.dk);
-        e = cudaFuncSetAttribute(states_kernel<T, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        e = allow_shared(states_kernel<T, NV>, serial_smem_most<NV>());
         if (e != cudaSuccess) return e;
         states_kernel<T, NV><<<(unsigned)blocks, 4 * NV, bytes, s>>>(bp, ntiles);
     } else {
         const size_t bytes = serial_smem_bytes<NV>(d.dk);
-        e = cudaFuncSetAttribute(chain_bwd_kernel<T, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        e = allow_shared(chain_bwd_kernel<T, NV>, serial_smem_most<NV>());
         if (e != cudaSuccess) return e;
         chain_bwd_kernel<T, NV><<<(unsigned)blocks, 4 * NV, bytes, s>>>(bp, ntiles);
     }

@@ -493,8 +493,9 @@ bool dterms_tc_supports(const gdn_desc &d) {
 
 cudaError_t launch_dterms_tc(const BwdProblem &bp, int64_t slots, cudaStream_t s) {
     const gdn_desc &d = bp.f.d;
-    const size_t bytes = 1024 + 32768 + 2 * 64 * (size_t)d.dv * 2;
-    cudaError_t e = cudaFuncSetAttribute(dterms_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    const auto smem = [](int dv) { return 1024 + 32768 + 2 * 64 * (size_t)dv * 2; };
+    const size_t bytes = smem(d.dv);
+    cudaError_t e = allow_shared(dterms_tc_kernel, smem(512));
     if (e != cudaSuccess) return e;
     dterms_tc_kernel<<<dim3((unsigned)slots, d.Hv), kOThreads, bytes, s>>>(bp);
     return cudaGetLastError();
@@ -506,8 +507,9 @@ bool out_tc_supports(const gdn_desc &d) {
 
 cudaError_t launch_out_tc(const BwdProblem &bp, int64_t slots, cudaStream_t s) {
     const gdn_desc &d = bp.f.d;
-    const size_t bytes = 1024 + 16384 + 64 * (size_t)d.dv * 2;
-    cudaError_t e = cudaFuncSetAttribute(out_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    const auto smem = [](int dv) { return 1024 + 16384 + 64 * (size_t)dv * 2; };
+    const size_t bytes = smem(d.dv);
+    cudaError_t e = allow_shared(out_tc_kernel, smem(512));
     if (e != cudaSuccess) return e;
     out_tc_kernel<<<dim3((unsigned)slots, d.Hv), kOThreads, bytes, s>>>(bp);
     return cudaGetLastError();
@@ -519,8 +521,9 @@ bool chunk_x_tc_supports(const gdn_desc &d) {
 
 cudaError_t launch_chunk_x_tc(const BwdProblem &bp, int64_t slots, cudaStream_t s) {
     const gdn_desc &d = bp.f.d;
-    const size_t bytes = 1024 + 32768 + 2 * (size_t)d.dk * 128;
-    cudaError_t e = cudaFuncSetAttribute(chunk_x_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    const auto smem = [](int dk) { return 1024 + 32768 + 2 * (size_t)dk * 128; };
+    const size_t bytes = smem(d.dk);
+    cudaError_t e = allow_shared(chunk_x_kernel, smem(256));
     if (e != cudaSuccess) return e;
     chunk_x_kernel<<<dim3((unsigned)slots, d.Hv), kXThreads, bytes, s>>>(bp);
     return cudaGetLastError();

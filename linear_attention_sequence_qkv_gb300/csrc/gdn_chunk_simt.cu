@@ -275,8 +275,8 @@ template <typename T, int NV>
 cudaError_t launch_nv(const Problem &p, cudaStream_t s) {
     const int ntiles = p.d.dv / NV;
     const size_t bytes = simt_smem_floats<NV>(p.d.dk) * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(chunk_simt_kernel<T, NV>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    // the widest dk of this tile (launch_t)
+    cudaError_t e = allow_shared(chunk_simt_kernel<T, NV>, simt_smem_floats<NV>(NV == 64 ? 256 : 512) * sizeof(float));
     if (e != cudaSuccess) return e;
     const int64_t blocks = (int64_t)p.d.N * p.d.Hv * ntiles;
     if (blocks == 0) return cudaSuccess;

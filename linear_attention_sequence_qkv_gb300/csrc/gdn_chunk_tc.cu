@@ -32,6 +32,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "gdn_common.cuh"
@@ -980,6 +981,12 @@ int max_dyn_smem() {
     return v;
 }
 
+// The chain kernel holds all 512 TMEM columns: it asks for enough shared memory that a second CTA never shares the SM
+// (its allocation would wait for this one).
+size_t chain_smem(const ChainSmem &cs, int maxs) { return std::max(cs.total, (size_t)(maxs / 2 + 1024)); }
+// the most that a kernel of this number of stages is launched with
+size_t chain_smem_most(int stages, int maxs) { return chain_smem(ChainSmem(stages == 3 ? 128 : 256), maxs); }
+
 }  // namespace
 
 bool encode_tile_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols) {
@@ -1068,13 +1075,11 @@ cudaError_t launch_chunk_tc(const Problem &p, cudaStream_t s) {
     }
     const int maxs = max_dyn_smem();
     const ChainSmem cs(d.dk);
-    // the kernel holds all 512 TMEM columns: request enough shared memory that a
-    // second CTA never shares the SM (its allocation would wait for this one)
-    const size_t smem = cs.total > (size_t)(maxs / 2 + 1024) ? cs.total : (size_t)(maxs / 2 + 1024);
+    const size_t smem = chain_smem(cs, maxs);
     if ((int)smem > maxs) return cudaErrorInvalidValue;
     auto chain = p.wait_immediate ? (cs.stages == 3 ? chunk_chain_kernel<3, false, true> : chunk_chain_kernel<2, false, true>)
                                   : (cs.stages == 3 ? chunk_chain_kernel<3> : chunk_chain_kernel<2>);
-    cudaError_t e = cudaFuncSetAttribute(chain, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_shared(chain, chain_smem_most(cs.stages, maxs));
     if (e != cudaSuccess) return e;
     const int ntiles = d.dv / 64;
     const int64_t blocks = (int64_t)d.N * d.Hv * ntiles;
@@ -1114,11 +1119,10 @@ cudaError_t launch_chunk_tc_rec(const Problem &p, cudaStream_t s) {
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int maxs = max_dyn_smem();
     const ChainSmem cs(d.dk);
-    const size_t smem = cs.total > (size_t)(maxs / 2 + 1024) ? cs.total : (size_t)(maxs / 2 + 1024);
+    const size_t smem = chain_smem(cs, maxs);
     if ((int)smem > maxs) return cudaErrorInvalidValue;
     auto chain = cs.stages == 3 ? chunk_chain_kernel<3, true> : chunk_chain_kernel<2, true>;
-    if ((e = cudaFuncSetAttribute(chain, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
-        return e;
+    if ((e = allow_shared(chain, chain_smem_most(cs.stages, maxs))) != cudaSuccess) return e;
     const int ntiles = d.dv / 64;
     const int64_t blocks = (int64_t)d.N * d.Hv * ntiles;
     if (blocks == 0) return cudaSuccess;
@@ -1170,13 +1174,11 @@ cudaError_t launch_chunk_tc_segmented(const Problem &p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int maxs = max_dyn_smem();
     const ChainSmem cs(d.dk);
-    const size_t smem = cs.total > (size_t)(maxs / 2 + 1024) ? cs.total : (size_t)(maxs / 2 + 1024);
+    const size_t smem = chain_smem(cs, maxs);
     if ((int)smem > maxs) return cudaErrorInvalidValue;
     auto chain = p.wait_immediate ? (cs.stages == 3 ? chunk_chain_kernel<3, false, true> : chunk_chain_kernel<2, false, true>)
                                   : (cs.stages == 3 ? chunk_chain_kernel<3> : chunk_chain_kernel<2>);
-    if ((e = cudaFuncSetAttribute(chain, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
-        cudaSuccess)
-        return e;
+    if ((e = allow_shared(chain, chain_smem_most(cs.stages, maxs))) != cudaSuccess) return e;
     const int ntiles = d.dv / 64;
     int dev = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;

@@ -19,6 +19,13 @@ namespace gdn {
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// A kernel's limit of dynamic shared memory belongs to the whole process: `most` is what any call of the kernel may launch
+// it with, not what this one does, so that no host thread lowers the limit of another's launch.
+template <typename K>
+cudaError_t allow_shared(K kernel, size_t most) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+}
+
 template <typename... KArgs, typename... Args>
 cudaError_t launch_kernel(bool pdl, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                           cudaStream_t s, Args &&...args) {

@@ -917,12 +917,10 @@ template <typename L> RecPlan make_plan(const gdn_recurrence_desc &d, int per_sm
 // Shared memory that the maps of a chain's CTAs take, by step parity
 template <typename L> constexpr size_t exchange_bytes(int cs) { return 2 * (size_t)cs * 2 * L::CH * sizeof(float); }
 
-// fixed: bytes of shared memory beside the exchanged maps. A kernel's limit is state of the whole process: set to what
-// the call at hand needs, it could be lowered by another host thread's call between this one's setting and its launch,
-// so it is what the largest cluster needs, whatever the call.
+// fixed: bytes of shared memory beside the exchanged maps
 template <typename L, typename K>
 cudaError_t launch_chains(K kernel, const RecPlan &pl, size_t fixed, cudaStream_t s, const RecProblem &p, const RecMaps &m) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(fixed + exchange_bytes<L>(kMaxCluster)));
+    cudaError_t e = allow_shared(kernel, fixed + exchange_bytes<L>(kMaxCluster));
     if (e == cudaSuccess && pl.cs > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};

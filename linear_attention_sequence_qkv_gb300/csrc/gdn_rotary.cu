@@ -274,8 +274,7 @@ cudaError_t launch_rotary(RotaryProblem p, cudaStream_t s) {
     const size_t smem = (size_t)tokens * d.rot * 4;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     if (smem > 48 * 1024) {
-        // the limit is the whole process's: the same for all calls, so that none lowers another's before its launch
-        const cudaError_t e = cudaFuncSetAttribute(rotary_kernel<T, V, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kMostRotated);
+        const cudaError_t e = allow_shared(rotary_kernel<T, V, HALF>, 4 * kMostRotated);
         if (e != cudaSuccess) return e;
     }
     rotary_kernel<T, V, HALF><<<dim3((unsigned)std::max<int64_t>(blocks, 1), (unsigned)split), kThreads, smem, s>>>(p);

@@ -59,8 +59,9 @@ __global__ void __launch_bounds__(kScanThreads) span_scan_kernel(int spans, int 
 
 cudaError_t launch_span_scan(int spans, int Hv, int dk, int dv, const float *A, const float *B, const float *h0,
                              float *H_in, cudaStream_t s) {
-    const size_t bytes = 2 * (size_t)dk * kScanCols * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(span_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    const auto smem = [](int dk) { return 2 * (size_t)dk * kScanCols * sizeof(float); };
+    const size_t bytes = smem(dk);
+    cudaError_t e = allow_shared(span_scan_kernel, smem(512));
     if (e != cudaSuccess) return e;
     span_scan_kernel<<<dim3(Hv, (dv + kScanCols - 1) / kScanCols), kScanThreads, bytes, s>>>(spans, Hv, dk, dv, A, B,
                                                                                             h0, H_in);
