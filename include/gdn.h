@@ -191,7 +191,8 @@ int gdn_device_status(const void *workspace, int *status, gdn_stream_t stream);
 const char *gdn_status_string(int status);
 
 /*
- * Test hook for the tensor-core kernels' bounded waits (GDN_ERR_DEVICE_TIMEOUT).
+ * Test hook for the bounded waits (GDN_ERR_DEVICE_TIMEOUT) of the tensor-core kernels
+ * and of the gated linear recurrence (below).
  * Every wait of those kernels on one of their own mbarriers gives up after about
  * a second; the CTA then records GDN_ERR_DEVICE_TIMEOUT, waits (again bounded) for
  * its own copies and products in flight, frees its tensor memory and returns.
@@ -411,7 +412,9 @@ int gdn_backward(const gdn_desc *d,
  *
  * Alignment: every tensor needs the alignment of its own element type; rows that
  * are 16-byte aligned (base pointer, strides and row length) take the vector
- * kernels, others element-wise ones with the same results.
+ * kernels, others element-wise ones. The two agree to the rounding of fp32
+ * arithmetic (the recurrence and the group norm add up in another order).
+ * "Run-to-run identical" below means calls of the same sizes and alignment.
  */
 
 /*
@@ -464,8 +467,9 @@ int gdn_recurrence_backward_workspace_bytes(const gdn_recurrence_desc *d, size_t
  *                  gdn_device_status reads its status word
  * x, a, b and out may be NULL when B*T == 0. initial_state and final_state may
  * alias; other outputs must not overlap the inputs. A malformed cu_seqlens sets
- * GDN_ERR_DEVICE_SEQLENS and nothing else is written. Copies into shared memory are
- * waited for about a second at most (GDN_ERR_DEVICE_TIMEOUT, results invalid).
+ * GDN_ERR_DEVICE_SEQLENS and nothing else is written. Copies into shared memory, and
+ * what the CTAs that share a row pass on to one another, are waited for about a second
+ * at most (GDN_ERR_DEVICE_TIMEOUT, results invalid).
  */
 int gdn_recurrence_forward(const gdn_recurrence_desc *d, const void *x, const void *a, const void *b,
                            const float *A_log, const float *dt_bias, const int32_t *cu_seqlens,

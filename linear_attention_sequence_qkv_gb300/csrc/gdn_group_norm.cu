@@ -17,7 +17,8 @@
 //
 // The backward has the same two forms, with the sums of t and t xh in the statistics'
 // place. Parameter gradients are summed per warp over its rows, written as partial rows
-// and added up by a last small kernel. Every order is fixed by the sizes.
+// and added up by a last small kernel. Every order is fixed by the sizes and
+// by whether vectors fit.
 //
 // Measured, of the copy rate: rows of 4096 in 32 groups, bf16, 131072 forward 380 us (83 %),
 // 65536 fp16 forward 193 us (82 %) and backward 347 us (68 %: 110 registers, two blocks per SM,

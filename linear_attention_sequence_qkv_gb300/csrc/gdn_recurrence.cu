@@ -18,9 +18,9 @@
 //     which cuts the chain: packed sequences are nothing special to the scan, whatever
 //     their lengths.
 //
-// The order of every composition and sum is fixed by the sizes alone, so results are
-// run-to-run identical. Tiles come in by TMA (from rows that are 16-byte aligned; other
-// tensors are read element by element, a tile ahead).
+// The order of every composition and sum is fixed by the sizes and by whether TMA can take
+// the rows, so results are run-to-run identical. Tiles come in by TMA (from rows that are
+// 16-byte aligned; other tensors are read element by element, a tile ahead).
 //
 // What bounds them, measured: fp32 the bandwidth (65536 x 4096 forward 642 us, 99 % of the
 // copy rate); 16-bit types the issue rate and the latency of a step, 42 instructions per
