@@ -82,3 +82,27 @@ def test_two_widths_of_states_across_spans(dev):
     assert both(calls, 3000) == []
     for H, want in checks:
         assert torch.equal(H, want)
+
+
+@pytest.mark.parametrize("dtype,dk,dv", [("bf16", 64, 64), ("bf16", 128, 128), ("fp32", 64, 64)])
+def test_stages_as_a_threads_first_calls(dev, dtype, dk, dv):
+    """The chunk stage encodes its tensor maps before it launches anything: the thread has no context yet."""
+    w = replace(WORKLOADS["tiny_fp32"], dtype=dtype, T=130, Hk=1, Hv=2, dk=dk, dv=dv)
+    inp = to_device(make_inputs(w), dev)
+    want = gdn.forward(inp)
+    d, bufs, stream, got = want.desc, gdn.alloc(want.desc, dev), torch.cuda.Stream().cuda_stream, []
+    gdn.gdn_prologue(d, inp.q_raw, inp.k_raw, inp.v_raw, inp.a, inp.b, inp.conv_w, inp.A_log, inp.dt_bias, None,
+                     bufs.workspace, bufs.ws_bytes)
+    torch.cuda.synchronize()
+
+    def rest():
+        got.append(gdn.gdn_chunk_rule(d, None, inp.initial_state, bufs.final_state, bufs.workspace, bufs.ws_bytes, stream,
+                                      check=False))
+        got.append(gdn.gdn_epilogue(d, inp.gate, inp.norm_w, bufs.out, bufs.workspace, bufs.ws_bytes, stream, check=False))
+
+    t = threading.Thread(target=rest)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert got == [gdn.GDN_OK] * 2
+    assert torch.equal(bufs.out, want.out) and torch.equal(bufs.final_state, want.final_state)

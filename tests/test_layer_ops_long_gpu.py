@@ -224,3 +224,29 @@ def test_parameter_gradients_over_many_tiles(dev, dtype, B, T, D):
         use = (np.abs(n64(t) - ref) / O.bound(ref, err, "fp32")).max()
         print(f"[recurrence, long] {name} {dtype}: bound_use={use:.3f} bound={(err / np.abs(ref)).max():.2e}")
         assert use <= 1.0, name
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 72), ("fp32", 9)])
+def test_thousands_of_short_sequences(dev, dtype, D):
+    """Five thousand sequences of none to five tokens, with runs of empty ones at both ends."""
+    rng = np.random.default_rng(D)
+    lengths = [0] * 300 + list(rng.integers(0, 6, 4000)) + [0] * 500 + [1] * 40 + [0] * 200
+    T, N = int(sum(lengths)), len(lengths)
+    cu = np.concatenate([[0], np.cumsum(lengths)])
+    g = torch.Generator().manual_seed(D)
+    randn = lambda *v: torch.randn(*v, generator=g)  # noqa: E731
+    s = {k: randn(1, T, D).to(ACT[dtype]).to(dev) for k in ("x", "a", "b", "dout")}
+    s.update(A_log=(0.5 * randn(D) - 1.0).to(dev), dt_bias=(randn(D) - 2.0).to(dev), h0=randn(N, D).to(dev),
+             dfinal=randn(N, D).to(dev), cu=torch.tensor(cu, dtype=torch.int32, device=dev))
+    f = forward(s, want_chunk_states=True)
+    got = backward(s, f.chunk_states)
+    assert gdn.gdn_device_status(got.workspace) == gdn.GDN_OK
+    flat = lambda t: n64(t).reshape(-1, D)  # noqa: E731
+    r = O.recurrence(flat(s["x"]), flat(s["a"]), flat(s["b"]), n64(s["A_log"]), n64(s["dt_bias"]), cu.tolist(), n64(s["h0"]),
+                     flat(s["dout"]), n64(s["dfinal"]))
+    for name, t in (("out", f.out), ("final", f.final_state), ("dx", got.dx), ("da", got.da), ("db", got.db),
+                    ("dA_log", got.dA_log), ("ddt_bias", got.ddt_bias), ("dstate", got.dinitial_state)):
+        tol = O.bound(r[name], r[name + "_err"], dtype if name in ("out", "dx", "da", "db") else "fp32")
+        use = (np.abs(n64(t).reshape(r[name].shape) - r[name]) / tol).max()
+        print(f"[recurrence, many] {name} {dtype}: bound_use={use:.3f}")
+        assert use <= 1.0, name
