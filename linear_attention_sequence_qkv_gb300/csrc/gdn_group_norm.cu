@@ -21,12 +21,12 @@
 // by whether vectors fit.
 //
 // Measured, of the copy rate: rows of 4096 in 32 groups, bf16, 131072 forward 380 us (83 %),
-// 65536 fp16 forward 193 us (82 %) and backward 347 us (68 %: 110 registers, two blocks per SM,
-// issue slots 58 % used); in one group, 131072 forward, 510 us (62 %: two block-wide sums a
-// row). Over positions: 60 x 16384 x 512 in 8 groups, forward, 473 us (63 %; 94 % counting the
-// second read); 2 x 2048 x 1536 in 6 groups 10 us and 17 us backward, launches and latency. Groups
-// that are no multiple of 16 bytes go element by element: 100000 rows of 4160 in 64 groups
-// 1060 us (23 %), issue-bound.
+// 65536 fp16 forward 195 us (81 %) and backward 349 us (68 %: 110 registers, two blocks per SM,
+// issue slots 58 % used); in one group, 131072 forward, 523 us (60 %: two block-wide sums a
+// row). Over positions: 60 x 16384 x 512 in 8 groups, forward, 472 us (63 %; 94 % counting the
+// second read); 2 x 2048 x 1536 in 6 groups 10 us and 17 us backward on the device, launches and
+// latency. Groups that are no multiple of 16 bytes go element by element: 100000 rows of 4160 in
+// 64 groups 1070 us (23 %), issue-bound.
 #include <string.h>
 
 #include <algorithm>
@@ -55,8 +55,8 @@ struct NormProblem {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 // Blocks per SM, resident at once: rows forward, general forward and backward. Three for the last is
-// slower (2 x 2048 x 1536 in 6 groups 24.9 against 20.7 us, 60 x 2000 x 2048 in 16 540 against 464 us): registers
-// hold two.
+// slower (2 x 2048 x 1536 in 6 groups 21.1 against 17.1 us on the device, 60 x 2000 x 2048 in 16 542 against 464 us):
+// registers hold two.
 constexpr int kBlocksForward = 3, kBlocksGeneral = 4, kBlocksSums = 2;
 // The rows backward: three where their registers fit (vectors of four fp32, or no activation's derivative: 65536 x 4096
 // in 32 groups fp32 526 against 625 us with two, in 64 without activation bf16 301 against 323), else two (in 32 with

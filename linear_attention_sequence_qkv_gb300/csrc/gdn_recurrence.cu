@@ -22,11 +22,12 @@
 // the rows, so results are run-to-run identical. Tiles come in by TMA (from rows that are
 // 16-byte aligned; other tensors are read element by element, a tile ahead).
 //
-// What bounds them, measured: fp32 the bandwidth (65536 x 4096 forward 642 us, 99 % of the
-// copy rate); 16-bit types the issue rate and the latency of a step, 42 instructions per
-// element forward and 67 backward (131072 x 4096 bf16 forward 1038 us, 61 % of the copy
-// rate; 65536 x 4096 in 16 sequences 613 us forward, which also writes the states, and
-// 1141 us backward). With few chains a step's latency alone.
+// What bounds them, measured: fp32 forward the bandwidth (65536 x 4096 634 us, the copy
+// rate); 16-bit types, and the backward, the issue rate and the latency of a step together, 42
+// instructions per element forward and 67 backward (131072 x 4096 bf16 forward 1036 us, 61 %
+// of the copy rate; 65536 x 4096 in 16 sequences 615 us forward, which also writes the states,
+// and 1149 us backward, 52 %; fp32 1626 us backward without sequences, 70 %). With few chains a
+// step's latency alone.
 #include <algorithm>
 #include <string.h>
 
@@ -166,7 +167,7 @@ template <int STEP> __device__ __forceinline__ void store_words(float *p, const 
 
 // The channels of lane q of a token's LR lanes, from a slab's first channel on: four adjacent ones, or without TMA
 // every LR-th, so that the lanes of an element-wise access are neighbours in memory (3 x 19422 x 1147 fp32 with its
-// gradient 919 us, with adjacent ones 1028).
+// gradient 940 us, with adjacent ones 1175).
 template <typename L, bool TMA> struct Columns {
     static constexpr int STEP = TMA ? 1 : L::LR;
     int ch, nc;   // the first, and how many exist
@@ -416,7 +417,7 @@ template <int STEP> __device__ __forceinline__ void channel_params(const RecProb
 }
 
 // While the carry of tile k - 1 travels, the compute warps work on tile k: its decays and writes need only the
-// inputs (unpipelined, 131072 x 4096 bf16 took 2377 us against 1038). Three CTAs an SM: fp32 and element-by-element
+// inputs (one tile after the other, 131072 x 4096 bf16 takes 1218 us against 1036). Three CTAs an SM: fp32 and element-by-element
 // reads hold more in registers and run two.
 template <typename T, bool TMA, bool PACKED>
 __global__ void __launch_bounds__(FwdTile<T>::THREADS, sizeof(T) == 2 && TMA ? 3 : 2)
@@ -596,8 +597,8 @@ rec_forward_kernel(const __grid_constant__ RecProblem p, const __grid_constant__
 
 // The reverse walk: c_t = alpha_t (v_t + c_{t+1}), delta_t = v_t + c_{t+1} with v = grad_out, tiles last to
 // first. The states before every 4th token come from the forward, so h_{t-1} is recomputed within a thread: 4 bytes
-// per 4 elements more to write and to read, against a second scan. With a state every 8 tokens and their values in
-// registers two CTAs an SM are left, and 65536 x 4096 bf16 takes 1621 us against 1141.
+// per 4 elements more to write and to read, against a second scan. A state every 8 tokens would halve that, but double
+// the tile and what a thread keeps of it in shared memory: 130 KB a CTA, and one on an SM in place of three.
 template <typename T, bool TMA, bool PACKED>
 __global__ void __launch_bounds__(BwdTile<T>::THREADS, sizeof(T) == 2 && TMA ? 3 : 2)
 rec_backward_kernel(const __grid_constant__ RecProblem p, const __grid_constant__ RecMaps maps) {
@@ -885,13 +886,14 @@ __global__ void __launch_bounds__(128) rec_step_kernel(const RecProblem p, float
 // ===================================================================== host
 // CTAs per chain: as many as leave all clusters resident, since a cluster that waits for another's end costs its whole
 // time again (a cluster stays within one of the chip's processing clusters, so larger ones fit worse than their sum of
-// CTAs says: the counts here are the occupancy calculator's). At two CTAs per SM up to 16, at three, where registers
-// allow that, up to 8: with more than two, larger clusters wait for the slowest SM. Backward over 16384 bf16 tokens:
-//     24 chains  10 CTAs 153 us, 8 168, 12 221      72 chains  6 CTAs 286 us, 5 325, 7 412
-//     36 chains   8 CTAs 191 us, 7 210, 10 277      84 chains  5 CTAs 332 us, 4 393, 6 449
-//     50 chains   8 CTAs 212 us, 7 238,  9 316     100 chains  4 CTAs 399 us, 3 514, 5 536
-//     56 chains   7 CTAs 244 us, 6 271,  8 340     128 chains  3 CTAs 528 us, 2 635, 4 637
-// (the forward's order is the same but for 24 to 43 chains, where 10 to 14 CTAs gain it up to 13 %).
+// CTAs says: the counts here are the occupancy calculator's answers for this chip). At two CTAs per SM up to 16, at
+// three, where registers allow that, up to 8: with more than two, larger clusters wait for the slowest SM. Backward over
+// 16384 bf16 tokens:
+//     24 chains  10 CTAs 157 us, 8 172, 12 225      72 chains  6 CTAs 296 us, 5 323, 7 413
+//     36 chains   8 CTAs 201 us, 7 220, 10 277      84 chains  5 CTAs 342 us, 4 383, 6 454
+//     50 chains   8 CTAs 218 us, 7 237,  9 319     100 chains  4 CTAs 403 us, 3 495, 5 538
+//     56 chains   7 CTAs 248 us, 6 270,  8 344     128 chains  3 CTAs 521 us, 2 631, 4 645
+// (the forward's order is the same).
 int cluster_size(int64_t chains, int64_t ntiles, int per_sm) {
     constexpr int kResident2[kMaxCluster] = {304, 152, 97, 74, 58, 46, 38, 36, 30, 28, 23, 23, 19, 14, 14, 14};
     constexpr int kResident3[8] = {456, 228, 148, 110, 87, 74, 59, 51};

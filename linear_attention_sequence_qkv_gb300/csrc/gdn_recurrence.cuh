@@ -24,9 +24,9 @@ constexpr float kLeastNormal = 1.17549435e-38f;
 
 // The constants of the pair operations. `pin` keeps the longer polynomial's in registers: a pair operation takes no
 // literal, and left to itself the compiler moves each constant into place before each use. Where 16-bit loads are
-// element by element (two CTAs an SM, registers to spare) that gains (40000 x 3001 bf16 with its gradient 1594 against
-// 1721 us); where three CTAs share an SM the registers count for more (65536 x 4096 1802 against 1752 us), and so
-// where fp32 elements on their way fill them (3 x 19422 x 1147 997 against 948 us).
+// element by element (two CTAs an SM, registers to spare) that gains (40000 x 3001 bf16 with its gradient 1518 against
+// 1669 us); where three CTAs share an SM the registers count for more (65536 x 4096 1803 against 1763 us), and so
+// where fp32 elements on their way fill them (3 x 19422 x 1147 994 against 940 us).
 struct GateConst {
     float2 sp[8], om[4], log2e, one, neg;
     __device__ __forceinline__ static float2 lit(float v) { return make_float2(v, v); }

@@ -7,8 +7,9 @@
 // tokens once, into shared memory, for all heads. A unit of work is one vector per
 // half of a rotated head (half layout), one vector of whole pairs (interleaved), or one
 // copied vector; a thread has several in flight. 131072 tokens of 32 heads of 128 in bf16
-// take 308 us (2.1 GB, 103 % of the copy rate). With few heads per token the table counts: one
-// head of 64 for 64 x 60000 tokens takes 390 us, 37 % of it.
+// take 309 us (2.1 GB, 102 % of the copy rate; 330 us in 64 packed sequences, whose positions
+// are looked up for every entry of the table). With few heads per token the table counts: one
+// head of 64 for 64 x 60000 tokens takes 389 us, 37 % of it.
 #include <math.h>
 #include <string.h>
 
@@ -50,7 +51,7 @@ __device__ __forceinline__ int64_t token_position(const RotaryProblem &p, int ro
 // turns, and its upper half as a signed fraction has 32 bits of the remaining angle. For
 // 16-bit outputs the hardware's functions on [-pi, pi] are exact enough (absolute error about
 // 2^-21, against a rounding of 2^-9 or 2^-12), and where a token has few heads they are what
-// bounds the kernel (one head of 64 for 64 x 60000 tokens: 545 us, 656 with sincospif).
+// bounds the kernel (one head of 64 for 64 x 60000 tokens: 389 us, 464 with sincospif).
 template <bool FAST>
 __device__ __forceinline__ float2 cos_sin(int64_t position, uint64_t turn) {
     const uint64_t phase = (uint64_t)position * turn;
@@ -177,8 +178,8 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
     };
     if (half <= kThreads && nt * half > 8 * kThreads) {
         // Long tables (few heads): a thread keeps its pair and steps over the tokens. 64 x 60000 tokens of one head
-        // of 64: 390 us, 545 with the loop below, which is the faster one for short tables (32 heads of 128: 305
-        // against 311 us, 4096 tokens of 12 heads of 256 with 64 rotated: 11.5 against 12.3).
+        // of 64: 389 us, 544 with the loop below, which is the faster one for short tables (131072 tokens of 32 heads
+        // of 128: 308 against 314 us; 4096 of 12 heads of 256 with 64 rotated: 11.2 against 11.7 on the device).
         const int tstep = kThreads / half, t0 = threadIdx.x / half, pr = threadIdx.x - t0 * half;
         const uint64_t turn = p.turns[pr];
         for (int t = t0 < tstep ? t0 : nt; t < nt; t += tstep) entry(t, position_of(t), pr, turn);
@@ -262,8 +263,8 @@ cudaError_t launch_rotary(RotaryProblem p, cudaStream_t s) {
     p.u_k = d.Hk * p.u_rot;
     p.c_q = p.q == p.qo ? 0 : d.Hq * p.u_copy;
     p.c_k = p.k == p.ko ? 0 : d.Hk * p.u_copy;
-    // tokens per CTA: about four batches of units for every thread (one: 336 us at 131072 x 32 heads, two: 323, four
-    // and eight: 320; 316 at the copy rate), as long as that leaves four CTAs per SM and the
+    // tokens per CTA: about four batches of units for every thread (131072 x 32 heads of 128: one 324 us, two 313, four
+    // 309, eight 314; 316 at the copy rate), as long as that leaves four CTAs per SM and the
     // table fits; few tokens are split over the heads instead
     const int64_t per = (int64_t)p.u_q + p.u_k + p.c_q + p.c_k;
     int64_t tokens = std::max<int64_t>(1, std::min<int64_t>(kBatches * kBatch * kThreads / per, ntok / (4 * kSms)));
