@@ -921,8 +921,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// The driver call behind the tensor maps needs a context, which a host thread has only after its first call of the
-// runtime that binds one: then the map is encoded again.
+// Encoding a tensor map needs a context, which a host thread has only after a call of the runtime that binds one. Where
+// it has none, one is bound and the map encoded again.
 template <typename... A>
 bool encode(A... args) {
     const auto fn = encode_fn();

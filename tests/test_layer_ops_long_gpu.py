@@ -32,8 +32,8 @@ def rotary_input(dev, B, T, width, dtype, pad=0, seed=0):
 
 
 # A CTA takes as many tokens as leave 608 of them (fewer with many heads or a wide table): 54003 tokens are 88 a CTA, the
-# last CTA's fewer, and a row's end falls inside one. With a head of 64, 66 pairs by 88 tokens take the loop for long
-# tables; rot 48 and 80 (24 and 40 pairs) do not divide its 256 threads.
+# last CTA's fewer, and a row's end falls inside one. 24 pairs and more by 88 tokens take the loop for long tables (over
+# 2048 entries), whose 256 threads 24 and 40 pairs do not divide.
 @pytest.mark.parametrize("B,T,Hq,Hk,d,rot,layout,dtype,pad", [
     (3, 18001, 1, 0, 64, 64, "half", "bf16", 0),
     (3, 18001, 1, 0, 64, 48, "half", "bf16", 0),
