@@ -632,6 +632,177 @@ int gdn_group_norm_backward(const gdn_group_norm_desc *d, const void *x, const v
                             const void *grad_out, void *dx, float *dweight, float *dbias,
                             void *workspace, size_t workspace_bytes, gdn_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Operators of the attention layers that stand between delta rule layers: the
+ * norm of every head of q and k together with the rotary positions, and causal
+ * softmax attention over a window of recent tokens plus a few first ones, for
+ * training, for prefill and for single tokens over a cache of fixed size. The
+ * conventions of the operators above hold; the definitions stand here in full.
+ */
+
+/*
+ * Head norm and rotary positions in one pass. For every token and head of q (of k),
+ * x the head's d channels and w its weight [d] (all heads of q share one weight, all
+ * heads of k another):
+ *     xh = x * rsqrt(mean_c x^2 + eps),  z = xh * w,  y = rotary(z),
+ * the rotation of gdn_rotary (positions, layouts, tables, scale). All arithmetic is
+ * fp32; y is rounded once. Results are run-to-run identical.
+ */
+typedef struct {
+    gdn_rotary_desc rotary; /* sizes, layout and strides as in gdn_rotary; inverse 0, d at most 1024 */
+    int32_t weight_dtype;   /* of q_weight and k_weight: rotary.dtype, or GDN_F32 */
+    float eps;              /* 1e-6 */
+} gdn_norm_rotary_desc;
+
+/* Fill *d as gdn_rotary_desc_init does, weights in the act dtype, eps 1e-6. */
+int gdn_norm_rotary_desc_init(gdn_norm_rotary_desc *d, int B, int T, int packed, int Hq, int Hk,
+                              int head_dim, int dtype);
+int gdn_norm_rotary_workspace_bytes(const gdn_norm_rotary_desc *d, size_t *bytes);
+int gdn_norm_rotary_backward_workspace_bytes(const gdn_norm_rotary_desc *d, size_t *bytes);
+
+/*
+ *   q, k, turns, positions, cu_seqlens, offsets, q_out, k_out, workspace
+ *                       as in gdn_rotary (in place allowed: the same strides then)
+ *   q_weight, k_weight  [d] or NULL (ones)
+ */
+int gdn_norm_rotary_forward(const gdn_norm_rotary_desc *d, const void *q, const void *k,
+                            const void *q_weight, const void *k_weight, const uint64_t *turns,
+                            const int32_t *positions, const int32_t *cu_seqlens,
+                            const int32_t *offsets, void *q_out, void *k_out, void *workspace,
+                            size_t workspace_bytes, gdn_stream_t stream);
+
+/*
+ * Gradients of sum(grad_q * q_out) + sum(grad_k * k_out); q and k are the forward's inputs.
+ *   grad_q, grad_k      [B,T,H*d] at the descriptor's q_out and k_out strides
+ *   dq, dk              [B,T,H*d] contiguous (dk NULL when Hk == 0); must not overlap inputs
+ *   dq_weight, dk_weight  NULL, or fp32 [d]: sums over all tokens and heads in a fixed
+ *                       order (written also when the weight is NULL; zeros when B*T == 0)
+ *   workspace           >= gdn_norm_rotary_backward_workspace_bytes(), 256-byte aligned.
+ *                       A malformed cu_seqlens sets GDN_ERR_DEVICE_SEQLENS and nothing
+ *                       else is written.
+ */
+int gdn_norm_rotary_backward(const gdn_norm_rotary_desc *d, const void *q, const void *k,
+                             const void *q_weight, const void *k_weight, const uint64_t *turns,
+                             const int32_t *positions, const int32_t *cu_seqlens,
+                             const int32_t *offsets, const void *grad_q, const void *grad_k,
+                             void *dq, void *dk, float *dq_weight, float *dk_weight,
+                             void *workspace, size_t workspace_bytes, gdn_stream_t stream);
+
+/*
+ * Window attention. A sequence has Lk keys and Lq queries, the queries being its last
+ * Lq positions: query i stands at position p = Lk - Lq + i. It sees the keys
+ *     j <= p  with  p - j < window  or  j < sinks,
+ * that is the `window` most recent tokens, itself among them, and the sequence's first
+ * `sinks` tokens, which stay visible. Head h of q reads head h / (Hq/Hk) of k and v:
+ *     s_j = scale * q . k_j,  P = softmax over the keys seen,  out = sum_j P_j v_j,
+ *     lse = log sum_j exp(s_j).
+ * A query that sees nothing (p < 0, where Lq > Lk) gets out = 0 and lse = -inf.
+ * Scores, softmax statistics and every sum are fp32; with 16-bit types the tensor-core
+ * kernels round P, and in the backward P and the scores' gradients, to that type as
+ * operands of their products. Results are run-to-run identical. What a query does not
+ * see has no influence on its output, also where it is infinite or NaN; in the backward
+ * this holds between sequences (inside one, a NaN may reach neighbouring gradients).
+ */
+typedef struct {
+    int32_t B;           /* batch rows; with cu_seqlens B = 1 */
+    int32_t Tq, Tk;      /* queries and keys per row; packed: totals. At most 2^31 - 2^16 */
+    int32_t N;           /* sequences: B without cu_seqlens, else cu_seqlens has N+1 entries */
+    int32_t Hq, Hk;      /* heads of q, of k and v (Hq % Hk == 0) */
+    int32_t d;           /* channels per head, 1..256 */
+    int32_t window;      /* >= 1; at least Tk: plain causal attention */
+    int32_t sinks;       /* >= 0 */
+    int32_t slots;       /* cache calls: slots per head, at least sinks + window */
+    int32_t dtype;       /* gdn_dtype of q, k, v, out, their gradients and the caches */
+    float scale;         /* 1/sqrt(d) */
+    /* (batch, token) element strides; a token's heads and channels are contiguous */
+    int64_t q_stride_b, q_stride_t, k_stride_b, k_stride_t, v_stride_b, v_stride_t;
+} gdn_window_attention_desc;
+
+/* Fill *d for contiguous q [B,Tq,Hq*d], k, v [B,Tk,Hk*d], scale 1/sqrt(d), slots
+ * sinks + window. packed as in gdn_desc_init. Returns the validation status. */
+int gdn_window_attention_desc_init(gdn_window_attention_desc *d, int B, int Tq, int Tk, int packed,
+                                   int Hq, int Hk, int head_dim, int window, int sinks, int dtype);
+int gdn_window_attention_workspace_bytes(const gdn_window_attention_desc *d, size_t *bytes);
+int gdn_window_attention_backward_workspace_bytes(const gdn_window_attention_desc *d, size_t *bytes);
+int gdn_window_attention_step_workspace_bytes(const gdn_window_attention_desc *d, size_t *bytes);
+int gdn_window_cache_write_workspace_bytes(const gdn_window_attention_desc *d, size_t *bytes);
+
+/* Which kernels serve *d in the forward and backward, given aligned tensors: 0 = fp32
+ * CUDA-core kernels, 1 = tcgen05 tensor-core kernels (16-bit types, d a multiple of 8 up
+ * to 128, every q, k and v base 16-byte aligned and every stride a multiple of 8). */
+int gdn_window_attention_kernel_kind(const gdn_window_attention_desc *d);
+
+/*
+ *   q, k, v        at their strides
+ *   cu_seqlens     NULL, or int32 [N+1] offsets of the queries (then B == 1)
+ *   cu_seqlens_k   NULL (the same as cu_seqlens; Tk == Tq then), or int32 [N+1] offsets of
+ *                  the keys
+ *   out            [B,Tq,Hq*d] contiguous
+ *   lse            NULL, or fp32 [Hq][B*Tq]: for the backward
+ *   workspace      >= gdn_window_attention_workspace_bytes(), 256-byte aligned;
+ *                  gdn_device_status reads its status word. Malformed offsets set
+ *                  GDN_ERR_DEVICE_SEQLENS and nothing else is written. Waits for copies
+ *                  and products give up after about a second (GDN_ERR_DEVICE_TIMEOUT).
+ * out and lse must not overlap the inputs or each other.
+ */
+int gdn_window_attention_forward(const gdn_window_attention_desc *d, const void *q, const void *k,
+                                 const void *v, const int32_t *cu_seqlens,
+                                 const int32_t *cu_seqlens_k, void *out, float *lse,
+                                 void *workspace, size_t workspace_bytes, gdn_stream_t stream);
+
+/*
+ * Gradients of sum(grad_out * out), with out and lse of the forward on the same inputs.
+ *   out, grad_out  [B,Tq,Hq*d] contiguous
+ *   dq             [B,Tq,Hq*d] contiguous;  dk, dv  [B,Tk,Hk*d] contiguous: written in
+ *                  full, each rounded once. They must not overlap the inputs or each other.
+ *   workspace      >= gdn_window_attention_backward_workspace_bytes(), 256-byte aligned;
+ *                  status as in the forward
+ */
+int gdn_window_attention_backward(const gdn_window_attention_desc *d, const void *q, const void *k,
+                                  const void *v, const void *out, const float *lse,
+                                  const void *grad_out, const int32_t *cu_seqlens,
+                                  const int32_t *cu_seqlens_k, void *dq, void *dk, void *dv,
+                                  void *workspace, size_t workspace_bytes, gdn_stream_t stream);
+
+/*
+ * The cache: per sequence and head `slots` rows of keys and of values,
+ * k_cache, v_cache [N][Hk][slots][d] contiguous, whatever the sequence's length. Position
+ * p is held in slot p for p < sinks, else in slot sinks + (p - sinks) % (slots - sinks),
+ * where it stays until a later position takes the slot over. lengths, int32 [N], counts
+ * the positions that a sequence has had before the call, 0 .. 2^31 - 2; the call does not
+ * change it (the layers of a model share it). A sequence whose length is negative takes
+ * no part: its cache is left as it is.
+ *
+ * gdn_window_cache_write puts tokens at positions lengths[n], lengths[n] + 1, ... of each
+ * sequence n, those that a later one of the same call would replace left out.
+ *   k, v           [B,Tk,Hk*d] at their strides (d->Tq and d->Hq are not read)
+ *   cu_seqlens     NULL, or int32 [N+1] (then B == 1): offsets into k and v
+ *   workspace      >= gdn_window_cache_write_workspace_bytes(), 256-byte aligned (status
+ *                  word; a malformed cu_seqlens writes nothing else)
+ */
+int gdn_window_cache_write(const gdn_window_attention_desc *d, const void *k, const void *v,
+                           const int32_t *cu_seqlens, const int32_t *lengths, void *k_cache,
+                           void *v_cache, void *workspace, size_t workspace_bytes,
+                           gdn_stream_t stream);
+
+/*
+ * One more token of each of B sequences (d->Tq == d->Tk == 1, N == B): k and v are written
+ * into the caches at position lengths[n], and the query attends to the cache with the mask
+ * of the window attention at that position. Positions never written must not be counted in
+ * lengths.
+ *   q [B,1,Hq*d], k, v [B,1,Hk*d] at their batch strides
+ *   out            [B,1,Hq*d] contiguous; zeros for a sequence that takes no part
+ *   workspace      >= gdn_window_attention_step_workspace_bytes(), 256-byte aligned; calls
+ *                  that share one must not overlap on the GPU
+ * The result is that of gdn_window_attention_forward on the whole sequence's last token
+ * (another order of the sums).
+ */
+int gdn_window_attention_step(const gdn_window_attention_desc *d, const void *q, const void *k,
+                              const void *v, const int32_t *lengths, void *k_cache, void *v_cache,
+                              void *out, void *workspace, size_t workspace_bytes,
+                              gdn_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

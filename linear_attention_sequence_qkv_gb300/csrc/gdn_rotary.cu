@@ -16,6 +16,7 @@
 #include <algorithm>
 
 #include "gdn_layer_ops.cuh"
+#include "gdn_rotary.cuh"
 
 namespace gdn {
 namespace {
@@ -34,34 +35,8 @@ struct RotaryProblem {
     int u_copy, copy_bytes; // units of a head's copied channels, and their size
 };
 
-// Position of token t of row `row` (see gdn_rotary in include/gdn.h)
 __device__ __forceinline__ int64_t token_position(const RotaryProblem &p, int row, int t) {
-    const gdn_rotary_desc &d = p.d;
-    if (p.pos) return p.pos[(int64_t)row * d.T + t];
-    int n = row;
-    int64_t at = t;
-    if (p.cu) {
-        n = upper_index(p.cu, d.N, t);
-        at -= p.cu[n];
-    }
-    return at + (p.off ? p.off[n] : 0);
-}
-
-// cos and sin of 2 pi frac(position * turn / 2^64): the 64-bit product wraps at whole
-// turns, and its upper half as a signed fraction has 32 bits of the remaining angle. For
-// 16-bit outputs the hardware's functions on [-pi, pi] are exact enough (absolute error about
-// 2^-21, against a rounding of 2^-9 or 2^-12), and where a token has few heads they are what
-// bounds the kernel (one head of 64 for 64 x 60000 tokens: 389 us, 464 with sincospif).
-template <bool FAST>
-__device__ __forceinline__ float2 cos_sin(int64_t position, uint64_t turn) {
-    const uint64_t phase = (uint64_t)position * turn;
-    if (FAST) {
-        const float a = (float)(int32_t)(phase >> 32) * 1.4629180792671596e-9f;   // 2 pi 2^-32
-        return make_float2(__cosf(a), __sinf(a));
-    }
-    float c, s;
-    sincospif((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31: in half turns
-    return make_float2(c, s);
+    return rotary_position(p.d, p.pos, p.cu, p.off, row, t);
 }
 
 template <int BYTES> struct Raw;
@@ -293,7 +268,9 @@ cudaError_t launch_by_vector(const RotaryProblem &p, cudaStream_t s) {
     return launch_rotary<T, 1, HALF>(p, s);
 }
 
-int check_desc(const gdn_rotary_desc *d, bool packed) {
+}  // namespace
+
+int rotary_check_desc(const gdn_rotary_desc *d, bool packed) {
     if (!d) return GDN_ERR_INVALID_ARG;
     if (d->B < 1 || d->T < 0 || d->N < 1 || d->Hq < 1 || d->Hk < 0 || d->d < 2) return GDN_ERR_INVALID_ARG;
     if (packed ? d->B != 1 : d->N != d->B) return GDN_ERR_INVALID_ARG;
@@ -317,7 +294,6 @@ int check_desc(const gdn_rotary_desc *d, bool packed) {
     return GDN_OK;
 }
 
-}  // namespace
 }  // namespace gdn
 
 using namespace gdn;
@@ -340,7 +316,7 @@ int gdn_rotary_desc_init(gdn_rotary_desc *d, int B, int T, int packed, int Hq, i
     d->k_stride_t = d->k_out_stride_t = (int64_t)Hk * head_dim;
     d->q_stride_b = d->q_out_stride_b = d->q_stride_t * T;
     d->k_stride_b = d->k_out_stride_b = d->k_stride_t * T;
-    return check_desc(d, packed != 0);
+    return rotary_check_desc(d, packed != 0);
 }
 
 int gdn_rotary_table(int rot, double theta, int scaling, double factor, double low, double high, double original,
@@ -370,7 +346,7 @@ int gdn_rotary_table(int rot, double theta, int scaling, double factor, double l
 
 int gdn_rotary_workspace_bytes(const gdn_rotary_desc *d, size_t *bytes) {
     if (!d || !bytes) return GDN_ERR_INVALID_ARG;
-    const int rc = check_desc(d, d->N != d->B);
+    const int rc = rotary_check_desc(d, d->N != d->B);
     if (rc != GDN_OK) return rc;
     *bytes = kStatusBytes;
     return GDN_OK;
@@ -379,7 +355,7 @@ int gdn_rotary_workspace_bytes(const gdn_rotary_desc *d, size_t *bytes) {
 int gdn_rotary(const gdn_rotary_desc *d, const void *q, const void *k, const uint64_t *turns, const int32_t *positions,
                const int32_t *cu_seqlens, const int32_t *offsets, void *q_out, void *k_out, void *workspace,
                size_t workspace_bytes, gdn_stream_t stream) {
-    int rc = check_desc(d, cu_seqlens != nullptr);
+    int rc = rotary_check_desc(d, cu_seqlens != nullptr);
     if (rc != GDN_OK) return rc;
     const bool tok = (int64_t)d->B * d->T > 0;   // token tensors may be empty (null)
     if (tok && (!q || !q_out || (d->Hk && (!k || !k_out)))) return GDN_ERR_INVALID_ARG;

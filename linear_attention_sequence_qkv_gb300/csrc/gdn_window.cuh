@@ -1,0 +1,161 @@
+// gdn_window.cuh -- what the window attention's kernels share: the problem, the place of a
+// sequence, which keys a query sees, and single rows computed by one warp (the kernels of
+// any type, size and alignment; the tensor-core kernels fall back on them for rows that
+// came out non-finite).
+#pragma once
+
+#include <math.h>
+
+#include "gdn_layer_ops.cuh"
+
+namespace gdn {
+
+constexpr int kMostHead = 256;   // channels per head
+
+struct WindowProblem {
+    gdn_window_attention_desc d;
+    const void *q, *k, *v, *out_in, *dout;
+    const int32_t *cu, *cuk;    // cuk: the keys' offsets (cu's without their own)
+    void *out, *dq, *dk, *dv;
+    float *lse;                 // forward: written or null; backward: read
+    float *delta;               // [Hq][B*Tq] sums of grad_out * out
+    int32_t *status;
+    int32_t *q_tiles, *k_tiles; // packed: [N+1] tiles of the sequences before n, by queries and by keys
+    int wait_immediate;
+};
+
+// A sequence: its first query and key among the flattened tokens, their numbers, and the
+// element offsets of its first rows
+struct WindowSpan {
+    int64_t q0, k0, qoff, koff, voff;
+    int Lq, Lk;
+};
+__device__ __forceinline__ WindowSpan window_span(const WindowProblem &p, int n) {
+    const gdn_window_attention_desc &d = p.d;
+    WindowSpan s;
+    if (p.cu) {
+        s.q0 = p.cu[n], s.Lq = p.cu[n + 1] - (int)s.q0;
+        s.k0 = p.cuk[n], s.Lk = p.cuk[n + 1] - (int)s.k0;
+        s.qoff = s.q0 * d.q_stride_t, s.koff = s.k0 * d.k_stride_t, s.voff = s.k0 * d.v_stride_t;
+    } else {
+        s.q0 = (int64_t)n * d.Tq, s.Lq = d.Tq;
+        s.k0 = (int64_t)n * d.Tk, s.Lk = d.Tk;
+        s.qoff = n * d.q_stride_b, s.koff = n * d.k_stride_b, s.voff = n * d.v_stride_b;
+    }
+    return s;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// The first key of the window of a query at `pos`, and the number of sinks before it
+__device__ __forceinline__ int window_first(int pos, int window) { return pos >= window ? pos - window + 1 : 0; }
+
+// ---------------------------------------------------------------- single rows
+// A row's channels over the lanes of a warp: channel 32 c + lane in r[c]
+template <typename T, int NC>
+__device__ __forceinline__ void row_load(const T *src, int d, int lane, float (&r)[NC]) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) r[c] = 32 * c + lane < d ? to_f<T>(src[32 * c + lane]) : 0.0f;
+}
+template <typename T, int NC>
+__device__ __forceinline__ void row_store(T *dst, int d, int lane, const float (&r)[NC]) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+        if (32 * c + lane < d) dst[32 * c + lane] = from_f<T>(r[c]);
+}
+// r . src, src a row of this lane's own
+template <typename T, int NC>
+__device__ __forceinline__ float row_dot(const float (&r)[NC], const T *src, int d) {
+    float s = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+        for (int l = 0; l < 32 && 32 * c + l < d; ++l) s = fmaf(__shfl_sync(0xffffffffu, r[c], l), to_f<T>(src[32 * c + l]), s);
+    return s;
+}
+// acc += w_j src_j over the lanes' rows j, taken in the lanes' order
+template <typename T, int NC>
+__device__ __forceinline__ void rows_add(float (&acc)[NC], float w, const T *src, int n, int d, int lane) {
+    for (int j = 0; j < n; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, w, j);
+        const T *sj = (const T *)__shfl_sync(0xffffffffu, (unsigned long long)src, j);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            if (32 * c + lane < d) acc[c] = fmaf(wj, to_f<T>(sj[32 * c + lane]), acc[c]);
+    }
+}
+
+// One query at position pos >= 0 of a sequence whose keys start at k, v: out (unrounded) and lse
+template <typename T, int NC>
+__device__ __noinline__ void row_forward(const T *q, const T *k, const T *v, int64_t kst, int64_t vst, int d, float scale,
+                                         int pos, int window, int sinks, int lane, float (&o)[NC], float &lse) {
+    float qr[NC];
+    row_load<T, NC>(q, d, lane, qr);
+    float m = -INFINITY, l = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) o[c] = 0.0f;
+    const int lo = window_first(pos, window), first = min(sinks, lo), total = first + pos - lo + 1;
+    for (int t0 = 0; t0 < total; t0 += 32) {
+        const int t = t0 + lane, n = min(32, total - t0);
+        const int j = t < first ? t : min(lo + t - first, pos);
+        const float s = row_dot<T, NC>(qr, k + j * kst, d) * scale;
+        const float x = lane < n ? s : -INFINITY;
+        const float mn = fmaxf(m, warp_max(x)), mm = mn == -INFINITY ? 0.0f : mn;
+        const float corr = expf(m - mm), w = lane < n ? expf(x - mm) : 0.0f;
+        l = l * corr + warp_sum(w);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) o[c] *= corr;
+        rows_add<T, NC>(o, w, v + j * vst, n, d, lane);
+        m = mn;
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) o[c] /= l;
+    lse = m + logf(l);
+}
+
+// The gradient of one query: dq = scale * sum_j P_j (dO . v_j - delta) k_j
+template <typename T, int NC>
+__device__ __noinline__ void row_dq(const T *q, const T *dout, const T *k, const T *v, int64_t kst, int64_t vst, int d, float scale,
+                                    int pos, int window, int sinks, float lse, float delta, int lane, float (&dq)[NC]) {
+    float qr[NC], gr[NC];
+    row_load<T, NC>(q, d, lane, qr);
+    row_load<T, NC>(dout, d, lane, gr);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) dq[c] = 0.0f;
+    const int lo = window_first(pos, window), first = min(sinks, lo), total = first + pos - lo + 1;
+    for (int t0 = 0; t0 < total; t0 += 32) {
+        const int t = t0 + lane, n = min(32, total - t0);
+        const int j = t < first ? t : min(lo + t - first, pos);
+        const float s = row_dot<T, NC>(qr, k + j * kst, d) * scale, dp = row_dot<T, NC>(gr, v + j * vst, d);
+        rows_add<T, NC>(dq, lane < n ? expf(s - lse) * (dp - delta) * scale : 0.0f, k + j * kst, n, d, lane);
+    }
+}
+
+// What the queries at positions [p0, p1) of one head give to the gradients of one key: rows of q and dout with these
+// strides, lse and delta of the sequence's first query, `past` = Lk - Lq
+template <typename T, int NC>
+__device__ __noinline__ void row_dkv(const T *q, const T *dout, const float (&kr)[NC], const float (&vr)[NC], int64_t qst, int64_t gst,
+                                     const float *lse, const float *delta, int d, float scale, int64_t p0, int64_t p1, int past, int lane,
+                                     float (&dk)[NC], float (&dv)[NC]) {
+    for (int64_t t0 = p0; t0 < p1; t0 += 32) {
+        const int n = (int)min((int64_t)32, p1 - t0);
+        const int64_t i = min(t0 + lane, p1 - 1) - past;
+        const float s = row_dot<T, NC>(kr, q + i * qst, d) * scale, dp = row_dot<T, NC>(vr, dout + i * gst, d);
+        const float w = lane < n ? expf(s - lse[i]) : 0.0f;
+        rows_add<T, NC>(dv, w, dout + i * gst, n, d, lane);
+        rows_add<T, NC>(dk, lane < n ? w * (dp - delta[i]) * scale : 0.0f, q + i * qst, n, d, lane);
+    }
+}
+
+// Status and, for packed sequences, the tiles' tables (tile: rows of a tile of queries, of keys)
+cudaError_t launch_window_tables(const WindowProblem &p, int q_tile, int k_tile, cudaStream_t s);
+
+}  // namespace gdn

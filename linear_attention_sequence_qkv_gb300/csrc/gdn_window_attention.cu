@@ -1,0 +1,329 @@
+// gdn_window_attention.cu -- causal attention over a window of recent tokens and a few
+// first ones (include/gdn.h): the C entry points of its forward and backward, the check
+// of packed offsets, and the kernels of any type, size and alignment, in which a warp
+// computes one row.
+#include <string.h>
+
+#include <algorithm>
+
+#include "gdn_window.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kRowWarps = 4;
+
+// Packed offsets checked, and the tiles of the sequences before each one counted
+__global__ void __launch_bounds__(1024) window_tables_kernel(const __grid_constant__ WindowProblem p, int q_tile, int k_tile) {
+    const gdn_window_attention_desc &d = p.d;
+    if (p.cu == nullptr) {
+        if (threadIdx.x == 0) *p.status = GDN_OK;
+        return;
+    }
+    bool ok = seqlens_ok(p.cu, d.N, d.Tq);
+    if (p.cuk != p.cu) ok = seqlens_ok(p.cuk, d.N, d.Tk) && ok;
+    if (threadIdx.x == 0) *p.status = ok ? GDN_OK : GDN_ERR_DEVICE_SEQLENS;
+    __shared__ int32_t sums[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int which = 0; which < 2; ++which) {
+        const int32_t *cu = which ? p.cuk : p.cu;
+        int32_t *to = which ? p.k_tiles : p.q_tiles;
+        const int tile = which ? k_tile : q_tile;
+        if (!to) continue;
+        int before = 0;
+        for (int base = 0; base < d.N; base += blockDim.x) {
+            const int n = base + threadIdx.x;
+            const int c = ok && n < d.N ? (int)(((int64_t)cu[n + 1] - cu[n] + tile - 1) / tile) : 0;
+            int x = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (lane == 31) sums[warp] = x;
+            __syncthreads();
+            int s = sums[lane];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += y;
+            }
+            const int ahead = warp ? __shfl_sync(0xffffffffu, s, warp - 1) : 0, all = __shfl_sync(0xffffffffu, s, 31);
+            if (n < d.N) to[n] = before + ahead + x - c;
+            before += all;
+            __syncthreads();
+        }
+        if (threadIdx.x == 0) to[d.N] = before;
+    }
+}
+
+// The sequence of a flattened token, by queries or by keys
+__device__ __forceinline__ int sequence_of(const int32_t *cu, int N, int T, int64_t token) {
+    return cu ? upper_index(cu, N, token) : (int)(token / T);
+}
+
+template <typename T, int NC>
+__global__ void __launch_bounds__(32 * kRowWarps) window_forward_rows(const __grid_constant__ WindowProblem p) {
+    if (*p.status != GDN_OK) return;
+    const gdn_window_attention_desc &d = p.d;
+    const int lane = threadIdx.x & 31;
+    const int64_t ntok = (int64_t)d.B * d.Tq, total = ntok * d.Hq;
+    for (int64_t i = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5); i < total; i += (int64_t)gridDim.x * kRowWarps) {
+        const int64_t tok = i / d.Hq;
+        const int h = (int)(i - tok * d.Hq), n = sequence_of(p.cu, d.N, d.Tq, tok), hk = h / (d.Hq / d.Hk);
+        const WindowSpan s = window_span(p, n);
+        const int at = (int)(tok - s.q0), pos = s.Lk - s.Lq + at;
+        float o[NC], lse = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) o[c] = 0.0f;
+        if (pos >= 0)
+            row_forward<T, NC>((const T *)p.q + s.qoff + at * d.q_stride_t + (int64_t)h * d.d, (const T *)p.k + s.koff + (int64_t)hk * d.d,
+                               (const T *)p.v + s.voff + (int64_t)hk * d.d, d.k_stride_t, d.v_stride_t, d.d, d.scale, pos, d.window,
+                               d.sinks, lane, o, lse);
+        row_store<T, NC>((T *)p.out + (tok * d.Hq + h) * d.d, d.d, lane, o);
+        if (p.lse && lane == 0) p.lse[h * ntok + tok] = lse;
+    }
+}
+
+// delta = sum of grad_out * out per query and head
+template <typename T>
+__global__ void __launch_bounds__(256) window_delta(const __grid_constant__ WindowProblem p) {
+    if (*p.status != GDN_OK) return;
+    const gdn_window_attention_desc &d = p.d;
+    const int lane = threadIdx.x & 31;
+    const int64_t ntok = (int64_t)d.B * d.Tq, total = ntok * d.Hq;
+    for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += (int64_t)gridDim.x * 8) {
+        const T *o = (const T *)p.out_in + i * d.d, *g = (const T *)p.dout + i * d.d;
+        float s = 0.0f;
+        for (int c = lane; c < d.d; c += 32) s = fmaf(to_f<T>(o[c]), to_f<T>(g[c]), s);
+        s = warp_sum(s);
+        const int64_t tok = i / d.Hq;
+        if (lane == 0) p.delta[(i - tok * d.Hq) * ntok + tok] = s;
+    }
+}
+
+template <typename T, int NC>
+__global__ void __launch_bounds__(32 * kRowWarps) window_dq_rows(const __grid_constant__ WindowProblem p) {
+    if (*p.status != GDN_OK) return;
+    const gdn_window_attention_desc &d = p.d;
+    const int lane = threadIdx.x & 31;
+    const int64_t ntok = (int64_t)d.B * d.Tq, total = ntok * d.Hq;
+    for (int64_t i = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5); i < total; i += (int64_t)gridDim.x * kRowWarps) {
+        const int64_t tok = i / d.Hq;
+        const int h = (int)(i - tok * d.Hq), n = sequence_of(p.cu, d.N, d.Tq, tok), hk = h / (d.Hq / d.Hk);
+        const WindowSpan s = window_span(p, n);
+        const int at = (int)(tok - s.q0), pos = s.Lk - s.Lq + at;
+        float r[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) r[c] = 0.0f;
+        if (pos >= 0)
+            row_dq<T, NC>((const T *)p.q + s.qoff + at * d.q_stride_t + (int64_t)h * d.d, (const T *)p.dout + i * d.d,
+                          (const T *)p.k + s.koff + (int64_t)hk * d.d, (const T *)p.v + s.voff + (int64_t)hk * d.d, d.k_stride_t,
+                          d.v_stride_t, d.d, d.scale, pos, d.window, d.sinks, p.lse[h * ntok + tok], p.delta[h * ntok + tok], lane, r);
+        row_store<T, NC>((T *)p.dq + i * d.d, d.d, lane, r);
+    }
+}
+
+template <typename T, int NC>
+__global__ void __launch_bounds__(32 * kRowWarps) window_dkv_rows(const __grid_constant__ WindowProblem p) {
+    if (*p.status != GDN_OK) return;
+    const gdn_window_attention_desc &d = p.d;
+    const int lane = threadIdx.x & 31, group = d.Hq / d.Hk;
+    const int64_t ntok = (int64_t)d.B * d.Tq, total = (int64_t)d.B * d.Tk * d.Hk;
+    for (int64_t i = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5); i < total; i += (int64_t)gridDim.x * kRowWarps) {
+        const int64_t tok = i / d.Hk;
+        const int hk = (int)(i - tok * d.Hk), n = sequence_of(p.cuk, d.N, d.Tk, tok);
+        const WindowSpan s = window_span(p, n);
+        const int j = (int)(tok - s.k0), past = s.Lk - s.Lq;
+        float kr[NC], vr[NC], dk[NC], dv[NC];
+        row_load<T, NC>((const T *)p.k + s.koff + j * d.k_stride_t + (int64_t)hk * d.d, d.d, lane, kr);
+        row_load<T, NC>((const T *)p.v + s.voff + j * d.v_stride_t + (int64_t)hk * d.d, d.d, lane, vr);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) dk[c] = dv[c] = 0.0f;
+        // queries from the key's own position on, as far as its window (or the sequence) goes
+        const int64_t p0 = max(j, past), p1 = j < d.sinks ? s.Lk : min((int64_t)s.Lk, (int64_t)j + d.window);
+        for (int h = hk * group; h < (hk + 1) * group; ++h)
+            row_dkv<T, NC>((const T *)p.q + s.qoff + (int64_t)h * d.d, (const T *)p.dout + (s.q0 * d.Hq + h) * d.d, kr, vr, d.q_stride_t,
+                           (int64_t)d.Hq * d.d, p.lse + h * ntok + s.q0, p.delta + h * ntok + s.q0, d.d, d.scale, p0, p1, past, lane, dk,
+                           dv);
+        row_store<T, NC>((T *)p.dk + i * d.d, d.d, lane, dk);
+        row_store<T, NC>((T *)p.dv + i * d.d, d.d, lane, dv);
+    }
+}
+
+unsigned row_blocks(int64_t rows, int per) { return (unsigned)std::min<int64_t>(std::max<int64_t>(cdiv64(rows, per), 1), 0x7fffffff); }
+
+template <typename T, int NC>
+cudaError_t forward_rows(const WindowProblem &p, cudaStream_t s) {
+    const int64_t rows = (int64_t)p.d.B * p.d.Tq * p.d.Hq;
+    if (rows == 0) return cudaSuccess;
+    window_forward_rows<T, NC><<<row_blocks(rows, kRowWarps), 32 * kRowWarps, 0, s>>>(p);
+    return cudaGetLastError();
+}
+template <typename T, int NC>
+cudaError_t backward_rows(const WindowProblem &p, cudaStream_t s) {
+    const int64_t rows = (int64_t)p.d.B * p.d.Tq * p.d.Hq, keys = (int64_t)p.d.B * p.d.Tk * p.d.Hk;
+    if (rows) window_dq_rows<T, NC><<<row_blocks(rows, kRowWarps), 32 * kRowWarps, 0, s>>>(p);
+    if (keys) window_dkv_rows<T, NC><<<row_blocks(keys, kRowWarps), 32 * kRowWarps, 0, s>>>(p);
+    return cudaGetLastError();
+}
+template <typename T>
+cudaError_t forward_any(const WindowProblem &p, cudaStream_t s) {
+    return p.d.d <= 64 ? forward_rows<T, 2>(p, s) : p.d.d <= 128 ? forward_rows<T, 4>(p, s) : forward_rows<T, 8>(p, s);
+}
+template <typename T>
+cudaError_t backward_any(const WindowProblem &p, cudaStream_t s) {
+    const int64_t rows = (int64_t)p.d.B * p.d.Tq * p.d.Hq;
+    if (rows) window_delta<T><<<row_blocks(rows, 8), 256, 0, s>>>(p);
+    return p.d.d <= 64 ? backward_rows<T, 2>(p, s) : p.d.d <= 128 ? backward_rows<T, 4>(p, s) : backward_rows<T, 8>(p, s);
+}
+
+struct WindowLayout {
+    size_t status, q_tiles, k_tiles, delta, total;
+};
+WindowLayout layout_of(const gdn_window_attention_desc &d, bool backward) {
+    WindowLayout L;
+    size_t off = 0;
+    L.status = off;  off += kStatusBytes;
+    L.q_tiles = off; off = align_up(off + 4 * ((size_t)d.N + 1), 256);
+    L.k_tiles = off; off = align_up(off + 4 * ((size_t)d.N + 1), 256);
+    L.delta = off;
+    if (backward) off = align_up(off + (size_t)d.B * d.Tq * d.Hq * 4, 256);
+    L.total = off;
+    return L;
+}
+
+}  // namespace
+
+cudaError_t launch_window_tables(const WindowProblem &p, int q_tile, int k_tile, cudaStream_t s) {
+    window_tables_kernel<<<1, p.cu ? 1024 : 32, 0, s>>>(p, q_tile, k_tile);
+    return cudaGetLastError();
+}
+
+int window_check_desc(const gdn_window_attention_desc *d, bool packed) {
+    if (!d) return GDN_ERR_INVALID_ARG;
+    if (d->B < 1 || d->Tq < 0 || d->Tk < 0 || d->N < 1 || d->Hq < 1 || d->Hk < 1 || d->d < 1) return GDN_ERR_INVALID_ARG;
+    if (packed ? d->B != 1 : d->N != d->B) return GDN_ERR_INVALID_ARG;
+    if (d->window < 1 || d->sinks < 0 || !(d->scale > 0.0f) || !isfinite(d->scale)) return GDN_ERR_INVALID_ARG;
+    const int64_t strides[] = {d->q_stride_b, d->q_stride_t, d->k_stride_b, d->k_stride_t, d->v_stride_b, d->v_stride_t};
+    for (const int64_t s : strides)
+        if (s < 0) return GDN_ERR_INVALID_ARG;
+    if (!dtype_ok(d->dtype) || d->Hq % d->Hk || d->d > kMostHead) return GDN_ERR_UNSUPPORTED;
+    const int64_t cq = (int64_t)d->Hq * d->d, ck = (int64_t)d->Hk * d->d;
+    if (cq > (1 << 24) || d->Tq > 0x7fffffff - 65536 || d->Tk > 0x7fffffff - 65536) return GDN_ERR_UNSUPPORTED;
+    if ((int64_t)d->B * d->Tq > 0x7fffffff || (int64_t)d->B * d->Tk > 0x7fffffff) return GDN_ERR_UNSUPPORTED;
+    if (d->Tq > 1 && d->q_stride_t < cq) return GDN_ERR_INVALID_ARG;
+    if (d->Tk > 1 && (d->k_stride_t < ck || d->v_stride_t < ck)) return GDN_ERR_INVALID_ARG;
+    if ((double)d->B * d->Tq * cq > 4.0e12 || (double)d->B * d->Tk * ck > 4.0e12) return GDN_ERR_UNSUPPORTED;
+    return GDN_OK;
+}
+
+namespace {
+
+// The checks that forward and backward share; on success p holds the inputs and the workspace
+int fill(WindowProblem &p, const gdn_window_attention_desc *d, const void *q, const void *k, const void *v, const int32_t *cu,
+         const int32_t *cuk, const void *out, const float *lse, void *workspace, size_t workspace_bytes, bool backward) {
+    int rc = window_check_desc(d, cu != nullptr);
+    if (rc != GDN_OK) return rc;
+    if (cuk && !cu) return GDN_ERR_INVALID_ARG;
+    if (cu && !cuk && d->Tq != d->Tk) return GDN_ERR_INVALID_ARG;
+    const bool nq = (int64_t)d->B * d->Tq > 0, nk = (int64_t)d->B * d->Tk > 0;   // token tensors may be empty (null)
+    if ((nq && (!q || !out)) || (nk && (!k || !v))) return GDN_ERR_INVALID_ARG;
+    const size_t es = act_size(d->dtype);
+    if (!ptr_aligned(q, es) || !ptr_aligned(k, es) || !ptr_aligned(v, es) || !ptr_aligned(out, es) || !ptr_aligned(lse, 4) ||
+        !ptr_aligned(cu, 4) || !ptr_aligned(cuk, 4))
+        return GDN_ERR_INVALID_ARG;
+    const WindowLayout L = layout_of(*d, backward);
+    if ((rc = check_workspace(workspace, workspace_bytes, L.total)) != GDN_OK) return rc;
+    char *ws = (char *)workspace;
+    memset(&p, 0, sizeof(p));
+    p.d = *d;
+    p.q = q, p.k = k, p.v = v;
+    p.cu = cu, p.cuk = cuk ? cuk : cu;
+    p.lse = const_cast<float *>(lse);
+    p.status = (int32_t *)ws;
+    p.q_tiles = (int32_t *)(ws + L.q_tiles);
+    p.k_tiles = (int32_t *)(ws + L.k_tiles);
+    p.delta = (float *)(ws + L.delta);
+    p.wait_immediate = wait_test_mode();
+    return GDN_OK;
+}
+
+int bytes_of(const gdn_window_attention_desc *d, size_t *bytes, bool backward) {
+    if (!d || !bytes) return GDN_ERR_INVALID_ARG;
+    const int rc = window_check_desc(d, d->N != d->B);
+    if (rc != GDN_OK) return rc;
+    *bytes = layout_of(*d, backward).total;
+    return GDN_OK;
+}
+
+}  // namespace
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+int gdn_window_attention_desc_init(gdn_window_attention_desc *d, int B, int Tq, int Tk, int packed, int Hq, int Hk, int head_dim,
+                                   int window, int sinks, int dtype) {
+    if (!d) return GDN_ERR_INVALID_ARG;
+    memset(d, 0, sizeof(*d));
+    d->B = B, d->Tq = Tq, d->Tk = Tk;
+    d->N = packed ? packed : B;
+    d->Hq = Hq, d->Hk = Hk, d->d = head_dim;
+    d->window = window, d->sinks = sinks;
+    d->slots = (int32_t)std::min<int64_t>((int64_t)window + sinks, 0x7fffffff);
+    d->dtype = dtype;
+    d->scale = head_dim > 0 ? (float)(1.0 / sqrt((double)head_dim)) : 0.0f;
+    d->q_stride_t = (int64_t)Hq * head_dim;
+    d->k_stride_t = d->v_stride_t = (int64_t)Hk * head_dim;
+    d->q_stride_b = d->q_stride_t * Tq;
+    d->k_stride_b = d->v_stride_b = d->k_stride_t * Tk;
+    return window_check_desc(d, packed != 0);
+}
+
+int gdn_window_attention_workspace_bytes(const gdn_window_attention_desc *d, size_t *bytes) { return bytes_of(d, bytes, false); }
+int gdn_window_attention_backward_workspace_bytes(const gdn_window_attention_desc *d, size_t *bytes) { return bytes_of(d, bytes, true); }
+
+int gdn_window_attention_kernel_kind(const gdn_window_attention_desc *d) { return 0; }
+
+int gdn_window_attention_forward(const gdn_window_attention_desc *d, const void *q, const void *k, const void *v, const int32_t *cu_seqlens,
+                                 const int32_t *cu_seqlens_k, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                 gdn_stream_t stream) {
+    WindowProblem p;
+    const int rc = fill(p, d, q, k, v, cu_seqlens, cu_seqlens_k, out, lse, workspace, workspace_bytes, false);
+    if (rc != GDN_OK) return rc;
+    p.out = out;
+    const cudaStream_t s = (cudaStream_t)stream;
+    const cudaError_t e = launch_window_tables(p, 128, 128, s);
+    if (e != cudaSuccess) return GDN_ERR_CUDA;
+    switch (d->dtype) {
+    case GDN_F32: return layer_status(forward_any<float>(p, s));
+    case GDN_BF16: return layer_status(forward_any<__nv_bfloat16>(p, s));
+    default: return layer_status(forward_any<__half>(p, s));
+    }
+}
+
+int gdn_window_attention_backward(const gdn_window_attention_desc *d, const void *q, const void *k, const void *v, const void *out,
+                                  const float *lse, const void *grad_out, const int32_t *cu_seqlens, const int32_t *cu_seqlens_k,
+                                  void *dq, void *dk, void *dv, void *workspace, size_t workspace_bytes, gdn_stream_t stream) {
+    WindowProblem p;
+    const int rc = fill(p, d, q, k, v, cu_seqlens, cu_seqlens_k, out, lse, workspace, workspace_bytes, true);
+    if (rc != GDN_OK) return rc;
+    const size_t es = act_size(d->dtype);
+    if ((int64_t)d->B * d->Tq > 0 && (!lse || !grad_out || !dq)) return GDN_ERR_INVALID_ARG;
+    if ((int64_t)d->B * d->Tk > 0 && (!dk || !dv)) return GDN_ERR_INVALID_ARG;
+    if (!ptr_aligned(grad_out, es) || !ptr_aligned(dq, es) || !ptr_aligned(dk, es) || !ptr_aligned(dv, es)) return GDN_ERR_INVALID_ARG;
+    p.out_in = out, p.dout = grad_out;
+    p.dq = dq, p.dk = dk, p.dv = dv;
+    const cudaStream_t s = (cudaStream_t)stream;
+    const cudaError_t e = launch_window_tables(p, 128, 128, s);
+    if (e != cudaSuccess) return GDN_ERR_CUDA;
+    switch (d->dtype) {
+    case GDN_F32: return layer_status(backward_any<float>(p, s));
+    case GDN_BF16: return layer_status(backward_any<__nv_bfloat16>(p, s));
+    default: return layer_status(backward_any<__half>(p, s));
+    }
+}
+
+}  // extern "C"

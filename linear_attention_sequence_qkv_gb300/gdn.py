@@ -45,7 +45,13 @@ EXPORTS = ("gdn_desc_init", "gdn_workspace_bytes", "gdn_workspace_offsets", "gdn
            "gdn_rotary_table", "gdn_rotary_workspace_bytes", "gdn_rotary",
            "gdn_group_norm_desc_init", "gdn_group_norm_workspace_bytes",
            "gdn_group_norm_backward_workspace_bytes", "gdn_group_norm_forward",
-           "gdn_group_norm_backward")
+           "gdn_group_norm_backward", "gdn_norm_rotary_desc_init", "gdn_norm_rotary_workspace_bytes",
+           "gdn_norm_rotary_backward_workspace_bytes", "gdn_norm_rotary_forward", "gdn_norm_rotary_backward",
+           "gdn_window_attention_desc_init", "gdn_window_attention_workspace_bytes",
+           "gdn_window_attention_backward_workspace_bytes", "gdn_window_attention_step_workspace_bytes",
+           "gdn_window_cache_write_workspace_bytes", "gdn_window_attention_kernel_kind",
+           "gdn_window_attention_forward", "gdn_window_attention_backward", "gdn_window_cache_write",
+           "gdn_window_attention_step")
 
 GDN_RECURRENCE_CHUNK = 4
 ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
@@ -103,6 +109,17 @@ class gdn_group_norm_desc(ctypes.Structure):
         ("eps", ctypes.c_float), ("x_stride_n", ctypes.c_int64), ("x_stride_l", ctypes.c_int64)]
 
 
+class gdn_norm_rotary_desc(ctypes.Structure):
+    _fields_ = [("rotary", gdn_rotary_desc), ("weight_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class gdn_window_attention_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "Tq", "Tk", "N", "Hq", "Hk", "d", "window", "sinks", "slots",
+                                              "dtype")] + [("scale", ctypes.c_float)] + [
+        (n, ctypes.c_int64) for n in ("q_stride_b", "q_stride_t", "k_stride_b", "k_stride_t", "v_stride_b",
+                                      "v_stride_t")]
+
+
 _lib = None
 
 
@@ -153,6 +170,21 @@ def load(path: str = LIB_PATH):
     L.gdn_group_norm_backward_workspace_bytes.argtypes = [np_, szp]
     L.gdn_group_norm_forward.argtypes = [np_] + [vp] * 6 + [vp, sz, vp]
     L.gdn_group_norm_backward.argtypes = [np_] + [vp] * 9 + [vp, sz, vp]
+    hp, wp = ctypes.POINTER(gdn_norm_rotary_desc), ctypes.POINTER(gdn_window_attention_desc)
+    L.gdn_norm_rotary_desc_init.argtypes = [hp] + [i32] * 7
+    L.gdn_norm_rotary_workspace_bytes.argtypes = [hp, szp]
+    L.gdn_norm_rotary_backward_workspace_bytes.argtypes = [hp, szp]
+    L.gdn_norm_rotary_forward.argtypes = [hp] + [vp] * 10 + [vp, sz, vp]
+    L.gdn_norm_rotary_backward.argtypes = [hp] + [vp] * 14 + [vp, sz, vp]
+    L.gdn_window_attention_desc_init.argtypes = [wp] + [i32] * 10
+    for name in ("gdn_window_attention_workspace_bytes", "gdn_window_attention_backward_workspace_bytes",
+                 "gdn_window_attention_step_workspace_bytes", "gdn_window_cache_write_workspace_bytes"):
+        getattr(L, name).argtypes = [wp, szp]
+    L.gdn_window_attention_kernel_kind.argtypes = [wp]
+    L.gdn_window_attention_forward.argtypes = [wp] + [vp] * 7 + [vp, sz, vp]
+    L.gdn_window_attention_backward.argtypes = [wp] + [vp] * 11 + [vp, sz, vp]
+    L.gdn_window_cache_write.argtypes = [wp] + [vp] * 6 + [vp, sz, vp]
+    L.gdn_window_attention_step.argtypes = [wp] + [vp] * 7 + [vp, sz, vp]
     for name in EXPORTS:
         if name != "gdn_status_string":
             getattr(L, name).restype = i32
@@ -464,6 +496,106 @@ def gdn_group_norm_backward(d, x, weight, bias, mean, rstd, grad_out, dx, dweigh
                                         int(workspace_bytes), _stream(stream))
     if check:
         _check(rc, "gdn_group_norm_backward")
+    return rc
+
+
+def gdn_norm_rotary_desc_init(B, T, packed, Hq, Hk, d, dtype) -> gdn_norm_rotary_desc:
+    r = gdn_norm_rotary_desc()
+    _check(load().gdn_norm_rotary_desc_init(ctypes.byref(r), B, T, packed, Hq, Hk, d, dtype), "gdn_norm_rotary_desc_init")
+    return r
+
+
+def gdn_norm_rotary_workspace_bytes(d) -> int:
+    return _query("gdn_norm_rotary_workspace_bytes", d)
+
+
+def gdn_norm_rotary_backward_workspace_bytes(d) -> int:
+    return _query("gdn_norm_rotary_backward_workspace_bytes", d)
+
+
+def gdn_norm_rotary_forward(d, q, k, q_weight, k_weight, turns, positions, cu_seqlens, offsets, q_out, k_out, workspace,
+                            workspace_bytes, stream=None, check=True) -> int:
+    rc = load().gdn_norm_rotary_forward(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(turns),
+                                        _ptr(positions), _ptr(cu_seqlens), _ptr(offsets), _ptr(q_out), _ptr(k_out),
+                                        _ptr(workspace), int(workspace_bytes), _stream(stream))
+    if check:
+        _check(rc, "gdn_norm_rotary_forward")
+    return rc
+
+
+def gdn_norm_rotary_backward(d, q, k, q_weight, k_weight, turns, positions, cu_seqlens, offsets, grad_q, grad_k, dq, dk,
+                             dq_weight, dk_weight, workspace, workspace_bytes, stream=None, check=True) -> int:
+    rc = load().gdn_norm_rotary_backward(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(turns),
+                                         _ptr(positions), _ptr(cu_seqlens), _ptr(offsets), _ptr(grad_q), _ptr(grad_k),
+                                         _ptr(dq), _ptr(dk), _ptr(dq_weight), _ptr(dk_weight), _ptr(workspace),
+                                         int(workspace_bytes), _stream(stream))
+    if check:
+        _check(rc, "gdn_norm_rotary_backward")
+    return rc
+
+
+def gdn_window_attention_desc_init(B, Tq, Tk, packed, Hq, Hk, d, window, sinks, dtype) -> gdn_window_attention_desc:
+    r = gdn_window_attention_desc()
+    _check(load().gdn_window_attention_desc_init(ctypes.byref(r), B, Tq, Tk, packed, Hq, Hk, d, window, sinks, dtype),
+           "gdn_window_attention_desc_init")
+    return r
+
+
+def gdn_window_attention_workspace_bytes(d) -> int:
+    return _query("gdn_window_attention_workspace_bytes", d)
+
+
+def gdn_window_attention_backward_workspace_bytes(d) -> int:
+    return _query("gdn_window_attention_backward_workspace_bytes", d)
+
+
+def gdn_window_attention_step_workspace_bytes(d) -> int:
+    return _query("gdn_window_attention_step_workspace_bytes", d)
+
+
+def gdn_window_cache_write_workspace_bytes(d) -> int:
+    return _query("gdn_window_cache_write_workspace_bytes", d)
+
+
+def gdn_window_attention_kernel_kind(d) -> int:
+    return load().gdn_window_attention_kernel_kind(ctypes.byref(d))
+
+
+def gdn_window_attention_forward(d, q, k, v, cu_seqlens, cu_seqlens_k, out, lse, workspace, workspace_bytes, stream=None,
+                                 check=True) -> int:
+    rc = load().gdn_window_attention_forward(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens),
+                                             _ptr(cu_seqlens_k), _ptr(out), _ptr(lse), _ptr(workspace),
+                                             int(workspace_bytes), _stream(stream))
+    if check:
+        _check(rc, "gdn_window_attention_forward")
+    return rc
+
+
+def gdn_window_attention_backward(d, q, k, v, out, lse, grad_out, cu_seqlens, cu_seqlens_k, dq, dk, dv, workspace,
+                                  workspace_bytes, stream=None, check=True) -> int:
+    rc = load().gdn_window_attention_backward(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
+                                              _ptr(grad_out), _ptr(cu_seqlens), _ptr(cu_seqlens_k), _ptr(dq), _ptr(dk),
+                                              _ptr(dv), _ptr(workspace), int(workspace_bytes), _stream(stream))
+    if check:
+        _check(rc, "gdn_window_attention_backward")
+    return rc
+
+
+def gdn_window_cache_write(d, k, v, cu_seqlens, lengths, k_cache, v_cache, workspace, workspace_bytes, stream=None,
+                           check=True) -> int:
+    rc = load().gdn_window_cache_write(ctypes.byref(d), _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(lengths), _ptr(k_cache),
+                                       _ptr(v_cache), _ptr(workspace), int(workspace_bytes), _stream(stream))
+    if check:
+        _check(rc, "gdn_window_cache_write")
+    return rc
+
+
+def gdn_window_attention_step(d, q, k, v, lengths, k_cache, v_cache, out, workspace, workspace_bytes, stream=None,
+                              check=True) -> int:
+    rc = load().gdn_window_attention_step(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(lengths), _ptr(k_cache),
+                                          _ptr(v_cache), _ptr(out), _ptr(workspace), int(workspace_bytes), _stream(stream))
+    if check:
+        _check(rc, "gdn_window_attention_step")
     return rc
 
 
@@ -930,3 +1062,264 @@ def group_norm_backward(x, weight, bias, mean, rstd, grad_out, *, groups, act="s
     gdn_group_norm_backward(d, x, weight, bias, mean, rstd, grad_out, grads.dx, grads.dweight, grads.dbias,
                             grads.workspace, grads.ws_bytes, stream)
     return grads
+
+
+# ------------------------------------------- operators of attention layers
+def norm_rotary_desc_for(q, k, q_out, k_out, q_weight=None, *, d, rot=None, layout="half", scale=1.0, eps=1e-6,
+                         cu_seqlens=None) -> gdn_norm_rotary_desc:
+    """Descriptor of ``norm_rotary`` for [B, T, H*d] views (k and k_out None: no k)."""
+    r = rotary_desc_for(q, k, q_out, k_out, d=d, rot=rot, layout=layout, scale=scale, cu_seqlens=cu_seqlens)
+    n = gdn_norm_rotary_desc()
+    n.rotary = r
+    n.weight_dtype = r.dtype if q_weight is None else DTYPE_CODES[q_weight.dtype]
+    n.eps = eps
+    return n
+
+
+@dataclass
+class NormRotaryGrads:
+    dq: torch.Tensor
+    dk: Optional[torch.Tensor]
+    dq_weight: Optional[torch.Tensor]
+    dk_weight: Optional[torch.Tensor]
+    workspace: torch.Tensor
+
+    @property
+    def ws_bytes(self) -> int:
+        return self.workspace.numel()
+
+
+def alloc_norm_rotary_grads(desc, device) -> NormRotaryGrads:
+    """Gradient buffers and workspace of gdn_norm_rotary_backward."""
+    r = desc.rotary
+    tok = lambda h: torch.empty((r.B, r.T, h * r.d), dtype=ACT_TORCH[r.dtype], device=device)  # noqa: E731
+    w = lambda: torch.empty(r.d, dtype=torch.float32, device=device)  # noqa: E731
+    return NormRotaryGrads(tok(r.Hq), tok(r.Hk) if r.Hk else None, w(), w() if r.Hk else None,
+                           torch.empty(gdn_norm_rotary_backward_workspace_bytes(desc), dtype=torch.uint8, device=device))
+
+
+def _check_norm_rotary(n, q, q_weight, k_weight, table, positions, cu_seqlens, offsets):
+    r = n.rotary
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        _expect(t, name, (r.d,), ACT_TORCH[n.weight_dtype], q.device)
+    _expect(table, "table", (r.rot // 2,), torch.int64, q.device)
+    _expect(positions, "positions", (r.B, r.T), torch.int32, q.device)
+    _expect(cu_seqlens, "cu_seqlens", (r.N + 1,), torch.int32, q.device)
+    _expect(offsets, "offsets", (r.N,), torch.int32, q.device)
+
+
+def norm_rotary(q, k, q_weight, k_weight, table, *, d, rot=None, layout="half", scale=1.0, eps=1e-6, positions=None,
+                cu_seqlens=None, offsets=None, q_out=None, k_out=None, workspace=None, stream=None):
+    """The norm of every head of q and k (k may be None) and its rotary position in one pass (see
+    gdn_norm_rotary_forward in include/gdn.h): (q_out, k_out). The other arguments are ``rotary``'s."""
+    _on_current(q)
+    with _allocating(stream):
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    n = norm_rotary_desc_for(q, k, q_out, k_out, q_weight if q_weight is not None else k_weight, d=d, rot=rot,
+                             layout=layout, scale=scale, eps=eps, cu_seqlens=cu_seqlens)
+    _check_norm_rotary(n, q, q_weight, k_weight, table, positions, cu_seqlens, offsets)
+    if workspace is None:
+        with _allocating(stream):
+            workspace = torch.empty(gdn_norm_rotary_workspace_bytes(n), dtype=torch.uint8, device=q.device)
+    _expect_workspace(workspace, q.device)
+    gdn_norm_rotary_forward(n, q, k, q_weight, k_weight, table, positions, cu_seqlens, offsets, q_out, k_out, workspace,
+                            workspace.numel(), stream)
+    return q_out, k_out
+
+
+def norm_rotary_backward(q, k, q_weight, k_weight, table, grad_q, grad_k, *, d, rot=None, layout="half", scale=1.0,
+                         eps=1e-6, positions=None, cu_seqlens=None, offsets=None,
+                         grads: Optional[NormRotaryGrads] = None, stream=None) -> NormRotaryGrads:
+    """Gradients of sum(grad_q * q_out) + sum(grad_k * k_out); q and k are the forward's inputs."""
+    _on_current(q)
+    n = norm_rotary_desc_for(q, k, grad_q, grad_k, q_weight if q_weight is not None else k_weight, d=d, rot=rot,
+                             layout=layout, scale=scale, eps=eps, cu_seqlens=cu_seqlens)
+    _check_norm_rotary(n, q, q_weight, k_weight, table, positions, cu_seqlens, offsets)
+    if grads is None:
+        with _allocating(stream):
+            grads = alloc_norm_rotary_grads(n, q.device)
+    else:
+        _expect(grads.dq, "grads.dq", q.shape, q.dtype, q.device)
+        if (k is None) != (grads.dk is None):
+            raise ValueError("k and grads.dk: both or neither")
+        if k is not None:
+            _expect(grads.dk, "grads.dk", k.shape, q.dtype, q.device)
+        for name in ("dq_weight", "dk_weight"):
+            _expect(getattr(grads, name), f"grads.{name}", (d,), torch.float32, q.device)
+        _expect_workspace(grads.workspace, q.device)
+    gdn_norm_rotary_backward(n, q, k, q_weight, k_weight, table, positions, cu_seqlens, offsets, grad_q, grad_k, grads.dq,
+                             grads.dk, grads.dq_weight, grads.dk_weight, grads.workspace, grads.ws_bytes, stream)
+    return grads
+
+
+def window_attention_desc_for(q, k, v, *, d, window, sinks=0, scale=None, slots=None,
+                              cu_seqlens=None) -> gdn_window_attention_desc:
+    """Descriptor of the window attention of [B, Tq, Hq*d] queries over [B, Tk, Hk*d] keys and values
+    (q None: of the cache's filling)."""
+    _expect(v, "v", k.shape, k.dtype, k.device, contiguous=False)
+    B, Tk, ck = k.shape
+    if q is None:
+        Tq, cq = Tk, ck
+    else:
+        _expect(q, "q", (B, q.shape[1], q.shape[-1]), k.dtype, k.device, contiguous=False)
+        Tq, cq = q.shape[1], q.shape[2]
+    for name, c in (("q", cq), ("k", ck)):
+        if d < 1 or c % d:
+            raise ValueError(f"{name}: {c} channels, not a multiple of the head's {d}")
+    r = gdn_window_attention_desc_init(B, Tq, Tk, 0 if cu_seqlens is None else cu_seqlens.numel() - 1, cq // d, ck // d, d,
+                                       window, sinks, DTYPE_CODES[k.dtype])
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t is not None:
+            sb, st = _strides(t, name)
+            setattr(r, f"{name}_stride_b", sb)
+            setattr(r, f"{name}_stride_t", st)
+    if scale is not None:
+        r.scale = scale
+    if slots is not None:
+        r.slots = slots
+    return r
+
+
+@dataclass
+class WindowAttentionBuffers:
+    desc: gdn_window_attention_desc
+    out: torch.Tensor
+    lse: Optional[torch.Tensor]
+    workspace: torch.Tensor
+
+    @property
+    def ws_bytes(self) -> int:
+        return self.workspace.numel()
+
+
+def alloc_window_attention(desc, device, want_lse=True) -> WindowAttentionBuffers:
+    """Output buffers of gdn_window_attention_forward; lse is what its backward reads."""
+    return WindowAttentionBuffers(
+        desc, torch.empty((desc.B, desc.Tq, desc.Hq * desc.d), dtype=ACT_TORCH[desc.dtype], device=device),
+        torch.empty((desc.Hq, desc.B * desc.Tq), dtype=torch.float32, device=device) if want_lse else None,
+        torch.empty(gdn_window_attention_workspace_bytes(desc), dtype=torch.uint8, device=device))
+
+
+@dataclass
+class WindowAttentionGrads:
+    dq: torch.Tensor
+    dk: torch.Tensor
+    dv: torch.Tensor
+    workspace: torch.Tensor
+
+    @property
+    def ws_bytes(self) -> int:
+        return self.workspace.numel()
+
+
+def alloc_window_attention_grads(desc, device) -> WindowAttentionGrads:
+    """Gradient buffers and workspace of gdn_window_attention_backward."""
+    tok = lambda t, h: torch.empty((desc.B, t, h * desc.d), dtype=ACT_TORCH[desc.dtype], device=device)  # noqa: E731
+    return WindowAttentionGrads(
+        tok(desc.Tq, desc.Hq), tok(desc.Tk, desc.Hk), tok(desc.Tk, desc.Hk),
+        torch.empty(gdn_window_attention_backward_workspace_bytes(desc), dtype=torch.uint8, device=device))
+
+
+def _check_window(r, k, cu_seqlens, cu_seqlens_k):
+    _on_current(k)
+    for t, name in ((cu_seqlens, "cu_seqlens"), (cu_seqlens_k, "cu_seqlens_k")):
+        _expect(t, name, (r.N + 1,), torch.int32, k.device)
+
+
+def window_attention_forward(q, k, v, *, d, window, sinks=0, scale=None, cu_seqlens=None, cu_seqlens_k=None, want_lse=True,
+                             bufs: Optional[WindowAttentionBuffers] = None, stream=None) -> WindowAttentionBuffers:
+    """Causal attention over the last ``window`` tokens and the first ``sinks`` ones (see
+    gdn_window_attention_forward in include/gdn.h) of [B, T, H*d] views; packed sequences with
+    cu_seqlens (int32 [N+1], B = 1), and cu_seqlens_k where keys precede the queries."""
+    r = window_attention_desc_for(q, k, v, d=d, window=window, sinks=sinks, scale=scale, cu_seqlens=cu_seqlens)
+    _check_window(r, k, cu_seqlens, cu_seqlens_k)
+    if bufs is None:
+        with _allocating(stream):
+            bufs = alloc_window_attention(r, k.device, want_lse)
+    else:
+        _expect(bufs.out, "bufs.out", q.shape, k.dtype, k.device)
+        _expect(bufs.lse, "bufs.lse", (r.Hq, r.B * r.Tq), torch.float32, k.device)
+        _expect_workspace(bufs.workspace, k.device)
+        bufs.desc = r
+    gdn_window_attention_forward(r, q, k, v, cu_seqlens, cu_seqlens_k, bufs.out, bufs.lse, bufs.workspace, bufs.ws_bytes,
+                                 stream)
+    return bufs
+
+
+def window_attention_backward(q, k, v, out, lse, grad_out, *, d, window, sinks=0, scale=None, cu_seqlens=None,
+                              cu_seqlens_k=None, grads: Optional[WindowAttentionGrads] = None,
+                              stream=None) -> WindowAttentionGrads:
+    """Gradients of sum(grad_out * out) with the forward's out and lse."""
+    r = window_attention_desc_for(q, k, v, d=d, window=window, sinks=sinks, scale=scale, cu_seqlens=cu_seqlens)
+    _check_window(r, k, cu_seqlens, cu_seqlens_k)
+    for t, name in ((out, "out"), (grad_out, "grad_out")):
+        _expect(t, name, q.shape, k.dtype, k.device)
+    _expect(lse, "lse", (r.Hq, r.B * r.Tq), torch.float32, k.device)
+    if grads is None:
+        with _allocating(stream):
+            grads = alloc_window_attention_grads(r, k.device)
+    else:
+        for name, like in (("dq", q), ("dk", k), ("dv", v)):
+            _expect(getattr(grads, name), f"grads.{name}", like.shape, k.dtype, k.device)
+        _expect_workspace(grads.workspace, k.device)
+    gdn_window_attention_backward(r, q, k, v, out, lse, grad_out, cu_seqlens, cu_seqlens_k, grads.dq, grads.dk, grads.dv,
+                                  grads.workspace, grads.ws_bytes, stream)
+    return grads
+
+
+@dataclass
+class WindowCache:
+    """Keys and values of N sequences, [N, Hk, slots, d] each, and what was written before: int32 [N]."""
+    k: torch.Tensor
+    v: torch.Tensor
+    lengths: torch.Tensor
+    window: int
+    sinks: int
+
+
+def alloc_window_cache(N, Hk, d, *, window, sinks=0, slots=None, dtype=torch.bfloat16, device="cuda") -> WindowCache:
+    """An empty cache; ``slots`` beyond sinks + window keep older tokens without showing them."""
+    slots = sinks + window if slots is None else slots
+    rows = lambda: torch.empty((N, Hk, slots, d), dtype=dtype, device=device)  # noqa: E731
+    return WindowCache(rows(), rows(), torch.zeros(N, dtype=torch.int32, device=device), window, sinks)
+
+
+def _check_cache(r, cache, k):
+    for name in ("k", "v"):
+        _expect(getattr(cache, name), f"cache.{name}", (r.N, r.Hk, r.slots, r.d), k.dtype, k.device)
+    _expect(cache.lengths, "cache.lengths", (r.N,), torch.int32, k.device)
+
+
+def window_cache_write(k, v, cache: WindowCache, *, cu_seqlens=None, workspace=None, stream=None) -> None:
+    """Write the tokens of [B, T, Hk*d] views (or packed ones) behind what the cache holds (see
+    gdn_window_cache_write in include/gdn.h). cache.lengths is left to the caller, whose layers share it."""
+    r = window_attention_desc_for(None, k, v, d=cache.k.shape[-1], window=cache.window, sinks=cache.sinks,
+                                  slots=cache.k.shape[2], cu_seqlens=cu_seqlens)
+    _check_window(r, k, cu_seqlens, None)
+    _check_cache(r, cache, k)
+    if workspace is None:
+        with _allocating(stream):
+            workspace = torch.empty(gdn_window_cache_write_workspace_bytes(r), dtype=torch.uint8, device=k.device)
+    _expect_workspace(workspace, k.device)
+    gdn_window_cache_write(r, k, v, cu_seqlens, cache.lengths, cache.k, cache.v, workspace, workspace.numel(), stream)
+
+
+def window_attention_step(q, k, v, cache: WindowCache, *, scale=None, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """One more token of each sequence: q [B, 1, Hq*d], k, v [B, 1, Hk*d] views; the cache takes k and v in at
+    position cache.lengths, which the caller then increases, once for all layers."""
+    r = window_attention_desc_for(q, k, v, d=cache.k.shape[-1], window=cache.window, sinks=cache.sinks, scale=scale,
+                                  slots=cache.k.shape[2])
+    _check_window(r, k, None, None)
+    _check_cache(r, cache, k)
+    with _allocating(stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if workspace is None:
+            workspace = torch.empty(gdn_window_attention_step_workspace_bytes(r), dtype=torch.uint8, device=k.device)
+    _expect(out, "out", q.shape, k.dtype, k.device)
+    _expect_workspace(workspace, k.device)
+    gdn_window_attention_step(r, q, k, v, cache.lengths, cache.k, cache.v, out, workspace, workspace.numel(), stream)
+    return out
