@@ -1016,6 +1016,17 @@ bool encode_token_map(CUtensorMap *m, int dtype, const void *base, uint64_t batc
                   CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
+bool encode_head_map(CUtensorMap *m, int dtype, const void *base, uint64_t batch, uint64_t tokens, uint64_t heads, uint64_t width,
+                     uint64_t pitch_b, uint64_t pitch_t, uint32_t box_t) {
+    const cuuint64_t dims[4] = {width, heads, tokens, batch};
+    const cuuint64_t strides[3] = {width * 2, pitch_t, pitch_b};
+    const cuuint32_t box[4] = {64, 1, box_t, 1};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return encode(m, dtype == GDN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                  const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
 bool chunk_tc_supports(const gdn_desc &d) {
     return (d.dtype == GDN_BF16 || d.dtype == GDN_F16) && (d.dk == 64 || d.dk == 128 || d.dk == 256) &&
            d.dv >= 64 && d.dv % 64 == 0;

@@ -6,7 +6,7 @@
 
 #include <algorithm>
 
-#include "gdn_window.cuh"
+#include "gdn_window_tc.cuh"
 
 namespace gdn {
 namespace {
@@ -285,7 +285,7 @@ int gdn_window_attention_desc_init(gdn_window_attention_desc *d, int B, int Tq, 
 int gdn_window_attention_workspace_bytes(const gdn_window_attention_desc *d, size_t *bytes) { return bytes_of(d, bytes, false); }
 int gdn_window_attention_backward_workspace_bytes(const gdn_window_attention_desc *d, size_t *bytes) { return bytes_of(d, bytes, true); }
 
-int gdn_window_attention_kernel_kind(const gdn_window_attention_desc *d) { return 0; }
+int gdn_window_attention_kernel_kind(const gdn_window_attention_desc *d) { return d && window_tc_fits(*d) ? 1 : 0; }
 
 int gdn_window_attention_forward(const gdn_window_attention_desc *d, const void *q, const void *k, const void *v, const int32_t *cu_seqlens,
                                  const int32_t *cu_seqlens_k, void *out, float *lse, void *workspace, size_t workspace_bytes,
@@ -295,6 +295,7 @@ int gdn_window_attention_forward(const gdn_window_attention_desc *d, const void 
     if (rc != GDN_OK) return rc;
     p.out = out;
     const cudaStream_t s = (cudaStream_t)stream;
+    if ((int64_t)d->B * d->Tq > 0 && d->Tk > 0 && window_tc_supports(p)) return layer_status(launch_window_forward_tc(p, s));
     const cudaError_t e = launch_window_tables(p, 128, 128, s);
     if (e != cudaSuccess) return GDN_ERR_CUDA;
     switch (d->dtype) {

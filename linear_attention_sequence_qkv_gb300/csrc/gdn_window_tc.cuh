@@ -1,0 +1,74 @@
+// gdn_window_tc.cuh -- what the window attention's tensor-core kernels share: tensor maps,
+// the tiles of keys that a tile of queries needs, masks, and packed conversions.
+#pragma once
+
+#include <type_traits>
+
+#include "gdn_tc.cuh"
+#include "gdn_window.cuh"
+
+namespace gdn {
+
+// q, k and v (and grad_out) per head; a batch stride of 0 becomes a map of one row
+struct WindowMaps {
+    CUtensorMap q, k, v, g;
+    int q_rows, k_rows, v_rows;   // 1: batch row n is coordinate n, 0: all rows are one
+};
+
+// The tiles of 128 keys that queries at positions [p0, p1] (p0 clamped to 0) need: [0, sinks) and [w0, w1]
+struct WindowTiles {
+    int ns, w0, w1;
+    __device__ __forceinline__ bool empty() const { return w1 < w0; }
+    __device__ __forceinline__ bool has(int t) const { return t < ns || (t >= w0 && t <= w1); }
+};
+__device__ __forceinline__ WindowTiles window_tiles(int p0, int p1, int window, int sinks) {
+    WindowTiles r;
+    if (p1 < 0) {
+        r.ns = 0, r.w0 = 0, r.w1 = -1;
+        return r;
+    }
+    const int lo = window_first(max(p0, 0), window);
+    r.w0 = lo >> 7;
+    r.w1 = p1 >> 7;
+    r.ns = min((int)(((int64_t)min(sinks, lo) + 127) >> 7), r.w0);
+    return r;
+}
+// Whether some query at positions [p0, p1] does not see all keys of tile t
+__device__ __forceinline__ bool window_partial(int t, int p0, int p1, int window, int sinks) {
+    const int64_t a = (int64_t)t * 128, b = a + 127;
+    return b > p0 || (a <= (int64_t)p1 - window && b >= sinks);
+}
+
+// the n lowest bits, none for n <= 0, all for n >= 32
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; }
+
+template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi) { return Pairs<T>::pack1(make_float2(lo, hi)); }
+
+// The kernels' waits: about a second each, then the CTA gives up (GDN_ERR_DEVICE_TIMEOUT); the first that does tells the others
+struct WindowWait {
+    volatile int *gave_up;   // shared memory
+    bool immediate;
+    __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const {
+        if (immediate ? tc::mbar_test_now(bar, parity) : tc::mbar_test(bar, parity)) return true;
+        if (*gave_up) return false;
+        if (!tc::mbar_wait(bar, parity, immediate)) {
+            *gave_up = 1;
+            return false;
+        }
+        return true;
+    }
+};
+
+// a wait of a whole warp, whose answer is the same for all lanes
+__device__ __forceinline__ bool warp_wait(const WindowWait &wait, uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait(bar, parity));
+}
+// the first lane's value, known to be the warp's
+__device__ __forceinline__ int of_warp(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// whether sizes and strides, and with them the pointers, suit the tensor-core kernels
+bool window_tc_fits(const gdn_window_attention_desc &d);
+bool window_tc_supports(const WindowProblem &p);
+cudaError_t launch_window_forward_tc(const WindowProblem &p, cudaStream_t s);
+
+}  // namespace gdn
