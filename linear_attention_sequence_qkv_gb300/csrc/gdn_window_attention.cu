@@ -172,14 +172,18 @@ cudaError_t forward_any(const WindowProblem &p, cudaStream_t s) {
     return p.d.d <= 64 ? forward_rows<T, 2>(p, s) : p.d.d <= 128 ? forward_rows<T, 4>(p, s) : forward_rows<T, 8>(p, s);
 }
 template <typename T>
-cudaError_t backward_any(const WindowProblem &p, cudaStream_t s) {
+cudaError_t backward_any(WindowProblem &p, cudaStream_t s) {
     const int64_t rows = (int64_t)p.d.B * p.d.Tq * p.d.Hq;
     if (rows) window_delta<T><<<row_blocks(rows, 8), 256, 0, s>>>(p);
+    if (rows && p.d.Tk > 0 && window_tc_supports(p)) {
+        window_rest_plan(p);
+        return launch_window_backward_tc(p, s);
+    }
     return p.d.d <= 64 ? backward_rows<T, 2>(p, s) : p.d.d <= 128 ? backward_rows<T, 4>(p, s) : backward_rows<T, 8>(p, s);
 }
 
 struct WindowLayout {
-    size_t status, q_tiles, k_tiles, delta, total;
+    size_t status, q_tiles, k_tiles, rest, delta, partial, total;
 };
 WindowLayout layout_of(const gdn_window_attention_desc &d, bool backward) {
     WindowLayout L;
@@ -187,8 +191,18 @@ WindowLayout layout_of(const gdn_window_attention_desc &d, bool backward) {
     L.status = off;  off += kStatusBytes;
     L.q_tiles = off; off = align_up(off + 4 * ((size_t)d.N + 1), 256);
     L.k_tiles = off; off = align_up(off + 4 * ((size_t)d.N + 1), 256);
-    L.delta = off;
-    if (backward) off = align_up(off + (size_t)d.B * d.Tq * d.Hq * 4, 256);
+    L.rest = L.delta = L.partial = off;
+    if (backward) {
+        off = align_up(off + 4 * ((size_t)d.N + 1), 256);
+        L.delta = off;   off = align_up(off + (size_t)d.B * d.Tq * d.Hq * 4, 256);
+        L.partial = off;
+        if (window_tc_fits(d)) {
+            WindowProblem p;
+            p.d = d;
+            window_rest_plan(p);
+            off = align_up(off + window_partial_bytes(p), 256);
+        }
+    }
     L.total = off;
     return L;
 }
@@ -244,7 +258,9 @@ int fill(WindowProblem &p, const gdn_window_attention_desc *d, const void *q, co
     p.status = (int32_t *)ws;
     p.q_tiles = (int32_t *)(ws + L.q_tiles);
     p.k_tiles = (int32_t *)(ws + L.k_tiles);
+    p.rest_off = (int32_t *)(ws + L.rest);
     p.delta = (float *)(ws + L.delta);
+    p.partial = (float *)(ws + L.partial);
     p.wait_immediate = wait_test_mode();
     return GDN_OK;
 }

@@ -441,7 +441,7 @@ bool window_tc_supports(const WindowProblem &p) {
            ptr_aligned(p.dv, 16);
 }
 
-static bool head_map(CUtensorMap *m, const gdn_window_attention_desc &d, const void *base, int heads, int tokens, int64_t sb, int64_t st,
+bool window_head_map(CUtensorMap *m, const gdn_window_attention_desc &d, const void *base, int heads, int tokens, int64_t sb, int64_t st,
                      int *rows, uint32_t box) {
     const bool one = d.B == 1 || sb == 0;
     *rows = one ? 0 : 1;
@@ -453,9 +453,9 @@ cudaError_t launch_window_forward_tc(const WindowProblem &p, cudaStream_t s) {
     const gdn_window_attention_desc &d = p.d;
     WindowMaps maps;
     memset(&maps, 0, sizeof(maps));
-    if (!head_map(&maps.q, d, p.q, d.Hq, d.Tq, d.q_stride_b, d.q_stride_t, &maps.q_rows, 128) ||
-        !head_map(&maps.k, d, p.k, d.Hk, d.Tk, d.k_stride_b, d.k_stride_t, &maps.k_rows, 128) ||
-        !head_map(&maps.v, d, p.v, d.Hk, d.Tk, d.v_stride_b, d.v_stride_t, &maps.v_rows, 128))
+    if (!window_head_map(&maps.q, d, p.q, d.Hq, d.Tq, d.q_stride_b, d.q_stride_t, &maps.q_rows, 128) ||
+        !window_head_map(&maps.k, d, p.k, d.Hk, d.Tk, d.k_stride_b, d.k_stride_t, &maps.k_rows, 128) ||
+        !window_head_map(&maps.v, d, p.v, d.Hk, d.Tk, d.v_stride_b, d.v_stride_t, &maps.v_rows, 128))
         return cudaErrorInvalidValue;
     const int pair_heads = d.Hq / d.Hk % 2 == 0, units = pair_heads ? d.Hq / 2 : d.Hq, rows = pair_heads ? 128 : 256;
     const int64_t tiles = p.cu ? cdiv64(d.Tq, rows) + d.N : (int64_t)d.B * cdiv64(d.Tq, rows);

@@ -9,6 +9,8 @@ import numpy as np
 
 from oracle.layer_ops import HALF_STEP, U32, bound, frequencies, rotary  # noqa: F401
 
+FLUSH = 2.0 ** -126   # fp32's smallest normal value
+
 
 def norm_rotary(x, w, positions, freq, rot, layout, eps, scale=1.0, dout=None, fast=False):
     """x [B, T, H, d] with integer positions [B, T]; a dict with y and, with dout, dx and dw; ``*_err`` bounds what fp32
@@ -72,6 +74,8 @@ def window_attention(q, k, v, window, sinks, scale, dtype, dout=None):
     1 (so that the sum l >= 1). l itself is added up in fp32 unrounded: n U32. The product with v adds 2n U32.
     Backward: P = exp(s - lse) with lse's own error; delta = sum dO O takes O's error and rounding; dS = scale P (dP - delta) is
     rounded to the type, as P is; the sums over n keys (or queries and heads) add 2n U32.
+    The hardware's exponential counts a result below 2^-126, the smallest normal fp32, as 0 (ex2.approx.ftz): a weight, whose
+    row's largest is at least 1, and a P are off by up to 2^-126 more.
     """
     q, k, v = (np.asarray(x, np.float64) for x in (q, k, v))
     Lq, Hq, d = q.shape
@@ -103,7 +107,7 @@ def window_attention(q, k, v, window, sinks, scale, dtype, dout=None):
         rp = np.where(see, es + U32 * (4 * (np.abs(np.where(see, s, 0.0)) + big) + 8), 0.0)
         mean_rp = (P * rp).sum(1)[:, None]
         O = P @ V
-        eO = (P * (eps + rp)) @ aV + (mean_rp + U32 * (3 * n_row + 16)) * (P @ aV) + least * (see @ aV)
+        eO = (P * (eps + rp)) @ aV + (mean_rp + U32 * (3 * n_row + 16)) * (P @ aV) + (least + FLUSH) * (see @ aV)
         lse = np.where(any_seen, top[:, 0] + np.log(l[:, 0]), -np.inf)
         elog = mean_rp[:, 0] + U32 * (n_row[:, 0] + 8 + 4 * np.abs(np.where(any_seen, lse, 0.0)) + 2 * big[:, 0])
         r["out"][:, h], r["out_err"][:, h] = O, eO
@@ -117,9 +121,9 @@ def window_attention(q, k, v, window, sinks, scale, dtype, dout=None):
         dP, edP = g @ V.T, U32 * (2 * d + 8) * (ag @ aV.T)
         rP = rp + elog[:, None] + U32 * (4 * np.abs(np.where(any_seen, lse, 0.0))[:, None] + 8)
         dS = scale * P * (dP - delta)
-        edS = scale * P * (rP * np.abs(dP - delta) + edP + edelta + 4 * U32 * (np.abs(dP) + np.abs(delta)))
+        edS = scale * FLUSH * see * (np.abs(dP - delta) + edP + edelta) + scale * P * (rP * np.abs(dP - delta) + edP + edelta + 4 * U32 * (np.abs(dP) + np.abs(delta)))
         edS = edS + eps * (np.abs(dS) + edS) + least * see
-        eP = P * (rP + eps * (1 + rP)) + least * see
+        eP = P * (rP + eps * (1 + rP)) + (least + FLUSH) * see
         r["dq"][:, h] = dS @ K
         r["dq_err"][:, h] = edS @ aK + 2 * U32 * n_row * (np.abs(dS) @ aK)
         r["dk"][:, h // G] += dS.T @ Q
