@@ -1,9 +1,11 @@
 // gdn_norm_rotary.cu -- the norm of every head of q and k with the rotary positions in the
 // same pass (include/gdn.h), forward and backward.
 //
-// A warp takes one head of one token at a time: its channels go through shared memory as
-// fp32, the sum of squares over the lanes, and every pair is normalised, weighted and turned
-// from there.
+// Streaming kernels, bound by HBM: a team of lanes (the power of two that a head's vectors
+// fill) takes a token, or a part of its heads, computes the token's cosines and sines once into
+// registers, and goes through the heads with four of them on their way; the other half of a pair
+// comes from its lane by shuffle, as raw bits. Where vectors do not fit (odd widths, unaligned
+// rows), a warp takes one head at a time through shared memory.
 #include <math.h>
 #include <string.h>
 
@@ -164,6 +166,275 @@ __global__ void __launch_bounds__(256) norm_rotary_weights(const __grid_constant
     if (lane == 0 && to) to[c < d ? c : c - d] = s;
 }
 
+// ------------------------------------------------------------- vectors in registers
+template <int BYTES> struct Raw;
+template <> struct Raw<16> { using type = uint4; };
+template <> struct Raw<8> { using type = uint2; };
+template <> struct Raw<4> { using type = uint32_t; };
+template <typename T, int V> union Vec {
+    typename Raw<V * sizeof(T)>::type raw;
+    uint32_t w[V * sizeof(T) / 4];
+    T e[V];
+};
+
+constexpr int kThreads = 256;
+constexpr int kFlight = 4;   // heads whose loads are on their way at once
+
+// A lane's place in its team: K vectors of V channels, lane + k team of them; for each the channel it starts at, what it
+// does in the turn, and for the half layout the lane and vector that hold the other half of its pairs
+template <int V, int K, bool HALF> struct Place {
+    int c[K], other[K];      // first channel (-1: none); the partner's vector
+    bool turned[K], upper[K];
+    __device__ __forceinline__ Place(const gdn_rotary_desc &d, int lane, int team) {
+        const int off = d.rot / 2 / V;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int v = k * team + lane;
+            c[k] = v * V < d.d ? v * V : -1;
+            turned[k] = v * V < d.rot;
+            upper[k] = HALF && v >= off;
+            other[k] = !HALF || !turned[k] ? v : upper[k] ? v - off : v + off;
+        }
+    }
+};
+// cosines and sines of a lane's pairs at a position, with the attention factor: 1 and 0 where nothing turns; the sine's
+// sign as y = x cos + other sin wants it (half layout)
+template <typename T, int V, int K, bool HALF>
+__device__ __forceinline__ void turns_of(const NormRotaryProblem &p, const Place<V, K, HALF> &at, int64_t pos, float (&co)[K][V], float (&si)[K][V]) {
+    const gdn_rotary_desc &d = p.n.rotary;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            if (!HALF && (e & 1)) continue;   // one entry for a pair
+            co[k][e] = 1.0f, si[k][e] = 0.0f;
+            if (at.turned[k]) {
+                const int pair = HALF ? at.c[k] + e - (at.upper[k] ? d.rot / 2 : 0) : (at.c[k] + e) / 2;
+                const float2 cs = cos_sin<sizeof(T) == 2>(pos, p.turns[pair]);
+                co[k][e] = cs.x * d.scale;
+                si[k][e] = HALF && !at.upper[k] ? -cs.y * d.scale : cs.y * d.scale;
+            }
+        }
+}
+// the other half's vectors
+template <typename T, int V, int K, bool HALF>
+__device__ __forceinline__ void partners(const Place<V, K, HALF> &at, const Vec<T, V> (&x)[K], Vec<T, V> (&o)[K], int team) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int w = 0; w < (int)(V * sizeof(T) / 4); ++w) {
+            uint32_t got = 0;
+#pragma unroll
+            for (int q = 0; q < K; ++q) {
+                const uint32_t v = __shfl_sync(0xffffffffu, x[q].w[w], at.other[k] & (team - 1), team);
+                if (K == 1 || at.other[k] / team == q) got = v;
+            }
+            o[k].w[w] = got;
+        }
+}
+template <int TEAM> __device__ __forceinline__ float team_sum(float v) {
+#pragma unroll
+    for (int o = TEAM / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// A team's item: a token and a run of its heads
+struct Item {
+    int row, t;
+    int64_t tok;
+    bool ok;
+};
+__device__ __forceinline__ Item item_at(const gdn_rotary_desc &d, int64_t i, int parts, int &part) {
+    Item x = {0, 0, 0, i < (int64_t)d.B * d.T * parts};
+    part = 0;
+    if (!x.ok) return x;
+    x.tok = i / parts;
+    part = (int)(i - x.tok * parts);
+    x.row = (int)(x.tok / d.T);
+    x.t = (int)(x.tok - (int64_t)x.row * d.T);
+    return x;
+}
+
+template <typename T, int V, int K, int TEAM, bool HALF>
+__global__ void __launch_bounds__(kThreads) norm_rotary_vectors(const __grid_constant__ NormRotaryProblem p, int parts, int per) {
+    const gdn_rotary_desc &d = p.n.rotary;
+    const bool ok = p.cu == nullptr || seqlens_ok(p.cu, d.N, d.T);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = ok ? GDN_OK : GDN_ERR_DEVICE_SEQLENS;
+    if (!ok) return;
+    const int lane = threadIdx.x % TEAM;
+    int part;
+    const Item it = item_at(d, (int64_t)blockIdx.x * (kThreads / TEAM) + threadIdx.x / TEAM, parts, part);
+    const Place<V, K, HALF> at(d, lane, TEAM);
+    const int h0 = part * per, h1 = it.ok ? min(h0 + per, d.Hq + d.Hk) : h0;   // the lanes of a warp stay together: empty runs loop too
+    float co[K][V], si[K][V];
+    turns_of<T, V, K, HALF>(p, at, it.ok ? rotary_position(d, p.pos, p.cu, p.off, it.row, it.t) : 0, co, si);
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+        const void *w = which ? p.kw : p.qw;
+        const int a = max(h0, which ? d.Hq : 0), b = min(h1, which ? d.Hq + d.Hk : d.Hq);
+        const T *src = (const T *)(which ? p.k : p.q) + it.row * (which ? d.k_stride_b : d.q_stride_b) + it.t * (which ? d.k_stride_t : d.q_stride_t);
+        T *dst = (T *)(which ? p.ko : p.qo) + it.row * (which ? d.k_out_stride_b : d.q_out_stride_b) + it.t * (which ? d.k_out_stride_t : d.q_out_stride_t);
+        const int first = which ? d.Hq : 0;
+        const int runs = max(0, b - a);
+        if (!__any_sync(0xffffffffu, runs > 0)) continue;
+        float wo[K][V], wp[K][V];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                wo[k][e] = at.c[k] >= 0 ? weight_at(w, p.n.weight_dtype, at.c[k] + e) : 0.0f;
+                if (HALF) wp[k][e] = at.c[k] >= 0 ? weight_at(w, p.n.weight_dtype, at.other[k] * V + e) : 0.0f;
+            }
+        const int most = __reduce_max_sync(0xffffffffu, runs);
+        for (int r0 = 0; r0 < most; r0 += kFlight) {
+            Vec<T, V> x[kFlight][K];
+#pragma unroll
+            for (int j = 0; j < kFlight; ++j)
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+#pragma unroll
+                    for (int q = 0; q < (int)(V * sizeof(T) / 4); ++q) x[j][k].w[q] = 0;
+                    if (r0 + j < runs && at.c[k] >= 0) x[j][k].raw = *(const decltype(x[j][k].raw) *)(src + (int64_t)(a + r0 + j - first) * d.d + at.c[k]);
+                }
+#pragma unroll
+            for (int j = 0; j < kFlight; ++j) {
+                if (r0 + j >= most) break;
+                float ss = 0.0f;
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) ss = fmaf(to_f<T>(x[j][k].e[e]), to_f<T>(x[j][k].e[e]), ss);
+                const float rstd = rsqrtf(team_sum<TEAM>(ss) / d.d + p.n.eps);
+                Vec<T, V> o[K], y[K];
+                if (HALF) partners<T, V, K, HALF>(at, x[j], o, TEAM);
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    if (HALF) {
+#pragma unroll
+                        for (int e = 0; e < V; ++e) {
+                            const float z = to_f<T>(x[j][k].e[e]) * rstd * wo[k][e], zo = to_f<T>(o[k].e[e]) * rstd * wp[k][e];
+                            y[k].e[e] = from_f<T>(at.turned[k] ? z * co[k][e] + zo * si[k][e] : z);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < V; e += 2) {
+                            const float z1 = to_f<T>(x[j][k].e[e]) * rstd * wo[k][e], z2 = to_f<T>(x[j][k].e[e + 1]) * rstd * wo[k][e + 1];
+                            y[k].e[e] = from_f<T>(z1 * co[k][e] - z2 * si[k][e]);
+                            y[k].e[e + 1] = from_f<T>(z2 * co[k][e] + z1 * si[k][e]);
+                        }
+                    }
+                    if (r0 + j < runs && at.c[k] >= 0) *(decltype(y[k].raw) *)(dst + (int64_t)(a + r0 + j - first) * d.d + at.c[k]) = y[k].raw;
+                }
+            }
+        }
+    }
+}
+
+template <typename T, int V, int K, int TEAM, bool HALF>
+__global__ void __launch_bounds__(kThreads) norm_rotary_vectors_backward(const __grid_constant__ NormRotaryProblem p, int parts, int per) {
+    extern __shared__ float sm[];   // [teams][2][d]
+    const gdn_rotary_desc &d = p.n.rotary;
+    const bool ok = p.cu == nullptr || seqlens_ok(p.cu, d.N, d.T);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = ok ? GDN_OK : GDN_ERR_DEVICE_SEQLENS;
+    if (!ok) return;
+    constexpr int kTeams = kThreads / TEAM, kF = kFlight / 2;   // two tensors' loads per head
+    const int lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
+    const Place<V, K, HALF> at(d, lane, TEAM);
+    float acc[2][K][V];
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[w][k][e] = 0.0f;
+    const int64_t items = (int64_t)d.B * d.T * parts;
+    for (int64_t i0 = (int64_t)blockIdx.x * kTeams; i0 < items; i0 += (int64_t)gridDim.x * kTeams) {
+        int part;
+        const Item it = item_at(d, i0 + team, parts, part);
+        const int h0 = part * per, h1 = it.ok ? min(h0 + per, d.Hq + d.Hk) : h0;
+        float co[K][V], si[K][V];
+        turns_of<T, V, K, HALF>(p, at, it.ok ? rotary_position(d, p.pos, p.cu, p.off, it.row, it.t) : 0, co, si);
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            const void *w = which ? p.kw : p.qw;
+            const int a = max(h0, which ? d.Hq : 0), b = min(h1, which ? d.Hq + d.Hk : d.Hq), first = which ? d.Hq : 0;
+            const T *src = (const T *)(which ? p.k : p.q) + it.row * (which ? d.k_stride_b : d.q_stride_b) + it.t * (which ? d.k_stride_t : d.q_stride_t);
+            const T *grd = (const T *)(which ? p.ko : p.qo) + it.row * (which ? d.k_out_stride_b : d.q_out_stride_b) +
+                           it.t * (which ? d.k_out_stride_t : d.q_out_stride_t);
+            T *dst = (T *)(which ? p.dk : p.dq) + it.tok * (which ? d.Hk : d.Hq) * d.d;
+            const int runs = max(0, b - a), most = __reduce_max_sync(0xffffffffu, runs);
+            if (most == 0) continue;
+            float wo[K][V];
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int e = 0; e < V; ++e) wo[k][e] = at.c[k] >= 0 ? weight_at(w, p.n.weight_dtype, at.c[k] + e) : 0.0f;
+            for (int r0 = 0; r0 < most; r0 += kF) {
+                Vec<T, V> x[kF][K], g[kF][K];
+#pragma unroll
+                for (int j = 0; j < kF; ++j)
+#pragma unroll
+                    for (int k = 0; k < K; ++k) {
+#pragma unroll
+                        for (int q = 0; q < (int)(V * sizeof(T) / 4); ++q) x[j][k].w[q] = g[j][k].w[q] = 0;
+                        if (r0 + j < runs && at.c[k] >= 0) {
+                            x[j][k].raw = *(const decltype(x[j][k].raw) *)(src + (int64_t)(a + r0 + j - first) * d.d + at.c[k]);
+                            g[j][k].raw = *(const decltype(g[j][k].raw) *)(grd + (int64_t)(a + r0 + j - first) * d.d + at.c[k]);
+                        }
+                    }
+#pragma unroll
+                for (int j = 0; j < kF; ++j) {
+                    if (r0 + j >= most) break;
+                    Vec<T, V> o[K];
+                    if (HALF) partners<T, V, K, HALF>(at, g[j], o, TEAM);
+                    float ss = 0.0f, st = 0.0f, dz[K][V];
+#pragma unroll
+                    for (int k = 0; k < K; ++k)
+#pragma unroll
+                        for (int e = 0; e < V; ++e) {
+                            const float xv = to_f<T>(x[j][k].e[e]), gv = to_f<T>(g[j][k].e[e]);
+                            if (HALF) {   // the turn back: the sine the other way round
+                                dz[k][e] = at.turned[k] ? gv * co[k][e] - to_f<T>(o[k].e[e]) * si[k][e] : gv;
+                            } else if (e & 1) {
+                                dz[k][e] = gv * co[k][e & ~1] - to_f<T>(g[j][k].e[e & ~1]) * si[k][e & ~1];
+                            } else {
+                                dz[k][e] = gv * co[k][e] + to_f<T>(g[j][k].e[e | 1]) * si[k][e];
+                            }
+                            ss = fmaf(xv, xv, ss);
+                            st = fmaf(dz[k][e] * wo[k][e], xv, st);
+                        }
+                    ss = team_sum<TEAM>(ss), st = team_sum<TEAM>(st);
+                    const float rstd = rsqrtf(ss / d.d + p.n.eps), mean = rstd * st / d.d;   // of t xh
+#pragma unroll
+                    for (int k = 0; k < K; ++k) {
+                        Vec<T, V> y;
+#pragma unroll
+                        for (int e = 0; e < V; ++e) {
+                            const float xh = to_f<T>(x[j][k].e[e]) * rstd;
+                            acc[which][k][e] = fmaf(dz[k][e], xh, acc[which][k][e]);
+                            y.e[e] = from_f<T>(rstd * (dz[k][e] * wo[k][e] - xh * mean));
+                        }
+                        if (r0 + j < runs && at.c[k] >= 0) *(decltype(y.raw) *)(dst + (int64_t)(a + r0 + j - first) * d.d + at.c[k]) = y.raw;
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (at.c[k] >= 0) sm[(team * 2 + w) * d.d + at.c[k] + e] = acc[w][k][e];
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * d.d; c += kThreads) {
+        float s = 0.0f;
+        for (int x = 0; x < kTeams; ++x) s += sm[x * 2 * d.d + c];
+        p.part[(int64_t)blockIdx.x * 2 * d.d + c] = s;
+    }
+}
+
 int check_desc(const gdn_norm_rotary_desc *n, bool packed) {
     if (!n) return GDN_ERR_INVALID_ARG;
     const int rc = rotary_check_desc(&n->rotary, packed);
@@ -178,24 +449,74 @@ int64_t heads_of(const gdn_rotary_desc &d) { return (int64_t)d.B * d.T * (d.Hq +
 int bwd_ctas(const gdn_rotary_desc &d) { return (int)std::min<int64_t>(std::max<int64_t>(cdiv64(heads_of(d), kWarps), 1), kBwdCtas); }
 size_t bwd_bytes(const gdn_rotary_desc &d) { return kStatusBytes + (size_t)bwd_ctas(d) * 2 * d.d * 4; }
 
-template <typename T>
-cudaError_t launch_forward(const NormRotaryProblem &p, cudaStream_t s) {
+// Whether vectors of v elements divide a head and its rotated part and fit every base and stride
+bool fits(const NormRotaryProblem &p, int v) {
     const gdn_rotary_desc &d = p.n.rotary;
-    const int64_t blocks = std::min<int64_t>(std::max<int64_t>(cdiv64(heads_of(d), kWarps), 1), 16 * kSms);
-    norm_rotary_rows<T><<<(unsigned)blocks, 32 * kWarps, (size_t)kWarps * d.d * 4, s>>>(p);
+    const size_t bytes = v * act_size(d.dtype);
+    const int width = d.layout == GDN_ROTARY_HALF ? d.rot / 2 : d.rot;
+    if (bytes < 4 || bytes > 16 || v < 2 || width % v || d.d % v || d.d / v > 64) return false;
+    const void *ptrs[] = {p.q, p.qo, p.k, p.ko, p.dq, p.dk};
+    for (const void *x : ptrs)
+        if (!ptr_aligned(x, bytes)) return false;
+    const int64_t st[] = {d.q_stride_t, d.q_out_stride_t, d.Hk ? d.k_stride_t : 0, d.Hk ? d.k_out_stride_t : 0};
+    const int64_t sb[] = {d.q_stride_b, d.q_out_stride_b, d.Hk ? d.k_stride_b : 0, d.Hk ? d.k_out_stride_b : 0};
+    for (int i = 0; i < 4; ++i)
+        if ((d.T > 1 && st[i] % v) || (d.B > 1 && sb[i] % v)) return false;
+    return true;
+}
+
+// Parts of a token's heads: until there are 16 warps per SM
+int parts_of(const gdn_rotary_desc &d, int team) {
+    const int64_t ntok = std::max<int64_t>((int64_t)d.B * d.T, 1), teams = (int64_t)kSms * 16 * (32 / team);
+    return (int)std::min<int64_t>(d.Hq + d.Hk, cdiv64(teams, ntok));
+}
+
+template <typename T, int V, int K, int TEAM, bool HALF>
+cudaError_t launch_vectors(NormRotaryProblem &p, bool backward, cudaStream_t s) {
+    const gdn_rotary_desc &d = p.n.rotary;
+    constexpr int kTeams = kThreads / TEAM;
+    const int heads = d.Hq + d.Hk, per = (int)cdiv64(heads, parts_of(d, TEAM)), parts = (int)cdiv64(heads, per);
+    const int64_t blocks = std::max<int64_t>(cdiv64((int64_t)d.B * d.T * parts, kTeams), 1);
+    if (!backward) {
+        if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+        norm_rotary_vectors<T, V, K, TEAM, HALF><<<(unsigned)blocks, kThreads, 0, s>>>(p, parts, per);
+        return cudaGetLastError();
+    }
+    const size_t smem = (size_t)kTeams * 2 * d.d * 4;   // at most 32 KB: a team's channels are at most 16 of its lanes' bytes
+    p.ctas = (int)std::min<int64_t>(blocks, p.ctas);
+    norm_rotary_vectors_backward<T, V, K, TEAM, HALF><<<(unsigned)p.ctas, kThreads, smem, s>>>(p, parts, per);
     return cudaGetLastError();
 }
+template <typename T, int V, bool HALF>
+cudaError_t launch_team(NormRotaryProblem &p, bool backward, cudaStream_t s) {
+    const int nv = p.n.rotary.d / V;
+    if (nv > 32) return launch_vectors<T, V, 2, 32, HALF>(p, backward, s);
+    if (nv > 16) return launch_vectors<T, V, 1, 32, HALF>(p, backward, s);
+    if (nv > 8) return launch_vectors<T, V, 1, 16, HALF>(p, backward, s);
+    return launch_vectors<T, V, 1, 8, HALF>(p, backward, s);
+}
 template <typename T>
-cudaError_t launch_backward_rows(const NormRotaryProblem &p, cudaStream_t s) {
+cudaError_t launch(NormRotaryProblem &p, bool backward, cudaStream_t s) {
     const gdn_rotary_desc &d = p.n.rotary;
-    const size_t smem = (size_t)kWarps * 4 * d.d * 4;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = allow_shared(norm_rotary_rows_backward<T>, (size_t)kWarps * 4 * kMostChannels * 4);
+    const bool half = d.layout == GDN_ROTARY_HALF;
+    cudaError_t e = cudaSuccess;
+    bool done = false;
+    if constexpr (sizeof(T) == 2)
+        if (fits(p, 8)) e = half ? launch_team<T, 8, true>(p, backward, s) : launch_team<T, 8, false>(p, backward, s), done = true;
+    if (!done && fits(p, 4)) e = half ? launch_team<T, 4, true>(p, backward, s) : launch_team<T, 4, false>(p, backward, s), done = true;
+    if (!done && fits(p, 2)) e = half ? launch_team<T, 2, true>(p, backward, s) : launch_team<T, 2, false>(p, backward, s), done = true;
+    if (!done && !backward) {
+        const int64_t blocks = std::min<int64_t>(std::max<int64_t>(cdiv64(heads_of(d), kWarps), 1), 16 * kSms);
+        norm_rotary_rows<T><<<(unsigned)blocks, 32 * kWarps, (size_t)kWarps * d.d * 4, s>>>(p);
+        e = cudaGetLastError();
+    } else if (!done) {
+        const size_t smem = (size_t)kWarps * 4 * d.d * 4;
+        if (smem > 48 * 1024) e = allow_shared(norm_rotary_rows_backward<T>, (size_t)kWarps * 4 * kMostChannels * 4);
         if (e != cudaSuccess) return e;
+        norm_rotary_rows_backward<T><<<(unsigned)p.ctas, 32 * kWarps, smem, s>>>(p);
+        e = cudaGetLastError();
     }
-    norm_rotary_rows_backward<T><<<(unsigned)p.ctas, 32 * kWarps, smem, s>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || (!p.dqw && !p.dkw)) return e;
+    if (e != cudaSuccess || !backward || (!p.dqw && !p.dkw)) return e;
     norm_rotary_weights<<<(unsigned)cdiv64(2 * d.d, 8), 256, 0, s>>>(p);
     return cudaGetLastError();
 }
@@ -273,9 +594,9 @@ int gdn_norm_rotary_forward(const gdn_norm_rotary_desc *n, const void *q, const 
         return GDN_ERR_INVALID_ARG;
     const cudaStream_t s = (cudaStream_t)stream;
     switch (d.dtype) {
-    case GDN_F32: return layer_status(launch_forward<float>(p, s));
-    case GDN_BF16: return layer_status(launch_forward<__nv_bfloat16>(p, s));
-    default: return layer_status(launch_forward<__half>(p, s));
+    case GDN_F32: return layer_status(launch<float>(p, false, s));
+    case GDN_BF16: return layer_status(launch<__nv_bfloat16>(p, false, s));
+    default: return layer_status(launch<__half>(p, false, s));
     }
 }
 
@@ -296,9 +617,9 @@ int gdn_norm_rotary_backward(const gdn_norm_rotary_desc *n, const void *q, const
     p.ctas = bwd_ctas(d);
     const cudaStream_t s = (cudaStream_t)stream;
     switch (d.dtype) {
-    case GDN_F32: return layer_status(launch_backward_rows<float>(p, s));
-    case GDN_BF16: return layer_status(launch_backward_rows<__nv_bfloat16>(p, s));
-    default: return layer_status(launch_backward_rows<__half>(p, s));
+    case GDN_F32: return layer_status(launch<float>(p, true, s));
+    case GDN_BF16: return layer_status(launch<__nv_bfloat16>(p, true, s));
+    default: return layer_status(launch<__half>(p, true, s));
     }
 }
 
