@@ -1,7 +1,6 @@
 // gdn_window.cuh -- what the window attention's kernels share: the problem, the place of a
-// sequence, which keys a query sees, and single rows computed by one warp (the kernels of
-// any type, size and alignment; the tensor-core kernels fall back on them for rows that
-// came out non-finite).
+// sequence, which keys a query sees, and a single query computed by one warp (for the queries
+// that see a value which is not finite).
 #pragma once
 
 #include <math.h>
@@ -127,41 +126,10 @@ __device__ __noinline__ void row_forward(const T *q, const T *k, const T *v, int
     lse = m + logf(l);
 }
 
-// The gradient of one query: dq = scale * sum_j P_j (dO . v_j - delta) k_j
-template <typename T, int NC>
-__device__ __noinline__ void row_dq(const T *q, const T *dout, const T *k, const T *v, int64_t kst, int64_t vst, int d, float scale,
-                                    int pos, int window, int sinks, float lse, float delta, int lane, float (&dq)[NC]) {
-    float qr[NC], gr[NC];
-    row_load<T, NC>(q, d, lane, qr);
-    row_load<T, NC>(dout, d, lane, gr);
-#pragma unroll
-    for (int c = 0; c < NC; ++c) dq[c] = 0.0f;
-    const int lo = window_first(pos, window), first = min(sinks, lo), total = first + pos - lo + 1;
-    for (int t0 = 0; t0 < total; t0 += 32) {
-        const int t = t0 + lane, n = min(32, total - t0);
-        const int j = t < first ? t : min(lo + t - first, pos);
-        const float s = row_dot<T, NC>(qr, k + j * kst, d) * scale, dp = row_dot<T, NC>(gr, v + j * vst, d);
-        rows_add<T, NC>(dq, lane < n ? expf(s - lse) * (dp - delta) * scale : 0.0f, k + j * kst, n, d, lane);
-    }
-}
-
-// What the queries at positions [p0, p1) of one head give to the gradients of one key: rows of q and dout with these
-// strides, lse and delta of the sequence's first query, `past` = Lk - Lq
-template <typename T, int NC>
-__device__ __noinline__ void row_dkv(const T *q, const T *dout, const float (&kr)[NC], const float (&vr)[NC], int64_t qst, int64_t gst,
-                                     const float *lse, const float *delta, int d, float scale, int64_t p0, int64_t p1, int past, int lane,
-                                     float (&dk)[NC], float (&dv)[NC]) {
-    for (int64_t t0 = p0; t0 < p1; t0 += 32) {
-        const int n = (int)min((int64_t)32, p1 - t0);
-        const int64_t i = min(t0 + lane, p1 - 1) - past;
-        const float s = row_dot<T, NC>(kr, q + i * qst, d) * scale, dp = row_dot<T, NC>(vr, dout + i * gst, d);
-        const float w = lane < n ? expf(s - lse[i]) : 0.0f;
-        rows_add<T, NC>(dv, w, dout + i * gst, n, d, lane);
-        rows_add<T, NC>(dk, lane < n ? w * (dp - delta[i]) * scale : 0.0f, q + i * qst, n, d, lane);
-    }
-}
-
 // Status and, for packed sequences, the tiles' tables (tile: rows of a tile of queries, of keys)
 cudaError_t launch_window_tables(const WindowProblem &p, int q_tile, int k_tile, cudaStream_t s);
+// the CUDA-core kernels, of any type, size and alignment (gdn_window_simt.cu); the backward after tables, delta and chunks
+cudaError_t launch_window_forward_simt(const WindowProblem &p, cudaStream_t s);
+cudaError_t launch_window_backward_simt(const WindowProblem &p, cudaStream_t s);
 
 }  // namespace gdn

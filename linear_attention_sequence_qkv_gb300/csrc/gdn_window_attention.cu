@@ -1,17 +1,15 @@
 // gdn_window_attention.cu -- causal attention over a window of recent tokens and a few
 // first ones (include/gdn.h): the C entry points of its forward and backward, the check
-// of packed offsets, and the kernels of any type, size and alignment, in which a warp
-// computes one row.
+// of packed offsets, and the sums of grad_out * out that the backward starts from.
 #include <string.h>
 
 #include <algorithm>
 
+#include "gdn_window_rest.cuh"
 #include "gdn_window_tc.cuh"
 
 namespace gdn {
 namespace {
-
-constexpr int kRowWarps = 4;
 
 // Packed offsets checked, and the tiles of the sequences before each one counted
 __global__ void __launch_bounds__(1024) window_tables_kernel(const __grid_constant__ WindowProblem p, int q_tile, int k_tile) {
@@ -57,32 +55,39 @@ __global__ void __launch_bounds__(1024) window_tables_kernel(const __grid_consta
     }
 }
 
-// The sequence of a flattened token, by queries or by keys
-__device__ __forceinline__ int sequence_of(const int32_t *cu, int N, int T, int64_t token) {
-    return cu ? upper_index(cu, N, token) : (int)(token / T);
-}
-
-template <typename T, int NC>
-__global__ void __launch_bounds__(32 * kRowWarps) window_forward_rows(const __grid_constant__ WindowProblem p) {
-    if (*p.status != GDN_OK) return;
-    const gdn_window_attention_desc &d = p.d;
-    const int lane = threadIdx.x & 31;
-    const int64_t ntok = (int64_t)d.B * d.Tq, total = ntok * d.Hq;
-    for (int64_t i = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5); i < total; i += (int64_t)gridDim.x * kRowWarps) {
-        const int64_t tok = i / d.Hq;
-        const int h = (int)(i - tok * d.Hq), n = sequence_of(p.cu, d.N, d.Tq, tok), hk = h / (d.Hq / d.Hk);
-        const WindowSpan s = window_span(p, n);
-        const int at = (int)(tok - s.q0), pos = s.Lk - s.Lq + at;
-        float o[NC], lse = -INFINITY;
+// The chunks of every sequence counted, for packed ones
+__global__ void __launch_bounds__(1024) window_rest_table(const __grid_constant__ WindowProblem p) {
+    __shared__ int32_t sums[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool ok = *p.status == GDN_OK;
+    int before = 0;
+    for (int base = 0; base < p.d.N; base += blockDim.x) {
+        const int n = base + threadIdx.x;
+        int c = 0;
+        if (ok && n < p.d.N) {
+            const WindowSpan s = window_span(p, n);
+            for (int t = 0; t < p.sink_tiles; ++t) c += rest_chunks(p, s, t);
+        }
+        int x = c;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) o[c] = 0.0f;
-        if (pos >= 0)
-            row_forward<T, NC>((const T *)p.q + s.qoff + at * d.q_stride_t + (int64_t)h * d.d, (const T *)p.k + s.koff + (int64_t)hk * d.d,
-                               (const T *)p.v + s.voff + (int64_t)hk * d.d, d.k_stride_t, d.v_stride_t, d.d, d.scale, pos, d.window,
-                               d.sinks, lane, o, lse);
-        row_store<T, NC>((T *)p.out + (tok * d.Hq + h) * d.d, d.d, lane, o);
-        if (p.lse && lane == 0) p.lse[h * ntok + tok] = lse;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) sums[warp] = x;
+        __syncthreads();
+        int s = sums[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        const int ahead = warp ? __shfl_sync(0xffffffffu, s, warp - 1) : 0, all = __shfl_sync(0xffffffffu, s, 31);
+        if (n < p.d.N) p.rest_off[n] = before + ahead + x - c;
+        before += all;
+        __syncthreads();
     }
+    if (threadIdx.x == 0) p.rest_off[p.d.N] = before;
 }
 
 // delta = sum of grad_out * out per query and head
@@ -102,84 +107,19 @@ __global__ void __launch_bounds__(256) window_delta(const __grid_constant__ Wind
     }
 }
 
-template <typename T, int NC>
-__global__ void __launch_bounds__(32 * kRowWarps) window_dq_rows(const __grid_constant__ WindowProblem p) {
-    if (*p.status != GDN_OK) return;
-    const gdn_window_attention_desc &d = p.d;
-    const int lane = threadIdx.x & 31;
-    const int64_t ntok = (int64_t)d.B * d.Tq, total = ntok * d.Hq;
-    for (int64_t i = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5); i < total; i += (int64_t)gridDim.x * kRowWarps) {
-        const int64_t tok = i / d.Hq;
-        const int h = (int)(i - tok * d.Hq), n = sequence_of(p.cu, d.N, d.Tq, tok), hk = h / (d.Hq / d.Hk);
-        const WindowSpan s = window_span(p, n);
-        const int at = (int)(tok - s.q0), pos = s.Lk - s.Lq + at;
-        float r[NC];
-#pragma unroll
-        for (int c = 0; c < NC; ++c) r[c] = 0.0f;
-        if (pos >= 0)
-            row_dq<T, NC>((const T *)p.q + s.qoff + at * d.q_stride_t + (int64_t)h * d.d, (const T *)p.dout + i * d.d,
-                          (const T *)p.k + s.koff + (int64_t)hk * d.d, (const T *)p.v + s.voff + (int64_t)hk * d.d, d.k_stride_t,
-                          d.v_stride_t, d.d, d.scale, pos, d.window, d.sinks, p.lse[h * ntok + tok], p.delta[h * ntok + tok], lane, r);
-        row_store<T, NC>((T *)p.dq + i * d.d, d.d, lane, r);
-    }
-}
-
-template <typename T, int NC>
-__global__ void __launch_bounds__(32 * kRowWarps) window_dkv_rows(const __grid_constant__ WindowProblem p) {
-    if (*p.status != GDN_OK) return;
-    const gdn_window_attention_desc &d = p.d;
-    const int lane = threadIdx.x & 31, group = d.Hq / d.Hk;
-    const int64_t ntok = (int64_t)d.B * d.Tq, total = (int64_t)d.B * d.Tk * d.Hk;
-    for (int64_t i = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5); i < total; i += (int64_t)gridDim.x * kRowWarps) {
-        const int64_t tok = i / d.Hk;
-        const int hk = (int)(i - tok * d.Hk), n = sequence_of(p.cuk, d.N, d.Tk, tok);
-        const WindowSpan s = window_span(p, n);
-        const int j = (int)(tok - s.k0), past = s.Lk - s.Lq;
-        float kr[NC], vr[NC], dk[NC], dv[NC];
-        row_load<T, NC>((const T *)p.k + s.koff + j * d.k_stride_t + (int64_t)hk * d.d, d.d, lane, kr);
-        row_load<T, NC>((const T *)p.v + s.voff + j * d.v_stride_t + (int64_t)hk * d.d, d.d, lane, vr);
-#pragma unroll
-        for (int c = 0; c < NC; ++c) dk[c] = dv[c] = 0.0f;
-        // queries from the key's own position on, as far as its window (or the sequence) goes
-        const int64_t p0 = max(j, past), p1 = j < d.sinks ? s.Lk : min((int64_t)s.Lk, (int64_t)j + d.window);
-        for (int h = hk * group; h < (hk + 1) * group; ++h)
-            row_dkv<T, NC>((const T *)p.q + s.qoff + (int64_t)h * d.d, (const T *)p.dout + (s.q0 * d.Hq + h) * d.d, kr, vr, d.q_stride_t,
-                           (int64_t)d.Hq * d.d, p.lse + h * ntok + s.q0, p.delta + h * ntok + s.q0, d.d, d.scale, p0, p1, past, lane, dk,
-                           dv);
-        row_store<T, NC>((T *)p.dk + i * d.d, d.d, lane, dk);
-        row_store<T, NC>((T *)p.dv + i * d.d, d.d, lane, dv);
-    }
-}
-
 unsigned row_blocks(int64_t rows, int per) { return (unsigned)std::min<int64_t>(std::max<int64_t>(cdiv64(rows, per), 1), 0x7fffffff); }
 
-template <typename T, int NC>
-cudaError_t forward_rows(const WindowProblem &p, cudaStream_t s) {
-    const int64_t rows = (int64_t)p.d.B * p.d.Tq * p.d.Hq;
-    if (rows == 0) return cudaSuccess;
-    window_forward_rows<T, NC><<<row_blocks(rows, kRowWarps), 32 * kRowWarps, 0, s>>>(p);
-    return cudaGetLastError();
-}
-template <typename T, int NC>
-cudaError_t backward_rows(const WindowProblem &p, cudaStream_t s) {
-    const int64_t rows = (int64_t)p.d.B * p.d.Tq * p.d.Hq, keys = (int64_t)p.d.B * p.d.Tk * p.d.Hk;
-    if (rows) window_dq_rows<T, NC><<<row_blocks(rows, kRowWarps), 32 * kRowWarps, 0, s>>>(p);
-    if (keys) window_dkv_rows<T, NC><<<row_blocks(keys, kRowWarps), 32 * kRowWarps, 0, s>>>(p);
-    return cudaGetLastError();
-}
-template <typename T>
-cudaError_t forward_any(const WindowProblem &p, cudaStream_t s) {
-    return p.d.d <= 64 ? forward_rows<T, 2>(p, s) : p.d.d <= 128 ? forward_rows<T, 4>(p, s) : forward_rows<T, 8>(p, s);
-}
 template <typename T>
 cudaError_t backward_any(WindowProblem &p, cudaStream_t s) {
+    const bool tc = (int64_t)p.d.B * p.d.Tq > 0 && p.d.Tk > 0 && window_tc_supports(p);
+    cudaError_t e = launch_window_tables(p, tc ? 128 : 64, tc ? 128 : 64, s);
+    if (e != cudaSuccess) return e;
     const int64_t rows = (int64_t)p.d.B * p.d.Tq * p.d.Hq;
     if (rows) window_delta<T><<<row_blocks(rows, 8), 256, 0, s>>>(p);
-    if (rows && p.d.Tk > 0 && window_tc_supports(p)) {
-        window_rest_plan(p);
-        return launch_window_backward_tc(p, s);
-    }
-    return p.d.d <= 64 ? backward_rows<T, 2>(p, s) : p.d.d <= 128 ? backward_rows<T, 4>(p, s) : backward_rows<T, 8>(p, s);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    window_rest_plan(p);
+    if ((e = launch_window_rest_table(p, s)) != cudaSuccess) return e;
+    return tc ? launch_window_backward_tc(p, s) : launch_window_backward_simt(p, s);
 }
 
 struct WindowLayout {
@@ -196,12 +136,10 @@ WindowLayout layout_of(const gdn_window_attention_desc &d, bool backward) {
         off = align_up(off + 4 * ((size_t)d.N + 1), 256);
         L.delta = off;   off = align_up(off + (size_t)d.B * d.Tq * d.Hq * 4, 256);
         L.partial = off;
-        if (window_tc_fits(d)) {
-            WindowProblem p;
-            p.d = d;
-            window_rest_plan(p);
-            off = align_up(off + window_partial_bytes(p), 256);
-        }
+        WindowProblem p;
+        p.d = d;
+        window_rest_plan(p);
+        off = align_up(off + window_partial_bytes(p), 256);
     }
     L.total = off;
     return L;
@@ -211,6 +149,44 @@ WindowLayout layout_of(const gdn_window_attention_desc &d, bool backward) {
 
 cudaError_t launch_window_tables(const WindowProblem &p, int q_tile, int k_tile, cudaStream_t s) {
     window_tables_kernel<<<1, p.cu ? 1024 : 32, 0, s>>>(p, q_tile, k_tile);
+    return cudaGetLastError();
+}
+
+// Chunks of the sinks' rest: as long as a CTA of keys walks within the window, 32 to 512 tiles
+void window_rest_plan(WindowProblem &p) {
+    const gdn_window_attention_desc &d = p.d;
+    const int64_t group = d.Hq / d.Hk;
+    p.rest_its = (int)std::min<int64_t>(512, std::max<int64_t>(32, group * (((int64_t)d.window + 127) / 64 + 1)));
+    p.sink_tiles = (int)cdiv64(std::min(d.sinks, d.Tk), 128);
+    p.sink_rows = std::min(128, std::min(d.sinks, d.Tk));
+    p.rest_per = 0;
+    p.rest_slots = 0;
+    if (p.sink_tiles == 0 || d.window >= d.Tk) {   // every key's window reaches the end
+        p.sink_tiles = 0;
+        return;
+    }
+    if (d.N == d.B) {   // not packed, or one sequence: the same chunks for all rows
+        for (int t = 0; t < p.sink_tiles; ++t) {
+            const int64_t past = (int64_t)d.Tk - d.Tq, j0 = (int64_t)t * 128, j1 = std::min<int64_t>(j0 + 127, d.Tk - 1);
+            const int64_t hi = std::min<int64_t>(d.Tq - 1, j1 + d.window - 1 - past), lo = std::max<int64_t>(0, j0 - past) >> 6;
+            const int64_t tiles = std::max<int64_t>(0, cdiv64(d.Tq, 64) - std::max<int64_t>(hi < 0 ? 0 : (hi >> 6) + 1, lo));
+            p.rest_per += (int)cdiv64(tiles * group, p.rest_its);
+        }
+        p.rest_slots = (int64_t)d.B * p.rest_per;
+    } else {            // at most: every sequence's last chunk begun
+        p.rest_slots = p.sink_tiles * (cdiv64(group * (cdiv64(d.Tq, 64) + d.N), p.rest_its) + d.N);
+    }
+    if (p.rest_slots == 0) p.sink_tiles = 0;
+}
+
+size_t window_partial_bytes(const WindowProblem &p) {
+    if (p.rest_slots == 0) return 0;
+    return (size_t)(p.rest_slots + (int64_t)p.d.N * p.sink_tiles) * p.d.Hk * p.sink_rows * 2 * (p.d.d <= 64 ? 64 : p.d.d <= 128 ? 128 : 256) * 4;
+}
+
+cudaError_t launch_window_rest_table(const WindowProblem &p, cudaStream_t s) {
+    if (!p.cu || p.sink_tiles == 0) return cudaSuccess;
+    window_rest_table<<<1, 1024, 0, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -312,13 +288,7 @@ int gdn_window_attention_forward(const gdn_window_attention_desc *d, const void 
     p.out = out;
     const cudaStream_t s = (cudaStream_t)stream;
     if ((int64_t)d->B * d->Tq > 0 && d->Tk > 0 && window_tc_supports(p)) return layer_status(launch_window_forward_tc(p, s));
-    const cudaError_t e = launch_window_tables(p, 128, 128, s);
-    if (e != cudaSuccess) return GDN_ERR_CUDA;
-    switch (d->dtype) {
-    case GDN_F32: return layer_status(forward_any<float>(p, s));
-    case GDN_BF16: return layer_status(forward_any<__nv_bfloat16>(p, s));
-    default: return layer_status(forward_any<__half>(p, s));
-    }
+    return layer_status(launch_window_forward_simt(p, s));
 }
 
 int gdn_window_attention_backward(const gdn_window_attention_desc *d, const void *q, const void *k, const void *v, const void *out,
@@ -334,8 +304,6 @@ int gdn_window_attention_backward(const gdn_window_attention_desc *d, const void
     p.out_in = out, p.dout = grad_out;
     p.dq = dq, p.dk = dk, p.dv = dv;
     const cudaStream_t s = (cudaStream_t)stream;
-    const cudaError_t e = launch_window_tables(p, 128, 128, s);
-    if (e != cudaSuccess) return GDN_ERR_CUDA;
     switch (d->dtype) {
     case GDN_F32: return layer_status(backward_any<float>(p, s));
     case GDN_BF16: return layer_status(backward_any<__nv_bfloat16>(p, s));

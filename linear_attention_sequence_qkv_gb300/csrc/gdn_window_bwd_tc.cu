@@ -19,6 +19,7 @@
 
 #include <algorithm>
 
+#include "gdn_window_rest.cuh"
 #include "gdn_window_tc.cuh"
 
 namespace gdn {
@@ -43,31 +44,6 @@ struct BwdShared {
     int gave_up;
     float lse[kStages][64], delta[kStages][64];   // of the tile's queries (keys kernel): lse log2 e, delta scale
 };
-
-// The queries that the sinks of key tile t still have to take beyond the tile's own CTA: tiles of 64 from e0 on, `tiles` of
-// them for each head
-struct SinkRest {
-    int e0, tiles;
-};
-__device__ __forceinline__ SinkRest sink_rest(int Lq, int Lk, int t, int window) {
-    const int64_t past = (int64_t)Lk - Lq, j0 = (int64_t)t * 128, j1 = min(j0 + 127, (int64_t)Lk - 1);
-    const int64_t hi = min((int64_t)Lq - 1, j1 + window - 1 - past);
-    const int64_t lo = max((int64_t)0, j0 - past) >> 6;
-    SinkRest r;
-    r.e0 = (int)max(hi < 0 ? (int64_t)0 : (hi >> 6) + 1, lo);
-    r.tiles = j0 < Lk ? max(0, ((Lq + 63) >> 6) - r.e0) : 0;
-    return r;
-}
-__device__ __forceinline__ int rest_chunks(const WindowProblem &p, const WindowSpan &s, int t) {
-    const int64_t its = (int64_t)sink_rest(s.Lq, s.Lk, t, p.d.window).tiles * (p.d.Hq / p.d.Hk);
-    return (int)((its + p.rest_its - 1) / p.rest_its);
-}
-
-// The partial sums' place: [slot][Hk][rows][2][D] fp32, slots of the chunks first, then one per sequence and sink tile
-template <int D>
-__device__ __forceinline__ float *partial_at(const WindowProblem &p, int64_t slot, int hk) {
-    return p.partial + (slot * p.d.Hk + hk) * ((int64_t)p.sink_rows * 2 * D);
-}
 
 template <typename T, int D, bool KEYS>
 __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_constant__ WindowMaps a_maps, const __grid_constant__ WindowMaps b_maps,
@@ -406,63 +382,6 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
     if (warp == 0) tmem_dealloc(tbase, 512);
 }
 
-// The chunks of every sequence counted, for packed ones
-__global__ void __launch_bounds__(1024) window_rest_table(const __grid_constant__ WindowProblem p) {
-    __shared__ int32_t sums[32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const bool ok = *p.status == GDN_OK;
-    int before = 0;
-    for (int base = 0; base < p.d.N; base += blockDim.x) {
-        const int n = base + threadIdx.x;
-        int c = 0;
-        if (ok && n < p.d.N) {
-            const WindowSpan s = window_span(p, n);
-            for (int t = 0; t < p.sink_tiles; ++t) c += rest_chunks(p, s, t);
-        }
-        int x = c;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        if (lane == 31) sums[warp] = x;
-        __syncthreads();
-        int s = sums[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += y;
-        }
-        const int ahead = warp ? __shfl_sync(0xffffffffu, s, warp - 1) : 0, all = __shfl_sync(0xffffffffu, s, 31);
-        if (n < p.d.N) p.rest_off[n] = before + ahead + x - c;
-        before += all;
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) p.rest_off[p.d.N] = before;
-}
-
-// The sinks' gradients: the CTA's own part and the chunks', in order
-template <typename T, int D>
-__global__ void __launch_bounds__(256) window_sink_sums(const __grid_constant__ WindowProblem p) {
-    if (*p.status != GDN_OK) return;
-    const gdn_window_attention_desc &d = p.d;
-    const int hk = blockIdx.x % d.Hk, n = blockIdx.x / d.Hk / p.sink_tiles, t = blockIdx.x / d.Hk % p.sink_tiles;
-    const WindowSpan sp = window_span(p, n);
-    const int chunks = rest_chunks(p, sp, t);
-    if (chunks == 0) return;
-    int64_t slot = p.cu ? p.rest_off[n] : (int64_t)n * p.rest_per;
-    for (int x = 0; x < t; ++x) slot += rest_chunks(p, sp, x);
-    const int rows = min(min(128, d.sinks - t * 128), sp.Lk - t * 128);
-    const float *own = partial_at<D>(p, p.rest_slots + (int64_t)n * p.sink_tiles + t, hk);
-    for (int x = threadIdx.x; x < rows * 2 * D; x += 256) {
-        const int r = x / (2 * D), b = x / D & 1, c = x % D;
-        if (c >= d.d) continue;
-        float s = own[x];
-        for (int i = 0; i < chunks; ++i) s += partial_at<D>(p, slot + i, hk)[x];
-        ((T *)(b ? p.dv : p.dk))[((sp.k0 + t * 128 + r) * d.Hk + hk) * d.d + c] = from_f<T>(s);
-    }
-}
-
 template <typename T, int D>
 cudaError_t launch_backward(const WindowProblem &p, cudaStream_t s) {
     const gdn_window_attention_desc &d = p.d;
@@ -479,10 +398,6 @@ cudaError_t launch_backward(const WindowProblem &p, cudaStream_t s) {
             return cudaErrorInvalidValue;
     }
     cudaError_t e;
-    if (p.cu && p.sink_tiles > 0) {
-        window_rest_table<<<1, 1024, 0, s>>>(p);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
     const size_t smem = std::max<size_t>(BwdShape<D>::kBytes, 117 * 1024);   // one CTA per SM: each holds all of the tensor memory
     auto go = [&](auto kernel, int64_t tiles, int units, int64_t rest) {
         if ((tiles + rest) * units > 0x7fffffff) return cudaErrorInvalidValue;
@@ -495,48 +410,10 @@ cudaError_t launch_backward(const WindowProblem &p, cudaStream_t s) {
     const int64_t kt = p.cu ? cdiv64(d.Tk, 128) + d.N : (int64_t)d.B * cdiv64(d.Tk, 128);
     if ((e = go(window_backward_tc<T, D, true>, kt, d.Hk, p.rest_slots)) != cudaSuccess) return e;
     if ((e = go(window_backward_tc<T, D, false>, qt, d.Hq, 0)) != cudaSuccess) return e;
-    if (p.rest_slots > 0) {
-        const int64_t blocks = (int64_t)d.N * p.sink_tiles * d.Hk;
-        if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-        window_sink_sums<T, D><<<(unsigned)blocks, 256, 0, s>>>(p);
-        e = cudaGetLastError();
-    }
-    return e;
+    return launch_window_sink_sums<T, D>(p, s);
 }
 
 }  // namespace
-
-// Chunks of the sinks' rest: as long as a CTA of keys walks within the window, 32 to 512 tiles
-void window_rest_plan(WindowProblem &p) {
-    const gdn_window_attention_desc &d = p.d;
-    const int64_t group = d.Hq / d.Hk;
-    p.rest_its = (int)std::min<int64_t>(512, std::max<int64_t>(32, group * (((int64_t)d.window + 127) / 64 + 1)));
-    p.sink_tiles = (int)cdiv64(std::min(d.sinks, d.Tk), 128);
-    p.sink_rows = std::min(128, std::min(d.sinks, d.Tk));
-    p.rest_per = 0;
-    p.rest_slots = 0;
-    if (p.sink_tiles == 0 || d.window >= d.Tk) {   // every key's window reaches the end
-        p.sink_tiles = 0;
-        return;
-    }
-    if (d.N == d.B) {   // not packed, or one sequence: the same chunks for all rows
-        for (int t = 0; t < p.sink_tiles; ++t) {
-            const int64_t past = (int64_t)d.Tk - d.Tq, j0 = (int64_t)t * 128, j1 = std::min<int64_t>(j0 + 127, d.Tk - 1);
-            const int64_t hi = std::min<int64_t>(d.Tq - 1, j1 + d.window - 1 - past), lo = std::max<int64_t>(0, j0 - past) >> 6;
-            const int64_t tiles = std::max<int64_t>(0, cdiv64(d.Tq, 64) - std::max<int64_t>(hi < 0 ? 0 : (hi >> 6) + 1, lo));
-            p.rest_per += (int)cdiv64(tiles * group, p.rest_its);
-        }
-        p.rest_slots = (int64_t)d.B * p.rest_per;
-    } else {            // at most: every sequence's last chunk begun
-        p.rest_slots = p.sink_tiles * (cdiv64(group * (cdiv64(d.Tq, 64) + d.N), p.rest_its) + d.N);
-    }
-    if (p.rest_slots == 0) p.sink_tiles = 0;
-}
-
-size_t window_partial_bytes(const WindowProblem &p) {
-    if (p.rest_slots == 0) return 0;
-    return (size_t)(p.rest_slots + (int64_t)p.d.N * p.sink_tiles) * p.d.Hk * p.sink_rows * 2 * (p.d.d <= 64 ? 64 : 128) * 4;
-}
 
 cudaError_t launch_window_backward_tc(const WindowProblem &p, cudaStream_t s) {
     if (p.d.d <= 64) return p.d.dtype == GDN_BF16 ? launch_backward<__nv_bfloat16, 64>(p, s) : launch_backward<__half, 64>(p, s);

@@ -530,12 +530,17 @@ bool step_aligned(const CacheProblem &p) {
            ptr_aligned(p.out, 16);
 }
 
-// CTAs per sequence and head: until there are four per SM, or a CTA has 128 keys
+// CTAs per sequence and head: as many as make the rounds of two CTAs per SM cheapest, a CTA costing its keys and a start
+// that is worth about 100 KB of them
 int step_splits(const gdn_window_attention_desc &d, int64_t units) {
-    const int64_t most = std::min<int64_t>((int64_t)d.sinks + d.window, d.slots);
-    int splits = 1;
-    while (splits < kMostSplits && units * splits < 4 * kSms && most / (2 * splits) >= 128) splits *= 2;
-    return splits;
+    const int64_t bytes = ((int64_t)d.sinks + d.window) * d.d * 2 * (int64_t)act_size(d.dtype);
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int s = 1; s <= kMostSplits; s *= 2) {
+        const int64_t cost = cdiv64(units * s, 2 * kSms) * (100000 + bytes / s);
+        if (cost < least) least = cost, best = s;
+    }
+    return best;
 }
 
 template <typename K>

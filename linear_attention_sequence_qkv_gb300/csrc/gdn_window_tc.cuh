@@ -72,9 +72,7 @@ bool window_tc_supports(const WindowProblem &p);
 cudaError_t launch_window_forward_tc(const WindowProblem &p, cudaStream_t s);
 bool window_head_map(CUtensorMap *m, const gdn_window_attention_desc &d, const void *base, int heads, int tokens, int64_t sb, int64_t st,
                      int *rows, uint32_t box);
-// the backward: fills the chunks' part of p from the sizes, the bytes of its partial sums, the launches (after delta)
-void window_rest_plan(WindowProblem &p);
-size_t window_partial_bytes(const WindowProblem &p);
+// after delta, with the chunks planned
 cudaError_t launch_window_backward_tc(const WindowProblem &p, cudaStream_t s);
 
 }  // namespace gdn
