@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
     if (tid == 0) {
         mbar_init(&sh.a_full, 1);
         for (int i = 0; i < kStages; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1), mbar_init(&sh.fit[i], 2);
-        for (int b = 0; b < 2; ++b) mbar_init(&sh.s_full[b], 1), mbar_init(&sh.p_ready[b], 128);
+        for (int b = 0; b < 2; ++b) mbar_init(&sh.s_full[b], 1), mbar_init(&sh.p_ready[b], 4);
         mbar_init(&sh.acc_full, 1), mbar_init(&sh.drain, 1);
         sh.gave_up = 0;
         mbar_init_fence();
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
                 for (int i = 1; i < 4; ++i) warp_mma_f16_ta(leader, acc, from + 64 + 8 * i, s1 + (uint32_t)(2048 * i >> 4), idesc_a, 1);
             };
             auto next_scores = [&](int b) -> bool {
-                if (!warp_wait(wait, &sh.full[si], sph) || !warp_wait(wait, &sh.fit[si], sph)) return false;
+                if (!warp_wait2(wait, &sh.full[si], sph, &sh.fit[si], sph)) return false;
                 fence_after_sync();
                 scores(b);
                 if (++si == kStages) si = 0, sph ^= 1;
@@ -250,11 +250,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
                     const int64_t at = head_at(it) * ntok + sp.q0 + r0 + x;
                     l = p.lse[at] * 1.4426950408889634f, dl = p.delta[at] * d.scale;
                 }
-                if (it >= kStages && !wait(&sh.empty[i], (uint32_t)(it / kStages - 1) & 1)) break;
+                if (it >= kStages && !warp_wait(wait, &sh.empty[i], (uint32_t)(it / kStages - 1) & 1)) break;
                 sh.lse[i][x] = l, sh.delta[i][x] = dl;
             }
             if (left < 64) {
-                if (!wait(&sh.full[i], (uint32_t)(it / kStages) & 1)) break;
+                if (!warp_wait(wait, &sh.full[i], (uint32_t)(it / kStages) & 1)) break;
                 unsigned char *t = sm + L::kBs + i * 2 * L::kB + w * L::kB;   // a warp for each of the two
                 for (int b = 0; b < D / 64; ++b)
                     for (int x = left * 8 + lane; x < 64 * 8; x += 32) *(uint4 *)(t + b * L::kRowB + 16 * x) = make_uint4(0, 0, 0, 0);
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.fit[i]);
             // one arrival for each use of the stage: never ahead of the products by a whole round
-            if (!KEYS && it >= kStages - 1 && it + 1 < count && !wait(&sh.empty[(it + 1) % kStages], (uint32_t)((it + 1) / kStages - 1) & 1)) break;
+            if (!KEYS && it >= kStages - 1 && it + 1 < count && !warp_wait(wait, &sh.empty[(it + 1) % kStages], (uint32_t)((it + 1) / kStages - 1) & 1)) break;
         }
     } else {
         // ------------------------------------------------------------ P and dS
@@ -296,8 +296,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
 #pragma unroll
                 for (int w = 0; w < 2; ++w) see[w] = low_bits(h - 32 * w) & (~low_bits(l - 32 * w) | low_bits(k - 32 * w));
             }
-            if (!(ok = wait(&sh.s_full[b], (uint32_t)(it >> 1) & 1))) break;
-            if (KEYS && !(ok = wait(&sh.fit[i], (uint32_t)(it / kStages) & 1))) break;
+            if (!(ok = KEYS ? warp_wait2(wait, &sh.s_full[b], (uint32_t)(it >> 1) & 1, &sh.fit[i], (uint32_t)(it / kStages) & 1)
+                            : warp_wait(wait, &sh.s_full[b], (uint32_t)(it >> 1) & 1)))
+                break;
             fence_after_sync();
             const bool all = __all_sync(0xffffffffu, (see[0] & see[1]) == 0xffffffffu);
 #pragma unroll
@@ -327,11 +328,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
                 tmem_st16_nw(ts + 64 + 16 * w, f);
             }
             tmem_wait_st();
-            fence_before_sync();
-            mbar_arrive(&sh.p_ready[b]);
+            warp_arrive(&sh.p_ready[b]);
         }
         if (count > 0) {
-            if (ok) ok = wait(&sh.acc_full, 0);
+            if (ok) ok = warp_wait(wait, &sh.acc_full, 0);
             fence_after_sync();
         }
         // ---- the sums, through the rows that stay in shared memory (no product reads them any more): the second

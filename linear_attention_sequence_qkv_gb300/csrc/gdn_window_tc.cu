@@ -39,7 +39,7 @@ template <int D> struct FwdShape {
 };
 
 struct FwdShared {
-    uint64_t q_full, k_full[4], k_empty[4], v_full[4], v_empty[4], v_ok[4], s_full[2], p_ready[2], o_full[2], drain;
+    uint64_t q_full, k_full[4], k_empty[4], v_full[4], v_empty[4], v_ok[4], s_full[2], p_half[2], p_ready[2], o_full[2], drain;
     uint32_t tmem;
     int gave_up, any_bad;
     int cut_tile[kCutTiles];
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_forward_tc(const __grid_co
             mbar_init(&sh.k_full[i], 1), mbar_init(&sh.k_empty[i], 1);
             mbar_init(&sh.v_full[i], 1), mbar_init(&sh.v_empty[i], 1), mbar_init(&sh.v_ok[i], 2);
         }
-        for (int s = 0; s < 2; ++s) mbar_init(&sh.s_full[s], 1), mbar_init(&sh.p_ready[s], 128), mbar_init(&sh.o_full[s], 1);
+        for (int s = 0; s < 2; ++s) mbar_init(&sh.s_full[s], 1), mbar_init(&sh.p_half[s], 4), mbar_init(&sh.p_ready[s], 4), mbar_init(&sh.o_full[s], 1);
         mbar_init(&sh.drain, 1);
         sh.gave_up = sh.any_bad = 0;
         mbar_init_fence();
@@ -194,14 +194,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_forward_tc(const __grid_co
                 }
                 warp_mma_commit(leader, &sh.s_full[s]);
             };
-            auto product = [&](int s) {
-                const uint64_t v = dv + (uint32_t)(vi * (L::kTile >> 4));
-                const uint32_t to = tb + L::kO + D * s, from = tb + 128 * s;
-                warp_mma_f16_ta(leader, to, from, v, idesc_o, done[s] > 0);
+            auto product = [&](int s, int half) {   // with 64 keys' values
+                const uint64_t v = dv + (uint32_t)(vi * (L::kTile >> 4) + half * (64 * 128 >> 4));
+                const uint32_t to = tb + L::kO + D * s, from = tb + 128 * s + 32 * half;
+                warp_mma_f16_ta(leader, to, from, v, idesc_o, done[s] > 0 || half);
 #pragma unroll
-                for (int i = 1; i < 8; ++i) warp_mma_f16_ta(leader, to, from + 8 * i, v + (uint32_t)(2048 * i >> 4), idesc_o, 1);
-                ++done[s];
-                if (done[s] == total[s]) warp_mma_commit(leader, &sh.o_full[s]);
+                for (int i = 1; i < 4; ++i) warp_mma_f16_ta(leader, to, from + 8 * i, v + (uint32_t)(2048 * i >> 4), idesc_o, 1);
             };
             auto tile_of = [&](int u) { return u < first ? u : w0 + u - first; };
             bool ok = warp_wait(wait, &sh.q_full, 0) && warp_wait(wait, &sh.k_full[0], 0);
@@ -216,13 +214,21 @@ __global__ void __launch_bounds__(kThreads, 1) window_forward_tc(const __grid_co
             for (int u = 0; ok && u < n_tiles; ++u) {
                 const int t = tile_of(u), tn = tile_of(u + 1);
                 const bool more = u + 1 < n_tiles;
-                ok = warp_wait(wait, &sh.v_full[vi], vph) && warp_wait(wait, &sh.v_ok[vi], vph) && (!more || warp_wait(wait, &sh.k_full[ki], kph));
+                ok = more ? warp_wait3(wait, &sh.v_full[vi], vph, &sh.v_ok[vi], vph, &sh.k_full[ki], kph)
+                          : warp_wait2(wait, &sh.v_full[vi], vph, &sh.v_ok[vi], vph);
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     if (ok && mine[s].has(t)) {
-                        ok = warp_wait(wait, &sh.p_ready[s], (uint32_t)done[s] & 1);
+                        ok = warp_wait(wait, &sh.p_half[s], (uint32_t)done[s] & 1);
                         fence_after_sync();
-                        if (ok) product(s);
+                        if (ok) product(s, 0);
+                        ok = ok && warp_wait(wait, &sh.p_ready[s], (uint32_t)done[s] & 1);
+                        fence_after_sync();
+                        if (ok) {
+                            product(s, 1);
+                            ++done[s];
+                            if (done[s] == total[s]) warp_mma_commit(leader, &sh.o_full[s]);
+                        }
                     }
                     if (ok && more && mine[s].has(tn)) scores(s);
                 }
@@ -243,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_forward_tc(const __grid_co
         int cuts = 0;
         for (int u = 0; u < count; ++u) {
             const int t = tile_at(u), i = u % L::kV;
-            if (!wait(&sh.v_full[i], (uint32_t)(u / L::kV) & 1)) break;
+            if (!warp_wait(wait, &sh.v_full[i], (uint32_t)(u / L::kV) & 1)) break;
             bool cut = false;
             for (int s = 0; s < 2; ++s) cut |= st[s].tiles.has(t) && window_partial(t, st[s].p0, st[s].p1, d.window, d.sinks);
             if (cut) {
@@ -290,28 +296,32 @@ __global__ void __launch_bounds__(kThreads, 1) window_forward_tc(const __grid_co
         for (int u = 0; u < count; ++u) {
             const int t = tile_at(u);
             if (!me.tiles.has(t)) continue;
-            if (!(ok = wait(&sh.s_full[s], (uint32_t)seen & 1))) break;
+            if (!(ok = warp_wait(wait, &sh.s_full[s], (uint32_t)seen & 1))) break;
             fence_after_sync();
-            float x[128];
-            tmem_ld128(ts, x);
-            if (window_partial(t, me.p0, me.p1, d.window, d.sinks)) {
-                // of this tile's keys: up to hi, and from lo on or below sk
+            float x[2][64];
+            tmem_ld64(ts, x[0]);
+            uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+            const bool cut = window_partial(t, me.p0, me.p1, d.window, d.sinks);
+            if (cut) {
+                // of this tile's keys: up to hi, and from lo on or below sk. As bits: element by element compared, the compiler
+                // makes a branch of each (7 us a tile, measured)
                 const int64_t a = (int64_t)t * 128;
                 const int hi = (int)max((int64_t)-1, min((int64_t)127, pos - a)), lo = (int)max((int64_t)0, min((int64_t)128, (int64_t)pos - d.window + 1 - a));
                 const int sk = (int)max((int64_t)0, min((int64_t)128, d.sinks - a));
-                // as bits: element by element compared, the compiler makes a branch of each (7 us a tile, measured)
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const uint32_t see = low_bits(hi + 1 - 32 * b) & (~low_bits(lo - 32 * b) | low_bits(sk - 32 * b));
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) x[32 * b + i] = see & (1u << i) ? x[32 * b + i] : -INFINITY;
-                }
+                for (int b = 0; b < 4; ++b) see[b] = low_bits(hi + 1 - 32 * b) & (~low_bits(lo - 32 * b) | low_bits(sk - 32 * b));
             }
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 128; i += 4) {
-                mx[0] = fmaxf(mx[0], x[i]), mx[1] = fmaxf(mx[1], x[i + 1]);
-                mx[2] = fmaxf(mx[2], x[i + 2]), mx[3] = fmaxf(mx[3], x[i + 3]);
+            for (int h = 0; h < 2; ++h) {
+                if (h) tmem_ld64(ts + 64, x[1]);
+                if (cut)
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) x[h][i] = see[2 * h + (i >> 5)] & (1u << (i & 31)) ? x[h][i] : -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 64; i += 8)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], x[h][i + 2 * q], x[h][i + 2 * q + 1]);
             }
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             // a first maximum, or one that grew by more than 2^8: the sums so far move to it
@@ -338,20 +348,23 @@ __global__ void __launch_bounds__(kThreads, 1) window_forward_tc(const __grid_co
                 float w[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    float2 e = fma2(make_float2(x[32 * b + 2 * i], x[32 * b + 2 * i + 1]), cc, mc);
+                    float2 e = fma2(make_float2(x[b >> 1][32 * (b & 1) + 2 * i], x[b >> 1][32 * (b & 1) + 2 * i + 1]), cc, mc);
                     e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
                     sum[i & 1] = add2(sum[i & 1], e);
                     w[i] = __uint_as_float(pack2<T>(e.x, e.y));
                 }
                 tmem_st16_nw(ts + 16 * b, w);
+                if (b == 1) {   // the product with the first 64 keys' values may start
+                    tmem_wait_st();
+                    warp_arrive(&sh.p_half[s]);
+                }
             }
             l += sum[0].x + sum[0].y + sum[1].x + sum[1].y;
             tmem_wait_st();
-            fence_before_sync();
-            mbar_arrive(&sh.p_ready[s]);
+            warp_arrive(&sh.p_ready[s]);
             ++seen;
         }
-        if (ok && seen > 0 && (ok = wait(&sh.o_full[s], 0))) fence_after_sync();
+        if (ok && seen > 0 && (ok = warp_wait(wait, &sh.o_full[s], 0))) fence_after_sync();
         // the checking warps are through with all tiles
         asm volatile("bar.sync 1, 320;" ::: "memory");
         const bool valid = r < me.rows && ok;

@@ -59,9 +59,26 @@ struct WindowWait {
     }
 };
 
-// a wait of a whole warp, whose answer is the same for all lanes
+// A wait of a whole warp, every lane polling, whose answer is the same for all; for two or three barriers the tests' round trips
+// overlap (about 100 cycles each, which the warp that issues the products has to wait out)
 __device__ __forceinline__ bool warp_wait(const WindowWait &wait, uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait(bar, parity));
+}
+__device__ __forceinline__ bool warp_wait2(const WindowWait &wait, uint64_t *b1, uint32_t p1, uint64_t *b2, uint32_t p2) {
+    bool ok = wait.immediate ? tc::mbar_test2<true>(b1, p1, b2, p2) : tc::mbar_test2<false>(b1, p1, b2, p2);
+    if (!ok) ok = wait(b1, p1) && wait(b2, p2);
+    return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ bool warp_wait3(const WindowWait &wait, uint64_t *b1, uint32_t p1, uint64_t *b2, uint32_t p2, uint64_t *b3, uint32_t p3) {
+    bool ok = wait.immediate ? tc::mbar_test3<true>(b1, p1, b2, p2, b3, p3) : tc::mbar_test3<false>(b1, p1, b2, p2, b3, p3);
+    if (!ok) ok = wait(b1, p1) && wait(b2, p2) && wait(b3, p3);
+    return __all_sync(0xffffffffu, ok);
+}
+// a warp's arrival, after what its lanes wrote to tensor or shared memory
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+    tc::fence_before_sync();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
 }
 // the first lane's value, known to be the warp's
 __device__ __forceinline__ int of_warp(int v) { return __shfl_sync(0xffffffffu, v, 0); }
