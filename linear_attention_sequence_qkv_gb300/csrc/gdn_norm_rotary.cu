@@ -197,25 +197,46 @@ template <int V, int K, bool HALF> struct Place {
         }
     }
 };
-// cosines and sines of a lane's pairs at a position, with the attention factor: 1 and 0 where nothing turns; the sine's
-// sign as y = x cos + other sin wants it (half layout)
+// Pairs of neighbouring channels, in one instruction where the SM has one for two. A turn is y = x A + o B with o the other
+// half's channels (half layout) or the pair swapped, and A, B of the lane's pairs at a position, the attention factor among
+// them: (cos, cos) and (-+sin, -+sin), or (cos, cos) and (-sin, sin); ones and zeros where nothing turns.
 template <typename T, int V, int K, bool HALF>
-__device__ __forceinline__ void turns_of(const NormRotaryProblem &p, const Place<V, K, HALF> &at, int64_t pos, float (&co)[K][V], float (&si)[K][V]) {
+__device__ __forceinline__ void turns_of(const NormRotaryProblem &p, const Place<V, K, HALF> &at, int64_t pos, float2 (&A)[K][V / 2], float2 (&B)[K][V / 2]) {
     const gdn_rotary_desc &d = p.n.rotary;
+    auto turn = [&](int pair) {
+        const float2 cs = cos_sin<sizeof(T) == 2>(pos, p.turns[pair]);
+        return make_float2(cs.x * d.scale, cs.y * d.scale);
+    };
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            if (!HALF && (e & 1)) continue;   // one entry for a pair
-            co[k][e] = 1.0f, si[k][e] = 0.0f;
-            if (at.turned[k]) {
-                const int pair = HALF ? at.c[k] + e - (at.upper[k] ? d.rot / 2 : 0) : (at.c[k] + e) / 2;
-                const float2 cs = cos_sin<sizeof(T) == 2>(pos, p.turns[pair]);
-                co[k][e] = cs.x * d.scale;
-                si[k][e] = HALF && !at.upper[k] ? -cs.y * d.scale : cs.y * d.scale;
+        for (int e = 0; e < V / 2; ++e) {
+            A[k][e] = splat2(1.0f), B[k][e] = splat2(0.0f);
+            if (!at.turned[k]) continue;
+            if (HALF) {
+                const int pair = at.c[k] + 2 * e - (at.upper[k] ? d.rot / 2 : 0);
+                const float2 a = turn(pair), b = turn(pair + 1);
+                A[k][e] = make_float2(a.x, b.x);
+                B[k][e] = at.upper[k] ? make_float2(a.y, b.y) : make_float2(-a.y, -b.y);
+            } else {
+                const float2 a = turn(at.c[k] / 2 + e);
+                A[k][e] = splat2(a.x);
+                B[k][e] = make_float2(-a.y, a.y);
             }
         }
 }
+template <typename T, int V> __device__ __forceinline__ float2 pair_of(const Vec<T, V> &v, int e) {
+    if constexpr (sizeof(T) == 4) return make_float2(v.e[2 * e], v.e[2 * e + 1]);
+    else return Pairs<T>::word(v.w[e]);
+}
+template <typename T, int V> __device__ __forceinline__ void set_pair(Vec<T, V> &v, int e, float2 x) {
+    if constexpr (sizeof(T) == 4) v.e[2 * e] = x.x, v.e[2 * e + 1] = x.y;
+    else v.w[e] = Pairs<T>::pack1(x);
+}
+__device__ __forceinline__ float2 swapped(float2 x) { return make_float2(x.y, x.x); }
+// two channels' weights
+__device__ __forceinline__ float2 weights_at(const void *w, int dtype, int c) { return make_float2(weight_at(w, dtype, c), weight_at(w, dtype, c + 1)); }
+
 // the other half's vectors
 template <typename T, int V, int K, bool HALF>
 __device__ __forceinline__ void partners(const Place<V, K, HALF> &at, const Vec<T, V> (&x)[K], Vec<T, V> (&o)[K], int team) {
@@ -256,7 +277,7 @@ __device__ __forceinline__ Item item_at(const gdn_rotary_desc &d, int64_t i, int
 }
 
 template <typename T, int V, int K, int TEAM, bool HALF>
-__global__ void __launch_bounds__(kThreads) norm_rotary_vectors(const __grid_constant__ NormRotaryProblem p, int parts, int per) {
+__global__ void __launch_bounds__(kThreads, K == 1 ? 3 : 1) norm_rotary_vectors(const __grid_constant__ NormRotaryProblem p, int parts, int per) {
     const gdn_rotary_desc &d = p.n.rotary;
     const bool ok = p.cu == nullptr || seqlens_ok(p.cu, d.N, d.T);
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = ok ? GDN_OK : GDN_ERR_DEVICE_SEQLENS;
@@ -266,26 +287,29 @@ __global__ void __launch_bounds__(kThreads) norm_rotary_vectors(const __grid_con
     const Item it = item_at(d, (int64_t)blockIdx.x * (kThreads / TEAM) + threadIdx.x / TEAM, parts, part);
     const Place<V, K, HALF> at(d, lane, TEAM);
     const int h0 = part * per, h1 = it.ok ? min(h0 + per, d.Hq + d.Hk) : h0;   // the lanes of a warp stay together: empty runs loop too
-    float co[K][V], si[K][V];
-    turns_of<T, V, K, HALF>(p, at, it.ok ? rotary_position(d, p.pos, p.cu, p.off, it.row, it.t) : 0, co, si);
+    constexpr int NP = V / 2;
+    const int64_t pos = it.ok ? rotary_position(d, p.pos, p.cu, p.off, it.row, it.t) : 0;
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
         const void *w = which ? p.kw : p.qw;
-        const int a = max(h0, which ? d.Hq : 0), b = min(h1, which ? d.Hq + d.Hk : d.Hq);
+        const int a = max(h0, which ? d.Hq : 0), b = min(h1, which ? d.Hq + d.Hk : d.Hq), first = which ? d.Hq : 0;
         const T *src = (const T *)(which ? p.k : p.q) + it.row * (which ? d.k_stride_b : d.q_stride_b) + it.t * (which ? d.k_stride_t : d.q_stride_t);
         T *dst = (T *)(which ? p.ko : p.qo) + it.row * (which ? d.k_out_stride_b : d.q_out_stride_b) + it.t * (which ? d.k_out_stride_t : d.q_out_stride_t);
-        const int first = which ? d.Hq : 0;
-        const int runs = max(0, b - a);
-        if (!__any_sync(0xffffffffu, runs > 0)) continue;
-        float wo[K][V], wp[K][V];
+        const int runs = max(0, b - a), most = __reduce_max_sync(0xffffffffu, runs);
+        if (most == 0) continue;
+        // the weights go into the turn: y = rstd (x A w + o B w'). It is computed again for k: kept beside the weighted one it
+        // takes registers of the loads on their way (32768 tokens of 48 heads of 128: 155 us, 141 so).
+        float2 A[K][NP], B[K][NP], Aw[K][NP], Bw[K][NP];
+        turns_of<T, V, K, HALF>(p, at, pos, A, B);
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                wo[k][e] = at.c[k] >= 0 ? weight_at(w, p.n.weight_dtype, at.c[k] + e) : 0.0f;
-                if (HALF) wp[k][e] = at.c[k] >= 0 ? weight_at(w, p.n.weight_dtype, at.other[k] * V + e) : 0.0f;
+            for (int e = 0; e < NP; ++e) {
+                const float2 own = at.c[k] >= 0 ? weights_at(w, p.n.weight_dtype, at.c[k] + 2 * e) : splat2(0.0f);
+                Aw[k][e] = mul2(A[k][e], own);
+                if (HALF) Bw[k][e] = at.turned[k] ? mul2(B[k][e], weights_at(w, p.n.weight_dtype, at.other[k] * V + 2 * e)) : splat2(0.0f);
+                else Bw[k][e] = mul2(B[k][e], swapped(own));
             }
-        const int most = __reduce_max_sync(0xffffffffu, runs);
         for (int r0 = 0; r0 < most; r0 += kFlight) {
             Vec<T, V> x[kFlight][K];
 #pragma unroll
@@ -299,29 +323,25 @@ __global__ void __launch_bounds__(kThreads) norm_rotary_vectors(const __grid_con
 #pragma unroll
             for (int j = 0; j < kFlight; ++j) {
                 if (r0 + j >= most) break;
-                float ss = 0.0f;
+                float2 xs[K][NP], s2 = splat2(0.0f);
 #pragma unroll
                 for (int k = 0; k < K; ++k)
 #pragma unroll
-                    for (int e = 0; e < V; ++e) ss = fmaf(to_f<T>(x[j][k].e[e]), to_f<T>(x[j][k].e[e]), ss);
-                const float rstd = rsqrtf(team_sum<TEAM>(ss) / d.d + p.n.eps);
+                    for (int e = 0; e < NP; ++e) {
+                        xs[k][e] = pair_of<T, V>(x[j][k], e);
+                        s2 = fma2(xs[k][e], xs[k][e], s2);
+                    }
+                const float2 rstd = splat2(rsqrtf(team_sum<TEAM>(s2.x + s2.y) / d.d + p.n.eps));
                 Vec<T, V> o[K], y[K];
                 if (HALF) partners<T, V, K, HALF>(at, x[j], o, TEAM);
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
-                    if (HALF) {
 #pragma unroll
-                        for (int e = 0; e < V; ++e) {
-                            const float z = to_f<T>(x[j][k].e[e]) * rstd * wo[k][e], zo = to_f<T>(o[k].e[e]) * rstd * wp[k][e];
-                            y[k].e[e] = from_f<T>(at.turned[k] ? z * co[k][e] + zo * si[k][e] : z);
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < V; e += 2) {
-                            const float z1 = to_f<T>(x[j][k].e[e]) * rstd * wo[k][e], z2 = to_f<T>(x[j][k].e[e + 1]) * rstd * wo[k][e + 1];
-                            y[k].e[e] = from_f<T>(z1 * co[k][e] - z2 * si[k][e]);
-                            y[k].e[e + 1] = from_f<T>(z2 * co[k][e] + z1 * si[k][e]);
-                        }
+                    for (int e = 0; e < NP; ++e) {
+                        float2 z = mul2(xs[k][e], Aw[k][e]);
+                        // (a partner that is not finite must not reach what does not turn)
+                        if (!HALF || at.turned[k]) z = fma2(HALF ? pair_of<T, V>(o[k], e) : swapped(xs[k][e]), Bw[k][e], z);
+                        set_pair<T, V>(y[k], e, mul2(z, rstd));
                     }
                     if (r0 + j < runs && at.c[k] >= 0) *(decltype(y[k].raw) *)(dst + (int64_t)(a + r0 + j - first) * d.d + at.c[k]) = y[k].raw;
                 }
@@ -331,7 +351,7 @@ __global__ void __launch_bounds__(kThreads) norm_rotary_vectors(const __grid_con
 }
 
 template <typename T, int V, int K, int TEAM, bool HALF>
-__global__ void __launch_bounds__(kThreads) norm_rotary_vectors_backward(const __grid_constant__ NormRotaryProblem p, int parts, int per) {
+__global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) norm_rotary_vectors_backward(const __grid_constant__ NormRotaryProblem p, int parts, int per) {
     extern __shared__ float sm[];   // [teams][2][d]
     const gdn_rotary_desc &d = p.n.rotary;
     const bool ok = p.cu == nullptr || seqlens_ok(p.cu, d.N, d.T);
@@ -340,20 +360,21 @@ __global__ void __launch_bounds__(kThreads) norm_rotary_vectors_backward(const _
     constexpr int kTeams = kThreads / TEAM, kF = kFlight / 2;   // two tensors' loads per head
     const int lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
     const Place<V, K, HALF> at(d, lane, TEAM);
-    float acc[2][K][V];
+    constexpr int NP = V / 2;
+    float2 acc[2][K][NP];
 #pragma unroll
     for (int w = 0; w < 2; ++w)
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int e = 0; e < V; ++e) acc[w][k][e] = 0.0f;
+            for (int e = 0; e < NP; ++e) acc[w][k][e] = splat2(0.0f);
     const int64_t items = (int64_t)d.B * d.T * parts;
     for (int64_t i0 = (int64_t)blockIdx.x * kTeams; i0 < items; i0 += (int64_t)gridDim.x * kTeams) {
         int part;
         const Item it = item_at(d, i0 + team, parts, part);
         const int h0 = part * per, h1 = it.ok ? min(h0 + per, d.Hq + d.Hk) : h0;
-        float co[K][V], si[K][V];
-        turns_of<T, V, K, HALF>(p, at, it.ok ? rotary_position(d, p.pos, p.cu, p.off, it.row, it.t) : 0, co, si);
+        float2 A[K][NP], B[K][NP];
+        turns_of<T, V, K, HALF>(p, at, it.ok ? rotary_position(d, p.pos, p.cu, p.off, it.row, it.t) : 0, A, B);
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             const void *w = which ? p.kw : p.qw;
@@ -364,11 +385,11 @@ __global__ void __launch_bounds__(kThreads) norm_rotary_vectors_backward(const _
             T *dst = (T *)(which ? p.dk : p.dq) + it.tok * (which ? d.Hk : d.Hq) * d.d;
             const int runs = max(0, b - a), most = __reduce_max_sync(0xffffffffu, runs);
             if (most == 0) continue;
-            float wo[K][V];
+            float2 wo[K][NP];
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
-                for (int e = 0; e < V; ++e) wo[k][e] = at.c[k] >= 0 ? weight_at(w, p.n.weight_dtype, at.c[k] + e) : 0.0f;
+                for (int e = 0; e < NP; ++e) wo[k][e] = at.c[k] >= 0 ? weights_at(w, p.n.weight_dtype, at.c[k] + 2 * e) : splat2(0.0f);
             for (int r0 = 0; r0 < most; r0 += kF) {
                 Vec<T, V> x[kF][K], g[kF][K];
 #pragma unroll
@@ -387,32 +408,30 @@ __global__ void __launch_bounds__(kThreads) norm_rotary_vectors_backward(const _
                     if (r0 + j >= most) break;
                     Vec<T, V> o[K];
                     if (HALF) partners<T, V, K, HALF>(at, g[j], o, TEAM);
-                    float ss = 0.0f, st = 0.0f, dz[K][V];
+                    float2 ss = splat2(0.0f), st = splat2(0.0f), dz[K][NP], xs[K][NP];
 #pragma unroll
                     for (int k = 0; k < K; ++k)
 #pragma unroll
-                        for (int e = 0; e < V; ++e) {
-                            const float xv = to_f<T>(x[j][k].e[e]), gv = to_f<T>(g[j][k].e[e]);
-                            if (HALF) {   // the turn back: the sine the other way round
-                                dz[k][e] = at.turned[k] ? gv * co[k][e] - to_f<T>(o[k].e[e]) * si[k][e] : gv;
-                            } else if (e & 1) {
-                                dz[k][e] = gv * co[k][e & ~1] - to_f<T>(g[j][k].e[e & ~1]) * si[k][e & ~1];
-                            } else {
-                                dz[k][e] = gv * co[k][e] + to_f<T>(g[j][k].e[e | 1]) * si[k][e];
-                            }
-                            ss = fmaf(xv, xv, ss);
-                            st = fmaf(dz[k][e] * wo[k][e], xv, st);
+                        for (int e = 0; e < NP; ++e) {
+                            const float2 gv = pair_of<T, V>(g[j][k], e);
+                            xs[k][e] = pair_of<T, V>(x[j][k], e);
+                            dz[k][e] = mul2(gv, A[k][e]);
+                            // the turn back: B the other way round
+                            if (!HALF || at.turned[k])
+                                dz[k][e] = fma2(HALF ? pair_of<T, V>(o[k], e) : swapped(gv), make_float2(-B[k][e].x, -B[k][e].y), dz[k][e]);
+                            ss = fma2(xs[k][e], xs[k][e], ss);
+                            st = fma2(mul2(dz[k][e], wo[k][e]), xs[k][e], st);
                         }
-                    ss = team_sum<TEAM>(ss), st = team_sum<TEAM>(st);
-                    const float rstd = rsqrtf(ss / d.d + p.n.eps), mean = rstd * st / d.d;   // of t xh
+                    const float rstd = rsqrtf(team_sum<TEAM>(ss.x + ss.y) / d.d + p.n.eps);
+                    const float2 r2 = splat2(rstd), mean = splat2(-rstd * team_sum<TEAM>(st.x + st.y) / d.d);   // of t xh
 #pragma unroll
                     for (int k = 0; k < K; ++k) {
                         Vec<T, V> y;
 #pragma unroll
-                        for (int e = 0; e < V; ++e) {
-                            const float xh = to_f<T>(x[j][k].e[e]) * rstd;
-                            acc[which][k][e] = fmaf(dz[k][e], xh, acc[which][k][e]);
-                            y.e[e] = from_f<T>(rstd * (dz[k][e] * wo[k][e] - xh * mean));
+                        for (int e = 0; e < NP; ++e) {
+                            const float2 xh = mul2(xs[k][e], r2);
+                            acc[which][k][e] = fma2(dz[k][e], xh, acc[which][k][e]);
+                            set_pair<T, V>(y, e, mul2(r2, fma2(xh, mean, mul2(dz[k][e], wo[k][e]))));
                         }
                         if (r0 + j < runs && at.c[k] >= 0) *(decltype(y.raw) *)(dst + (int64_t)(a + r0 + j - first) * d.d + at.c[k]) = y.raw;
                     }
@@ -425,8 +444,8 @@ __global__ void __launch_bounds__(kThreads) norm_rotary_vectors_backward(const _
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                if (at.c[k] >= 0) sm[(team * 2 + w) * d.d + at.c[k] + e] = acc[w][k][e];
+            for (int e = 0; e < NP; ++e)
+                if (at.c[k] >= 0) *(float2 *)&sm[(team * 2 + w) * d.d + at.c[k] + 2 * e] = acc[w][k][e];
     __syncthreads();
     for (int c = threadIdx.x; c < 2 * d.d; c += kThreads) {
         float s = 0.0f;
@@ -465,9 +484,9 @@ bool fits(const NormRotaryProblem &p, int v) {
     return true;
 }
 
-// Parts of a token's heads: until there are 16 warps per SM
+// Parts of a token's heads: until there are 32 warps per SM
 int parts_of(const gdn_rotary_desc &d, int team) {
-    const int64_t ntok = std::max<int64_t>((int64_t)d.B * d.T, 1), teams = (int64_t)kSms * 16 * (32 / team);
+    const int64_t ntok = std::max<int64_t>((int64_t)d.B * d.T, 1), teams = (int64_t)kSms * 32 * (32 / team);
     return (int)std::min<int64_t>(d.Hq + d.Hk, cdiv64(teams, ntok));
 }
 
