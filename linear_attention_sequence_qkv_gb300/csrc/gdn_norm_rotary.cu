@@ -153,17 +153,22 @@ __global__ void __launch_bounds__(32 * kWarps) norm_rotary_rows_backward(const _
     }
 }
 
-// The sum of the CTAs' partial weight gradients: a warp per channel.
-__global__ void __launch_bounds__(256) norm_rotary_weights(const __grid_constant__ NormRotaryProblem p) {
+// The sum of the CTAs' partial weight gradients, in order: a warp reads 32 channels of every 32nd CTA's row.
+__global__ void __launch_bounds__(1024) norm_rotary_weights(const __grid_constant__ NormRotaryProblem p) {
+    __shared__ float part[32][33];
     if (*p.status != GDN_OK) return;
-    const int d = p.n.rotary.d, lane = threadIdx.x & 31;
-    const int c = blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (c >= 2 * d) return;
+    const int d = p.n.rotary.d, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float s = 0.0f;
-    for (int i = lane; i < p.ctas; i += 32) s += p.part[(int64_t)i * 2 * d + c];
-    s = warp_sum(s);
-    float *to = c < d ? p.dqw : p.dkw;
-    if (lane == 0 && to) to[c < d ? c : c - d] = s;
+    if (c < 2 * d)
+#pragma unroll 8
+        for (int i = warp; i < p.ctas; i += 32) s += p.part[(int64_t)i * 2 * d + c];
+    part[warp][lane] = s;
+    __syncthreads();
+    // a warp adds up one channel
+    s = warp_sum(part[lane][warp]);
+    const int w = blockIdx.x * 32 + warp;
+    float *to = w < d ? p.dqw : p.dkw;
+    if (lane == 0 && w < 2 * d && to) to[w < d ? w : w - d] = s;
 }
 
 // ------------------------------------------------------------- vectors in registers
@@ -536,7 +541,7 @@ cudaError_t launch(NormRotaryProblem &p, bool backward, cudaStream_t s) {
         e = cudaGetLastError();
     }
     if (e != cudaSuccess || !backward || (!p.dqw && !p.dkw)) return e;
-    norm_rotary_weights<<<(unsigned)cdiv64(2 * d.d, 8), 256, 0, s>>>(p);
+    norm_rotary_weights<<<(unsigned)cdiv64(2 * d.d, 32), 1024, 0, s>>>(p);
     return cudaGetLastError();
 }
 

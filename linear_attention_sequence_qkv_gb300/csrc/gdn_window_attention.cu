@@ -90,20 +90,58 @@ __global__ void __launch_bounds__(1024) window_rest_table(const __grid_constant_
     if (threadIdx.x == 0) p.rest_off[p.d.N] = before;
 }
 
-// delta = sum of grad_out * out per query and head
-template <typename T>
-__global__ void __launch_bounds__(256) window_delta(const __grid_constant__ WindowProblem p) {
+// delta = sum of grad_out * out per query and head, 32 rows (of a token's heads, tokens after one another) per warp step.
+// VEC: rows of whole 16 bytes, shared by the power of two of lanes that they fill; a lane keeps two rows' loads on their way.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) window_delta(const __grid_constant__ WindowProblem p, int team) {
     if (*p.status != GDN_OK) return;
     const gdn_window_attention_desc &d = p.d;
     const int lane = threadIdx.x & 31;
     const int64_t ntok = (int64_t)d.B * d.Tq, total = ntok * d.Hq;
-    for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += (int64_t)gridDim.x * 8) {
-        const T *o = (const T *)p.out_in + i * d.d, *g = (const T *)p.dout + i * d.d;
-        float s = 0.0f;
-        for (int c = lane; c < d.d; c += 32) s = fmaf(to_f<T>(o[c]), to_f<T>(g[c]), s);
-        s = warp_sum(s);
+    const T *o = (const T *)p.out_in, *g = (const T *)p.dout;
+    auto put = [&](int64_t i, float s) {
         const int64_t tok = i / d.Hq;
-        if (lane == 0) p.delta[(i - tok * d.Hq) * ntok + tok] = s;
+        p.delta[(i - tok * d.Hq) * ntok + tok] = s;
+    };
+    if (!VEC) {
+        for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += (int64_t)gridDim.x * 8) {
+            float s = 0.0f;
+            for (int c = lane; c < d.d; c += 32) s = fmaf(to_f<T>(o[i * d.d + c]), to_f<T>(g[i * d.d + c]), s);
+            s = warp_sum(s);
+            if (lane == 0) put(i, s);
+        }
+        return;
+    }
+    constexpr int N = Vec16<T>::N, kR = 4;
+    const int sub = lane % team, per = 32 / team, c = sub * N;
+    const int64_t step = (int64_t)gridDim.x * 8 * per;
+    for (int64_t i0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * per + lane / team; i0 - lane / team < total; i0 += kR * step) {
+        uint4 a[kR][2], b[kR][2];
+#pragma unroll
+        for (int j = 0; j < kR; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {   // rows of more than 32 lanes' 16 bytes: two of them per lane
+                const int64_t i = i0 + j * step;
+                const int x = c + h * 32 * N;
+                const bool in = i < total && x < d.d && (h == 0 || team == 32);
+                a[j][h] = in ? *(const uint4 *)(o + i * d.d + x) : make_uint4(0, 0, 0, 0);
+                b[j][h] = in ? *(const uint4 *)(g + i * d.d + x) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+        for (int j = 0; j < kR; ++j) {
+            float2 s2 = splat2(0.0f);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float2 x[N / 2], y[N / 2];
+                Pairs<T>::unpack(a[j][h], x);
+                Pairs<T>::unpack(b[j][h], y);
+#pragma unroll
+                for (int e = 0; e < N / 2; ++e) s2 = fma2(x[e], y[e], s2);
+            }
+            float s = s2.x + s2.y;
+            for (int x = team / 2; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+            if (sub == 0 && i0 + j * step < total) put(i0 + j * step, s);
+        }
     }
 }
 
@@ -115,7 +153,14 @@ cudaError_t backward_any(WindowProblem &p, cudaStream_t s) {
     cudaError_t e = launch_window_tables(p, tc ? 128 : 64, tc ? 128 : 64, s);
     if (e != cudaSuccess) return e;
     const int64_t rows = (int64_t)p.d.B * p.d.Tq * p.d.Hq;
-    if (rows) window_delta<T><<<row_blocks(rows, 8), 256, 0, s>>>(p);
+    constexpr int N = 16 / (int)sizeof(T);
+    if (rows && p.d.d % N == 0 && ptr_aligned(p.out_in, 16) && ptr_aligned(p.dout, 16)) {
+        int team = 1;
+        while (team < 32 && team * N < p.d.d) team *= 2;
+        window_delta<T, true><<<(unsigned)std::min<int64_t>(cdiv64(rows, 8 * (32 / team)), 16 * kSms), 256, 0, s>>>(p, team);
+    } else if (rows) {
+        window_delta<T, false><<<row_blocks(rows, 8), 256, 0, s>>>(p, 32);
+    }
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     window_rest_plan(p);
     if ((e = launch_window_rest_table(p, s)) != cudaSuccess) return e;

@@ -255,16 +255,15 @@ __global__ void __launch_bounds__(kThreads) window_forward_simt(const __grid_con
     }
 }
 
+// The part of a backward CTA that has a tile of queries
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) window_dq_simt(const __grid_constant__ WindowProblem p) {
+__device__ __forceinline__ void dq_tile(const WindowProblem &p, float *sm, int64_t block) {
     constexpr int kPitch = D + 4, kW = kWalk + 4;
-    extern __shared__ float sm[];
     float *Q = sm, *G = Q + kRows * kPitch, *K = G + kRows * kPitch, *V = K + kWalk * kPitch, *S = V + kWalk * kPitch;
-    if (*p.status != GDN_OK) return;
     const gdn_window_attention_desc &d = p.d;
-    const int h = (int)(blockIdx.x % d.Hq), hk = h / (d.Hq / d.Hk);
+    const int h = (int)(block % d.Hq), hk = h / (d.Hq / d.Hk);
     int n, tile, tiles;
-    if (!tile_of(p, p.q_tiles, blockIdx.x / d.Hq, d.Tq, n, tile, tiles)) return;
+    if (!tile_of(p, p.q_tiles, block / d.Hq, d.Tq, n, tile, tiles)) return;
     const int i0 = (tiles - 1 - tile) * kRows;
     const WindowSpan sp = window_span(p, n);
     const int past = sp.Lk - sp.Lq, rows = min(kRows, sp.Lq - i0);
@@ -313,16 +312,27 @@ __global__ void __launch_bounds__(kThreads) window_dq_simt(const __grid_constant
     store_rows<T, D>((T *)p.dq + (tok0 * d.Hq + h) * d.d, gst, d.d, ty, tx, 0, rows, o, one);
 }
 
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 of_rank(const float *own, uint32_t rank) {
+    uint32_t a;
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(own)), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
+}
+
+// The part that has a tile of keys, or a chunk of the sinks' rest: the `splits` CTAs of a cluster take every splits-th step,
+// and their sums are added up in the ranks' order. All of a cluster have the same block.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) window_dkv_simt(const __grid_constant__ WindowProblem p, int64_t rest_blocks) {
+__device__ __forceinline__ void dkv_tile(const WindowProblem &p, float *sm, int64_t block_of_all, int64_t rest_blocks, int rank, int splits) {
     constexpr int kPitch = D + 4, kW = kWalk + 4;
-    extern __shared__ float sm[];
     float *K = sm, *V = K + kRows * kPitch, *Q = V + kRows * kPitch, *G = Q + kWalk * kPitch, *P = G + kWalk * kPitch, *S = P + kRows * kW;
     __shared__ float lse[kWalk], delta[kWalk];
-    if (*p.status != GDN_OK) return;
     const gdn_window_attention_desc &d = p.d;
-    const bool rest = blockIdx.x < rest_blocks;
-    const int64_t block = rest ? blockIdx.x : blockIdx.x - rest_blocks;
+    const bool rest = block_of_all < rest_blocks;
+    const int64_t block = rest ? block_of_all : block_of_all - rest_blocks;
     const int hk = (int)(block % d.Hk), group = d.Hq / d.Hk;
     int n, row0, tile = 0, chunk = 0;
     int64_t slot = block / d.Hk;
@@ -378,7 +388,7 @@ __global__ void __launch_bounds__(kThreads) window_dkv_simt(const __grid_constan
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int e = 0; e < D / 64; ++e) dk[i][e] = dv[i][e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int64_t it = 2 * it0; it < 2 * it1; ++it) {   // halves of 32 queries
+    for (int64_t it = 2 * it0 + rank; it < 2 * it1; it += splits) {   // halves of 32 queries
         const int h = hk * group + (int)((it >> 1) / per_head);
         const int i0 = (int)(first + (it >> 1) % per_head) * 64 + (it & 1) * kWalk, left = min(kWalk, sp.Lq - i0);
         if (left <= 0) continue;
@@ -410,6 +420,33 @@ __global__ void __launch_bounds__(kThreads) window_dkv_simt(const __grid_constan
         tile_add<D>(P, kW, G, kWalk, ty, tx, dv);
         tile_add<D>(S, kW, Q, kWalk, ty, tx, dk);
     }
+    if (splits > 1) {   // K and V make room for the sums; a rank has the rows r with r / 4 % splits == rank in the end
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < D / 64; ++e) {
+                *(float4 *)(K + (4 * ty + i) * kPitch + 4 * tx + 64 * e) = dk[i][e];
+                *(float4 *)(V + (4 * ty + i) * kPitch + 4 * tx + 64 * e) = dv[i][e];
+            }
+        cluster_sync();
+        if (ty % splits == rank) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < D / 64; ++e) {
+                    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
+                    for (int x = 0; x < splits; ++x) {
+                        const float4 u = of_rank(K + (4 * ty + i) * kPitch + 4 * tx + 64 * e, x), w = of_rank(V + (4 * ty + i) * kPitch + 4 * tx + 64 * e, x);
+                        a.x += u.x, a.y += u.y, a.z += u.z, a.w += u.w;
+                        b.x += w.x, b.y += w.y, b.z += w.z, b.w += w.w;
+                    }
+                    dk[i][e] = a, dv[i][e] = b;
+                }
+        }
+        cluster_sync();   // no CTA leaves while another reads its sums
+        if (ty % splits != rank) return;
+    }
     // rows of sinks whose sum has other parts stay in fp32
     const int apart = rest ? kRows : row0 < d.sinks && rest_chunks(p, sp, tile) > 0 ? min(kRows, d.sinks - row0) : 0;
     const int64_t part = rest ? slot : p.rest_slots + (int64_t)n * p.sink_tiles + tile;
@@ -430,28 +467,54 @@ __global__ void __launch_bounds__(kThreads) window_dkv_simt(const __grid_constan
     store_rows<T, D>((T *)p.dv + at, st, d.d, ty, tx, apart, rows, dv, one);
 }
 
+// Clusters of tiles of keys first (the longer ones), then tiles of queries
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) window_backward_simt(const __grid_constant__ WindowProblem p, int64_t key_blocks, int64_t rest_blocks, int64_t query_blocks,
+                                                                  int splits) {
+    extern __shared__ float sm[];
+    if (*p.status != GDN_OK) return;
+    const int64_t cluster = blockIdx.x / splits;
+    const int rank = blockIdx.x % splits;
+    if (cluster < key_blocks) dkv_tile<T, D>(p, sm, cluster, rest_blocks, rank, splits);
+    else if (blockIdx.x - key_blocks * splits < query_blocks) dq_tile<T, D>(p, sm, blockIdx.x - key_blocks * splits);
+}
+
 template <typename K, typename... A>
-cudaError_t go(K kernel, int64_t blocks, size_t smem, cudaStream_t s, A... args) {
+cudaError_t go(K kernel, int64_t blocks, int cluster, size_t smem, cudaStream_t s, A... args) {
     if (blocks <= 0) return cudaSuccess;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     const cudaError_t e = allow_shared(kernel, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)blocks, kThreads, smem, s>>>(args...);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 int64_t tiles_of(const WindowProblem &p, int T) { return p.cu ? cdiv64(T, kRows) + p.d.N : (int64_t)p.d.B * cdiv64(T, kRows); }
 
 template <typename T, int D>
 cudaError_t forward(const WindowProblem &p, cudaStream_t s) {
-    return go(window_forward_simt<T, D>, p.d.Tq ? tiles_of(p, p.d.Tq) * p.d.Hq : 0, (size_t)3 * 64 * (D + 4) * 4, s, p);
+    return go(window_forward_simt<T, D>, p.d.Tq ? tiles_of(p, p.d.Tq) * p.d.Hq : 0, 1, (size_t)3 * 64 * (D + 4) * 4, s, p);
 }
 template <typename T, int D>
 cudaError_t backward(const WindowProblem &p, cudaStream_t s) {
-    const size_t rows = (size_t)(2 * kRows + 2 * kWalk) * (D + 4) * 4, w = (size_t)kRows * (kWalk + 4) * 4;
-    cudaError_t e = go(window_dq_simt<T, D>, p.d.Tq ? tiles_of(p, p.d.Tq) * p.d.Hq : 0, rows + w, s, p);
+    const size_t smem = ((size_t)(2 * kRows + 2 * kWalk) * (D + 4) + 2 * kRows * (kWalk + 4)) * 4;
+    const int64_t rest = 2 * p.rest_slots * p.d.Hk, keys = p.d.Tk ? tiles_of(p, p.d.Tk) * p.d.Hk + rest : 0;
+    const int64_t queries = p.d.Tq ? tiles_of(p, p.d.Tq) * p.d.Hq : 0;
+    // few tiles of keys: CTAs share one, as long as each has a few steps and all fit the SMs at once
+    const int64_t steps = std::min<int64_t>(cdiv64(p.d.Tq, kWalk), cdiv64((int64_t)p.d.window + kRows, kWalk) + 1) * (p.d.Hq / p.d.Hk);
+    int splits = 1;
+    while (splits < 8 && keys * splits * 2 + queries <= 2 * kSms && steps >= 4 * splits) splits *= 2;
+    const cudaError_t e = go(window_backward_simt<T, D>, keys * splits + align_up((size_t)queries, splits), splits, smem, s, p, keys, rest, queries, splits);
     if (e != cudaSuccess) return e;
-    const int64_t rest = 2 * p.rest_slots * p.d.Hk;
-    if ((e = go(window_dkv_simt<T, D>, p.d.Tk ? tiles_of(p, p.d.Tk) * p.d.Hk + rest : 0, rows + 2 * w, s, p, rest)) != cudaSuccess) return e;
     return launch_window_sink_sums<T, D>(p, s);
 }
 template <typename T>
