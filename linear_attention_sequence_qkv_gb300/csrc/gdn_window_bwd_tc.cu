@@ -6,10 +6,12 @@
 //   keys:    K_j, V_j stay; per head of the group and tile of queries
 //            S' = K Q^T, dP' = V dO^T, P' = exp2(c S' - lse), dS' = P' (dP' - delta) scale,
 //            dV += P' dO, dK += dS' Q
-//   queries: Q_i, dO_i stay; per tile of keys  S, dP as above (not transposed), dQ += dS K
+//   queries: Q_i, dO_i stay; per tile of keys  S, dP as above (not transposed), dQ += dS K;
+//            of two heads that share keys and values where the group's size is even
 // P and dS take the place of S and dP in tensor memory, from where they are operands of the
 // second pair of products. Two such buffers, each with a warpgroup of its own (a thread per
-// row): while one tile's P and dS are computed the tensor cores work on the other's products.
+// row), for tiles by turns or for the two heads: while one's P and dS are computed the tensor
+// cores work on the other's products.
 // Seven products instead of five recompute S and dP, which is the price of no atomics.
 //
 // Keys below `sinks` are seen by all later queries. A CTA of keys takes the queries within the
@@ -28,29 +30,29 @@ namespace {
 using namespace tc;
 
 constexpr int kThreads = 384;   // warps 0 TMA, 1 MMA, 2-3 statistics and rows behind a sequence, 4-7 and 8-11 P and dS
-constexpr int kStages = 4;
-
-template <int D> struct BwdShape {
+template <int D, bool PAIR> struct BwdShape {
+    static constexpr int kStages = PAIR ? 3 : 4, kHold = PAIR ? 2 : 1;   // stages of the walked side; pairs of tiles that stay
     static constexpr int kRowA = 128 * 128, kRowB = 64 * 128;   // bytes of 128 (64) rows x 64 channels
     static constexpr int kA = D / 64 * kRowA, kB = D / 64 * kRowB;
-    static constexpr int kA1 = 0, kA2 = kA, kBs = 2 * kA, kEnd = kBs + kStages * 2 * kB;
+    static constexpr int kA1 = 0, kA2 = kA, kBs = kHold * 2 * kA, kEnd = kBs + kStages * 2 * kB;
     static constexpr int kBytes = kEnd + 1024;
     static constexpr uint32_t kAcc = 256;   // TMEM columns: buffer b's S at 128 b, dP at 128 b + 64; sums from here, D each
 };
 
-struct BwdShared {
-    uint64_t a_full, full[kStages], empty[kStages], fit[kStages], s_full[2], p_ready[2], acc_full, drain;
+template <bool KEYS> struct BwdShared {
+    uint64_t a_full, full[4], empty[4], fit[4], s_full[2], p_ready[2], acc_full, drain;
     uint32_t tmem;
     int gave_up;
-    float lse[kStages][64], delta[kStages][64];   // of the tile's queries (keys kernel): lse log2 e, delta scale
+    float lse[KEYS ? 4 : 1][64], delta[KEYS ? 4 : 1][64];   // of the tile's queries: lse log2 e, delta scale
 };
 
-template <typename T, int D, bool KEYS>
+template <typename T, int D, bool KEYS, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_constant__ WindowMaps a_maps, const __grid_constant__ WindowMaps b_maps,
                                                                   const __grid_constant__ WindowProblem p, int units, int64_t rest_blocks) {
-    using L = BwdShape<D>;
+    using L = BwdShape<D, PAIR>;
+    constexpr int kStages = L::kStages;
     extern __shared__ unsigned char smraw[];
-    __shared__ BwdShared sh;
+    __shared__ BwdShared<KEYS> sh;
     unsigned char *sm = (unsigned char *)(((uintptr_t)smraw + 1023) & ~(uintptr_t)1023);
     const gdn_window_attention_desc &d = p.d;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -60,7 +62,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
     const int group = d.Hq / d.Hk;
     const bool rest = KEYS && blockIdx.x < rest_blocks;
     const int64_t block = rest ? blockIdx.x : blockIdx.x - rest_blocks;
-    const int unit = (int)(block % units);                 // keys: head of k and v; queries: head of q
+    const int unit = (int)(block % units);                 // keys: head of k and v; queries: head of q, or two of a group
     const int64_t slot = block / units;
     int n, tile, chunk = 0;
     const int32_t *table = rest ? p.rest_off : KEYS ? p.k_tiles : p.q_tiles;
@@ -88,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
     } else if (!KEYS) {
         tile = p.q_tiles[n + 1] - p.q_tiles[n] - 1 - tile;
     }
-    const int hk = KEYS ? unit : unit / group;
+    const int head0 = PAIR ? 2 * unit : unit, hk = KEYS ? unit : head0 / group;
     const int row0 = tile * 128, rows = min(128, (KEYS ? sp.Lk : sp.Lq) - row0);   // the rows that stay
 
     // ---- what it walks over: `count` tiles of 64 rows
@@ -116,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
         }
     }
     // tile `it`: its head of queries and its first row
-    auto head_at = [&](int it) { return KEYS ? hk * group + (int)(((int64_t)chunk * p.rest_its + it) / per_head) : unit; };
+    auto head_at = [&](int it) { return KEYS ? hk * group + (int)(((int64_t)chunk * p.rest_its + it) / per_head) : head0; };
     auto row_at = [&](int it) {
         if (KEYS) return (first + (int)(((int64_t)chunk * p.rest_its + it) % per_head)) * 64;
         return (it < sinks64 ? it : first + it - sinks64) * 64;
@@ -148,14 +150,16 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
             const int64_t qrow = p.cu ? sp.q0 : 0, krow = p.cu ? sp.k0 : 0;
             const int qb = p.cu ? 0 : n * a_maps.q_rows, kb = p.cu ? 0 : n * a_maps.k_rows, vb = p.cu ? 0 : n * a_maps.v_rows;
             const int gb = p.cu || d.B == 1 ? 0 : n;
-            mbar_expect_tx(&sh.a_full, 2 * L::kA);
+            mbar_expect_tx(&sh.a_full, L::kHold * 2 * L::kA);
             for (int b = 0; b < D / 64; ++b) {
                 if (KEYS) {
                     tma_load_4d(sm + L::kA1 + b * L::kRowA, &a_maps.k, 64 * b, hk, (int)(krow + row0), kb, &sh.a_full);
                     tma_load_4d(sm + L::kA2 + b * L::kRowA, &a_maps.v, 64 * b, hk, (int)(krow + row0), vb, &sh.a_full);
                 } else {
-                    tma_load_4d(sm + L::kA1 + b * L::kRowA, &a_maps.q, 64 * b, unit, (int)(qrow + row0), qb, &sh.a_full);
-                    tma_load_4d(sm + L::kA2 + b * L::kRowA, &a_maps.g, 64 * b, unit, (int)(qrow + row0), gb, &sh.a_full);
+                    for (int s = 0; s < L::kHold; ++s) {
+                        tma_load_4d(sm + s * 2 * L::kA + L::kA1 + b * L::kRowA, &a_maps.q, 64 * b, head0 + s, (int)(qrow + row0), qb, &sh.a_full);
+                        tma_load_4d(sm + s * 2 * L::kA + L::kA2 + b * L::kRowA, &a_maps.g, 64 * b, head0 + s, (int)(qrow + row0), gb, &sh.a_full);
+                    }
                 }
             }
             int it = 0;
@@ -188,24 +192,25 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
                            bk = sw128_desc(base + L::kBs, 0, 1024), bn = sw128_desc(base + L::kBs, L::kRowB, 1024);
             int si = 0, pi = 0;        // stages of the next scores and of the next sums
             uint32_t sph = 0;
-            auto scores = [&](int b) {
+            auto scores = [&](int b) {   // into buffer b; with pairs of the b-th head
+                const uint32_t hold = PAIR ? (uint32_t)(b * (2 * L::kA >> 4)) : 0u;
                 const uint64_t s1 = bk + (uint32_t)(si * (2 * L::kB >> 4)), s2 = s1 + (uint32_t)(L::kB >> 4);
                 const uint32_t to = tb + 128 * b;
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                     const uint32_t aa = ((i >> 2) * L::kRowA + (i & 3) * 32) >> 4, ab = ((i >> 2) * L::kRowB + (i & 3) * 32) >> 4;
-                    warp_mma_f16(leader, to, a1 + aa, s1 + ab, idesc_s, i > 0);
+                    warp_mma_f16(leader, to, a1 + hold + aa, s1 + ab, idesc_s, i > 0);
                 }
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                     const uint32_t aa = ((i >> 2) * L::kRowA + (i & 3) * 32) >> 4, ab = ((i >> 2) * L::kRowB + (i & 3) * 32) >> 4;
-                    warp_mma_f16(leader, to + 64, a2 + aa, s2 + ab, idesc_s, i > 0);
+                    warp_mma_f16(leader, to + 64, a2 + hold + aa, s2 + ab, idesc_s, i > 0);
                 }
                 warp_mma_commit(leader, &sh.s_full[b]);
             };
             auto sums = [&](int b, uint32_t more) {
                 const uint64_t s1 = bn + (uint32_t)(pi * (2 * L::kB >> 4)), s2 = s1 + (uint32_t)(L::kB >> 4);
-                const uint32_t from = tb + 128 * b, acc = tb + L::kAcc;
+                const uint32_t from = tb + 128 * b, acc = tb + L::kAcc + (PAIR ? D * b : 0);
                 if (KEYS) {   // dV += P dO
                     warp_mma_f16_ta(leader, acc + D, from, s2, idesc_a, more);
 #pragma unroll
@@ -215,23 +220,53 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
 #pragma unroll
                 for (int i = 1; i < 4; ++i) warp_mma_f16_ta(leader, acc, from + 64 + 8 * i, s1 + (uint32_t)(2048 * i >> 4), idesc_a, 1);
             };
-            auto next_scores = [&](int b) -> bool {
-                if (!warp_wait2(wait, &sh.full[si], sph, &sh.fit[si], sph)) return false;
+            auto here = [&]() -> bool {   // the next tile of the walked side
+                const bool come = warp_wait2(wait, &sh.full[si], sph, &sh.fit[si], sph);
                 fence_after_sync();
-                scores(b);
-                if (++si == kStages) si = 0, sph ^= 1;
-                return true;
+                return come;
             };
-            bool ok = warp_wait(wait, &sh.a_full, 0) && next_scores(0) && (total < 2 || next_scores(1));
-            for (int it = 0; ok && it < total; ++it) {
-                const int b = it & 1;
-                ok = warp_wait(wait, &sh.p_ready[b], (uint32_t)(it >> 1) & 1);
-                if (!ok) break;
-                fence_after_sync();
-                sums(b, it > 0);
+            auto scored = [&] {
+                if (++si == kStages) si = 0, sph ^= 1;
+            };
+            auto summed = [&] {
                 warp_mma_commit(leader, &sh.empty[pi]);
                 if (++pi == kStages) pi = 0;
-                if (it + 2 < total) ok = next_scores(b);
+            };
+            bool ok = warp_wait(wait, &sh.a_full, 0);
+            if (PAIR) {   // every tile for both heads
+                ok = ok && here();
+                if (ok) scores(0), scores(1), scored();
+                for (int it = 0; ok && it < total; ++it) {
+                    const bool more = it + 1 < total;
+                    ok = !more || here();
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        ok = ok && warp_wait(wait, &sh.p_ready[b], (uint32_t)it & 1);
+                        fence_after_sync();
+                        if (ok) sums(b, it > 0);
+                        if (ok && more) scores(b);
+                    }
+                    if (!ok) break;
+                    summed();
+                    if (more) scored();
+                }
+            } else {      // tiles by turns
+                for (int b = 0; ok && b < 2 && b < total; ++b) {
+                    ok = here();
+                    if (ok) scores(b), scored();
+                }
+                for (int it = 0; ok && it < total; ++it) {
+                    const int b = it & 1;
+                    ok = warp_wait(wait, &sh.p_ready[b], (uint32_t)(it >> 1) & 1);
+                    if (!ok) break;
+                    fence_after_sync();
+                    sums(b, it > 0);
+                    summed();
+                    if (it + 2 < total) {
+                        ok = here();
+                        if (ok) scores(b), scored();
+                    }
+                }
             }
             if (ok) warp_mma_commit(leader, &sh.acc_full);
             warp_mma_commit(leader, &sh.drain);
@@ -272,12 +307,14 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
         const float c = d.scale * 1.4426950408889634f;
         const int64_t ntok = (int64_t)d.B * d.Tq;
         float lse = 0.0f, delta = 0.0f;
+        const int head = KEYS ? unit : PAIR ? head0 + b : unit;
         if (!KEYS && r < rows) {
-            lse = p.lse[unit * ntok + sp.q0 + row0 + r] * 1.4426950408889634f;
-            delta = p.delta[unit * ntok + sp.q0 + row0 + r] * d.scale;
+            lse = p.lse[head * ntok + sp.q0 + row0 + r] * 1.4426950408889634f;
+            delta = p.delta[head * ntok + sp.q0 + row0 + r] * d.scale;
         }
         bool ok = true;
-        for (int it = b; it < count; it += 2) {
+        for (int it = PAIR ? 0 : b; it < count; it += PAIR ? 1 : 2) {
+            const uint32_t ph = (uint32_t)(PAIR ? it : it >> 1) & 1;
             const int i = it % kStages, r0 = row_at(it);
             // this row's columns [lo, hi), and those below sk
             uint32_t see[2];
@@ -296,8 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
 #pragma unroll
                 for (int w = 0; w < 2; ++w) see[w] = low_bits(h - 32 * w) & (~low_bits(l - 32 * w) | low_bits(k - 32 * w));
             }
-            if (!(ok = KEYS ? warp_wait2(wait, &sh.s_full[b], (uint32_t)(it >> 1) & 1, &sh.fit[i], (uint32_t)(it / kStages) & 1)
-                            : warp_wait(wait, &sh.s_full[b], (uint32_t)(it >> 1) & 1)))
+            if (!(ok = KEYS ? warp_wait2(wait, &sh.s_full[b], ph, &sh.fit[i], (uint32_t)(it / kStages) & 1) : warp_wait(wait, &sh.s_full[b], ph)))
                 break;
             fence_after_sync();
             const bool all = __all_sync(0xffffffffu, (see[0] & see[1]) == 0xffffffffu);
@@ -335,11 +371,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
             fence_after_sync();
         }
         // ---- the sums, through the rows that stay in shared memory (no product reads them any more): the second
-        // warpgroup takes dV, or the other half of dQ's channels
-        constexpr int kCols = KEYS ? D : D / 2;
+        // warpgroup takes dV, the other head's dQ, or the other half of dQ's channels
+        constexpr int kCols = KEYS || PAIR ? D : D / 2;
         const uint32_t from = tbase + L::kAcc + b * kCols + ((uint32_t)(warp & 3) << 21);
-        unsigned char *stage = sm + (KEYS ? b * L::kA : 0);
-        const int c0 = KEYS ? 0 : b * kCols;
+        unsigned char *stage = sm + (KEYS ? b * L::kA : PAIR ? b * 2 * L::kA : 0);
+        const int c0 = KEYS || PAIR ? 0 : b * kCols;
         // rows of sinks whose sum has other parts stay in fp32
         const int apart = !KEYS || !ok ? 0 : rest ? 128 : row0 < d.sinks && rest_chunks(p, sp, tile) > 0 ? min(128, d.sinks - row0) : 0;
         const int64_t part_slot = !KEYS ? 0 : rest ? slot : p.rest_slots + (int64_t)n * p.sink_tiles + tile;
@@ -366,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
         }
         __syncwarp();
         const int w0 = r & ~31;
-        const int heads = KEYS ? d.Hk : d.Hq, head = unit;
+        const int heads = KEYS ? d.Hk : d.Hq;
         T *out = (T *)(KEYS ? (b ? p.dv : p.dk) : p.dq) + (((KEYS ? sp.k0 : sp.q0) + row0 + w0) * heads + head) * (int64_t)d.d;
         const int n_rows = ok ? max(0, min(32, rows - w0)) : 0;
         for (int x = lane; x < n_rows * (kCols / 8); x += 32) {
@@ -398,8 +434,8 @@ cudaError_t launch_backward(const WindowProblem &p, cudaStream_t s) {
             return cudaErrorInvalidValue;
     }
     cudaError_t e;
-    const size_t smem = std::max<size_t>(BwdShape<D>::kBytes, 117 * 1024);   // one CTA per SM: each holds all of the tensor memory
-    auto go = [&](auto kernel, int64_t tiles, int units, int64_t rest) {
+    auto go = [&](auto kernel, size_t bytes, int64_t tiles, int units, int64_t rest) {
+        const size_t smem = std::max<size_t>(bytes, 117 * 1024);   // one CTA per SM: each holds all of the tensor memory
         if ((tiles + rest) * units > 0x7fffffff) return cudaErrorInvalidValue;
         const cudaError_t a = allow_shared(kernel, smem);
         if (a != cudaSuccess) return a;
@@ -408,8 +444,10 @@ cudaError_t launch_backward(const WindowProblem &p, cudaStream_t s) {
     };
     const int64_t qt = p.cu ? cdiv64(d.Tq, 128) + d.N : (int64_t)d.B * cdiv64(d.Tq, 128);
     const int64_t kt = p.cu ? cdiv64(d.Tk, 128) + d.N : (int64_t)d.B * cdiv64(d.Tk, 128);
-    if ((e = go(window_backward_tc<T, D, true>, kt, d.Hk, p.rest_slots)) != cudaSuccess) return e;
-    if ((e = go(window_backward_tc<T, D, false>, qt, d.Hq, 0)) != cudaSuccess) return e;
+    if ((e = go(window_backward_tc<T, D, true, false>, BwdShape<D, false>::kBytes, kt, d.Hk, p.rest_slots)) != cudaSuccess) return e;
+    if (d.Hq / d.Hk % 2 == 0) e = go(window_backward_tc<T, D, false, true>, BwdShape<D, true>::kBytes, qt, d.Hq / 2, 0);
+    else e = go(window_backward_tc<T, D, false, false>, BwdShape<D, false>::kBytes, qt, d.Hq, 0);
+    if (e != cudaSuccess) return e;
     return launch_window_sink_sums<T, D>(p, s);
 }
 
