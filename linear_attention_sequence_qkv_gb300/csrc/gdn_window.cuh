@@ -21,10 +21,11 @@ struct WindowProblem {
     int32_t *status;
     int32_t *q_tiles, *k_tiles; // packed: [N+1] tiles of the sequences before n, by queries and by keys
     int wait_immediate;
-    // the tensor-core backward: what the sinks' keys take beyond their tile's own CTA (gdn_window_bwd_tc.cu)
+    // the backward: what the sinks' keys take beyond their tile's own CTA (gdn_window_rest.cuh)
     float *partial;             // partial sums of their gradients
     int32_t *rest_off;          // packed: [N+1] chunks of the sequences before n
     int64_t rest_slots;         // chunks at most
+    int rest_shift;             // tiles of 2^rest_shift queries
     int rest_its, rest_per;     // tiles per chunk; chunks per row without packing
     int sink_tiles, sink_rows;  // tiles that hold sinks (0: no rest), rows of their partial sums
 };

@@ -162,7 +162,7 @@ cudaError_t backward_any(WindowProblem &p, cudaStream_t s) {
         window_delta<T, false><<<row_blocks(rows, 8), 256, 0, s>>>(p, 32);
     }
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    window_rest_plan(p);
+    window_rest_plan(p, tc ? 7 : 6);
     if ((e = launch_window_rest_table(p, s)) != cudaSuccess) return e;
     return tc ? launch_window_backward_tc(p, s) : launch_window_backward_simt(p, s);
 }
@@ -183,8 +183,12 @@ WindowLayout layout_of(const gdn_window_attention_desc &d, bool backward) {
         L.partial = off;
         WindowProblem p;
         p.d = d;
-        window_rest_plan(p);
-        off = align_up(off + window_partial_bytes(p), 256);
+        size_t most = 0;   // of either kernels: which it is the pointers say
+        for (int shift = 6; shift <= 7; ++shift) {
+            window_rest_plan(p, shift);
+            most = std::max(most, window_partial_bytes(p));
+        }
+        off = align_up(off + most, 256);
     }
     L.total = off;
     return L;
@@ -197,11 +201,12 @@ cudaError_t launch_window_tables(const WindowProblem &p, int q_tile, int k_tile,
     return cudaGetLastError();
 }
 
-// Chunks of the sinks' rest: as long as a CTA of keys walks within the window, 32 to 512 tiles
-void window_rest_plan(WindowProblem &p) {
+// Chunks of the sinks' rest: as long as a CTA of keys walks within the window, 2048 to 32768 queries
+void window_rest_plan(WindowProblem &p, int shift) {
     const gdn_window_attention_desc &d = p.d;
-    const int64_t group = d.Hq / d.Hk;
-    p.rest_its = (int)std::min<int64_t>(512, std::max<int64_t>(32, group * (((int64_t)d.window + 127) / 64 + 1)));
+    const int64_t group = d.Hq / d.Hk, unit = (int64_t)1 << shift;
+    p.rest_shift = shift;
+    p.rest_its = (int)std::min<int64_t>(32768 / unit, std::max<int64_t>(2048 / unit, group * (((int64_t)d.window + 127) / unit + 1)));
     p.sink_tiles = (int)cdiv64(std::min(d.sinks, d.Tk), 128);
     p.sink_rows = std::min(128, std::min(d.sinks, d.Tk));
     p.rest_per = 0;
@@ -213,13 +218,13 @@ void window_rest_plan(WindowProblem &p) {
     if (d.N == d.B) {   // not packed, or one sequence: the same chunks for all rows
         for (int t = 0; t < p.sink_tiles; ++t) {
             const int64_t past = (int64_t)d.Tk - d.Tq, j0 = (int64_t)t * 128, j1 = std::min<int64_t>(j0 + 127, d.Tk - 1);
-            const int64_t hi = std::min<int64_t>(d.Tq - 1, j1 + d.window - 1 - past), lo = std::max<int64_t>(0, j0 - past) >> 6;
-            const int64_t tiles = std::max<int64_t>(0, cdiv64(d.Tq, 64) - std::max<int64_t>(hi < 0 ? 0 : (hi >> 6) + 1, lo));
+            const int64_t hi = std::min<int64_t>(d.Tq - 1, j1 + d.window - 1 - past), lo = std::max<int64_t>(0, j0 - past) >> shift;
+            const int64_t tiles = std::max<int64_t>(0, cdiv64(d.Tq, unit) - std::max<int64_t>(hi < 0 ? 0 : (hi >> shift) + 1, lo));
             p.rest_per += (int)cdiv64(tiles * group, p.rest_its);
         }
         p.rest_slots = (int64_t)d.B * p.rest_per;
     } else {            // at most: every sequence's last chunk begun
-        p.rest_slots = p.sink_tiles * (cdiv64(group * (cdiv64(d.Tq, 64) + d.N), p.rest_its) + d.N);
+        p.rest_slots = p.sink_tiles * (cdiv64(group * (cdiv64(d.Tq, unit) + d.N), p.rest_its) + d.N);
     }
     if (p.rest_slots == 0) p.sink_tiles = 0;
 }

@@ -8,22 +8,22 @@
 
 namespace gdn {
 
-// The queries that the sinks of key tile t still have to take beyond the tile's own CTA: tiles of 64 from e0 on, `tiles` of
-// them for each head
+// The queries that the sinks of key tile t still have to take beyond the tile's own CTA: tiles of 2^shift queries from e0 on,
+// `tiles` of them for each head
 struct SinkRest {
     int e0, tiles;
 };
-__device__ __forceinline__ SinkRest sink_rest(int Lq, int Lk, int t, int window) {
+__device__ __forceinline__ SinkRest sink_rest(int Lq, int Lk, int t, int window, int shift) {
     const int64_t past = (int64_t)Lk - Lq, j0 = (int64_t)t * 128, j1 = min(j0 + 127, (int64_t)Lk - 1);
     const int64_t hi = min((int64_t)Lq - 1, j1 + window - 1 - past);
-    const int64_t lo = max((int64_t)0, j0 - past) >> 6;
+    const int64_t lo = max((int64_t)0, j0 - past) >> shift;
     SinkRest r;
-    r.e0 = (int)max(hi < 0 ? (int64_t)0 : (hi >> 6) + 1, lo);
-    r.tiles = j0 < Lk ? max(0, ((Lq + 63) >> 6) - r.e0) : 0;
+    r.e0 = (int)max(hi < 0 ? (int64_t)0 : (hi >> shift) + 1, lo);
+    r.tiles = j0 < Lk ? max(0, (int)(((int64_t)Lq + (1 << shift) - 1) >> shift) - r.e0) : 0;
     return r;
 }
 __device__ __forceinline__ int rest_chunks(const WindowProblem &p, const WindowSpan &s, int t) {
-    const int64_t its = (int64_t)sink_rest(s.Lq, s.Lk, t, p.d.window).tiles * (p.d.Hq / p.d.Hk);
+    const int64_t its = (int64_t)sink_rest(s.Lq, s.Lk, t, p.d.window, p.rest_shift).tiles * (p.d.Hq / p.d.Hk);
     return (int)((its + p.rest_its - 1) / p.rest_its);
 }
 
@@ -64,9 +64,9 @@ cudaError_t launch_window_sink_sums(const WindowProblem &p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// fills the chunks' part of p from the sizes; the bytes of the partial sums; the packed sequences' table of chunks
+// fills the chunks' part of p from the sizes, for tiles of 2^shift queries; the bytes of the partial sums; the packed sequences' table of chunks
 // (gdn_window_attention.cu)
-void window_rest_plan(WindowProblem &p);
+void window_rest_plan(WindowProblem &p, int shift);
 size_t window_partial_bytes(const WindowProblem &p);
 cudaError_t launch_window_rest_table(const WindowProblem &p, cudaStream_t s);
 

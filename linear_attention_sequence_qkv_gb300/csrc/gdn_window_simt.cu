@@ -368,7 +368,7 @@ __device__ __forceinline__ void dkv_tile(const WindowProblem &p, float *sm, int6
     // its chunks begin), or a chunk of the rest
     int64_t first = 0, per_head = 0, it0 = 0, it1;
     if (rest) {
-        const SinkRest r = sink_rest(sp.Lq, sp.Lk, tile, d.window);
+        const SinkRest r = sink_rest(sp.Lq, sp.Lk, tile, d.window, p.rest_shift);
         first = r.e0, per_head = r.tiles;
         it0 = (int64_t)chunk * p.rest_its, it1 = min(it0 + p.rest_its, per_head * group);
     } else {
