@@ -6,7 +6,8 @@
 //   keys:    K_j, V_j stay; per head of the group and tile of queries
 //            S' = K Q^T, dP' = V dO^T, P' = exp2(c S' - lse), dS' = P' (dP' - delta) scale,
 //            dV += P' dO, dK += dS' Q
-//   queries: Q_i, dO_i stay; per tile of keys  S, dP as above (not transposed), dQ += dS K
+//   queries: Q_i, dO_i stay; per tile of keys  S, dP as above (not transposed), dQ += dS K;
+//            gdn_window_dq_tc.cu has it for two heads at once
 // P and dS take the place of S and dP in tensor memory, from where they are operands of the
 // second products. Two warpgroups work on a tile, a thread per row and half of the columns. The
 // products of tile t and the scores of t + 1 alternate so that the tensor cores have work while
@@ -437,7 +438,7 @@ cudaError_t launch_backward(const WindowProblem &p, cudaStream_t s) {
     const int64_t qt = p.cu ? cdiv64(d.Tq, 128) + d.N : (int64_t)d.B * cdiv64(d.Tq, 128);
     const int64_t kt = p.cu ? cdiv64(d.Tk, 128) + d.N : (int64_t)d.B * cdiv64(d.Tk, 128);
     cudaError_t e = go(window_backward_tc<T, D, true>, kt, d.Hk, p.rest_slots);
-    if (e == cudaSuccess) e = go(window_backward_tc<T, D, false>, qt, d.Hq, 0);
+    if (e == cudaSuccess) e = window_dq_pairs(d) ? launch_window_dq_pair(maps, p, s) : go(window_backward_tc<T, D, false>, qt, d.Hq, 0);
     return e == cudaSuccess ? launch_window_sink_sums<T, D>(p, s) : e;
 }
 

@@ -91,5 +91,8 @@ bool window_head_map(CUtensorMap *m, const gdn_window_attention_desc &d, const v
                      int *rows, uint32_t box);
 // after delta, with the chunks planned
 cudaError_t launch_window_backward_tc(const WindowProblem &p, cudaStream_t s);
+// its dq, where two heads at once are faster; `wide`: maps of 128 rows
+bool window_dq_pairs(const gdn_window_attention_desc &d);
+cudaError_t launch_window_dq_pair(const WindowMaps &wide, const WindowProblem &p, cudaStream_t s);
 
 }  // namespace gdn
