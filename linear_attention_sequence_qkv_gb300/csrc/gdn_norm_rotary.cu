@@ -20,6 +20,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kMostChannels = 1024;   // of a head: a warp keeps four rows of them in shared memory
 constexpr int kBwdCtas = 4 * kSms;    // CTAs of the backward, each with a row of partial weight gradients
+constexpr int kVectorCtas = 2 * kSms; // of its vector kernel, whose registers leave room for two per SM: twice as many take 2 us more
 
 struct NormRotaryProblem {
     gdn_norm_rotary_desc n;
@@ -355,6 +356,8 @@ __global__ void __launch_bounds__(kThreads, K == 1 ? 3 : 1) norm_rotary_vectors(
     }
 }
 
+// Both tensors of kFlight heads are on their way at once: with two heads' 4474 GB/s instead of 5480 (32768 tokens of 48 heads of
+// 128, 16 bits), with six, or a third CTA per SM, the registers spill (5092 and 3455 GB/s).
 template <typename T, int V, int K, int TEAM, bool HALF>
 __global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) norm_rotary_vectors_backward(const __grid_constant__ NormRotaryProblem p, int parts, int per) {
     extern __shared__ float sm[];   // [teams][2][d]
@@ -362,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) norm_rotary_vectors_
     const bool ok = p.cu == nullptr || seqlens_ok(p.cu, d.N, d.T);
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = ok ? GDN_OK : GDN_ERR_DEVICE_SEQLENS;
     if (!ok) return;
-    constexpr int kTeams = kThreads / TEAM, kF = kFlight / 2;   // two tensors' loads per head
+    constexpr int kTeams = kThreads / TEAM;
     const int lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
     const Place<V, K, HALF> at(d, lane, TEAM);
     constexpr int NP = V / 2;
@@ -395,10 +398,10 @@ __global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) norm_rotary_vectors_
             for (int k = 0; k < K; ++k)
 #pragma unroll
                 for (int e = 0; e < NP; ++e) wo[k][e] = at.c[k] >= 0 ? weights_at(w, p.n.weight_dtype, at.c[k] + 2 * e) : splat2(0.0f);
-            for (int r0 = 0; r0 < most; r0 += kF) {
-                Vec<T, V> x[kF][K], g[kF][K];
+            for (int r0 = 0; r0 < most; r0 += kFlight) {
+                Vec<T, V> x[kFlight][K], g[kFlight][K];
 #pragma unroll
-                for (int j = 0; j < kF; ++j)
+                for (int j = 0; j < kFlight; ++j)
 #pragma unroll
                     for (int k = 0; k < K; ++k) {
 #pragma unroll
@@ -409,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) norm_rotary_vectors_
                         }
                     }
 #pragma unroll
-                for (int j = 0; j < kF; ++j) {
+                for (int j = 0; j < kFlight; ++j) {
                     if (r0 + j >= most) break;
                     Vec<T, V> o[K];
                     if (HALF) partners<T, V, K, HALF>(at, g[j], o, TEAM);
@@ -507,7 +510,7 @@ cudaError_t launch_vectors(NormRotaryProblem &p, bool backward, cudaStream_t s) 
         return cudaGetLastError();
     }
     const size_t smem = (size_t)kTeams * 2 * d.d * 4;   // at most 32 KB: a team's channels are at most 16 of its lanes' bytes
-    p.ctas = (int)std::min<int64_t>(blocks, p.ctas);
+    p.ctas = (int)std::min<int64_t>({blocks, p.ctas, kVectorCtas});
     norm_rotary_vectors_backward<T, V, K, TEAM, HALF><<<(unsigned)p.ctas, kThreads, smem, s>>>(p, parts, per);
     return cudaGetLastError();
 }
