@@ -60,7 +60,6 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
     unsigned char *sm = smraw;
     const gdn_window_attention_desc &d = p.d;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (*p.status == GDN_ERR_DEVICE_SEQLENS) return;
     if (smem_u32(smraw) & 1023) {   // (never: see above) the swizzled tiles would be read wrongly
         if (tid == 0) *p.status = GDN_ERR_DEVICE_TIMEOUT;
         return;
@@ -75,8 +74,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
     int n, tile, chunk = 0;
     const int32_t *table = rest ? p.rest_off : KEYS ? p.k_tiles : p.q_tiles;
     if (p.cu) {
-        if (slot >= table[d.N]) return;
-        n = upper_index(table, d.N, slot);
+        const int32_t status = *p.status, tiles = table[d.N];   // on their way with the search's
+        n = warp_upper_index(table, d.N, slot);
+        if (status == GDN_ERR_DEVICE_SEQLENS || slot >= tiles) return;
         tile = (int)(slot - table[n]);
     } else {
         const int per = rest ? p.rest_per : ((KEYS ? d.Tk : d.Tq) + 127) / 128;

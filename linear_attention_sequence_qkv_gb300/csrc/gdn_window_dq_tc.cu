@@ -51,15 +51,15 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_pair(const __grid_const
     unsigned char *sm = (unsigned char *)(((uintptr_t)smraw + 1023) & ~(uintptr_t)1023);
     const gdn_window_attention_desc &d = p.d;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (*p.status == GDN_ERR_DEVICE_SEQLENS) return;
 
     // ---- the CTA's place; later queries, which see the most, first
     const int units = d.Hq / 2, head0 = 2 * (int)(blockIdx.x % units), hk = head0 / (d.Hq / d.Hk);
     const int64_t slot = blockIdx.x / units;
     int n, tile;
     if (p.cu) {
-        if (slot >= p.q_tiles[d.N]) return;
-        n = upper_index(p.q_tiles, d.N, slot);
+        const int32_t status = *p.status, tiles = p.q_tiles[d.N];   // on their way with the search's
+        n = warp_upper_index(p.q_tiles, d.N, slot);
+        if (status == GDN_ERR_DEVICE_SEQLENS || slot >= tiles) return;
         tile = p.q_tiles[n + 1] - 1 - (int)slot;
     } else {
         const int per = (d.Tq + 127) / 128;

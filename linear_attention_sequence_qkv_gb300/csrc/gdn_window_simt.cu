@@ -121,7 +121,7 @@ __device__ __forceinline__ void store_rows(T *dst, int64_t stride, int d, int ty
 __device__ __forceinline__ bool tile_of(const WindowProblem &p, const int32_t *table, int64_t slot, int T, int &n, int &tile, int &tiles) {
     if (p.cu) {
         if (slot >= table[p.d.N]) return false;
-        n = upper_index(table, p.d.N, slot);
+        n = warp_upper_index(table, p.d.N, slot);
         tile = (int)(slot - table[n]);
         tiles = table[n + 1] - table[n];
     } else {
@@ -341,7 +341,7 @@ __device__ __forceinline__ void dkv_tile(const WindowProblem &p, float *sm, int6
         slot >>= 1;
         if (p.cu) {
             if (slot >= p.rest_off[d.N]) return;
-            n = upper_index(p.rest_off, d.N, slot);
+            n = warp_upper_index(p.rest_off, d.N, slot);
             chunk = (int)(slot - p.rest_off[n]);
         } else {
             n = (int)(slot / p.rest_per);

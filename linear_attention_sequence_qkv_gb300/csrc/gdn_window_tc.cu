@@ -72,7 +72,6 @@ __global__ void __launch_bounds__(kThreads, 1) window_forward_tc(const __grid_co
     unsigned char *sm = (unsigned char *)(((uintptr_t)smraw + 1023) & ~(uintptr_t)1023);
     const gdn_window_attention_desc &d = p.d;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (p.cu && *p.status != GDN_OK) return;
     if (!p.cu && blockIdx.x == 0 && tid == 0) *p.status = GDN_OK;
 
     // ---- the CTA's place: later tiles of queries, which see the most keys, first
@@ -81,8 +80,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_forward_tc(const __grid_co
     const int rows_per = pair_heads ? 128 : 256;
     int n, qt;
     if (p.cu) {
-        if (slot >= p.q_tiles[d.N]) return;
-        n = upper_index(p.q_tiles, d.N, slot);
+        const int32_t status = *p.status, tiles = p.q_tiles[d.N];   // on their way with the search's
+        n = warp_upper_index(p.q_tiles, d.N, slot);
+        if (status != GDN_OK || slot >= tiles) return;
         qt = (int)(p.q_tiles[n + 1] - 1 - slot);
     } else {
         const int per = (d.Tq + rows_per - 1) / rows_per;
