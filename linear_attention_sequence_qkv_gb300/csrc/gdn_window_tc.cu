@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_forward_tc(const __grid_co
     unsigned char *sm = (unsigned char *)(((uintptr_t)smraw + 1023) & ~(uintptr_t)1023);
     const gdn_window_attention_desc &d = p.d;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) tma_prefetch_map(&maps.q), tma_prefetch_map(&maps.k), tma_prefetch_map(&maps.v);
     if (!p.cu && blockIdx.x == 0 && tid == 0) *p.status = GDN_OK;
 
     // ---- the CTA's place: later tiles of queries, which see the most keys, first
@@ -112,6 +113,14 @@ __global__ void __launch_bounds__(kThreads, 1) window_forward_tc(const __grid_co
     auto tile_at = [&](int u) { return u < all.ns ? u : all.w0 + u - all.ns; };
     const int hk = st[0].head / (d.Hq / d.Hk);
 
+    // K or V of the u-th tile into its stage
+    auto load = [&](int u, bool is_v) {
+        const int i = u % (is_v ? L::kV : L::kK), krow = p.cu ? (int)sp.k0 : 0, batch = p.cu ? 0 : n * (is_v ? maps.v_rows : maps.k_rows);
+        uint64_t *full = is_v ? &sh.v_full[i] : &sh.k_full[i];
+        unsigned char *to = sm + (is_v ? L::kVs : L::kKs) + i * L::kTile;
+        mbar_expect_tx(full, L::kTile);
+        for (int b = 0; b < D / 64; ++b) tma_load_4d(to + b * L::kRow, is_v ? &maps.v : &maps.k, 64 * b, hk, krow + tile_at(u) * 128, batch, full);
+    };
     if (tid == 0) {
         mbar_init(&sh.q_full, 1);
         for (int i = 0; i < 4; ++i) {
@@ -122,8 +131,21 @@ __global__ void __launch_bounds__(kThreads, 1) window_forward_tc(const __grid_co
         mbar_init(&sh.drain, 1);
         sh.gave_up = sh.any_bad = 0;
         mbar_init_fence();
+        if (count > 0) {   // the first copies are on their way while the CTA gets its tensor memory
+            fence_async_smem();
+            const int qrow = p.cu ? (int)sp.q0 : 0, qb = p.cu ? 0 : n * maps.q_rows;
+            int q_bytes = 0;
+            for (int s = 0; s < 2; ++s) q_bytes += st[s].tiles.empty() ? 0 : L::kTile;
+            mbar_expect_tx(&sh.q_full, q_bytes);
+            for (int s = 0; s < 2; ++s)
+                if (!st[s].tiles.empty())
+                    for (int b = 0; b < D / 64; ++b)
+                        tma_load_4d(sm + L::kQ + s * L::kTile + b * L::kRow, &maps.q, 64 * b, st[s].head, qrow + st[s].i0, qb, &sh.q_full);
+            load(0, false);
+            load(0, true);
+        }
     }
-    if (warp == 0) tmem_alloc(&sh.tmem, 512);
+    if (warp == 1) tmem_alloc(&sh.tmem, 512);
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
@@ -135,30 +157,13 @@ __global__ void __launch_bounds__(kThreads, 1) window_forward_tc(const __grid_co
     if (warp == 0) {
         // ------------------------------------------------------------ copies
         if (lane == 0 && count > 0) {
-            const int64_t qrow = p.cu ? sp.q0 : 0, krow = p.cu ? sp.k0 : 0;
-            const int qb = p.cu ? 0 : n * maps.q_rows, kb = p.cu ? 0 : n * maps.k_rows, vb = p.cu ? 0 : n * maps.v_rows;
-            int q_bytes = 0;
-            for (int s = 0; s < 2; ++s) q_bytes += st[s].tiles.empty() ? 0 : L::kTile;
-            mbar_expect_tx(&sh.q_full, q_bytes);
-            for (int s = 0; s < 2; ++s)
-                if (!st[s].tiles.empty())
-                    for (int b = 0; b < D / 64; ++b)
-                        tma_load_4d(sm + L::kQ + s * L::kTile + b * L::kRow, &maps.q, 64 * b, st[s].head, (int)(qrow + st[s].i0), qb, &sh.q_full);
-            int ku = 0, vu = 0;
-            auto load = [&](int u, bool is_v) -> bool {
-                const int stages = is_v ? L::kV : L::kK, i = u % stages;
-                uint64_t *full = is_v ? &sh.v_full[i] : &sh.k_full[i], *empty = is_v ? &sh.v_empty[i] : &sh.k_empty[i];
-                if (u >= stages && !wait(empty, (uint32_t)(u / stages - 1) & 1)) return false;
-                unsigned char *to = sm + (is_v ? L::kVs : L::kKs) + i * L::kTile;
-                mbar_expect_tx(full, L::kTile);
-                for (int b = 0; b < D / 64; ++b)
-                    tma_load_4d(to + b * L::kRow, is_v ? &maps.v : &maps.k, 64 * b, hk, (int)(krow + (int64_t)tile_at(u) * 128), is_v ? vb : kb, full);
-                return true;
-            };
-            for (int u = 0; u < count; ++u) {
-                if (!load(u, false)) break;
+            int ku = 1, vu = 1;   // loaded so far
+            for (int u = 1; u < count; ++u) {
+                if (u >= L::kK && !wait(&sh.k_empty[u % L::kK], (uint32_t)(u / L::kK - 1) & 1)) break;
+                load(u, false);
                 ++ku;
-                if (!load(u, true)) break;
+                if (u >= L::kV && !wait(&sh.v_empty[u % L::kV], (uint32_t)(u / L::kV - 1) & 1)) break;
+                load(u, true);
                 ++vu;
             }
             // what is in flight lands before the CTA leaves (a wait of a second each at most)
@@ -433,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_forward_tc(const __grid_co
     fence_before_sync();
     __syncthreads();
     if (tid == 0 && sh.gave_up) *p.status = GDN_ERR_DEVICE_TIMEOUT;
-    if (warp == 0) tmem_dealloc(tbase, 512);
+    if (warp == 1) tmem_dealloc(tbase, 512);
 }
 
 bool strides_fit(const gdn_window_attention_desc &d) {
