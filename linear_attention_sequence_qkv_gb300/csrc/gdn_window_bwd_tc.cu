@@ -60,6 +60,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
     unsigned char *sm = smraw;
     const gdn_window_attention_desc &d = p.d;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) tma_prefetch_map(&maps.q), tma_prefetch_map(&maps.k), tma_prefetch_map(&maps.v), tma_prefetch_map(&maps.g);
     if (smem_u32(smraw) & 1023) {   // (never: see above) the swizzled tiles would be read wrongly
         if (tid == 0) *p.status = GDN_ERR_DEVICE_TIMEOUT;
         return;
@@ -125,6 +126,22 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
     };
     const int other = KEYS ? sp.Lq : sp.Lk;                // rows of the side walked over
 
+    const int qrow = p.cu ? (int)sp.q0 : 0, krow = p.cu ? (int)sp.k0 : 0;
+    const int qb = p.cu ? 0 : n * maps.q_rows, kb = p.cu ? 0 : n * maps.k_rows, vb = p.cu ? 0 : n * maps.v_rows, gb = p.cu || d.B == 1 ? 0 : n;
+    auto copy = [&](int to, const CUtensorMap *map, int head, int row, int batch, uint64_t *bar) {
+        for (int b = 0; b < D / 64; ++b) tma_load_4d(sm + to + b * L::kRow, map, 64 * b, head, row, batch, bar);
+    };
+    // the walked side's operands of the it-th tile
+    auto load1 = [&](int it) {
+        const int i = it % kFirst;
+        mbar_expect_tx(&sh.full1[i], L::kTile);
+        copy(L::kB1 + i * L::kTile, KEYS ? &maps.q : &maps.k, KEYS ? head_at(it) : hk, (KEYS ? qrow : krow) + row_at(it), KEYS ? qb : kb, &sh.full1[i]);
+    };
+    auto load2 = [&](int it) {
+        const int j = it % kSecond;
+        mbar_expect_tx(&sh.full2[j], L::kTile);
+        copy(L::kB2 + j * L::kTile, KEYS ? &maps.g : &maps.v, KEYS ? head_at(it) : hk, (KEYS ? qrow : krow) + row_at(it), KEYS ? gb : vb, &sh.full2[j]);
+    };
     if (tid == 0) {
         mbar_init(&sh.a_full, 1);
         for (int i = 0; i < kFirst; ++i) mbar_init(&sh.full1[i], 1), mbar_init(&sh.empty1[i], 1), mbar_init(&sh.fit[i], 2);
@@ -133,8 +150,16 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
         mbar_init(&sh.acc_full, 1), mbar_init(&sh.drain, 1);
         sh.gave_up = 0;
         mbar_init_fence();
+        if (count > 0) {   // the first copies are on their way while the CTA gets its tensor memory
+            fence_async_smem();
+            mbar_expect_tx(&sh.a_full, 2 * L::kTile);
+            copy(L::kA1, KEYS ? &maps.k : &maps.q, unit, (KEYS ? krow : qrow) + row0, KEYS ? kb : qb, &sh.a_full);
+            load1(0);
+            copy(L::kA2, KEYS ? &maps.v : &maps.g, unit, (KEYS ? krow : qrow) + row0, KEYS ? vb : gb, &sh.a_full);
+            load2(0);
+        }
     }
-    if (warp == 0) tmem_alloc(&sh.tmem, 512);
+    if (warp == 1) tmem_alloc(&sh.tmem, 512);
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
@@ -147,30 +172,13 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
     if (warp == 0) {
         // ------------------------------------------------------------ copies
         if (lane == 0 && count > 0) {
-            const int qrow = p.cu ? (int)sp.q0 : 0, krow = p.cu ? (int)sp.k0 : 0;
-            const int qb = p.cu ? 0 : n * maps.q_rows, kb = p.cu ? 0 : n * maps.k_rows, vb = p.cu ? 0 : n * maps.v_rows;
-            const int gb = p.cu || d.B == 1 ? 0 : n;
-            auto copy = [&](int to, const CUtensorMap *map, int head, int row, int batch, uint64_t *bar) {
-                for (int b = 0; b < D / 64; ++b) tma_load_4d(sm + to + b * L::kRow, map, 64 * b, head, row, batch, bar);
-            };
-            mbar_expect_tx(&sh.a_full, 2 * L::kTile);
-            if (KEYS) {
-                copy(L::kA1, &maps.k, hk, krow + row0, kb, &sh.a_full);
-                copy(L::kA2, &maps.v, hk, krow + row0, vb, &sh.a_full);
-            } else {
-                copy(L::kA1, &maps.q, unit, qrow + row0, qb, &sh.a_full);
-                copy(L::kA2, &maps.g, unit, qrow + row0, gb, &sh.a_full);
-            }
-            int n1 = 0, n2 = 0;
-            for (int it = 0; it < count; ++it) {
-                const int h = head_at(it), r = row_at(it), i = it % kFirst, j = it % kSecond;
-                if (it >= kFirst && !wait(&sh.empty1[i], (uint32_t)(it / kFirst - 1) & 1)) break;
-                mbar_expect_tx(&sh.full1[i], L::kTile);
-                copy(L::kB1 + i * L::kTile, KEYS ? &maps.q : &maps.k, KEYS ? h : hk, (KEYS ? qrow : krow) + r, KEYS ? qb : kb, &sh.full1[i]);
+            int n1 = 1, n2 = 1;   // loaded so far
+            for (int it = 1; it < count; ++it) {
+                if (it >= kFirst && !wait(&sh.empty1[it % kFirst], (uint32_t)(it / kFirst - 1) & 1)) break;
+                load1(it);
                 ++n1;
-                if (it >= kSecond && !wait(&sh.empty2[j], (uint32_t)(it / kSecond - 1) & 1)) break;
-                mbar_expect_tx(&sh.full2[j], L::kTile);
-                copy(L::kB2 + j * L::kTile, KEYS ? &maps.g : &maps.v, KEYS ? h : hk, (KEYS ? qrow : krow) + r, KEYS ? gb : vb, &sh.full2[j]);
+                if (it >= kSecond && !wait(&sh.empty2[it % kSecond], (uint32_t)(it / kSecond - 1) & 1)) break;
+                load2(it);
                 ++n2;
             }
             // what is in flight lands before the CTA leaves
@@ -413,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
     fence_before_sync();
     __syncthreads();
     if (tid == 0 && sh.gave_up) *p.status = GDN_ERR_DEVICE_TIMEOUT;
-    if (warp == 0) tmem_dealloc(tbase, 512);
+    if (warp == 1) tmem_dealloc(tbase, 512);
 }
 
 template <typename T, int D>

@@ -51,6 +51,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_pair(const __grid_const
     unsigned char *sm = (unsigned char *)(((uintptr_t)smraw + 1023) & ~(uintptr_t)1023);
     const gdn_window_attention_desc &d = p.d;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) tma_prefetch_map(&a_maps.q), tma_prefetch_map(&a_maps.g), tma_prefetch_map(&b_maps.k), tma_prefetch_map(&b_maps.v);
 
     // ---- the CTA's place; later queries, which see the most, first
     const int units = d.Hq / 2, head0 = 2 * (int)(blockIdx.x % units), hk = head0 / (d.Hq / d.Hk);
@@ -80,6 +81,17 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_pair(const __grid_const
     }
     auto row_at = [&](int it) { return (it < sinks64 ? it : first + it - sinks64) * 64; };
 
+    const int qrow = p.cu ? (int)sp.q0 : 0, krow = p.cu ? (int)sp.k0 : 0;
+    const int qb = p.cu ? 0 : n * a_maps.q_rows, kb = p.cu ? 0 : n * a_maps.k_rows, vb = p.cu ? 0 : n * a_maps.v_rows, gb = p.cu || d.B == 1 ? 0 : n;
+    auto load = [&](int it) {   // the it-th tile's keys and values
+        const int i = it % kStages, r = row_at(it);
+        unsigned char *b1 = sm + L::kBs + i * 2 * L::kB, *b2 = b1 + L::kB;
+        mbar_expect_tx(&sh.full[i], 2 * L::kB);
+        for (int b = 0; b < D / 64; ++b) {
+            tma_load_4d(b1 + b * L::kRowB, &b_maps.k, 64 * b, hk, krow + r, kb, &sh.full[i]);
+            tma_load_4d(b2 + b * L::kRowB, &b_maps.v, 64 * b, hk, krow + r, vb, &sh.full[i]);
+        }
+    };
     if (tid == 0) {
         mbar_init(&sh.a_full, 1);
         for (int i = 0; i < kStages; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1), mbar_init(&sh.fit[i], 2);
@@ -87,8 +99,18 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_pair(const __grid_const
         mbar_init(&sh.acc_full, 1), mbar_init(&sh.drain, 1);
         sh.gave_up = 0;
         mbar_init_fence();
+        if (count > 0) {   // the first copies are on their way while the CTA gets its tensor memory
+            fence_async_smem();
+            mbar_expect_tx(&sh.a_full, 4 * L::kA);
+            for (int s = 0; s < 2; ++s)
+                for (int b = 0; b < D / 64; ++b) {
+                    tma_load_4d(sm + 2 * s * L::kA + b * L::kRowA, &a_maps.q, 64 * b, head0 + s, qrow + row0, qb, &sh.a_full);
+                    tma_load_4d(sm + (2 * s + 1) * L::kA + b * L::kRowA, &a_maps.g, 64 * b, head0 + s, qrow + row0, gb, &sh.a_full);
+                }
+            load(0);
+        }
     }
-    if (warp == 0) tmem_alloc(&sh.tmem, 512);
+    if (warp == 1) tmem_alloc(&sh.tmem, 512);
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
@@ -101,25 +123,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_pair(const __grid_const
     if (warp == 0) {
         // ------------------------------------------------------------ copies
         if (lane == 0 && count > 0) {
-            const int qrow = p.cu ? (int)sp.q0 : 0, krow = p.cu ? (int)sp.k0 : 0;
-            const int qb = p.cu ? 0 : n * a_maps.q_rows, kb = p.cu ? 0 : n * a_maps.k_rows, vb = p.cu ? 0 : n * a_maps.v_rows;
-            const int gb = p.cu || d.B == 1 ? 0 : n;
-            mbar_expect_tx(&sh.a_full, 4 * L::kA);
-            for (int s = 0; s < 2; ++s)
-                for (int b = 0; b < D / 64; ++b) {
-                    tma_load_4d(sm + 2 * s * L::kA + b * L::kRowA, &a_maps.q, 64 * b, head0 + s, qrow + row0, qb, &sh.a_full);
-                    tma_load_4d(sm + (2 * s + 1) * L::kA + b * L::kRowA, &a_maps.g, 64 * b, head0 + s, qrow + row0, gb, &sh.a_full);
-                }
-            int it = 0;
+            int it = 1;
             for (; it < count; ++it) {
-                const int i = it % kStages, r = row_at(it);
-                if (it >= kStages && !wait(&sh.empty[i], (uint32_t)(it / kStages - 1) & 1)) break;
-                unsigned char *b1 = sm + L::kBs + i * 2 * L::kB, *b2 = b1 + L::kB;
-                mbar_expect_tx(&sh.full[i], 2 * L::kB);
-                for (int b = 0; b < D / 64; ++b) {
-                    tma_load_4d(b1 + b * L::kRowB, &b_maps.k, 64 * b, hk, krow + r, kb, &sh.full[i]);
-                    tma_load_4d(b2 + b * L::kRowB, &b_maps.v, 64 * b, hk, krow + r, vb, &sh.full[i]);
-                }
+                if (it >= kStages && !wait(&sh.empty[it % kStages], (uint32_t)(it / kStages - 1) & 1)) break;
+                load(it);
             }
             // what is in flight lands before the CTA leaves
             mbar_wait(&sh.a_full, 0);
@@ -276,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_pair(const __grid_const
     fence_before_sync();
     __syncthreads();
     if (tid == 0 && sh.gave_up) *p.status = GDN_ERR_DEVICE_TIMEOUT;
-    if (warp == 0) tmem_dealloc(tbase, 512);
+    if (warp == 1) tmem_dealloc(tbase, 512);
 }
 
 template <typename T, int D>
