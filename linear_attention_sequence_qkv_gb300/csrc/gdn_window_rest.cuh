@@ -33,7 +33,8 @@ __device__ __forceinline__ float *partial_at(const WindowProblem &p, int64_t slo
     return p.partial + (slot * p.d.Hk + hk) * ((int64_t)p.sink_rows * 2 * D);
 }
 
-// The sinks' gradients: the CTA's own part and the chunks', in order
+// The sinks' gradients: the CTA's own part and the chunks', in order. Bound by the loads' latency: a thread has one sum and eight
+// chunks on their way (one CTA per head and one chunk at a time: 13 us for 14 chunks of 4 sinks of 128 channels, 5 so).
 template <typename T, int D>
 static __global__ void __launch_bounds__(256) window_sink_sums(const __grid_constant__ WindowProblem p) {
     if (*p.status != GDN_OK) return;
@@ -46,11 +47,14 @@ static __global__ void __launch_bounds__(256) window_sink_sums(const __grid_cons
     for (int x = 0; x < t; ++x) slot += rest_chunks(p, sp, x);
     const int rows = min(min(128, d.sinks - t * 128), sp.Lk - t * 128);
     const float *own = partial_at<D>(p, p.rest_slots + (int64_t)n * p.sink_tiles + t, hk);
-    for (int x = threadIdx.x; x < rows * 2 * D; x += 256) {
+    for (int x = blockIdx.y * 256 + threadIdx.x; x < rows * 2 * D; x += gridDim.y * 256) {
         const int r = x / (2 * D), b = x / D & 1, c = x % D;
         if (c >= d.d) continue;
         float s = own[x];
-        for (int i = 0; i < chunks; ++i) s += partial_at<D>(p, slot + i, hk)[x];
+        const float *part = partial_at<D>(p, slot, hk) + x;
+        const int64_t apart = (int64_t)d.Hk * p.sink_rows * 2 * D;
+#pragma unroll 8
+        for (int i = 0; i < chunks; ++i) s += part[i * apart];
         ((T *)(b ? p.dv : p.dk))[((sp.k0 + t * 128 + r) * d.Hk + hk) * d.d + c] = from_f<T>(s);
     }
 }
@@ -60,7 +64,8 @@ cudaError_t launch_window_sink_sums(const WindowProblem &p, cudaStream_t s) {
     if (p.rest_slots == 0) return cudaSuccess;
     const int64_t blocks = (int64_t)p.d.N * p.sink_tiles * p.d.Hk;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    window_sink_sums<T, D><<<(unsigned)blocks, 256, 0, s>>>(p);
+    const unsigned parts = (unsigned)std::min<int64_t>(cdiv64((int64_t)p.sink_rows * 2 * D, 256), 64);
+    window_sink_sums<T, D><<<dim3((unsigned)blocks, parts), 256, 0, s>>>(p);
     return cudaGetLastError();
 }
 
