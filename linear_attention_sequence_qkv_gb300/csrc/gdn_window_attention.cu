@@ -91,7 +91,8 @@ __global__ void __launch_bounds__(1024) window_rest_table(const __grid_constant_
 }
 
 // delta = sum of grad_out * out per query and head, 32 rows (of a token's heads, tokens after one another) per warp step.
-// VEC: rows of whole 16 bytes, shared by the power of two of lanes that they fill; a lane keeps two rows' loads on their way.
+// VEC: rows of whole 16 bytes, shared by the power of two of lanes that they fill; a lane keeps four rows' loads on their way.
+// Bound by HBM (16384 x 16 rows of 128, 134 MB: 34 us).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) window_delta(const __grid_constant__ WindowProblem p, int team) {
     if (*p.status != GDN_OK) return;

@@ -6,7 +6,9 @@
 // over 32 queries of each head of the group. Thread (ty, tx) of 16 x 16 computes the scores
 // of rows 4 ty .. 4 ty + 3 with columns tx, tx + 16, .. (a row's pitch of four words more than
 // a multiple of 32 spreads these over the banks), hands P (dS) over through shared memory and
-// owns channels 4 tx + 64 c of its rows' sums. Bound by shared memory and FMA issue.
+// owns channels 4 tx + 64 c of its rows' sums. Bound by shared memory and FMA issue; small calls
+// by latency: 2 x 100 tokens of 6 heads of 64 in fp32, forward 23 us, gradients 30 us
+// under a profiler.
 #include <algorithm>
 
 #include "gdn_window_rest.cuh"
