@@ -58,9 +58,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
     // 3 KB that start on a multiple of 1024 bytes, so that the tiles behind them do too: together all that a CTA can have
     __shared__ __align__(1024) union {
         BwdShared sh;
-        unsigned char all[3072];
+        unsigned char all[3 * 1024];
     } head_sh;
-    static_assert(sizeof(head_sh) == 3072, "the tiles follow");
+    static_assert(sizeof(head_sh) == 3 * 1024, "the tiles follow");
     BwdShared &sh = head_sh.sh;
     unsigned char *sm = smraw;
     const gdn_window_attention_desc &d = p.d;
