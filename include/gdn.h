@@ -712,7 +712,7 @@ typedef struct {
     int32_t d;           /* channels per head, 1..256 */
     int32_t window;      /* >= 1; at least Tk: plain causal attention */
     int32_t sinks;       /* >= 0 */
-    int32_t slots;       /* cache calls: slots per head, at least sinks + window */
+    int32_t slots;       /* cache calls: slots per head, sinks + window to 2^31 - 2^16 */
     int32_t dtype;       /* gdn_dtype of q, k, v, out, their gradients and the caches */
     float scale;         /* 1/sqrt(d) */
     /* (batch, token) element strides; a token's heads and channels are contiguous */
@@ -766,7 +766,7 @@ int gdn_window_attention_backward(const gdn_window_attention_desc *d, const void
                                   void *workspace, size_t workspace_bytes, gdn_stream_t stream);
 
 /*
- * The cache: per sequence and head `slots` rows of keys and of values,
+ * The cache (Hk at most 65535): per sequence and head `slots` rows of keys and of values,
  * k_cache, v_cache [N][Hk][slots][d] contiguous, whatever the sequence's length. Position
  * p is held in slot p for p < sinks, else in slot sinks + (p - sinks) % (slots - sinks),
  * where it stays until a later position takes the slot over. lengths, int32 [N], counts

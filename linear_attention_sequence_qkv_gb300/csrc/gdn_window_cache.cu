@@ -619,7 +619,7 @@ int check_cache(const gdn_window_attention_desc *d, bool packed) {
     const int rc = window_check_desc(d, packed);
     if (rc != GDN_OK) return rc;
     if (d->slots < (int64_t)d->sinks + d->window) return GDN_ERR_INVALID_ARG;
-    if (d->Hk > 65535) return GDN_ERR_UNSUPPORTED;
+    if (d->Hk > 65535 || d->slots > 0x7fffffff - 65535) return GDN_ERR_UNSUPPORTED;   // keys are counted in groups, in 32 bits
     return GDN_OK;
 }
 

@@ -149,3 +149,12 @@ def test_python_functions_refuse_what_the_kernels_would_trust(lib):
                  lambda: gdn.window_cache_write(k, k, cache), lambda: gdn.window_attention_step(q[:, :1], k[:, :1], k[:, :1], cache)):
         with pytest.raises((ValueError, RuntimeError, AssertionError)):   # CPU tensors: no fallback
             call()
+
+
+def test_caches_whose_keys_32_bits_do_not_count(lib):
+    """Groups of 16 keys are counted from the keys in 32 bits, which must have room for the last group's rounding up."""
+    d = gdn.gdn_window_attention_desc_init(1, 1, 1, 0, 1, 1, 8, 5, 2, gdn.GDN_BF16)
+    for slots, want in ((2 ** 31 - 2 ** 16, WORKSPACE), (2 ** 31 - 2 ** 16 + 1, UNSUPPORTED), (2 ** 31 - 1, UNSUPPORTED)):
+        d.slots = slots
+        assert lib.gdn_window_attention_step(ctypes.byref(d), *[FAKE] * 7, None, 0, None) == want
+        assert lib.gdn_window_cache_write(ctypes.byref(d), FAKE, FAKE, None, FAKE, FAKE, FAKE, None, 0, None) == want
