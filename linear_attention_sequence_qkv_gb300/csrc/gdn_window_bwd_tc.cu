@@ -75,19 +75,18 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
     const int group = d.Hq / d.Hk;
     const bool rest = KEYS && blockIdx.x < rest_blocks;
     const int64_t block = rest ? blockIdx.x : blockIdx.x - rest_blocks;
-    const int unit = (int)(block % units);                 // keys: head of k and v; queries: head of q
-    const int64_t slot = block / units;
+    const int slot = (int)((uint32_t)block / (uint32_t)units), unit = (int)block - slot * units;   // unit: head of k and v (queries: of q)
     int n, tile, chunk = 0;
     const int32_t *table = rest ? p.rest_off : KEYS ? p.k_tiles : p.q_tiles;
     if (p.cu) {
         const int32_t status = *p.status, tiles = table[d.N];   // on their way with the search's
         n = warp_upper_index(table, d.N, slot);
         if (status == GDN_ERR_DEVICE_SEQLENS || slot >= tiles) return;
-        tile = (int)(slot - table[n]);
+        tile = slot - table[n];
     } else {
         const int per = rest ? p.rest_per : ((KEYS ? d.Tk : d.Tq) + 127) / 128;
-        n = (int)(slot / per);
-        tile = (int)(slot - (int64_t)n * per);
+        n = slot / per;
+        tile = slot - n * per;
     }
     const WindowSpan sp = window_span(p, n);
     const int past = sp.Lk - sp.Lq;
@@ -416,9 +415,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
         const int w0 = r & ~31, heads = KEYS ? d.Hk : d.Hq;
         T *out = (T *)(KEYS ? (half ? p.dv : p.dk) : p.dq) + (((KEYS ? sp.k0 : sp.q0) + row0 + w0) * heads + unit) * (int64_t)d.d;
         const int n_rows = ok ? max(0, min(32, rows - w0)) : 0;
-        for (int x = lane; x < n_rows * (kCols / 8); x += 32) {
+#pragma unroll
+        for (int x = lane; x < 32 * (kCols / 8); x += 32) {
             const int q = x / (kCols / 8), ch = c0 / 8 + x % (kCols / 8);
-            if (8 * ch < d.d && w0 + q >= apart)
+            if (q < n_rows && 8 * ch < d.d && w0 + q >= apart)
                 *(uint4 *)(out + (int64_t)q * heads * d.d + 8 * ch) =
                     *(const uint4 *)(stage + (ch >> 3) * L::kRow + (w0 + q) * 128 + (((ch & 7) ^ ((w0 + q) & 7)) << 4));
         }

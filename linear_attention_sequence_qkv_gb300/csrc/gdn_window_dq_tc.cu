@@ -54,18 +54,17 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_pair(const __grid_const
     if (tid == 0) tma_prefetch_map(&a_maps.q), tma_prefetch_map(&a_maps.g), tma_prefetch_map(&b_maps.k), tma_prefetch_map(&b_maps.v);
 
     // ---- the CTA's place; later queries, which see the most, first
-    const int units = d.Hq / 2, head0 = 2 * (int)(blockIdx.x % units), hk = head0 / (d.Hq / d.Hk);
-    const int64_t slot = blockIdx.x / units;
+    const int units = d.Hq / 2, slot = (int)blockIdx.x / units, head0 = 2 * ((int)blockIdx.x - slot * units), hk = head0 / (d.Hq / d.Hk);
     int n, tile;
     if (p.cu) {
         const int32_t status = *p.status, tiles = p.q_tiles[d.N];   // on their way with the search's
         n = warp_upper_index(p.q_tiles, d.N, slot);
         if (status == GDN_ERR_DEVICE_SEQLENS || slot >= tiles) return;
-        tile = p.q_tiles[n + 1] - 1 - (int)slot;
+        tile = p.q_tiles[n + 1] - 1 - slot;
     } else {
         const int per = (d.Tq + 127) / 128;
-        n = (int)(slot / per);
-        tile = per - 1 - (int)(slot - (int64_t)n * per);
+        n = slot / per;
+        tile = per - 1 - (slot - n * per);
     }
     const WindowSpan sp = window_span(p, n);
     const int past = sp.Lk - sp.Lq, row0 = tile * 128, rows = min(128, sp.Lq - row0);
@@ -273,9 +272,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_pair(const __grid_const
         __syncwarp();
         const int w0 = r & ~31, n_rows = ok ? max(0, min(32, rows - w0)) : 0;
         T *out = (T *)p.dq + ((sp.q0 + row0 + w0) * d.Hq + head) * (int64_t)d.d;
-        for (int x = lane; x < n_rows * (D / 8); x += 32) {
+#pragma unroll
+        for (int x = lane; x < 32 * (D / 8); x += 32) {
             const int q = x / (D / 8), ch = x % (D / 8);
-            if (8 * ch < d.d)
+            if (q < n_rows && 8 * ch < d.d)
                 *(uint4 *)(out + (int64_t)q * d.Hq * d.d + 8 * ch) =
                     *(const uint4 *)(stage + (ch >> 3) * L::kRowA + (w0 + q) * 128 + (((ch & 7) ^ ((w0 + q) & 7)) << 4));
         }

@@ -86,19 +86,18 @@ __global__ void __launch_bounds__(kThreads, 1) window_forward_tc(const __grid_co
     if (!p.cu && blockIdx.x == 0 && tid == 0) *p.status = GDN_OK;
 
     // ---- the CTA's place: later tiles of queries, which see the most keys, first
-    const int unit = (int)(blockIdx.x % units);
-    const int64_t slot = blockIdx.x / units;
+    const int slot = (int)(blockIdx.x / units), unit = (int)blockIdx.x - slot * units;
     const int rows_per = pair_heads ? 128 : 256;
     int n, qt;
     if (p.cu) {
         const int32_t status = *p.status, tiles = p.q_tiles[d.N];   // on their way with the search's
         n = warp_upper_index(p.q_tiles, d.N, slot);
         if (status != GDN_OK || slot >= tiles) return;
-        qt = (int)(p.q_tiles[n + 1] - 1 - slot);
+        qt = p.q_tiles[n + 1] - 1 - slot;
     } else {
         const int per = (d.Tq + rows_per - 1) / rows_per;
-        n = (int)(slot / per);
-        qt = per - 1 - (int)(slot - (int64_t)n * per);
+        n = slot / per;
+        qt = per - 1 - (slot - n * per);
     }
     const WindowSpan sp = window_span(p, n);
     const int past = sp.Lk - sp.Lq;
@@ -405,9 +404,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_forward_tc(const __grid_co
         __syncwarp();
         const int row0 = r & ~31, rows = ok ? min(32, me.rows - row0) : 0;
         T *out = (T *)p.out + ((sp.q0 + me.i0 + row0) * d.Hq + me.head) * d.d;
-        for (int x = lane; x < rows * (D / 8); x += 32) {
+#pragma unroll
+        for (int x = lane; x < 32 * (D / 8); x += 32) {
             const int q = x / (D / 8), ch = x % (D / 8);
-            if (8 * ch < d.d)
+            if (q < rows && 8 * ch < d.d)
                 *(uint4 *)(out + (int64_t)q * d.Hq * d.d + 8 * ch) =
                     *(const uint4 *)(stage + (ch >> 3) * L::kRow + (row0 + q) * 128 + (((ch & 7) ^ ((row0 + q) & 7)) << 4));
         }
