@@ -188,28 +188,39 @@ template <typename T, int V> union Vec {
 constexpr int kThreads = 256;
 constexpr int kFlight = 4;   // heads whose loads are on their way at once
 
-// A lane's place in its team: K vectors of V channels, lane + k team of them; for each the channel it starts at, what it
-// does in the turn, and for the half layout the lane and vector that hold the other half of its pairs
-template <int V, int K, bool HALF> struct Place {
-    int c[K], other[K];      // first channel (-1: none); the partner's vector
-    bool turned[K], upper[K];
+// How channels turn: pairs of neighbours, halves, or halves of an odd number of segments
+enum Turn { kNeighbours, kHalves, kOddHalves };
+
+// A lane's place in its team: K vectors of V channels, lane + k team of them; for each the channel it starts at, and for its
+// segments of SEG channels what they do in the turn and, for the half layouts, the vector that holds the other half of their
+// pairs. Eight 16-bit channels are two segments, so that half the turned channels need only be a multiple of four: with an odd
+// number of segments the other half of one lies in the other of its vector (131072 tokens of 8 heads of 96, 24 turned: 160 us,
+// with vectors of four channels 213; where halves are whole vectors segments would cost up to 8 %).
+template <typename T, int V, int K, Turn M> struct Place {
+    static constexpr int S = sizeof(T) == 2 && V == 8 && M != kHalves ? 2 : 1, SEG = V / S;
+    int c[K], other[K][S];   // first channel (-1: none); the partner's vector
+    bool turned[K][S], upper[K][S];
     __device__ __forceinline__ Place(const gdn_rotary_desc &d, int lane, int team) {
-        const int off = d.rot / 2 / V;
+        const int off = d.rot / 2 / SEG;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int v = k * team + lane;
             c[k] = v * V < d.d ? v * V : -1;
-            turned[k] = v * V < d.rot;
-            upper[k] = HALF && v >= off;
-            other[k] = !HALF || !turned[k] ? v : upper[k] ? v - off : v + off;
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const int g = v * S + s;
+                turned[k][s] = g * SEG < d.rot;
+                upper[k][s] = M != kNeighbours && g >= off;
+                other[k][s] = M == kNeighbours || !turned[k][s] ? v : (upper[k][s] ? g - off : g + off) / S;
+            }
         }
     }
 };
 // Pairs of neighbouring channels, in one instruction where the SM has one for two. A turn is y = x A + o B with o the other
 // half's channels (half layout) or the pair swapped, and A, B of the lane's pairs at a position, the attention factor among
 // them: (cos, cos) and (-+sin, -+sin), or (cos, cos) and (-sin, sin); ones and zeros where nothing turns.
-template <typename T, int V, int K, bool HALF>
-__device__ __forceinline__ void turns_of(const NormRotaryProblem &p, const Place<V, K, HALF> &at, int64_t pos, float2 (&A)[K][V / 2], float2 (&B)[K][V / 2]) {
+template <typename T, int V, int K, Turn M>
+__device__ __forceinline__ void turns_of(const NormRotaryProblem &p, const Place<T, V, K, M> &at, int64_t pos, float2 (&A)[K][V / 2], float2 (&B)[K][V / 2]) {
     const gdn_rotary_desc &d = p.n.rotary;
     auto turn = [&](int pair) {
         const float2 cs = cos_sin<sizeof(T) == 2>(pos, p.turns[pair]);
@@ -220,12 +231,13 @@ __device__ __forceinline__ void turns_of(const NormRotaryProblem &p, const Place
 #pragma unroll
         for (int e = 0; e < V / 2; ++e) {
             A[k][e] = splat2(1.0f), B[k][e] = splat2(0.0f);
-            if (!at.turned[k]) continue;
-            if (HALF) {
-                const int pair = at.c[k] + 2 * e - (at.upper[k] ? d.rot / 2 : 0);
+            const int s = 2 * e / at.SEG;
+            if (!at.turned[k][s]) continue;
+            if (M != kNeighbours) {
+                const int pair = at.c[k] + 2 * e - (at.upper[k][s] ? d.rot / 2 : 0);
                 const float2 a = turn(pair), b = turn(pair + 1);
                 A[k][e] = make_float2(a.x, b.x);
-                B[k][e] = at.upper[k] ? make_float2(a.y, b.y) : make_float2(-a.y, -b.y);
+                B[k][e] = at.upper[k][s] ? make_float2(a.y, b.y) : make_float2(-a.y, -b.y);
             } else {
                 const float2 a = turn(at.c[k] / 2 + e);
                 A[k][e] = splat2(a.x);
@@ -246,17 +258,19 @@ __device__ __forceinline__ float2 swapped(float2 x) { return make_float2(x.y, x.
 __device__ __forceinline__ float2 weights_at(const void *w, int dtype, int c) { return make_float2(weight_at(w, dtype, c), weight_at(w, dtype, c + 1)); }
 
 // the other half's vectors
-template <typename T, int V, int K, bool HALF>
-__device__ __forceinline__ void partners(const Place<V, K, HALF> &at, const Vec<T, V> (&x)[K], Vec<T, V> (&o)[K], int team) {
+template <typename T, int V, int K, Turn M>
+__device__ __forceinline__ void partners(const Place<T, V, K, M> &at, const Vec<T, V> (&x)[K], Vec<T, V> (&o)[K], int team) {
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int w = 0; w < (int)(V * sizeof(T) / 4); ++w) {
+            constexpr int S = Place<T, V, K, M>::S;
+            const int other = at.other[k][S == 2 ? w / 2 : 0];
             uint32_t got = 0;
 #pragma unroll
             for (int q = 0; q < K; ++q) {
-                const uint32_t v = __shfl_sync(0xffffffffu, x[q].w[w], at.other[k] & (team - 1), team);
-                if (K == 1 || at.other[k] / team == q) got = v;
+                const uint32_t v = __shfl_sync(0xffffffffu, x[q].w[S == 2 ? w ^ 2 : w], other & (team - 1), team);
+                if (K == 1 || other / team == q) got = v;
             }
             o[k].w[w] = got;
         }
@@ -284,7 +298,7 @@ __device__ __forceinline__ Item item_at(const gdn_rotary_desc &d, int64_t i, int
     return x;
 }
 
-template <typename T, int V, int K, int TEAM, bool HALF>
+template <typename T, int V, int K, int TEAM, Turn M>
 __global__ void __launch_bounds__(kThreads, K == 1 ? 3 : 1) norm_rotary_vectors(const __grid_constant__ NormRotaryProblem p, int parts, int per) {
     const gdn_rotary_desc &d = p.n.rotary;
     const bool ok = p.cu == nullptr || seqlens_ok(p.cu, d.N, d.T);
@@ -293,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, K == 1 ? 3 : 1) norm_rotary_vectors(
     const int lane = threadIdx.x % TEAM;
     int part;
     const Item it = item_at(d, (int64_t)blockIdx.x * (kThreads / TEAM) + threadIdx.x / TEAM, parts, part);
-    const Place<V, K, HALF> at(d, lane, TEAM);
+    const Place<T, V, K, M> at(d, lane, TEAM);
     const int h0 = part * per, h1 = it.ok ? min(h0 + per, d.Hq + d.Hk) : h0;   // the lanes of a warp stay together: empty runs loop too
     constexpr int NP = V / 2;
     const int64_t pos = it.ok ? rotary_position(d, p.pos, p.cu, p.off, it.row, it.t) : 0;
@@ -308,14 +322,15 @@ __global__ void __launch_bounds__(kThreads, K == 1 ? 3 : 1) norm_rotary_vectors(
         // the weights go into the turn: y = rstd (x A w + o B w'). It is computed again for k: kept beside the weighted one it
         // takes registers of the loads on their way (32768 tokens of 48 heads of 128: 155 us, 141 so).
         float2 A[K][NP], B[K][NP], Aw[K][NP], Bw[K][NP];
-        turns_of<T, V, K, HALF>(p, at, pos, A, B);
+        turns_of<T, V, K, M>(p, at, pos, A, B);
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int e = 0; e < NP; ++e) {
                 const float2 own = at.c[k] >= 0 ? weights_at(w, p.n.weight_dtype, at.c[k] + 2 * e) : splat2(0.0f);
                 Aw[k][e] = mul2(A[k][e], own);
-                if (HALF) Bw[k][e] = at.turned[k] ? mul2(B[k][e], weights_at(w, p.n.weight_dtype, at.other[k] * V + 2 * e)) : splat2(0.0f);
+                const int s = 2 * e / at.SEG, half = at.upper[k][s] ? -d.rot / 2 : d.rot / 2;
+                if (M != kNeighbours) Bw[k][e] = at.turned[k][s] ? mul2(B[k][e], weights_at(w, p.n.weight_dtype, at.c[k] + 2 * e + half)) : splat2(0.0f);
                 else Bw[k][e] = mul2(B[k][e], swapped(own));
             }
         for (int r0 = 0; r0 < most; r0 += kFlight) {
@@ -341,14 +356,14 @@ __global__ void __launch_bounds__(kThreads, K == 1 ? 3 : 1) norm_rotary_vectors(
                     }
                 const float2 rstd = splat2(rsqrtf(team_sum<TEAM>(s2.x + s2.y) / d.d + p.n.eps));
                 Vec<T, V> o[K], y[K];
-                if (HALF) partners<T, V, K, HALF>(at, x[j], o, TEAM);
+                if (M != kNeighbours) partners<T, V, K, M>(at, x[j], o, TEAM);
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
 #pragma unroll
                     for (int e = 0; e < NP; ++e) {
                         float2 z = mul2(xs[k][e], Aw[k][e]);
                         // (a partner that is not finite must not reach what does not turn)
-                        if (!HALF || at.turned[k]) z = fma2(HALF ? pair_of<T, V>(o[k], e) : swapped(xs[k][e]), Bw[k][e], z);
+                        if (M == kNeighbours || at.turned[k][2 * e / at.SEG]) z = fma2(M != kNeighbours ? pair_of<T, V>(o[k], e) : swapped(xs[k][e]), Bw[k][e], z);
                         set_pair<T, V>(y[k], e, mul2(z, rstd));
                     }
                     if (r0 + j < runs && at.c[k] >= 0) *(decltype(y[k].raw) *)(dst + (int64_t)(a + r0 + j - first) * d.d + at.c[k]) = y[k].raw;
@@ -360,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, K == 1 ? 3 : 1) norm_rotary_vectors(
 
 // Both tensors of kFlight heads are on their way at once: with two heads' 4474 GB/s instead of 5480 (32768 tokens of 48 heads of
 // 128, 16 bits), with six, or a third CTA per SM, the registers spill (5092 and 3455 GB/s).
-template <typename T, int V, int K, int TEAM, bool HALF>
+template <typename T, int V, int K, int TEAM, Turn M>
 __global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) norm_rotary_vectors_backward(const __grid_constant__ NormRotaryProblem p, int parts, int per) {
     extern __shared__ float sm[];   // [teams][2][d]
     const gdn_rotary_desc &d = p.n.rotary;
@@ -369,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) norm_rotary_vectors_
     if (!ok) return;
     constexpr int kTeams = kThreads / TEAM;
     const int lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
-    const Place<V, K, HALF> at(d, lane, TEAM);
+    const Place<T, V, K, M> at(d, lane, TEAM);
     constexpr int NP = V / 2;
     float2 acc[2][K][NP];
 #pragma unroll
@@ -384,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) norm_rotary_vectors_
         const Item it = item_at(d, i0 + team, parts, part);
         const int h0 = part * per, h1 = it.ok ? min(h0 + per, d.Hq + d.Hk) : h0;
         float2 A[K][NP], B[K][NP];
-        turns_of<T, V, K, HALF>(p, at, it.ok ? rotary_position(d, p.pos, p.cu, p.off, it.row, it.t) : 0, A, B);
+        turns_of<T, V, K, M>(p, at, it.ok ? rotary_position(d, p.pos, p.cu, p.off, it.row, it.t) : 0, A, B);
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             const void *w = which ? p.kw : p.qw;
@@ -417,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) norm_rotary_vectors_
                 for (int j = 0; j < kFlight; ++j) {
                     if (r0 + j >= most) break;
                     Vec<T, V> o[K];
-                    if (HALF) partners<T, V, K, HALF>(at, g[j], o, TEAM);
+                    if (M != kNeighbours) partners<T, V, K, M>(at, g[j], o, TEAM);
                     float2 ss = splat2(0.0f), st = splat2(0.0f), dz[K][NP], xs[K][NP];
 #pragma unroll
                     for (int k = 0; k < K; ++k)
@@ -427,8 +442,8 @@ __global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) norm_rotary_vectors_
                             xs[k][e] = pair_of<T, V>(x[j][k], e);
                             dz[k][e] = mul2(gv, A[k][e]);
                             // the turn back: B the other way round
-                            if (!HALF || at.turned[k])
-                                dz[k][e] = fma2(HALF ? pair_of<T, V>(o[k], e) : swapped(gv), make_float2(-B[k][e].x, -B[k][e].y), dz[k][e]);
+                            if (M == kNeighbours || at.turned[k][2 * e / at.SEG])
+                                dz[k][e] = fma2(M != kNeighbours ? pair_of<T, V>(o[k], e) : swapped(gv), make_float2(-B[k][e].x, -B[k][e].y), dz[k][e]);
                             ss = fma2(xs[k][e], xs[k][e], ss);
                             st = fma2(mul2(dz[k][e], wo[k][e]), xs[k][e], st);
                         }
@@ -482,8 +497,8 @@ size_t bwd_bytes(const gdn_rotary_desc &d) { return kStatusBytes + (size_t)bwd_c
 bool fits(const NormRotaryProblem &p, int v) {
     const gdn_rotary_desc &d = p.n.rotary;
     const size_t bytes = v * act_size(d.dtype);
-    const int width = d.layout == GDN_ROTARY_HALF ? d.rot / 2 : d.rot;
-    if (bytes < 4 || bytes > 16 || v < 2 || width % v || d.d % v || d.d / v > 64) return false;
+    const int width = d.layout == GDN_ROTARY_HALF ? d.rot / 2 : d.rot;   // made of whole segments (Place)
+    if (bytes < 4 || bytes > 16 || v < 2 || width % (v == 8 ? 4 : v) || d.d % v || d.d / v > 64) return false;
     const void *ptrs[] = {p.q, p.qo, p.k, p.ko, p.dq, p.dk};
     for (const void *x : ptrs)
         if (!ptr_aligned(x, bytes)) return false;
@@ -500,7 +515,7 @@ int parts_of(const gdn_rotary_desc &d, int team) {
     return (int)std::min<int64_t>(d.Hq + d.Hk, cdiv64(teams, ntok));
 }
 
-template <typename T, int V, int K, int TEAM, bool HALF>
+template <typename T, int V, int K, int TEAM, Turn M>
 cudaError_t launch_vectors(NormRotaryProblem &p, bool backward, cudaStream_t s) {
     const gdn_rotary_desc &d = p.n.rotary;
     constexpr int kTeams = kThreads / TEAM;
@@ -508,21 +523,21 @@ cudaError_t launch_vectors(NormRotaryProblem &p, bool backward, cudaStream_t s) 
     const int64_t blocks = std::max<int64_t>(cdiv64((int64_t)d.B * d.T * parts, kTeams), 1);
     if (!backward) {
         if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-        norm_rotary_vectors<T, V, K, TEAM, HALF><<<(unsigned)blocks, kThreads, 0, s>>>(p, parts, per);
+        norm_rotary_vectors<T, V, K, TEAM, M><<<(unsigned)blocks, kThreads, 0, s>>>(p, parts, per);
         return cudaGetLastError();
     }
     const size_t smem = (size_t)kTeams * 2 * d.d * 4;   // at most 32 KB: a team's channels are at most 16 of its lanes' bytes
     p.ctas = (int)std::min<int64_t>({blocks, p.ctas, kVectorCtas});
-    norm_rotary_vectors_backward<T, V, K, TEAM, HALF><<<(unsigned)p.ctas, kThreads, smem, s>>>(p, parts, per);
+    norm_rotary_vectors_backward<T, V, K, TEAM, M><<<(unsigned)p.ctas, kThreads, smem, s>>>(p, parts, per);
     return cudaGetLastError();
 }
-template <typename T, int V, bool HALF>
+template <typename T, int V, Turn M>
 cudaError_t launch_team(NormRotaryProblem &p, bool backward, cudaStream_t s) {
     const int nv = p.n.rotary.d / V;
-    if (nv > 32) return launch_vectors<T, V, 2, 32, HALF>(p, backward, s);
-    if (nv > 16) return launch_vectors<T, V, 1, 32, HALF>(p, backward, s);
-    if (nv > 8) return launch_vectors<T, V, 1, 16, HALF>(p, backward, s);
-    return launch_vectors<T, V, 1, 8, HALF>(p, backward, s);
+    if (nv > 32) return launch_vectors<T, V, 2, 32, M>(p, backward, s);
+    if (nv > 16) return launch_vectors<T, V, 1, 32, M>(p, backward, s);
+    if (nv > 8) return launch_vectors<T, V, 1, 16, M>(p, backward, s);
+    return launch_vectors<T, V, 1, 8, M>(p, backward, s);
 }
 template <typename T>
 cudaError_t launch(NormRotaryProblem &p, bool backward, cudaStream_t s) {
@@ -531,9 +546,11 @@ cudaError_t launch(NormRotaryProblem &p, bool backward, cudaStream_t s) {
     cudaError_t e = cudaSuccess;
     bool done = false;
     if constexpr (sizeof(T) == 2)
-        if (fits(p, 8)) e = half ? launch_team<T, 8, true>(p, backward, s) : launch_team<T, 8, false>(p, backward, s), done = true;
-    if (!done && fits(p, 4)) e = half ? launch_team<T, 4, true>(p, backward, s) : launch_team<T, 4, false>(p, backward, s), done = true;
-    if (!done && fits(p, 2)) e = half ? launch_team<T, 2, true>(p, backward, s) : launch_team<T, 2, false>(p, backward, s), done = true;
+        if (fits(p, 8))
+            e = !half ? launch_team<T, 8, kNeighbours>(p, backward, s)
+                : d.rot % 16 ? launch_team<T, 8, kOddHalves>(p, backward, s) : launch_team<T, 8, kHalves>(p, backward, s), done = true;
+    if (!done && fits(p, 4)) e = half ? launch_team<T, 4, kHalves>(p, backward, s) : launch_team<T, 4, kNeighbours>(p, backward, s), done = true;
+    if (!done && fits(p, 2)) e = half ? launch_team<T, 2, kHalves>(p, backward, s) : launch_team<T, 2, kNeighbours>(p, backward, s), done = true;
     if (!done && !backward) {
         const int64_t blocks = std::min<int64_t>(std::max<int64_t>(cdiv64(heads_of(d), kWarps), 1), 16 * kSms);
         norm_rotary_rows<T><<<(unsigned)blocks, 32 * kWarps, (size_t)kWarps * d.d * 4, s>>>(p);

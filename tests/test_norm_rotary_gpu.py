@@ -156,3 +156,25 @@ def test_zero_rows_and_non_finite_heads_stay_apart(dev):
     assert got.view(6, 4, 128)[3, 1].isnan().all()
     same[3, 1] = True
     assert bool(same.all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("B,T,Hq,Hk,d,rot", [(2, 37, 6, 2, 96, 24), (1, 50, 3, 1, 80, 40), (1, 9, 2, 2, 64, 8), (2, 21, 5, 0, 256, 24),
+                                             (1, 18, 2, 1, 512, 72), (1, 13, 3, 2, 16, 8), (1, 11, 1, 1, 128, 120), (1, 12, 2, 1, 8, 8)])
+def test_halves_that_are_an_odd_number_of_segments(dev, B, T, Hq, Hk, d, rot, layout, dtype):
+    """Half of the turned channels is a multiple of four but not of eight: partners lie across vectors of eight channels."""
+    test_rows(dev, B, T, Hq, Hk, d, rot, layout, dtype)
+
+
+@pytest.mark.parametrize("poison", [float("nan"), float("inf")])
+def test_a_channel_that_does_not_turn_keeps_to_its_head(dev, poison):
+    """A value that is not finite reaches its own head alone (the norm takes it everywhere there), across segments too."""
+    s = make(dev, 1, 8, 4, 2, 96, "bf16")
+    table = gdn.rotary_table(24, device=dev)
+    clean = gdn.norm_rotary(s["q"], s["k"], s["qw"], s["kw"], table, d=96, rot=24)
+    s["q"][0, 3, 96 + 13] = poison
+    got = gdn.norm_rotary(s["q"], s["k"], s["qw"], s["kw"], table, d=96, rot=24)
+    keep = torch.ones_like(clean[0], dtype=torch.bool)
+    keep[0, 3, 96:192] = False
+    assert torch.equal(got[0][keep], clean[0][keep]) and torch.equal(got[1], clean[1])
