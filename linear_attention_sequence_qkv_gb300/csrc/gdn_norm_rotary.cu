@@ -447,7 +447,8 @@ __global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) norm_rotary_vectors_
                             ss = fma2(xs[k][e], xs[k][e], ss);
                             st = fma2(mul2(dz[k][e], wo[k][e]), xs[k][e], st);
                         }
-                    const float rstd = rsqrtf(team_sum<TEAM>(ss.x + ss.y) / d.d + p.n.eps);
+                    // a team whose run is shorter than its warp's has no head here (and eps may be 0: no 0 x inf into the sums)
+                    const float sum = team_sum<TEAM>(ss.x + ss.y), rstd = r0 + j < runs ? rsqrtf(sum / d.d + p.n.eps) : 0.0f;
                     const float2 r2 = splat2(rstd), mean = splat2(-rstd * team_sum<TEAM>(st.x + st.y) / d.d);   // of t xh
 #pragma unroll
                     for (int k = 0; k < K; ++k) {
