@@ -700,7 +700,8 @@ int gdn_norm_rotary_backward(const gdn_norm_rotary_desc *d, const void *q, const
  * A query that sees nothing (p < 0, where Lq > Lk) gets out = 0 and lse = -inf.
  * Scores, softmax statistics and every sum are fp32; with 16-bit types the tensor-core
  * kernels round P, and in the backward P and the scores' gradients, to that type as
- * operands of their products. Results are run-to-run identical. What a query does not
+ * operands of their products, fp16 ones times powers of two that keep them in its range
+ * (in the backward by the largest finite rows of grad_out and v of a sequence and head of k). Results are run-to-run identical. What a query does not
  * see has no influence on its output, also where it is infinite or NaN; in the backward
  * this holds between sequences (inside one, a NaN may reach neighbouring gradients).
  */

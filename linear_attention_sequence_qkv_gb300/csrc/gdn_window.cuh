@@ -18,6 +18,8 @@ struct WindowProblem {
     void *out, *dq, *dk, *dv;
     float *lse;                 // forward: written or null; backward: read
     float *delta;               // [Hq][B*Tq] sums of grad_out * out
+    uint32_t *norms;            // backward on tensor cores, fp16 (else null): [2][N][Hk] the largest squared 2-norms of rows of
+                                // grad_out (of a group's heads) and of v that are finite, as bits (gdn_window_tc.cuh)
     int32_t *status;
     int32_t *q_tiles, *k_tiles; // packed: [N+1] tiles of the sequences before n, by queries and by keys
     int wait_immediate;

@@ -4,6 +4,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "gdn_window_rest.cuh"
 #include "gdn_window_tc.cuh"
@@ -14,6 +15,8 @@ namespace {
 // Packed offsets checked, and the tiles of the sequences before each one counted
 __global__ void __launch_bounds__(1024) window_tables_kernel(const __grid_constant__ WindowProblem p, int q_tile, int k_tile) {
     const gdn_window_attention_desc &d = p.d;
+    if (p.norms)
+        for (int64_t i = threadIdx.x; i < 2 * (int64_t)d.N * d.Hk; i += blockDim.x) p.norms[i] = 0;
     if (p.cu == nullptr) {
         if (threadIdx.x == 0) *p.status = GDN_OK;
         return;
@@ -90,59 +93,194 @@ __global__ void __launch_bounds__(1024) window_rest_table(const __grid_constant_
     if (threadIdx.x == 0) p.rest_off[p.d.N] = before;
 }
 
-// delta = sum of grad_out * out per query and head, 32 rows (of a token's heads, tokens after one another) per warp step.
-// VEC: rows of whole 16 bytes, shared by the power of two of lanes that they fill; a lane keeps four rows' loads on their way.
-// Bound by HBM (16384 x 16 rows of 128, 134 MB: 34 us).
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) window_delta(const __grid_constant__ WindowProblem p, int team) {
+// fp16's norms (gdn_window_tc.cuh): the largest squared norms of a CTA's rows, per sequence and head of keys, go through shared
+// memory where its range of tokens has few of them, then into the call's words. A word is read before it is raised, so that few
+// CTAs end in atomics; the largest does not depend on their order. Rows that are not finite are passed over.
+constexpr int kTable = 1024;
+constexpr float kFinite = 3.402823466e38f;
+struct RowNorms {
+    uint32_t *words, *table;    // the call's [N][Hk], the CTA's
+    const int32_t *cu;
+    int N, T, Hk, n0, n1;       // the sequences of the CTA's tokens
+    // all threads call it, as they do flush
+    __device__ __forceinline__ RowNorms(const WindowProblem &p, bool is_v, uint32_t *sm, int64_t first, int64_t last)
+        : words(p.norms + (is_v ? (int64_t)p.d.N * p.d.Hk : 0)), table(sm), cu(p.cu ? (is_v ? p.cuk : p.cu) : nullptr), N(p.d.N),
+          T(is_v ? p.d.Tk : p.d.Tq), Hk(p.d.Hk) {
+        n0 = of(first, 0, N), n1 = of(last, n0, N);
+        if ((int64_t)(n1 - n0 + 1) * Hk > kTable) table = nullptr;
+        else
+            for (int x = threadIdx.x; x < (n1 - n0 + 1) * Hk; x += blockDim.x) table[x] = 0;
+        __syncthreads();
+    }
+    __device__ __forceinline__ int of(int64_t tok, int lo, int hi) const { return cu ? lo + upper_index(cu + lo, hi - lo, tok) : (int)(tok / T); }
+    __device__ __forceinline__ void raise(uint32_t *to, uint32_t bits) const {
+        if (bits > __ldcg(to)) atomicMax(to, bits);
+    }
+    __device__ __forceinline__ void add(int64_t tok, int hk, float squared) const {
+        if (!(squared <= kFinite)) return;
+        const int n = n0 == n1 ? n0 : of(tok, n0, n1 + 1);
+        if (table) atomicMax(&table[(n - n0) * Hk + hk], __float_as_uint(squared));
+        else raise(words + (int64_t)n * Hk + hk, __float_as_uint(squared));
+    }
+    __device__ __forceinline__ void flush() const {
+        __syncthreads();
+        if (table)
+            for (int x = threadIdx.x; x < (n1 - n0 + 1) * Hk; x += blockDim.x)
+                if (table[x]) raise(words + (int64_t)n0 * Hk + x, table[x]);
+        __syncthreads();
+    }
+};
+
+// A row's token and head, a fixed number of rows on at a time (64-bit divisions would be most of a row's instructions)
+struct RowAt {
+    int64_t tok, by_tok;
+    int head, by_head, heads;
+    __device__ __forceinline__ RowAt(int64_t i, int step, int heads_) : tok(i / heads_), by_tok(step / heads_), by_head(step % heads_), heads(heads_) {
+        head = (int)(i - tok * heads);
+    }
+    __device__ __forceinline__ void next() {
+        tok += by_tok, head += by_head;
+        if (head >= heads) head -= heads, ++tok;
+    }
+};
+
+// delta = sum of grad_out * out per query and head, 32 rows (of a token's heads, tokens after one another) per warp step, each
+// CTA a range of `len` rows. VEC: rows of whole 16 bytes, shared by the power of two of lanes that they fill, ROW of them per lane; a
+// lane keeps four rows' loads on their way. Bound by HBM (32768 x 32 rows of 128, 537 MB: 96 us). For fp16 on the tensor cores
+// norms are taken besides, and a CTA looks through `v_len` rows of v: 134 MB more, 150 us.
+template <typename T, bool VEC, int ROW>
+__global__ void __launch_bounds__(256, 3) window_delta(const __grid_constant__ WindowProblem p, int team, int64_t len, int64_t v_len) {
     if (*p.status != GDN_OK) return;
     const gdn_window_attention_desc &d = p.d;
-    const int lane = threadIdx.x & 31;
+    constexpr bool kNorms = VEC && ROW == 1 && std::is_same<T, __half>::value;
+    __shared__ uint32_t table[kNorms ? kTable : 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t ntok = (int64_t)d.B * d.Tq, total = ntok * d.Hq;
     const T *o = (const T *)p.out_in, *g = (const T *)p.dout;
-    auto put = [&](int64_t i, float s) {
-        const int64_t tok = i / d.Hq;
-        p.delta[(i - tok * d.Hq) * ntok + tok] = s;
-    };
     if (!VEC) {
-        for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += (int64_t)gridDim.x * 8) {
+        for (int64_t i = (int64_t)blockIdx.x * 8 + warp; i < total; i += (int64_t)gridDim.x * 8) {
             float s = 0.0f;
             for (int c = lane; c < d.d; c += 32) s = fmaf(to_f<T>(o[i * d.d + c]), to_f<T>(g[i * d.d + c]), s);
             s = warp_sum(s);
-            if (lane == 0) put(i, s);
+            const int64_t tok = i / d.Hq;
+            if (lane == 0) p.delta[(i - tok * d.Hq) * ntok + tok] = s;
         }
         return;
     }
     constexpr int N = Vec16<T>::N, kR = 4;
-    const int sub = lane % team, per = 32 / team, c = sub * N;
-    const int64_t step = (int64_t)gridDim.x * 8 * per;
-    for (int64_t i0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * per + lane / team; i0 - lane / team < total; i0 += kR * step) {
-        uint4 a[kR][2], b[kR][2];
+    const int sub = lane % team, per = 32 / team, c = sub * N, step = 8 * per;
+    const int64_t first = blockIdx.x * len, end = min(first + len, total);
+    // note: where a row's norm goes, `one`: a lane's j-th row is of the same sequence and head of keys in every step, whose largest
+    // it keeps
+    auto rows = [&](bool one, auto note) {
+        float best[kR] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const RowAt start(first + warp * per + lane / team, step, d.Hq);
+        RowAt at = start;
+        for (int64_t i0 = first + warp * per + lane / team; i0 - lane / team < end; i0 += kR * step) {
+            uint4 a[kR][ROW], b[kR][ROW];
 #pragma unroll
-        for (int j = 0; j < kR; ++j)
+            for (int j = 0; j < kR; ++j)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {   // rows of more than 32 lanes' 16 bytes: two of them per lane
-                const int64_t i = i0 + j * step;
-                const int x = c + h * 32 * N;
-                const bool in = i < total && x < d.d && (h == 0 || team == 32);
-                a[j][h] = in ? *(const uint4 *)(o + i * d.d + x) : make_uint4(0, 0, 0, 0);
-                b[j][h] = in ? *(const uint4 *)(g + i * d.d + x) : make_uint4(0, 0, 0, 0);
+                for (int h = 0; h < ROW; ++h) {
+                    const int64_t i = i0 + j * step;
+                    const int x = c + h * 32 * N;
+                    const bool in = i < end && x < d.d;
+                    a[j][h] = in ? *(const uint4 *)(o + i * d.d + x) : make_uint4(0, 0, 0, 0);
+                    b[j][h] = in ? *(const uint4 *)(g + i * d.d + x) : make_uint4(0, 0, 0, 0);
+                }
+            float s[kR], norm[kR];
+#pragma unroll
+            for (int j = 0; j < kR; ++j) {
+                float2 s2 = splat2(0.0f), n2 = s2;
+#pragma unroll
+                for (int h = 0; h < ROW; ++h) {
+                    float2 x[N / 2], y[N / 2];
+                    Pairs<T>::unpack(a[j][h], x);
+                    Pairs<T>::unpack(b[j][h], y);
+#pragma unroll
+                    for (int e = 0; e < N / 2; ++e) {
+                        s2 = fma2(x[e], y[e], s2);
+                        if (kNorms) n2 = fma2(y[e], y[e], n2);
+                    }
+                }
+                s[j] = s2.x + s2.y, norm[j] = n2.x + n2.y;
             }
+            for (int x = team / 2; x; x >>= 1)   // the rows' shuffles side by side
 #pragma unroll
-        for (int j = 0; j < kR; ++j) {
-            float2 s2 = splat2(0.0f);
+                for (int j = 0; j < kR; ++j) {
+                    s[j] += __shfl_xor_sync(0xffffffffu, s[j], x);
+                    if (kNorms) norm[j] += __shfl_xor_sync(0xffffffffu, norm[j], x);
+                }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float2 x[N / 2], y[N / 2];
-                Pairs<T>::unpack(a[j][h], x);
-                Pairs<T>::unpack(b[j][h], y);
-#pragma unroll
-                for (int e = 0; e < N / 2; ++e) s2 = fma2(x[e], y[e], s2);
+            for (int j = 0; j < kR; ++j) {
+                if (sub == 0 && i0 + j * step < end) {
+                    p.delta[at.head * ntok + at.tok] = s[j];
+                    if (kNorms && !one) note(at, norm[j]);
+                }
+                if (kNorms) best[j] = norm[j] <= kFinite ? fmaxf(best[j], norm[j]) : best[j];
+                at.next();
             }
-            float s = s2.x + s2.y;
-            for (int x = team / 2; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-            if (sub == 0 && i0 + j * step < total) put(i0 + j * step, s);
         }
+        at = start;
+        if (kNorms && one)
+#pragma unroll
+            for (int j = 0; j < kR; ++j, at.next())
+                if (sub == 0 && best[j] > 0.0f) note(at, best[j]);
+    };
+    if (first >= end) {
+    } else if (kNorms && p.norms) {
+        const RowNorms norms(p, false, table, first / d.Hq, (end - 1) / d.Hq);
+        const unsigned group = d.Hq / d.Hk;
+        rows(norms.n0 == norms.n1 && kR * step % d.Hq == 0, [&](const RowAt &at, float s) { norms.add(at.tok, (unsigned)at.head / group, s); });
+        norms.flush();
+    } else {
+        rows(false, [](const RowAt &, float) {});
+    }
+    const int64_t v_rows = p.norms ? (int64_t)d.B * d.Tk * d.Hk : 0;
+    if (kNorms && blockIdx.x * v_len < v_rows) {   // v (a row fits 32 lanes' 16 bytes: heads of up to 128 channels)
+        const int64_t first = blockIdx.x * v_len, end = min(first + v_len, v_rows);
+        const RowNorms norms(p, true, table, first / d.Hk, (end - 1) / d.Hk);
+        const bool flat = p.cu || d.B == 1 || d.v_stride_b == d.Tk * d.v_stride_t;   // rows of the batch follow one another
+        const bool one = norms.n0 == norms.n1 && kR * step % d.Hk == 0;
+        float best[kR] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const RowAt start(first + warp * per + lane / team, step, d.Hk);
+        RowAt at = start;
+        for (int64_t i0 = first + warp * per + lane / team; i0 - lane / team < end; i0 += kR * step) {
+            uint4 a[kR];
+            RowAt ahead = at;
+#pragma unroll
+            for (int j = 0; j < kR; ++j) {
+                const int64_t row = flat ? 0 : ahead.tok / d.Tk;
+                a[j] = make_uint4(0, 0, 0, 0);
+                if (i0 + j * step < end && c < d.d)
+                    a[j] = *(const uint4 *)((const T *)p.v + row * d.v_stride_b + (ahead.tok - row * d.Tk) * d.v_stride_t + (int64_t)ahead.head * d.d + c);
+                ahead.next();
+            }
+            float s[kR];
+#pragma unroll
+            for (int j = 0; j < kR; ++j) {
+                float2 x[N / 2], s2 = splat2(0.0f);
+                Pairs<T>::unpack(a[j], x);
+#pragma unroll
+                for (int e = 0; e < N / 2; ++e) s2 = fma2(x[e], x[e], s2);
+                s[j] = s2.x + s2.y;
+            }
+            for (int x = team / 2; x; x >>= 1)
+#pragma unroll
+                for (int j = 0; j < kR; ++j) s[j] += __shfl_xor_sync(0xffffffffu, s[j], x);
+#pragma unroll
+            for (int j = 0; j < kR; ++j) {
+                if (!one && sub == 0 && i0 + j * step < end) norms.add(at.tok, at.head, s[j]);
+                best[j] = s[j] <= kFinite ? fmaxf(best[j], s[j]) : best[j];
+                at.next();
+            }
+        }
+        at = start;
+        if (one)
+#pragma unroll
+            for (int j = 0; j < kR; ++j, at.next())
+                if (sub == 0 && best[j] > 0.0f) norms.add(at.tok, at.head, best[j]);
+        norms.flush();
     }
 }
 
@@ -151,6 +289,7 @@ unsigned row_blocks(int64_t rows, int per) { return (unsigned)std::min<int64_t>(
 template <typename T>
 cudaError_t backward_any(WindowProblem &p, cudaStream_t s) {
     const bool tc = (int64_t)p.d.B * p.d.Tq > 0 && p.d.Tk > 0 && window_tc_supports(p);
+    if (!tc) p.norms = nullptr;
     cudaError_t e = launch_window_tables(p, tc ? 128 : 64, tc ? 128 : 64, s);
     if (e != cudaSuccess) return e;
     const int64_t rows = (int64_t)p.d.B * p.d.Tq * p.d.Hq;
@@ -158,9 +297,14 @@ cudaError_t backward_any(WindowProblem &p, cudaStream_t s) {
     if (rows && p.d.d % N == 0 && ptr_aligned(p.out_in, 16) && ptr_aligned(p.dout, 16)) {
         int team = 1;
         while (team < 32 && team * N < p.d.d) team *= 2;
-        window_delta<T, true><<<(unsigned)std::min<int64_t>(cdiv64(rows, 8 * (32 / team)), 16 * kSms), 256, 0, s>>>(p, team);
+        const int64_t step = 32 * (32 / team), v_rows = p.norms ? (int64_t)p.d.B * p.d.Tk * p.d.Hk : 0;   // a CTA's rows on their way
+        const auto len_of = [&](int64_t n) { return std::max<int64_t>(cdiv64(cdiv64(n, step), (p.norms ? 12 : 16) * kSms), 1) * step; };
+        const int64_t len = len_of(rows), v_len = len_of(v_rows);
+        const unsigned blocks = (unsigned)std::max(cdiv64(rows, len), cdiv64(v_rows, v_len));
+        if (p.d.d <= 32 * N) window_delta<T, true, 1><<<blocks, 256, 0, s>>>(p, team, len, v_len);
+        else window_delta<T, true, 2><<<blocks, 256, 0, s>>>(p, team, len, v_len);
     } else if (rows) {
-        window_delta<T, false><<<row_blocks(rows, 8), 256, 0, s>>>(p, 32);
+        window_delta<T, false, 1><<<row_blocks(rows, 8), 256, 0, s>>>(p, 32, 0, 0);
     }
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     window_rest_plan(p, tc ? 7 : 6);
@@ -169,7 +313,7 @@ cudaError_t backward_any(WindowProblem &p, cudaStream_t s) {
 }
 
 struct WindowLayout {
-    size_t status, q_tiles, k_tiles, rest, delta, partial, total;
+    size_t status, q_tiles, k_tiles, rest, delta, norms, partial, total;
 };
 WindowLayout layout_of(const gdn_window_attention_desc &d, bool backward) {
     WindowLayout L;
@@ -177,10 +321,11 @@ WindowLayout layout_of(const gdn_window_attention_desc &d, bool backward) {
     L.status = off;  off += kStatusBytes;
     L.q_tiles = off; off = align_up(off + 4 * ((size_t)d.N + 1), 256);
     L.k_tiles = off; off = align_up(off + 4 * ((size_t)d.N + 1), 256);
-    L.rest = L.delta = L.partial = off;
+    L.rest = L.delta = L.norms = L.partial = off;
     if (backward) {
         off = align_up(off + 4 * ((size_t)d.N + 1), 256);
         L.delta = off;   off = align_up(off + (size_t)d.B * d.Tq * d.Hq * 4, 256);
+        L.norms = off;   off = align_up(off + (d.dtype == GDN_F16 ? 8 * (size_t)d.N * d.Hk : 0), 256);
         L.partial = off;
         WindowProblem p;
         p.d = d;
@@ -198,7 +343,7 @@ WindowLayout layout_of(const gdn_window_attention_desc &d, bool backward) {
 }  // namespace
 
 cudaError_t launch_window_tables(const WindowProblem &p, int q_tile, int k_tile, cudaStream_t s) {
-    window_tables_kernel<<<1, p.cu ? 1024 : 32, 0, s>>>(p, q_tile, k_tile);
+    window_tables_kernel<<<1, p.cu || p.norms ? 1024 : 32, 0, s>>>(p, q_tile, k_tile);
     return cudaGetLastError();
 }
 
@@ -287,6 +432,7 @@ int fill(WindowProblem &p, const gdn_window_attention_desc *d, const void *q, co
     p.k_tiles = (int32_t *)(ws + L.k_tiles);
     p.rest_off = (int32_t *)(ws + L.rest);
     p.delta = (float *)(ws + L.delta);
+    p.norms = backward && d->dtype == GDN_F16 ? (uint32_t *)(ws + L.norms) : nullptr;   // the tensor cores' alone
     p.partial = (float *)(ws + L.partial);
     p.wait_immediate = wait_test_mode();
     return GDN_OK;

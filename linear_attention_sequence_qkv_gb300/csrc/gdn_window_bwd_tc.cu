@@ -4,8 +4,8 @@
 // Two kernels of one shape, so that every sum has a fixed order (no atomics): one CTA keeps
 // 128 rows and walks over tiles of 128 rows of the other side.
 //   keys:    K_j, V_j stay; per head of the group and tile of queries
-//            S' = K Q^T, dP' = V dO^T, P' = exp2(c S' - lse), dS' = P' (dP' - delta) scale,
-//            dV += P' dO, dK += dS' Q
+//            S' = K Q^T, dP' = V dO^T, P' = exp2(c S' - lse), dS' = P' (dP' - delta),
+//            dV += P' dO, dK += dS' Q (scale taken out of the sums, fp16 in units: gdn_window_tc.cuh)
 //   queries: Q_i, dO_i stay; per tile of keys  S, dP as above (not transposed), dQ += dS K;
 //            gdn_window_dq_tc.cu has it for two heads at once
 // P and dS take the place of S and dP in tensor memory, from where they are operands of the
@@ -47,7 +47,7 @@ struct BwdShared {
     uint64_t a_full, full1[kFirst], empty1[kFirst], fit[kFirst], full2[kSecond], empty2[kSecond], s_full, d_full, p_ready, ds_ready, acc_full, drain;
     uint32_t tmem;
     int gave_up;
-    float lse[2][128], delta[2][128];   // of the tile's queries (keys kernel): lse log2 e, delta scale
+    float lse[2][128], delta[2][128];   // of the tile's queries (keys kernel): lse log2 e, delta, in P's and dP's units
 };
 
 template <typename T, int D, bool KEYS>
@@ -260,6 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
         // -------------------------- the queries' statistics, and zeros in rows behind the sequence (0 x NaN is NaN)
         const int w = warp - 2;
         const int64_t ntok = (int64_t)d.B * d.Tq;
+        const float up = KEYS ? grad_factor<T>(p, n, hk) : 1.0f;
         for (int it = 0; it < count; ++it) {
             const int i = it % kFirst, j = it % kSecond, r0 = row_at(it), left = other - r0;
             float l[2] = {0.0f, 0.0f}, dl[2] = {0.0f, 0.0f};
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
                     const int x = 64 * w + 32 * h + lane;
                     if (x < left) {
                         const int64_t at = head_at(it) * ntok + sp.q0 + r0 + x;
-                        l[h] = p.lse[at] * 1.4426950408889634f, dl[h] = p.delta[at] * d.scale;
+                        l[h] = fmaf(p.lse[at], 1.4426950408889634f, -(float)kWeightBits<T>), dl[h] = p.delta[at] * up;
                     }
                 }
             // tile it - 2 is through with its statistics once its dK is; also keeps this warp near the products
@@ -297,10 +298,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
         const uint32_t ts = tbase + 64 * half + ((uint32_t)(warp & 3) << 21);   // this thread's half of S; dP's is kP further
         const float c = d.scale * 1.4426950408889634f;
         const int64_t ntok = (int64_t)d.B * d.Tq;
+        const float up = grad_factor<T>(p, n, hk);
         float lse = 0.0f, delta = 0.0f;
         if (!KEYS && r < rows) {
-            lse = p.lse[unit * ntok + sp.q0 + row0 + r] * 1.4426950408889634f;
-            delta = p.delta[unit * ntok + sp.q0 + row0 + r] * d.scale;
+            lse = fmaf(p.lse[unit * ntok + sp.q0 + row0 + r], 1.4426950408889634f, -(float)kWeightBits<T>);
+            delta = p.delta[unit * ntok + sp.q0 + row0 + r] * up;
         }
         bool ok = true;
         for (int it = 0; it < count; ++it) {
@@ -366,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
                         const float2 a = *(const float2 *)&sh.delta[it & 1][64 * half + 32 * w + q];
                         dl = make_float2(-a.x, -a.y);
                     }
-                    float2 u = mul2(make_float2(x[32 * w + q], x[32 * w + q + 1]), fma2(make_float2(g[q], g[q + 1]), splat2(d.scale), dl));
+                    float2 u = mul2(make_float2(x[32 * w + q], x[32 * w + q + 1]), fma2(make_float2(g[q], g[q + 1]), splat2(up), dl));
                     if (!all) {   // P is 0, but dP may be anything
                         u.x = see[w] & (1u << q) ? u.x : 0.0f, u.y = see[w] & (2u << q) ? u.y : 0.0f;
                     }
@@ -389,12 +391,18 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
         const int c0 = KEYS ? 0 : half * kCols;
         // rows of sinks whose sum has other parts stay in fp32
         const int apart = !KEYS || !ok ? 0 : rest ? 128 : row0 < d.sinks && rest_chunks(p, sp, tile) > 0 ? min(128, d.sinks - row0) : 0;
+        const float2 back = splat2(KEYS && half ? kWeightUnit<T> : d.scale * kWeightUnit<T> / up);   // out of the operands' units
         const int64_t part_slot = !KEYS ? 0 : rest ? slot : p.rest_slots + (int64_t)n * p.sink_tiles + tile;
 #pragma unroll
         for (int q = 0; q < kCols; q += 32) {
             float o[32];
             if (count > 0) {
                 tmem_ld32(from + q, o);
+#pragma unroll
+                for (int x = 0; x < 32; x += 2) {
+                    const float2 s = mul2(make_float2(o[x], o[x + 1]), back);
+                    o[x] = s.x, o[x + 1] = s.y;
+                }
             } else {
 #pragma unroll
                 for (int x = 0; x < 32; ++x) o[x] = 0.0f;

@@ -2,7 +2,8 @@
 // window attention's backward), on the tensor cores.
 //
 // One CTA keeps 128 queries of both heads (Q_i, dO_i) and walks over tiles of 64 keys:
-//   S = Q K^T, dP = dO V^T, P = exp2(c S - lse), dS = P (dP - delta) scale, dQ += dS K
+//   S = Q K^T, dP = dO V^T, P = exp2(c S - lse), dS = P (dP - delta), dQ += dS K (scale
+//   taken out of the sums, fp16 in units: gdn_window_tc.cuh)
 // dS takes the place of dP in tensor memory, from where it is an operand of the second product.
 // Each head has a warpgroup of its own, a thread per query: while one's dS is computed the
 // tensor cores work on the other's products. Four tiles that stay and three stages of K and V
@@ -209,10 +210,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_pair(const __grid_const
         const uint32_t ts = tbase + 128 * b + ((uint32_t)(warp & 3) << 21);
         const float c = d.scale * 1.4426950408889634f;
         const int64_t ntok = (int64_t)d.B * d.Tq;
+        const float up = grad_factor<T>(p, n, hk);
         float lse = 0.0f, delta = 0.0f;
         if (r < rows) {
-            lse = p.lse[head * ntok + sp.q0 + row0 + r] * 1.4426950408889634f;
-            delta = p.delta[head * ntok + sp.q0 + row0 + r] * d.scale;
+            lse = fmaf(p.lse[head * ntok + sp.q0 + row0 + r], 1.4426950408889634f, -(float)kWeightBits<T>);
+            delta = p.delta[head * ntok + sp.q0 + row0 + r] * up;
         }
         bool ok = true;
         for (int it = 0; it < count; ++it) {
@@ -237,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_pair(const __grid_const
                 for (int x = 0; x < 32; x += 2) {
                     float2 t = fma2(make_float2(s[x], s[x + 1]), splat2(c), splat2(-lse));
                     t = make_float2(ex2_approx(t.x), ex2_approx(t.y));
-                    float2 u = mul2(t, fma2(make_float2(g[x], g[x + 1]), splat2(d.scale), splat2(-delta)));
+                    float2 u = mul2(t, fma2(make_float2(g[x], g[x + 1]), splat2(up), splat2(-delta)));
                     if (!all) u.x = see[w] & (1u << x) ? u.x : 0.0f, u.y = see[w] & (2u << x) ? u.y : 0.0f;
                     f[x / 2] = __uint_as_float(pack2<T>(u.x, u.y));
                 }
@@ -253,11 +255,17 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_pair(const __grid_const
         // ---- dQ, through the head's own Q in shared memory (no product reads it any more)
         const uint32_t from = tbase + L::kAcc + b * D + ((uint32_t)(warp & 3) << 21);
         unsigned char *stage = sm + b * 2 * L::kA;
+        const float2 back = splat2(d.scale * kWeightUnit<T> / up);   // out of the operands' units
 #pragma unroll
         for (int q = 0; q < D; q += 32) {
             float o[32];
             if (count > 0) {
                 tmem_ld32(from + q, o);
+#pragma unroll
+                for (int x = 0; x < 32; x += 2) {
+                    const float2 s = mul2(make_float2(o[x], o[x + 1]), back);
+                    o[x] = s.x, o[x + 1] = s.y;
+                }
             } else {
 #pragma unroll
                 for (int x = 0; x < 32; ++x) o[x] = 0.0f;

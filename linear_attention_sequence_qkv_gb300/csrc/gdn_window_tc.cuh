@@ -42,6 +42,23 @@ __device__ __forceinline__ bool window_partial(int t, int p0, int p1, int window
 // the n lowest bits, none for n <= 0, all for n >= 32
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; }
 
+// fp16 ends at 6e-5 (6e-8 with lost bits) and at 65504, which P of many keys and the scores' gradients of a small or a large
+// grad_out pass. As operands they are held times powers of two, which the fp32 sums are divided by: P times 2^12 (at most 1, and
+// room for what rounding adds where scores are huge), P (dP - delta) times 2^12 f. |dP - delta| is at most
+// b = 2 max |dO| max |v|, of rows of the sequence and of the heads that share keys; f is the power of two with f b in [2, 4].
+// (dq of 1000 queries and keys of 128 channels, grad_out of size 2^-10 | 2^-16: off by 3.1e-4 | 3.1e-4, without 3.7e-3 | 0.18.)
+template <typename T> constexpr int kWeightBits = std::is_same<T, __half>::value ? 12 : 0;
+template <typename T> constexpr float kWeightUnit = std::is_same<T, __half>::value ? 1.0f / 4096 : 1.0f;
+template <typename T> __device__ __forceinline__ float grad_factor(const WindowProblem &p, int n, int hk) {
+    if (!std::is_same<T, __half>::value) return 1.0f;
+    const int64_t at = (int64_t)n * p.d.Hk + hk;
+    const float b2 = 4.0f * __uint_as_float(p.norms[at]) * __uint_as_float(p.norms[at + (int64_t)p.d.N * p.d.Hk]);
+    if (b2 == 0.0f) return 1.0f;
+    // b < 2^(x / 2), x the exponent after b2's own: f = 2^-ceil(x / 2) * 4 (b2 is in [2^-94, 2^82]: inputs are fp16 values)
+    const int x = (int)(__float_as_uint(b2) >> 23) - 127 + 1;
+    return __uint_as_float((uint32_t)(127 - ((x + 1) >> 1) + 2) << 23);
+}
+
 template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi) { return Pairs<T>::pack1(make_float2(lo, hi)); }
 
 // The kernels' waits: about a second each, then the CTA gives up (GDN_ERR_DEVICE_TIMEOUT); the first that does tells the others

@@ -73,7 +73,9 @@ def window_attention(q, k, v, window, sinks, scale, dtype, dout=None):
     relative eps = half a step, and absolutely `least`, half of the type's smallest step, of weights whose largest is at least
     1 (so that the sum l >= 1). l itself is added up in fp32 unrounded: n U32. The product with v adds 2n U32.
     Backward: P = exp(s - lse) with lse's own error; delta = sum dO O takes O's error and rounding; dS = scale P (dP - delta) is
-    rounded to the type, as P is; the sums over n keys (or queries and heads) add 2n U32.
+    rounded to the type, as P is; the sums over n keys (or queries and heads) add 2n U32. fp16 holds P in units of 2^-12 and
+    P (dP - delta) in units of 2^-12 / f, with a power of two f >= 2 / b, where b = 2 max |dO| max |v| (2-norms of rows, over the
+    sequence and the heads that share keys) bounds |dP - delta|: absolutely least 2^-12, and least scale b 2^-13.
     The hardware's exponential counts a result below 2^-126, the smallest normal fp32, as 0 (ex2.approx.ftz): a weight, whose
     row's largest is at least 1, and a P are off by up to 2^-126 more.
     """
@@ -83,6 +85,8 @@ def window_attention(q, k, v, window, sinks, scale, dtype, dout=None):
     G = Hq // Hk
     eps, least = HALF_STEP[dtype] if dtype != "fp32" else (0.0, 0.0)
     step = HALF_STEP[dtype][0]
+    half = dtype == "fp16"
+    least_p = least * 2.0 ** -12 if half else least
     see = visible(Lq, Lk, window, sinks)
     any_seen = see.any(1)
     r = {"out": np.zeros((Lq, Hq, d)), "out_err": np.zeros((Lq, Hq, d)), "lse": np.full((Hq, Lq), -np.inf), "lse_err": np.zeros((Hq, Lq))}
@@ -122,8 +126,12 @@ def window_attention(q, k, v, window, sinks, scale, dtype, dout=None):
         rP = rp + elog[:, None] + U32 * (4 * np.abs(np.where(any_seen, lse, 0.0))[:, None] + 8)
         dS = scale * P * (dP - delta)
         edS = scale * FLUSH * see * (np.abs(dP - delta) + edP + edelta) + scale * P * (rP * np.abs(dP - delta) + edP + edelta + 4 * U32 * (np.abs(dP) + np.abs(delta)))
-        edS = edS + eps * (np.abs(dS) + edS) + least * see
-        eP = P * (rP + eps * (1 + rP)) + (least + FLUSH) * see
+        least_s = least
+        if half:
+            heads = slice(h // G * G, h // G * G + G)
+            least_s = least * scale * 2 * np.sqrt((dout[:, heads] ** 2).sum(-1).max() * (V ** 2).sum(-1).max()) * 2.0 ** -13
+        edS = edS + eps * (np.abs(dS) + edS) + least_s * see
+        eP = P * (rP + eps * (1 + rP)) + (least_p + FLUSH) * see
         r["dq"][:, h] = dS @ K
         r["dq_err"][:, h] = edS @ aK + 2 * U32 * n_row * (np.abs(dS) @ aK)
         r["dk"][:, h // G] += dS.T @ Q
