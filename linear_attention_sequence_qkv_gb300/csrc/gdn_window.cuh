@@ -5,11 +5,18 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 #include "gdn_layer_ops.cuh"
 
 namespace gdn {
 
 constexpr int kMostHead = 256;   // channels per head
+
+// fp16 weights that are operands of a product are held times 2^6. Against a row's maximum they are at most 2^8 (it is raised only
+// where it grew by more), which leaves room for what rounding adds where scores are huge; and the smallest that count are
+// 2^-31 of it (without: 2^-25, and 40000 keys of weight 2.5e-8 beside one of weight 1 added up to nothing).
+template <typename T> constexpr float kRaised = std::is_same<T, __half>::value ? 6.0f : 0.0f;
 
 struct WindowProblem {
     gdn_window_attention_desc d;

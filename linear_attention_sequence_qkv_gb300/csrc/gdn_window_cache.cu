@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(32 * kStepWarps, 2) step_mma(const __grid_cons
                 for (int e = 0; e < 2; ++e) {
                     float w = 0.0f;
                     if (x == 0 || WIDE) {
-                        w = ex2_approx(fmaf(s[r][2 * x + e], c, m[x] == -INFINITY ? 0.0f : -m[x] * c));
+                        w = ex2_approx(fmaf(s[r][2 * x + e], c, m[x] == -INFINITY ? 0.0f : fmaf(-m[x], c, kRaised<T>)));
                         l[x] += w;
                     }
                     pr[r][2 * x + e] = w;

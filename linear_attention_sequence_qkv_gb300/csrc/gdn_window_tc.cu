@@ -9,7 +9,7 @@
 // other. They are two heads that share keys and values where the group's size is even (the
 // same mask, half the traffic of K and V), else two neighbouring tiles of one head.
 // Softmax in one pass: a row's maximum m is raised, and O scaled, only where it grew by more
-// than 2^8 (P stays below 2^8, in range of fp16), so O is rarely read back. P is rounded to the
+// than 2^8 (P stays below 2^8, in range of fp16, which takes it times 2^6), so O is rarely read back. P is rounded to the
 // tensors' type, which the second product takes; sums, maxima and O are fp32.
 //
 // Bound by the tensor cores where rows see many keys (causal, 16384 tokens of 16 heads of 128 on
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_forward_tc(const __grid_co
                     }
                 }
             }
-            const float2 cc = splat2(c), mc = splat2(m == -INFINITY ? 0.0f : -m * c);
+            const float2 cc = splat2(c), mc = splat2(m == -INFINITY ? 0.0f : fmaf(-m, c, kRaised<T>));
             float2 sum[2] = {splat2(0.0f), splat2(0.0f)};
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_forward_tc(const __grid_co
                     *(const uint4 *)(stage + (ch >> 3) * L::kRow + (row0 + q) * 128 + (((ch & 7) ^ ((row0 + q) & 7)) << 4));
         }
         __syncwarp();
-        float lse = pos < 0 ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f;
+        float lse = pos < 0 ? -INFINITY : (m * c + (log2f(l) - kRaised<T>)) * 0.6931471805599453f;
         // rows that see a value that is not finite
         if (*(volatile int *)&sh.any_bad) {
             bool dirty = false;

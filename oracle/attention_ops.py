@@ -70,8 +70,9 @@ def window_attention(q, k, v, window, sinks, scale, dtype, dout=None):
     Bounds. A score is a sum of d products that are exact (16 bits) or rounded, in fp32, in any order, an addition
     rounding or cutting off: es = (2d + 8) U32 scale sum |q||k|. exp's argument and value: rp = es + U32 (4 (|s| + the
     row's largest |s|) + 8) relative to P. For 16-bit types the weights are rounded to the type before the product with v:
-    relative eps = half a step, and absolutely `least`, half of the type's smallest step, of weights whose largest is at least
-    1 (so that the sum l >= 1). l itself is added up in fp32 unrounded: n U32. The product with v adds 2n U32.
+    relative eps = half a step, and absolutely, of weights whose largest is at least 1 (so that the sum l >= 1), `least`, half of
+    the type's smallest step, for fp16 in units of 2^-6, in which they are held. l itself is added up in fp32 unrounded: n U32.
+    The product with v adds 2n U32.
     Backward: P = exp(s - lse) with lse's own error; delta = sum dO O takes O's error and rounding; dS = scale P (dP - delta) is
     rounded to the type, as P is; the sums over n keys (or queries and heads) add 2n U32. fp16 holds P in units of 2^-12 and
     P (dP - delta) in units of 2^-12 / f, with a power of two f >= 2 / b, where b = 2 max |dO| max |v| (2-norms of rows, over the
@@ -86,7 +87,7 @@ def window_attention(q, k, v, window, sinks, scale, dtype, dout=None):
     eps, least = HALF_STEP[dtype] if dtype != "fp32" else (0.0, 0.0)
     step = HALF_STEP[dtype][0]
     half = dtype == "fp16"
-    least_p = least * 2.0 ** -12 if half else least
+    least_w, least_p = (least * 2.0 ** -6, least * 2.0 ** -12) if half else (least, least)
     see = visible(Lq, Lk, window, sinks)
     any_seen = see.any(1)
     r = {"out": np.zeros((Lq, Hq, d)), "out_err": np.zeros((Lq, Hq, d)), "lse": np.full((Hq, Lq), -np.inf), "lse_err": np.zeros((Hq, Lq))}
@@ -111,7 +112,7 @@ def window_attention(q, k, v, window, sinks, scale, dtype, dout=None):
         rp = np.where(see, es + U32 * (4 * (np.abs(np.where(see, s, 0.0)) + big) + 8), 0.0)
         mean_rp = (P * rp).sum(1)[:, None]
         O = P @ V
-        eO = (P * (eps + rp)) @ aV + (mean_rp + U32 * (3 * n_row + 16)) * (P @ aV) + (least + FLUSH) * (see @ aV)
+        eO = (P * (eps + rp)) @ aV + (mean_rp + U32 * (3 * n_row + 16)) * (P @ aV) + (least_w + FLUSH) * (see @ aV)
         lse = np.where(any_seen, top[:, 0] + np.log(l[:, 0]), -np.inf)
         elog = mean_rp[:, 0] + U32 * (n_row[:, 0] + 8 + 4 * np.abs(np.where(any_seen, lse, 0.0)) + 2 * big[:, 0])
         r["out"][:, h], r["out_err"][:, h] = O, eO

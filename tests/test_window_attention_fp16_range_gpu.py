@@ -1,4 +1,5 @@
-"""What fp16's range does to the window attention's 16-bit operands: gradients of any size against the fp64 definition. The oracle's bounds count a rounding of P and of dS relative to their values; how far below
+"""What fp16's range does to the window attention's 16-bit operands: weights far below a row's largest, and gradients of any
+size, against the fp64 definition. The oracle's bounds count a rounding of P and of dS relative to their values; how far below
 fp16's smallest they may fall it takes from the operands' powers of two (oracle/attention_ops.py)."""
 import numpy as np
 import pytest
@@ -6,7 +7,7 @@ import torch
 
 from linear_attention_sequence_qkv_gb300 import gdn
 from oracle import attention_ops as A
-from test_window_attention_gpu import dev, held, make, n64  # noqa: F401
+from test_window_attention_gpu import check, dev, held, make, n64  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -123,3 +124,42 @@ def test_many_short_sequences_each_of_its_own_size(dev, packed):  # noqa: F811
         for x in ("dq", "dv"):
             tol = A.bound(r[x], r[x + "_err"], "fp16")
             assert (np.abs(at(getattr(grads, x)) - r[x]) <= tol).all(), (x, n)
+
+
+def far_weights(dev, Tk, dtype="fp16"):
+    """One key of score 0 whose value is 0, all others of score -17.5 and value 1: their weights of 2.5e-8 are below half of
+    fp16's smallest value, and add up to Tk 2.5e-8."""
+    act = {"fp16": torch.float16, "bf16": torch.bfloat16}[dtype]
+    q, k, v = (torch.zeros((1, n, 64), dtype=act, device=dev) for n in (2, Tk, Tk))
+    q[..., 0] = 1.0
+    k[:, 1:, 0], v[:, 1:] = -17.5, 1.0
+    return q, k, v
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_many_small_weights(dev, dtype):  # noqa: F811
+    Tk = 40000
+    q, k, v = far_weights(dev, Tk, dtype)
+    dout = torch.randn(q.shape, generator=torch.Generator().manual_seed(1)).to(q.dtype).to(dev) * 4096.0
+    kw = dict(d=64, window=Tk, sinks=0, scale=1.0)
+    f = gdn.window_attention_forward(q, k, v, **kw)
+    g = gdn.window_attention_backward(q, k, v, f.out, f.lse, dout, **kw)
+    check(q, k, v, dout, f, g, [(0, 0, 2, 0, Tk)], 64, Tk, 0, 1.0, dtype)
+
+
+@pytest.mark.parametrize("group", [1, 12])
+def test_many_small_weights_in_a_step(dev, group):  # noqa: F811
+    """As many sequences as leave each to one CTA, and a key of score 0 for each of its warps, so that all of the others are small."""
+    N, Hk, Tk, d = 38, 8, 40000, 8
+    c = gdn.alloc_window_cache(N, Hk, d, window=Tk, dtype=torch.float16, device=dev)
+    c.k.zero_(), c.v.fill_(1.0)
+    c.k[..., 0] = -17.5
+    c.k[:, :, 0:64:16], c.v[:, :, 0:64:16] = 0.0, 0.0
+    c.lengths.fill_(Tk - 1)
+    q = torch.zeros((N, 1, group * Hk, d), dtype=torch.float16, device=dev)
+    q[..., 0] = 1.0
+    k, v = c.k[:, :, -1].reshape(N, 1, Hk * d), c.v[:, :, -1].reshape(N, 1, Hk * d)
+    got = gdn.window_attention_step(q.view(N, 1, -1), k, v, c, scale=1.0)
+    r = A.window_attention(n64(q[0, :, :1]), n64(c.k[0, 0])[:, None], n64(c.v[0, 0])[:, None], Tk, 0, 1.0, "fp16")
+    wide = lambda x: np.broadcast_to(x, (N, group * Hk, d))  # noqa: E731
+    held(got, wide(r["out"]), wide(r["out_err"]), "fp16", "step over many small weights")
