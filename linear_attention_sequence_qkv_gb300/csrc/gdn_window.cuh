@@ -32,11 +32,14 @@ struct WindowProblem {
     int wait_immediate;
     // the backward: what the sinks' keys take beyond their tile's own CTA (gdn_window_rest.cuh)
     float *partial;             // partial sums of their gradients
-    int32_t *rest_off;          // packed: [N+1] chunks of the sequences before n
     int64_t rest_slots;         // chunks at most
     int rest_shift;             // tiles of 2^rest_shift queries
     int rest_its, rest_per;     // tiles per chunk; chunks per row without packing
-    int sink_tiles, sink_rows;  // tiles that hold sinks (0: no rest), rows of their partial sums
+    int rest_packed;            // the sequences differ
+    int sink_tiles, sink_rows;  // tiles of a sequence's sinks that can have a rest (0: none), rows of their partial sums
+    int rest_all;               // such tiles of all sequences, at most
+    int32_t *rest_of;           // packed: [N+1] tiles with a rest of the sequences before n
+    int32_t *rest_tiles;        // [rest_all (packed, else sink_tiles) + 1] chunks before each of them
 };
 
 // A sequence: its first query and key among the flattened tokens, their numbers, and the

@@ -12,6 +12,29 @@
 namespace gdn {
 namespace {
 
+// The sum of c over the threads before this one, and over all (1024 threads; the next call may follow at once)
+__device__ __forceinline__ int before_thread(int c, int32_t (&sums)[32], int &all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    int s = sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+    }
+    all = __shfl_sync(0xffffffffu, s, 31);
+    const int ahead = __shfl_sync(0xffffffffu, s, warp ? warp - 1 : 0);
+    __syncthreads();
+    return (warp ? ahead : 0) + x - c;
+}
+
 // Packed offsets checked, and the tiles of the sequences before each one counted
 __global__ void __launch_bounds__(1024) window_tables_kernel(const __grid_constant__ WindowProblem p, int q_tile, int k_tile) {
     const gdn_window_attention_desc &d = p.d;
@@ -25,72 +48,53 @@ __global__ void __launch_bounds__(1024) window_tables_kernel(const __grid_consta
     if (p.cuk != p.cu) ok = seqlens_ok(p.cuk, d.N, d.Tk) && ok;
     if (threadIdx.x == 0) *p.status = ok ? GDN_OK : GDN_ERR_DEVICE_SEQLENS;
     __shared__ int32_t sums[32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int which = 0; which < 2; ++which) {
         const int32_t *cu = which ? p.cuk : p.cu;
         int32_t *to = which ? p.k_tiles : p.q_tiles;
         const int tile = which ? k_tile : q_tile;
         if (!to) continue;
-        int before = 0;
+        int before = 0, all;
         for (int base = 0; base < d.N; base += blockDim.x) {
             const int n = base + threadIdx.x;
             const int c = ok && n < d.N ? (int)(((int64_t)cu[n + 1] - cu[n] + tile - 1) / tile) : 0;
-            int x = c;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += y;
-            }
-            if (lane == 31) sums[warp] = x;
-            __syncthreads();
-            int s = sums[lane];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, s, o);
-                if (lane >= o) s += y;
-            }
-            const int ahead = warp ? __shfl_sync(0xffffffffu, s, warp - 1) : 0, all = __shfl_sync(0xffffffffu, s, 31);
-            if (n < d.N) to[n] = before + ahead + x - c;
+            const int at = before + before_thread(c, sums, all);
+            if (n < d.N) to[n] = at;
             before += all;
-            __syncthreads();
         }
         if (threadIdx.x == 0) to[d.N] = before;
     }
 }
 
-// The chunks of every sequence counted, for packed ones
+// For packed sequences the sink tiles with a rest of those before each one, and for all the chunks before each such tile
 __global__ void __launch_bounds__(1024) window_rest_table(const __grid_constant__ WindowProblem p) {
     __shared__ int32_t sums[32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const bool ok = *p.status == GDN_OK;
-    int before = 0;
-    for (int base = 0; base < p.d.N; base += blockDim.x) {
-        const int n = base + threadIdx.x;
-        int c = 0;
-        if (ok && n < p.d.N) {
-            const WindowSpan s = window_span(p, n);
-            for (int t = 0; t < p.sink_tiles; ++t) c += rest_chunks(p, s, t);
+    if (*p.status != GDN_OK) return;
+    int tiles = p.sink_tiles, all;
+    if (p.rest_packed) {
+        tiles = 0;
+        for (int base = 0; base < p.d.N; base += blockDim.x) {
+            const int n = base + threadIdx.x;
+            const int at = tiles + before_thread(n < p.d.N ? rest_count(p, window_span(p, n)) : 0, sums, all);
+            if (n < p.d.N) p.rest_of[n] = at;
+            tiles += all;
         }
-        int x = c;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        if (lane == 31) sums[warp] = x;
-        __syncthreads();
-        int s = sums[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += y;
-        }
-        const int ahead = warp ? __shfl_sync(0xffffffffu, s, warp - 1) : 0, all = __shfl_sync(0xffffffffu, s, 31);
-        if (n < p.d.N) p.rest_off[n] = before + ahead + x - c;
-        before += all;
-        __syncthreads();
+        if (threadIdx.x == 0) p.rest_of[p.d.N] = tiles;
+        __syncthreads();   // they are read below
     }
-    if (threadIdx.x == 0) p.rest_off[p.d.N] = before;
+    const int total = p.rest_packed ? p.rest_all : p.sink_tiles;
+    int before = 0;
+    for (int base = 0; base < total; base += blockDim.x) {
+        const int x = base + threadIdx.x;
+        int c = 0;
+        if (x < tiles) {
+            const int n = p.rest_packed ? upper_index(p.rest_of, p.d.N, x) : 0;
+            c = rest_chunks(p, window_span(p, n), x - (p.rest_packed ? p.rest_of[n] : 0));
+        }
+        const int at = before + before_thread(c, sums, all);
+        if (x < total) p.rest_tiles[x] = at;
+        before += all;
+    }
+    if (threadIdx.x == 0) p.rest_tiles[total] = before;
 }
 
 // fp16's norms (gdn_window_tc.cuh): the largest squared norms of a CTA's rows, per sequence and head of keys, go through shared
@@ -313,7 +317,7 @@ cudaError_t backward_any(WindowProblem &p, cudaStream_t s) {
 }
 
 struct WindowLayout {
-    size_t status, q_tiles, k_tiles, rest, delta, norms, partial, total;
+    size_t status, q_tiles, k_tiles, rest_of, rest_tiles, delta, norms, partial, total;
 };
 WindowLayout layout_of(const gdn_window_attention_desc &d, bool backward) {
     WindowLayout L;
@@ -321,20 +325,21 @@ WindowLayout layout_of(const gdn_window_attention_desc &d, bool backward) {
     L.status = off;  off += kStatusBytes;
     L.q_tiles = off; off = align_up(off + 4 * ((size_t)d.N + 1), 256);
     L.k_tiles = off; off = align_up(off + 4 * ((size_t)d.N + 1), 256);
-    L.rest = L.delta = L.norms = L.partial = off;
+    L.rest_of = L.rest_tiles = L.delta = L.norms = L.partial = off;
     if (backward) {
-        off = align_up(off + 4 * ((size_t)d.N + 1), 256);
-        L.delta = off;   off = align_up(off + (size_t)d.B * d.Tq * d.Hq * 4, 256);
-        L.norms = off;   off = align_up(off + (d.dtype == GDN_F16 ? 8 * (size_t)d.N * d.Hk : 0), 256);
-        L.partial = off;
         WindowProblem p;
         p.d = d;
-        size_t most = 0;   // of either kernels: which it is the pointers say
+        size_t partial = 0, tiles = 0;   // of either kernels: which it is the pointers say
         for (int shift = 6; shift <= 7; ++shift) {
             window_rest_plan(p, shift);
-            most = std::max(most, window_partial_bytes(p));
+            partial = std::max(partial, window_partial_bytes(p));
+            tiles = std::max(tiles, (size_t)(p.rest_packed ? p.rest_all : p.sink_tiles) + 1);
         }
-        off = align_up(off + most, 256);
+        L.rest_of = off;    off = align_up(off + (p.rest_packed ? 4 * ((size_t)d.N + 1) : 0), 256);
+        L.rest_tiles = off; off = align_up(off + 4 * tiles, 256);
+        L.delta = off;   off = align_up(off + (size_t)d.B * d.Tq * d.Hq * 4, 256);
+        L.norms = off;   off = align_up(off + (d.dtype == GDN_F16 ? 8 * (size_t)d.N * d.Hk : 0), 256);
+        L.partial = off; off = align_up(off + partial, 256);
     }
     L.total = off;
     return L;
@@ -347,41 +352,48 @@ cudaError_t launch_window_tables(const WindowProblem &p, int q_tile, int k_tile,
     return cudaGetLastError();
 }
 
-// Chunks of the sinks' rest: as long as a CTA of keys walks within the window, 2048 to 32768 queries
+// The sinks' rest. A sink tile has one only where its last key lies more than `window` before the sequence's last, so that of packed
+// sequences at most Tk / (window + 128) have any. A chunk is as long as a CTA of keys walks within the window, 2048 to 32768
+// queries.
 void window_rest_plan(WindowProblem &p, int shift) {
     const gdn_window_attention_desc &d = p.d;
-    const int64_t group = d.Hq / d.Hk, unit = (int64_t)1 << shift;
+    const int64_t group = d.Hq / d.Hk, unit = (int64_t)1 << shift, q_tiles = cdiv64(d.Tq, unit);
     p.rest_shift = shift;
-    p.rest_its = (int)std::min<int64_t>(32768 / unit, std::max<int64_t>(2048 / unit, group * (((int64_t)d.window + 127) / unit + 1)));
-    p.sink_tiles = (int)cdiv64(std::min(d.sinks, d.Tk), 128);
+    p.rest_packed = d.N != d.B;   // (one packed sequence is a row like another)
+    p.sink_tiles = d.window >= d.Tk ? 0 : (int)std::min<int64_t>(cdiv64(std::min(d.sinks, d.Tk), 128), ((int64_t)d.Tk - d.window) / 128);
     p.sink_rows = std::min(128, std::min(d.sinks, d.Tk));
+    const int64_t rows = p.rest_packed ? std::min<int64_t>(d.N, d.Tk / ((int64_t)d.window + 128)) : d.B;   // that can have one
+    p.rest_all = (int)std::min<int64_t>(rows * p.sink_tiles, (int64_t)d.B * d.Tk / 128);
     p.rest_per = 0;
     p.rest_slots = 0;
-    if (p.sink_tiles == 0 || d.window >= d.Tk) {   // every key's window reaches the end
-        p.sink_tiles = 0;
-        return;
-    }
-    if (d.N == d.B) {   // not packed, or one sequence: the same chunks for all rows
-        for (int t = 0; t < p.sink_tiles; ++t) {
-            const int64_t past = (int64_t)d.Tk - d.Tq, j0 = (int64_t)t * 128, j1 = std::min<int64_t>(j0 + 127, d.Tk - 1);
-            const int64_t hi = std::min<int64_t>(d.Tq - 1, j1 + d.window - 1 - past), lo = std::max<int64_t>(0, j0 - past) >> shift;
-            const int64_t tiles = std::max<int64_t>(0, cdiv64(d.Tq, unit) - std::max<int64_t>(hi < 0 ? 0 : (hi >> shift) + 1, lo));
-            p.rest_per += (int)cdiv64(tiles * group, p.rest_its);
-        }
+    // tiles of queries behind the window of sink tile t, for rows that are alike
+    const auto rest_tiles = [&](int64_t t) {
+        const int64_t past = (int64_t)d.Tk - d.Tq, j0 = t * 128, j1 = std::min<int64_t>(j0 + 127, d.Tk - 1);
+        const int64_t hi = std::min<int64_t>(d.Tq - 1, j1 + d.window - 1 - past), lo = std::max<int64_t>(0, j0 - past) >> shift;
+        return std::max<int64_t>(0, q_tiles - std::max<int64_t>(hi < 0 ? 0 : (hi >> shift) + 1, lo));
+    };
+    int64_t visits = 0;   // of all rows, at most
+    if (p.rest_packed) visits = p.sink_tiles * (q_tiles + rows);
+    else
+        for (int t = 0; t < p.sink_tiles; ++t) visits += d.B * rest_tiles(t);
+    const int64_t window_its = std::min<int64_t>(32768 / unit, std::max<int64_t>(2048 / unit, group * (((int64_t)d.window + 127) / unit + 1)));
+    p.rest_its = (int)window_its;
+    if (p.rest_packed) {   // at most: every tile's last chunk begun
+        p.rest_slots = p.rest_all ? (int64_t)((double)visits * group / p.rest_its) + 1 + p.rest_all : 0;
+    } else {
+        for (int t = 0; t < p.sink_tiles; ++t) p.rest_per += (int)cdiv64(rest_tiles(t) * group, p.rest_its);
         p.rest_slots = (int64_t)d.B * p.rest_per;
-    } else {            // at most: every sequence's last chunk begun
-        p.rest_slots = p.sink_tiles * (cdiv64(group * (cdiv64(d.Tq, unit) + d.N), p.rest_its) + d.N);
     }
-    if (p.rest_slots == 0) p.sink_tiles = 0;
+    if (p.rest_slots == 0) p.sink_tiles = p.rest_all = 0;
 }
 
 size_t window_partial_bytes(const WindowProblem &p) {
     if (p.rest_slots == 0) return 0;
-    return (size_t)(p.rest_slots + (int64_t)p.d.N * p.sink_tiles) * p.d.Hk * p.sink_rows * 2 * (p.d.d <= 64 ? 64 : p.d.d <= 128 ? 128 : 256) * 4;
+    return (size_t)(p.rest_slots + p.rest_all) * p.d.Hk * p.sink_rows * 2 * (p.d.d <= 64 ? 64 : p.d.d <= 128 ? 128 : 256) * 4;
 }
 
 cudaError_t launch_window_rest_table(const WindowProblem &p, cudaStream_t s) {
-    if (!p.cu || p.sink_tiles == 0) return cudaSuccess;
+    if (p.sink_tiles == 0 || (!p.rest_packed && p.sink_tiles == 1)) return cudaSuccess;   // one tile a row: no table is read
     window_rest_table<<<1, 1024, 0, s>>>(p);
     return cudaGetLastError();
 }
@@ -430,7 +442,7 @@ int fill(WindowProblem &p, const gdn_window_attention_desc *d, const void *q, co
     p.status = (int32_t *)ws;
     p.q_tiles = (int32_t *)(ws + L.q_tiles);
     p.k_tiles = (int32_t *)(ws + L.k_tiles);
-    p.rest_off = (int32_t *)(ws + L.rest);
+    p.rest_of = (int32_t *)(ws + L.rest_of), p.rest_tiles = (int32_t *)(ws + L.rest_tiles);
     p.delta = (float *)(ws + L.delta);
     p.norms = backward && d->dtype == GDN_F16 ? (uint32_t *)(ws + L.norms) : nullptr;   // the tensor cores' alone
     p.partial = (float *)(ws + L.partial);

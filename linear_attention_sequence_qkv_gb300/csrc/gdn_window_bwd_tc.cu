@@ -77,28 +77,25 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
     const int64_t block = rest ? blockIdx.x : blockIdx.x - rest_blocks;
     const int slot = (int)((uint32_t)block / (uint32_t)units), unit = (int)block - slot * units;   // unit: head of k and v (queries: of q)
     int n, tile, chunk = 0;
-    const int32_t *table = rest ? p.rest_off : KEYS ? p.k_tiles : p.q_tiles;
-    if (p.cu) {
+    const int32_t *table = KEYS ? p.k_tiles : p.q_tiles;
+    if (rest) {
+        RestAt at;
+        const bool found = rest_at(p, slot, at);
+        if (*p.status == GDN_ERR_DEVICE_SEQLENS || !found) return;
+        n = at.n, tile = at.tile, chunk = at.chunk;
+    } else if (p.cu) {
         const int32_t status = *p.status, tiles = table[d.N];   // on their way with the search's
         n = warp_upper_index(table, d.N, slot);
         if (status == GDN_ERR_DEVICE_SEQLENS || slot >= tiles) return;
         tile = slot - table[n];
     } else {
-        const int per = rest ? p.rest_per : ((KEYS ? d.Tk : d.Tq) + 127) / 128;
+        const int per = ((KEYS ? d.Tk : d.Tq) + 127) / 128;
         n = slot / per;
         tile = slot - n * per;
     }
     const WindowSpan sp = window_span(p, n);
     const int past = sp.Lk - sp.Lq;
-    if (rest) {   // `tile` counts the sequence's chunks so far
-        chunk = tile;
-        for (tile = 0; tile < p.sink_tiles; ++tile) {
-            const int c = rest_chunks(p, sp, tile);
-            if (chunk < c) break;
-            chunk -= c;
-        }
-        if (tile >= p.sink_tiles) return;
-    } else if (!KEYS) {                                    // later queries, which see the most, first
+    if (!KEYS) {                                           // later queries, which see the most, first
         tile = (p.cu ? p.q_tiles[n + 1] - p.q_tiles[n] : (d.Tq + 127) / 128) - 1 - tile;
     }
     const int hk = KEYS ? unit : unit / group;
@@ -392,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
         // rows of sinks whose sum has other parts stay in fp32
         const int apart = !KEYS || !ok ? 0 : rest ? 128 : row0 < d.sinks && rest_chunks(p, sp, tile) > 0 ? min(128, d.sinks - row0) : 0;
         const float2 back = splat2(KEYS && half ? kWeightUnit<T> : d.scale * kWeightUnit<T> / up);   // out of the operands' units
-        const int64_t part_slot = !KEYS ? 0 : rest ? slot : p.rest_slots + (int64_t)n * p.sink_tiles + tile;
+        const int64_t part_slot = !apart ? 0 : rest ? slot : own_slot(p, n, tile);
 #pragma unroll
         for (int q = 0; q < kCols; q += 32) {
             float o[32];

@@ -27,10 +27,47 @@ __device__ __forceinline__ int rest_chunks(const WindowProblem &p, const WindowS
     return (int)((its + p.rest_its - 1) / p.rest_its);
 }
 
-// The partial sums' place: [slot][Hk][rows][2][D] fp32, slots of the chunks first, then one per sequence and sink tile
+// How many of the sequence's tiles of sinks have one: the first ones
+__device__ __forceinline__ int rest_count(const WindowProblem &p, const WindowSpan &s) {
+    int lo = 0, hi = min(p.sink_tiles, max(0, s.Lk - p.d.window) / 128);
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (rest_chunks(p, s, mid) > 0) lo = mid + 1;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// The chunk at `slot`: its sequence, sink tile and number there; false behind the last one. Whole warps call it; bad packed offsets are
+// to be looked for before its answer is used.
+struct RestAt {
+    int n, tile, chunk;
+};
+__device__ __forceinline__ bool rest_at(const WindowProblem &p, int64_t slot, RestAt &at) {
+    if (p.rest_packed) {
+        if (slot >= p.rest_tiles[p.rest_all]) return false;
+        const int x = warp_upper_index(p.rest_tiles, p.rest_all, slot);
+        at.n = warp_upper_index(p.rest_of, p.d.N, x);
+        at.tile = x - p.rest_of[at.n];
+        at.chunk = (int)(slot - p.rest_tiles[x]);
+    } else {
+        at.n = (int)(slot / p.rest_per);
+        at.chunk = (int)(slot - (int64_t)at.n * p.rest_per), at.tile = 0;
+        if (p.sink_tiles > 1) {
+            at.tile = warp_upper_index(p.rest_tiles, p.sink_tiles, at.chunk);
+            at.chunk -= p.rest_tiles[at.tile];
+        }
+    }
+    return true;
+}
+
+// The partial sums' place: [slot][Hk][rows][2][D] fp32, slots of the chunks first, then one for each tile with a rest
 template <int D>
 __device__ __forceinline__ float *partial_at(const WindowProblem &p, int64_t slot, int hk) {
     return p.partial + (slot * p.d.Hk + hk) * ((int64_t)p.sink_rows * 2 * D);
+}
+__device__ __forceinline__ int64_t own_slot(const WindowProblem &p, int n, int tile) {
+    return p.rest_slots + (p.rest_packed ? p.rest_of[n] : n * p.sink_tiles) + tile;
 }
 
 // The sinks' gradients: the CTA's own part and the chunks', in order. Bound by the loads' latency: a thread has one sum and eight
@@ -39,14 +76,17 @@ template <typename T, int D>
 static __global__ void __launch_bounds__(256) window_sink_sums(const __grid_constant__ WindowProblem p) {
     if (*p.status != GDN_OK) return;
     const gdn_window_attention_desc &d = p.d;
-    const int hk = blockIdx.x % d.Hk, n = blockIdx.x / d.Hk / p.sink_tiles, t = blockIdx.x / d.Hk % p.sink_tiles;
-    const WindowSpan sp = window_span(p, n);
-    const int chunks = rest_chunks(p, sp, t);
+    const int hk = blockIdx.x % d.Hk, x = blockIdx.x / d.Hk;   // of all tiles
+    if (p.rest_packed && x >= p.rest_of[d.N]) return;
+    const int n = p.rest_packed ? upper_index(p.rest_of, d.N, x) : x / p.sink_tiles, t = x - (p.rest_packed ? p.rest_of[n] : n * p.sink_tiles);
+    const bool one = !p.rest_packed && p.sink_tiles == 1;
+    const int32_t *table = p.rest_tiles + (p.rest_packed ? x : t);
+    const int chunks = one ? p.rest_per : table[1] - table[0];
     if (chunks == 0) return;
-    int64_t slot = p.cu ? p.rest_off[n] : (int64_t)n * p.rest_per;
-    for (int x = 0; x < t; ++x) slot += rest_chunks(p, sp, x);
+    const int64_t slot = (p.rest_packed ? 0 : (int64_t)n * p.rest_per) + (one ? 0 : table[0]);
+    const WindowSpan sp = window_span(p, n);
     const int rows = min(min(128, d.sinks - t * 128), sp.Lk - t * 128);
-    const float *own = partial_at<D>(p, p.rest_slots + (int64_t)n * p.sink_tiles + t, hk);
+    const float *own = partial_at<D>(p, own_slot(p, n, t), hk);
     for (int x = blockIdx.y * 256 + threadIdx.x; x < rows * 2 * D; x += gridDim.y * 256) {
         const int r = x / (2 * D), b = x / D & 1, c = x % D;
         if (c >= d.d) continue;
@@ -62,14 +102,14 @@ static __global__ void __launch_bounds__(256) window_sink_sums(const __grid_cons
 template <typename T, int D>
 cudaError_t launch_window_sink_sums(const WindowProblem &p, cudaStream_t s) {
     if (p.rest_slots == 0) return cudaSuccess;
-    const int64_t blocks = (int64_t)p.d.N * p.sink_tiles * p.d.Hk;
+    const int64_t blocks = (int64_t)p.rest_all * p.d.Hk;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     const unsigned parts = (unsigned)std::min<int64_t>(cdiv64((int64_t)p.sink_rows * 2 * D, 256), 64);
     window_sink_sums<T, D><<<dim3((unsigned)blocks, parts), 256, 0, s>>>(p);
     return cudaGetLastError();
 }
 
-// fills the chunks' part of p from the sizes, for tiles of 2^shift queries; the bytes of the partial sums; the packed sequences' table of chunks
+// fills the chunks' part of p from the sizes, for tiles of 2^shift queries; the bytes of the partial sums; the tables
 // (gdn_window_attention.cu)
 void window_rest_plan(WindowProblem &p, int shift);
 size_t window_partial_bytes(const WindowProblem &p);

@@ -341,23 +341,11 @@ __device__ __forceinline__ void dkv_tile(const WindowProblem &p, float *sm, int6
     if (rest) {   // a chunk of a sink tile of 128 keys, and which half of it
         const int half = (int)(slot & 1);
         slot >>= 1;
-        if (p.cu) {
-            if (slot >= p.rest_off[d.N]) return;
-            n = warp_upper_index(p.rest_off, d.N, slot);
-            chunk = (int)(slot - p.rest_off[n]);
-        } else {
-            n = (int)(slot / p.rest_per);
-            chunk = (int)(slot - (int64_t)n * p.rest_per);
-        }
-        const WindowSpan s = window_span(p, n);
-        for (tile = 0; tile < p.sink_tiles; ++tile) {
-            const int x = rest_chunks(p, s, tile);
-            if (chunk < x) break;
-            chunk -= x;
-        }
-        if (tile >= p.sink_tiles) return;
+        RestAt at;
+        if (!rest_at(p, slot, at)) return;
+        n = at.n, tile = at.tile, chunk = at.chunk;
         row0 = tile * 128 + 64 * half;
-        if (row0 >= min(d.sinks, s.Lk)) return;
+        if (row0 >= min(d.sinks, window_span(p, n).Lk)) return;
     } else {
         int tiles;
         if (!tile_of(p, p.k_tiles, slot, d.Tk, n, row0, tiles)) return;
@@ -451,7 +439,7 @@ __device__ __forceinline__ void dkv_tile(const WindowProblem &p, float *sm, int6
     }
     // rows of sinks whose sum has other parts stay in fp32
     const int apart = rest ? kRows : row0 < d.sinks && rest_chunks(p, sp, tile) > 0 ? min(kRows, d.sinks - row0) : 0;
-    const int64_t part = rest ? slot : p.rest_slots + (int64_t)n * p.sink_tiles + tile;
+    const int64_t part = !apart ? 0 : rest ? slot : own_slot(p, n, tile);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * ty + i, in_tile = row0 + r - tile * 128;
