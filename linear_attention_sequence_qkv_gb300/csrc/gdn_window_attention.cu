@@ -353,8 +353,9 @@ cudaError_t launch_window_tables(const WindowProblem &p, int q_tile, int k_tile,
 }
 
 // The sinks' rest. A sink tile has one only where its last key lies more than `window` before the sequence's last, so that of packed
-// sequences at most Tk / (window + 128) have any. A chunk is as long as a CTA of keys walks within the window, 2048 to 32768
-// queries.
+// sequences at most Tk / (window + 128) have any. A chunk is as long as a CTA of keys walks within the window (2048 to 32768
+// queries), or longer, so that there are about eight CTAs of them for an SM: each holds 128 KB of partial sums (128 rows of 128
+// channels), and more of them than that would grow with the sinks times the queries.
 void window_rest_plan(WindowProblem &p, int shift) {
     const gdn_window_attention_desc &d = p.d;
     const int64_t group = d.Hq / d.Hk, unit = (int64_t)1 << shift, q_tiles = cdiv64(d.Tq, unit);
@@ -377,7 +378,8 @@ void window_rest_plan(WindowProblem &p, int shift) {
     else
         for (int t = 0; t < p.sink_tiles; ++t) visits += d.B * rest_tiles(t);
     const int64_t window_its = std::min<int64_t>(32768 / unit, std::max<int64_t>(2048 / unit, group * (((int64_t)d.window + 127) / unit + 1)));
-    p.rest_its = (int)window_its;
+    const int64_t even_its = visits > ((int64_t)1 << 60) / d.Hq ? 1 << 30 : cdiv64(visits * d.Hq, 8 * kSms);
+    p.rest_its = (int)std::min<int64_t>(std::max(window_its, even_its), 1 << 30);
     if (p.rest_packed) {   // at most: every tile's last chunk begun
         p.rest_slots = p.rest_all ? (int64_t)((double)visits * group / p.rest_its) + 1 + p.rest_all : 0;
     } else {

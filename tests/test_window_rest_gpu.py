@@ -1,5 +1,5 @@
 """The sinks' queries beyond the window in the window attention's backward: many tiles of sinks, packed sequences of which only
-some have such queries."""
+some have such queries, chunks that the plan makes longer."""
 import numpy as np
 import pytest
 import torch
@@ -41,3 +41,45 @@ def test_packed_sequences_with_and_without(dev, lengths, keys, Hq, Hk, d, window
     f, g = both(q, k, v, dout, kw)
     some = sorted(range(len(lengths)), key=lambda n: -lengths[n])[:6] + list(range(0, len(lengths), 300))
     check(q, k, v, dout, f, g, [(0, cuq[n], lengths[n], cuk[n], keys_[n]) for n in sorted(set(some))], d, window, sinks, f.desc.scale, dtype)
+
+
+def reference(q, k, v, dout, window, sinks, scale, rows=2048):
+    """Gradients in fp64, queries by the block against the sinks and their band."""
+    T = q.shape[0]
+    q, k, v, dout = (x.double() for x in (q, k, v, dout))
+    dq, dk, dv = (torch.zeros_like(x) for x in (q, k, v))
+    for a in range(0, T, rows):
+        b = min(a + rows, T)
+        lo = max(0, a - window + 1)
+        key = torch.cat([torch.arange(0, min(sinks, lo), device=q.device), torch.arange(lo, b, device=q.device)])
+        pos = torch.arange(a, b, device=q.device)[:, None]
+        seen = (key <= pos) & ((pos - key < window) | (key < sinks))
+        kb, vb = k[key], v[key]
+        P = torch.softmax(torch.where(seen, scale * (q[a:b] @ kb.T), -torch.inf), -1)
+        g = dout[a:b]
+        dP = g @ vb.T
+        dS = scale * P * (dP - (P * dP).sum(-1, keepdim=True))
+        dq[a:b] = dS @ kb
+        dk.index_add_(0, key, dS.T @ q[a:b])
+        dv.index_add_(0, key, P.T @ g)
+    return dq, dk, dv
+
+
+# Relative error in the 2-norm. 16 bits: half a step each for dS (or P), for delta's rounded output and for the result. fp32: a score's
+# error, (2 d + 8) 2^-24 sum |q||k| scale, is 136 x 6e-8 x 4.1 x ... = 3.3e-5 x 1.3 at most, the sums' far below it.
+@pytest.mark.parametrize("dtype,tol", [("bf16", 3 * 2.0 ** -8), ("fp16", 3 * 2.0 ** -11), ("fp32", 4.4e-5)])
+def test_chunks_that_grow_with_the_sinks(dev, dtype, tol):  # noqa: F811
+    T, H, d, window, sinks = 65536, 2, 64, 128, 4096
+    q, k, v, dout = make(dev, 1, T, T, H, H, d, dtype, q_std=1.0)
+    f, g = both(q, k, v, dout, dict(d=d, window=window, sinks=sinks))
+    # partial sums of 64 KB (128 rows of 2 x 64 in fp32): 8 x 152 chunks, rounded up for a head, one begun and one own for each of 32 tiles
+    assert g.ws_bytes <= (8 * 152 + H * (1 + 2 * 32)) * 65536 + (1 << 20)
+    for h in range(H):
+        at = lambda x: x[0].view(T, H, d)[:, h] if x.is_contiguous() else x[0].reshape(T, H, d)[:, h]  # noqa: E731
+        ref = reference(at(q), at(k), at(v), at(dout), window, sinks, f.desc.scale)
+        for n, r in zip(("dq", "dk", "dv"), ref):
+            x = at(getattr(g, n)).double()
+            for what, part in (("all", slice(None)), ("sinks", slice(0, sinks))):
+                rel = float((x[part] - r[part]).norm() / r[part].norm())
+                print(f"[rest] {dtype} head {h} {n} {what}: {rel:.2e}")
+                assert rel <= tol, (n, what, rel)
