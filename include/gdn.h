@@ -777,7 +777,8 @@ int gdn_window_attention_backward(const gdn_window_attention_desc *d, const void
  *
  * gdn_window_cache_write puts tokens at positions lengths[n], lengths[n] + 1, ... of each
  * sequence n, those that a later one of the same call would replace left out.
- *   k, v           [B,Tk,Hk*d] at their strides (d->Tq and d->Hq are not read)
+ *   k, v           [B,Tk,Hk*d] at their strides (Tq, Hq, scale and q's strides have no effect, but
+ *                  have to be valid, as gdn_window_attention_desc_init fills them: Hq % Hk == 0)
  *   cu_seqlens     NULL, or int32 [N+1] (then B == 1): offsets into k and v
  *   workspace      >= gdn_window_cache_write_workspace_bytes(), 256-byte aligned (status
  *                  word; a malformed cu_seqlens writes nothing else)
