@@ -74,6 +74,10 @@ __device__ __forceinline__ float warp_max(float v) {
     return v;
 }
 
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
 // upper_index for x below arr[N], by a whole warp: 32 entries at a time, so that a CTA begins after two round trips to memory where
 // 64 sequences take the search by halves six (32768 tokens in 16 sequences, training step: 2336 -> 2311 us)
 __device__ __forceinline__ int warp_upper_index(const int32_t *arr, int N, int64_t x) {

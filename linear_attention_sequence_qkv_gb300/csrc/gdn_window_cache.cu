@@ -92,9 +92,6 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
 __device__ __forceinline__ float of_rank(const float *own, uint32_t rank) {
     uint32_t a;
     float v;
@@ -551,9 +548,9 @@ cudaError_t launch_split(K kernel, const CacheProblem &p, int heads, int width, 
     const int64_t units = (int64_t)d.B * d.Hk * head_tiles;
     const int splits = step_splits(d, units);
     if (units * splits > 0x7fffffff) return cudaErrorInvalidValue;
-    const size_t smem = (size_t)kStepWarps * heads * (width + 2) * 4;
+    static_assert(kStepWarps * 16 * (128 + 2) * 4 <= 40 * 1024, "what every kernel has without asking, beside its static part");
+    const size_t smem = (size_t)kStepWarps * heads * (width + 2) * 4;   // at most 16 heads of 128
     cudaError_t e = cudaSuccess;
-    if (smem > 40 * 1024 && (e = allow_shared(kernel, 64 * 1024)) != cudaSuccess) return e;
     if (splits > 8 && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * splits));

@@ -314,9 +314,6 @@ __device__ __forceinline__ void dq_tile(const WindowProblem &p, float *sm, int64
     store_rows<T, D>((T *)p.dq + (tok0 * d.Hq + h) * d.d, gst, d.d, ty, tx, 0, rows, o, one);
 }
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
 __device__ __forceinline__ float4 of_rank(const float *own, uint32_t rank) {
     uint32_t a;
     float4 v;
