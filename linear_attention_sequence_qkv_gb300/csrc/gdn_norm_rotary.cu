@@ -447,8 +447,7 @@ __global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) norm_rotary_vectors_
                             ss = fma2(xs[k][e], xs[k][e], ss);
                             st = fma2(mul2(dz[k][e], wo[k][e]), xs[k][e], st);
                         }
-                    // a team whose run is shorter than its warp's has no head here (and eps may be 0: no 0 x inf into the sums)
-                    const float sum = team_sum<TEAM>(ss.x + ss.y), rstd = r0 + j < runs ? rsqrtf(sum / d.d + p.n.eps) : 0.0f;
+                    const float rstd = rsqrtf(team_sum<TEAM>(ss.x + ss.y) / d.d + p.n.eps);
                     const float2 r2 = splat2(rstd), mean = splat2(-rstd * team_sum<TEAM>(st.x + st.y) / d.d);   // of t xh
 #pragma unroll
                     for (int k = 0; k < K; ++k) {
@@ -456,7 +455,8 @@ __global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) norm_rotary_vectors_
 #pragma unroll
                         for (int e = 0; e < NP; ++e) {
                             const float2 xh = mul2(xs[k][e], r2);
-                            acc[which][k][e] = fma2(dz[k][e], xh, acc[which][k][e]);
+                            // (a team whose run is shorter than its warp's has no head here, and eps may be 0: no 0 x inf into the sums)
+                            if (r0 + j < runs) acc[which][k][e] = fma2(dz[k][e], xh, acc[which][k][e]);
                             set_pair<T, V>(y, e, mul2(r2, fma2(xh, mean, mul2(dz[k][e], wo[k][e]))));
                         }
                         if (r0 + j < runs && at.c[k] >= 0) *(decltype(y.raw) *)(dst + (int64_t)(a + r0 + j - first) * d.d + at.c[k]) = y.raw;
