@@ -341,7 +341,9 @@ __global__ void __launch_bounds__(32 * kStepWarps, 2) step_mma(const __grid_cons
 }
 
 // fp32 with 16-byte aligned rows of up to 32 NG channels, a multiple of 4: 8 lanes share a key, a lane has the channels
-// 32 i + 4 (lane % 8) .. + 3, a warp four keys at a time for up to 4 heads. Bound by HBM, products and sums in fp32.
+// 32 i + 4 (lane % 8) .. + 3, a warp four keys at a time for up to 4 heads. Products and sums in fp32. Bound by HBM where a head of
+// keys serves one of queries (128 sequences of 2052 keys, 16 heads of 128: 4.3 GB in 703 us, 90 % of the copy rate), else by the
+// products of a step, during which no next keys are on their way (256 sequences, 32 heads on 8: 935 us, 68 %).
 template <int NG>
 __global__ void __launch_bounds__(32 * kStepWarps) step_f32(const __grid_constant__ CacheProblem p, int splits, int head_tiles) {
     constexpr int kHeads = 4, kKeys = 2;   // heads of a CTA; keys of a lane's group in flight
@@ -530,7 +532,10 @@ bool step_aligned(const CacheProblem &p) {
 }
 
 // CTAs per sequence and head: as many as make the rounds of two CTAs per SM cheapest, a CTA costing its keys and a start
-// that is worth about 100 KB of them
+// that is worth about 100 KB of them. By measurement, us a call with 1 | 2 | 4 | 8 | 16 (cache not in L2; * the rule's):
+//   1 sequence of 1028, 32 heads of 128 on 8, bf16:  27 | 21 | 17 | 15* | 15    of 8196:  148 | 83 | 48 | 31 | 23*
+//   8 of 1028, 32 on 16:  33 | 27* | 33 | 46 | 85     32 of them:  68* | 83 | 95 | 142 | 296
+//   64 of 4100, 8 heads of 64, fp32:  295 | 244 | 224* | 267 | 367
 int step_splits(const gdn_window_attention_desc &d, int64_t units) {
     const int64_t bytes = ((int64_t)d.sinks + d.window) * d.d * 2 * (int64_t)act_size(d.dtype);
     int best = 1;

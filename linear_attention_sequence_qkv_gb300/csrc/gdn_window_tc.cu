@@ -9,8 +9,10 @@
 // other. They are two heads that share keys and values where the group's size is even (the
 // same mask, half the traffic of K and V), else two neighbouring tiles of one head.
 // Softmax in one pass: a row's maximum m is raised, and O scaled, only where it grew by more
-// than 2^8 (P stays below 2^8, in range of fp16, which takes it times 2^6), so O is rarely read back. P is rounded to the
-// tensors' type, which the second product takes; sums, maxima and O are fp32.
+// than 2^8 (P stays below 2^8; fp16 takes it times 2^6), so O is rarely read back. P is rounded
+// to the tensors' type, which the second product takes; sums, maxima and O are fp32. The methods
+// are published ones: one pass by Milakov and Gimelshein (2018), tiles in turns for the tensor
+// cores before these (2024), a maximum that moves only where it has to for these (2025).
 //
 // Bound by the tensor cores where rows see many keys (causal, 16384 tokens of 16 heads of 128 on
 // 8: 702 us, 1566 TFLOP/s), else by a CTA's start and end (about 8000 cycles, in which nothing
