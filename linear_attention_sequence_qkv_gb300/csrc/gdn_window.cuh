@@ -93,6 +93,11 @@ __device__ __forceinline__ int warp_upper_index(const int32_t *arr, int N, int64
     return lo;
 }
 
+// A query that sees one key has P = 1 and no scores' gradient; dP - delta of rounded sums is not exactly 0, so its dq is stored
+// as 0, and dk of keys that only such queries see (in the sums of other keys it is within their rounding)
+__device__ __forceinline__ bool sees_one(int64_t pos, int window, int sinks) { return pos == 0 || (window == 1 && sinks == 0); }
+__device__ __forceinline__ bool seen_by_such(int Lk, int window, int sinks) { return Lk == 1 || (window == 1 && sinks == 0); }
+
 // The first key of the window of a query at `pos`, and the number of sinks before it
 __device__ __forceinline__ int window_first(int pos, int window) { return pos >= window ? pos - window + 1 : 0; }
 

@@ -388,7 +388,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_backward_tc(const __grid_c
         const int c0 = KEYS ? 0 : half * kCols;
         // rows of sinks whose sum has other parts stay in fp32
         const int apart = !KEYS || !ok ? 0 : rest ? 128 : row0 < d.sinks && rest_chunks(p, sp, tile) > 0 ? min(128, d.sinks - row0) : 0;
-        const float2 back = splat2(KEYS && half ? kWeightUnit<T> : d.scale * kWeightUnit<T> / up);   // out of the operands' units
+        const bool none = KEYS ? !half && seen_by_such(sp.Lk, d.window, d.sinks) : sees_one((int64_t)past + row0 + r, d.window, d.sinks);
+        const float2 back = splat2(none ? 0.0f : KEYS && half ? kWeightUnit<T> : d.scale * kWeightUnit<T> / up);   // out of the operands' units
         const int64_t part_slot = !apart ? 0 : rest ? slot : own_slot(p, n, tile);
 #pragma unroll
         for (int q = 0; q < kCols; q += 32) {

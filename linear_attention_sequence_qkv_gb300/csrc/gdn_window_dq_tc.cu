@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_pair(const __grid_const
         // ---- dQ, through the head's own Q in shared memory (no product reads it any more)
         const uint32_t from = tbase + L::kAcc + b * D + ((uint32_t)(warp & 3) << 21);
         unsigned char *stage = sm + b * 2 * L::kA;
-        const float2 back = splat2(d.scale * kWeightUnit<T> / up);   // out of the operands' units
+        const float2 back = splat2(sees_one((int64_t)past + row0 + r, d.window, d.sinks) ? 0.0f : d.scale * kWeightUnit<T> / up);   // out of the operands' units
 #pragma unroll
         for (int q = 0; q < D; q += 32) {
             float o[32];

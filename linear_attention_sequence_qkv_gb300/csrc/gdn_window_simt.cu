@@ -310,7 +310,9 @@ __device__ __forceinline__ void dq_tile(const WindowProblem &p, float *sm, int64
         __syncthreads();
         tile_add<D>(S, kW, K, kWalk, ty, tx, o);
     }
-    const float one[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+    float one[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) one[i] = sees_one((int64_t)past + i0 + 4 * ty + i, d.window, d.sinks) ? 0.0f : 1.0f;
     store_rows<T, D>((T *)p.dq + (tok0 * d.Hq + h) * d.d, gst, d.d, ty, tx, 0, rows, o, one);
 }
 
@@ -450,7 +452,8 @@ __device__ __forceinline__ void dkv_tile(const WindowProblem &p, float *sm, int6
     }
     const float one[4] = {1.0f, 1.0f, 1.0f, 1.0f};
     const int64_t at = ((sp.k0 + row0) * d.Hk + hk) * d.d, st = (int64_t)d.Hk * d.d;
-    store_rows<T, D>((T *)p.dk + at, st, d.d, ty, tx, apart, rows, dk, one);
+    const float k1 = seen_by_such(sp.Lk, d.window, d.sinks) ? 0.0f : 1.0f, of_k[4] = {k1, k1, k1, k1};
+    store_rows<T, D>((T *)p.dk + at, st, d.d, ty, tx, apart, rows, dk, of_k);
     store_rows<T, D>((T *)p.dv + at, st, d.d, ty, tx, apart, rows, dv, one);
 }
 
