@@ -12,7 +12,7 @@
 namespace gdn {
 namespace {
 
-// The sum of c over the threads before this one, and over all (1024 threads; the next call may follow at once)
+// The sum of c over the threads before this one, and over all (the next call may follow at once; sums begins as zeros)
 __device__ __forceinline__ int before_thread(int c, int32_t (&sums)[32], int &all) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int x = c;
@@ -48,6 +48,8 @@ __global__ void __launch_bounds__(1024) window_tables_kernel(const __grid_consta
     if (p.cuk != p.cu) ok = seqlens_ok(p.cuk, d.N, d.Tk) && ok;
     if (threadIdx.x == 0) *p.status = ok ? GDN_OK : GDN_ERR_DEVICE_SEQLENS;
     __shared__ int32_t sums[32];
+    if (threadIdx.x < 32) sums[threadIdx.x] = 0;
+    __syncthreads();
     for (int which = 0; which < 2; ++which) {
         const int32_t *cu = which ? p.cuk : p.cu;
         int32_t *to = which ? p.k_tiles : p.q_tiles;
@@ -63,38 +65,6 @@ __global__ void __launch_bounds__(1024) window_tables_kernel(const __grid_consta
         }
         if (threadIdx.x == 0) to[d.N] = before;
     }
-}
-
-// For packed sequences the sink tiles with a rest of those before each one, and for all the chunks before each such tile
-__global__ void __launch_bounds__(1024) window_rest_table(const __grid_constant__ WindowProblem p) {
-    __shared__ int32_t sums[32];
-    if (*p.status != GDN_OK) return;
-    int tiles = p.sink_tiles, all;
-    if (p.rest_packed) {
-        tiles = 0;
-        for (int base = 0; base < p.d.N; base += blockDim.x) {
-            const int n = base + threadIdx.x;
-            const int at = tiles + before_thread(n < p.d.N ? rest_count(p, window_span(p, n)) : 0, sums, all);
-            if (n < p.d.N) p.rest_of[n] = at;
-            tiles += all;
-        }
-        if (threadIdx.x == 0) p.rest_of[p.d.N] = tiles;
-        __syncthreads();   // they are read below
-    }
-    const int total = p.rest_packed ? p.rest_all : p.sink_tiles;
-    int before = 0;
-    for (int base = 0; base < total; base += blockDim.x) {
-        const int x = base + threadIdx.x;
-        int c = 0;
-        if (x < tiles) {
-            const int n = p.rest_packed ? upper_index(p.rest_of, p.d.N, x) : 0;
-            c = rest_chunks(p, window_span(p, n), x - (p.rest_packed ? p.rest_of[n] : 0));
-        }
-        const int at = before + before_thread(c, sums, all);
-        if (x < total) p.rest_tiles[x] = at;
-        before += all;
-    }
-    if (threadIdx.x == 0) p.rest_tiles[total] = before;
 }
 
 // fp16's norms (gdn_window_tc.cuh): the largest squared norms of a CTA's rows, per sequence and head of keys, go through shared
@@ -154,7 +124,8 @@ struct RowAt {
 // norms are taken besides, and a CTA looks through `v_len` rows of v: 134 MB more, 150 us.
 template <typename T, bool VEC, int ROW>
 __global__ void __launch_bounds__(256, 3) window_delta(const __grid_constant__ WindowProblem p, int team, int64_t len, int64_t v_len) {
-    if (*p.status != GDN_OK) return;
+    if (p.cu && *p.status != GDN_OK) return;
+    if (!p.cu && blockIdx.x == 0 && threadIdx.x == 0) *p.status = GDN_OK;
     const gdn_window_attention_desc &d = p.d;
     constexpr bool kNorms = VEC && ROW == 1 && std::is_same<T, __half>::value;
     __shared__ uint32_t table[kNorms ? kTable : 1];
@@ -288,16 +259,105 @@ __global__ void __launch_bounds__(256, 3) window_delta(const __grid_constant__ W
     }
 }
 
-unsigned row_blocks(int64_t rows, int per) { return (unsigned)std::min<int64_t>(std::max<int64_t>(cdiv64(rows, per), 1), 0x7fffffff); }
+// delta of a short sequence's first positions as sum_j P_j (grad_out . v_j), a warp for each and head. With 16-bit types the output is
+// rounded, and where a few keys share the weight dP - delta cancels: dq of 2 tokens (one head of 64, scores of deviation 2, bf16, the
+// worst of 30) was off by 0.83, of 4 by 0.020, of 8 by 0.0075, of 16 by 0.0056, where rounding dS and dq costs 0.0035. From
+// 64 keys on the other positions hold it to 0.0040, and such sequences are left as they are: the launch costs 6 us of a call.
+constexpr int kFew = 8, kShort = 64;
+template <typename T>
+__device__ __forceinline__ void few_rows(const WindowProblem &p, int64_t first, int64_t apart) {
+    const gdn_window_attention_desc &d = p.d;
+    const int lane = threadIdx.x & 31;
+    const int64_t total = (int64_t)d.N * (kFew - 1) * d.Hq;
+    for (int64_t x = first; x < total; x += apart) {
+        const int head = (int)(x % d.Hq), hk = head / (d.Hq / d.Hk);
+        const int64_t at = x / d.Hq;
+        const int n = (int)(at / (kFew - 1)), pos = (int)(at - (int64_t)n * (kFew - 1)) + 1;
+        const WindowSpan s = window_span(p, n);
+        const int64_t i = (int64_t)pos - s.Lk + s.Lq;
+        if (i < 0 || i >= s.Lq || s.Lk > kShort) continue;
+        const T *q = (const T *)p.q + s.qoff + i * d.q_stride_t + (int64_t)head * d.d, *g = (const T *)p.dout + ((s.q0 + i) * d.Hq + head) * d.d;
+        const T *k = (const T *)p.k + s.koff + (int64_t)hk * d.d, *v = (const T *)p.v + s.voff + (int64_t)hk * d.d;
+        float sc[kFew], dp[kFew];
+        bool see[kFew];
+#pragma unroll
+        for (int j = 0; j < kFew; ++j) sc[j] = dp[j] = 0.0f, see[j] = j <= pos && (pos - j < d.window || j < d.sinks);
+#pragma unroll 2
+        for (int c = lane; c < d.d; c += 32) {
+            const float qc = to_f<T>(q[c]), gc = to_f<T>(g[c]);
+#pragma unroll
+            for (int j = 0; j < kFew; ++j)
+                if (see[j]) sc[j] = fmaf(qc, to_f<T>(k[j * d.k_stride_t + c]), sc[j]), dp[j] = fmaf(gc, to_f<T>(v[j * d.v_stride_t + c]), dp[j]);
+        }
+        float top = -INFINITY, l = 0.0f, sum = 0.0f;
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+#pragma unroll
+            for (int j = 0; j < kFew; ++j) sc[j] += __shfl_xor_sync(0xffffffffu, sc[j], o), dp[j] += __shfl_xor_sync(0xffffffffu, dp[j], o);
+#pragma unroll
+        for (int j = 0; j < kFew; ++j) {
+            sc[j] = see[j] ? sc[j] * d.scale : -INFINITY;
+            top = fmaxf(top, sc[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kFew; ++j)
+            if (see[j]) {
+                const float w = expf(sc[j] - top);
+                l += w, sum = fmaf(w, dp[j], sum);
+            }
+        if (lane == 0) p.delta[head * ((int64_t)d.B * d.Tq) + s.q0 + i] = sum / l;
+    }
+}
+
+// For packed sequences the sink tiles with a rest of those before each one, and for all the chunks before each such tile
+__device__ __forceinline__ void rest_table(const WindowProblem &p) {
+    __shared__ int32_t sums[32];
+    if (threadIdx.x < 32) sums[threadIdx.x] = 0;
+    __syncthreads();
+    int tiles = p.sink_tiles, all;
+    if (p.rest_packed) {
+        tiles = 0;
+        for (int base = 0; base < p.d.N; base += blockDim.x) {
+            const int n = base + threadIdx.x;
+            const int at = tiles + before_thread(n < p.d.N ? rest_count(p, window_span(p, n)) : 0, sums, all);
+            if (n < p.d.N) p.rest_of[n] = at;
+            tiles += all;
+        }
+        if (threadIdx.x == 0) p.rest_of[p.d.N] = tiles;
+        __syncthreads();   // they are read below
+    }
+    const int total = p.rest_packed ? p.rest_all : p.sink_tiles;
+    int before = 0;
+    for (int base = 0; base < total; base += blockDim.x) {
+        const int x = base + threadIdx.x;
+        int c = 0;
+        if (x < tiles) {
+            const int n = p.rest_packed ? upper_index(p.rest_of, p.d.N, x) : 0;
+            c = rest_chunks(p, window_span(p, n), x - (p.rest_packed ? p.rest_of[n] : 0));
+        }
+        const int at = before + before_thread(c, sums, all);
+        if (x < total) p.rest_tiles[x] = at;
+        before += all;
+    }
+    if (threadIdx.x == 0) p.rest_tiles[total] = before;
+}
+
+// Between delta and the gradients: CTA 0 makes the tables of the sinks' rest, the others the first positions' delta
+template <typename T>
+__global__ void __launch_bounds__(256, 3) window_between(const __grid_constant__ WindowProblem p, int table) {
+    if (*p.status != GDN_OK) return;
+    if (table && blockIdx.x == 0) rest_table(p);
+    else if (sizeof(T) == 2) few_rows<T>(p, (int64_t)(blockIdx.x - table) * 8 + (threadIdx.x >> 5), (int64_t)(gridDim.x - table) * 8);
+}
 
 template <typename T>
 cudaError_t backward_any(WindowProblem &p, cudaStream_t s) {
     const bool tc = (int64_t)p.d.B * p.d.Tq > 0 && p.d.Tk > 0 && window_tc_supports(p);
     if (!tc) p.norms = nullptr;
-    cudaError_t e = launch_window_tables(p, tc ? 128 : 64, tc ? 128 : 64, s);
-    if (e != cudaSuccess) return e;
     const int64_t rows = (int64_t)p.d.B * p.d.Tq * p.d.Hq;
     constexpr int N = 16 / (int)sizeof(T);
+    cudaError_t e = cudaSuccess;   // without packing and norms to begin from 0, delta sets the status word
+    if ((p.cu || p.norms || !rows) && (e = launch_window_tables(p, tc ? 128 : 64, tc ? 128 : 64, s)) != cudaSuccess) return e;
     if (rows && p.d.d % N == 0 && ptr_aligned(p.out_in, 16) && ptr_aligned(p.dout, 16)) {
         int team = 1;
         while (team < 32 && team * N < p.d.d) team *= 2;
@@ -308,11 +368,14 @@ cudaError_t backward_any(WindowProblem &p, cudaStream_t s) {
         if (p.d.d <= 32 * N) window_delta<T, true, 1><<<blocks, 256, 0, s>>>(p, team, len, v_len);
         else window_delta<T, true, 2><<<blocks, 256, 0, s>>>(p, team, len, v_len);
     } else if (rows) {
-        window_delta<T, false, 1><<<row_blocks(rows, 8), 256, 0, s>>>(p, 32, 0, 0);
+        window_delta<T, false, 1><<<(unsigned)std::min<int64_t>(cdiv64(rows, 8), 64 * kSms), 256, 0, s>>>(p, 32, 0, 0);
     }
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     window_rest_plan(p, tc ? 7 : 6);
-    if ((e = launch_window_rest_table(p, s)) != cudaSuccess) return e;
+    const int table = p.sink_tiles > 0 && (p.rest_packed || p.sink_tiles > 1);   // one tile a row: no table is read
+    const int few = sizeof(T) == 4 || !rows || (!p.rest_packed && p.d.Tk > kShort) ? 0 : (int)std::min<int64_t>(cdiv64((int64_t)p.d.N * (kFew - 1) * p.d.Hq, 8), 16 * kSms);
+    if (table + few) window_between<T><<<table + few, 256, 0, s>>>(p, table);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     return tc ? launch_window_backward_tc(p, s) : launch_window_backward_simt(p, s);
 }
 
@@ -392,12 +455,6 @@ void window_rest_plan(WindowProblem &p, int shift) {
 size_t window_partial_bytes(const WindowProblem &p) {
     if (p.rest_slots == 0) return 0;
     return (size_t)(p.rest_slots + p.rest_all) * p.d.Hk * p.sink_rows * 2 * (p.d.d <= 64 ? 64 : p.d.d <= 128 ? 128 : 256) * 4;
-}
-
-cudaError_t launch_window_rest_table(const WindowProblem &p, cudaStream_t s) {
-    if (p.sink_tiles == 0 || (!p.rest_packed && p.sink_tiles == 1)) return cudaSuccess;   // one tile a row: no table is read
-    window_rest_table<<<1, 1024, 0, s>>>(p);
-    return cudaGetLastError();
 }
 
 int window_check_desc(const gdn_window_attention_desc *d, bool packed) {

@@ -109,10 +109,9 @@ cudaError_t launch_window_sink_sums(const WindowProblem &p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// fills the chunks' part of p from the sizes, for tiles of 2^shift queries; the bytes of the partial sums; the tables
+// fills the chunks' part of p from the sizes, for tiles of 2^shift queries; the bytes of the partial sums
 // (gdn_window_attention.cu)
 void window_rest_plan(WindowProblem &p, int shift);
 size_t window_partial_bytes(const WindowProblem &p);
-cudaError_t launch_window_rest_table(const WindowProblem &p, cudaStream_t s);
 
 }  // namespace gdn
