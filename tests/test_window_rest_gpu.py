@@ -83,3 +83,22 @@ def test_chunks_that_grow_with_the_sinks(dev, dtype, tol):  # noqa: F811
                 rel = float((x[part] - r[part]).norm() / r[part].norm())
                 print(f"[rest] {dtype} head {h} {n} {what}: {rel:.2e}")
                 assert rel <= tol, (n, what, rel)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("lengths,Hq,Hk,d,window,sinks", [([900, 0, 30, 1300, 129, 1, 500], 4, 2, 64, 50, 300), ([3] * 500 + [700], 3, 1, 128, 130, 4),
+                                                          ([2000], 2, 2, 96, 7, 1500), ([300, 300], 6, 3, 33, 20, 140), ([60], 8, 1, 64, 9, 3)])
+def test_nothing_is_written_behind_the_workspace(dev, lengths, Hq, Hk, d, window, sinks, dtype):  # noqa: F811
+    at = np.cumsum([0] + lengths).tolist()
+    q, k, v, dout = make(dev, 1, at[-1], at[-1], Hq, Hk, d, dtype)
+    kw = dict(d=d, window=window, sinks=sinks, cu_seqlens=torch.tensor(at, dtype=torch.int32, device=dev))
+    f = gdn.window_attention_forward(q, k, v, **kw)
+    need = gdn.gdn_window_attention_backward_workspace_bytes(f.desc)
+    big = torch.full((need + 2 * 4096,), 0xa5, dtype=torch.uint8, device=dev)
+    g = gdn.alloc_window_attention_grads(f.desc, dev)
+    g.workspace = big[4096:4096 + need]
+    gdn.window_attention_backward(q, k, v, f.out, f.lse, dout, grads=g, **kw)
+    assert gdn.gdn_device_status(g.workspace) == gdn.GDN_OK
+    assert bool((big[:4096] == 0xa5).all()) and bool((big[4096 + need:] == 0xa5).all())
+    check(q, k, v, dout, f, g, [(0, at[n], lengths[n], at[n], lengths[n]) for n in sorted(set(np.argsort(lengths)[-4:].tolist()))], d, window, sinks,
+          f.desc.scale, dtype)
